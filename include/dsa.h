@@ -65,7 +65,8 @@ typedef enum {
     DSA_ERR_WORKSPACE = 3,    /* workspace pointer missing or smaller than required */
     DSA_ERR_CUDA = 4,         /* a CUDA runtime/driver call or launch failed */
     DSA_ERR_TIMEOUT = 5,      /* a bounded device-side wait gave up (see dsa_check_device_error) */
-    DSA_ERR_BAD_INDEX = 6     /* idx named a pool outside 0..elig(t)-1 (entry skipped) */
+    DSA_ERR_BAD_INDEX = 6,    /* idx named a pool outside 0..elig(t)-1 (entry skipped) */
+    DSA_ERR_BAD_PAGE = 7      /* a page, length or offset outside the paged cache (skipped; dsa_decode.h) */
 } dsa_status;
 
 typedef enum { DSA_FP32 = 0, DSA_BF16 = 1 } dsa_dtype;
@@ -289,7 +290,8 @@ dsa_status dsa_layer_bwd(const dsa_dims *dims, const void *q, const void *k, con
 /* Synchronise `stream`, then read and clear the device error word that the
  * kernels set instead of trapping.  Returns DSA_OK, DSA_ERR_TIMEOUT (a
  * bounded wait gave up; the kernel freed its resources and returned),
- * DSA_ERR_BAD_INDEX, or DSA_ERR_CUDA if the synchronisation itself failed. */
+ * DSA_ERR_BAD_INDEX, DSA_ERR_BAD_PAGE, or DSA_ERR_CUDA if the synchronisation
+ * itself failed. */
 dsa_status dsa_check_device_error(dsa_stream_t stream);
 
 /* Test and measurement hook: the route dsa_indexer_topk (and so

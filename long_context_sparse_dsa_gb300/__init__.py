@@ -10,8 +10,11 @@ Entry points (same names as the C ABI, without the ``dsa_`` prefix):
 pool_keys, indexer_score, topk, indexer_topk, sparse_attn_fwd, sparse_attn_bwd, sparse_attn_bwd_det,
 layer_fwd, layer_bwd, check_device_error, workspace_bytes, indexer_topk_workspace_bytes,
 bwd_workspace_bytes,
-validate_dims, layer_fwd_noalloc; and the measurement probe probe_traffic
-(``include/dsa_probe.h``).
+validate_dims, layer_fwd_noalloc; the measurement probe probe_traffic
+(``include/dsa_probe.h``); and decoding from a paged cache (``decode.py``,
+``include/dsa_decode.h``): cache_append, decode_indexer_topk, decode_attn,
+decode_step, with PagedCache, alloc_paged_cache, make_rotation,
+decode_workspace_bytes, alloc_decode_workspace, validate_decode_dims.
 """
 from __future__ import annotations
 
@@ -26,7 +29,7 @@ INCLUDE_DIR = os.path.join(os.path.dirname(_HERE), "include")
 HEADER_PATH = os.path.join(INCLUDE_DIR, "dsa.h")
 
 DSA_OK, DSA_ERR_INVALID_ARG, DSA_ERR_UNSUPPORTED, DSA_ERR_WORKSPACE = 0, 1, 2, 3
-DSA_ERR_CUDA, DSA_ERR_TIMEOUT, DSA_ERR_BAD_INDEX = 4, 5, 6
+DSA_ERR_CUDA, DSA_ERR_TIMEOUT, DSA_ERR_BAD_INDEX, DSA_ERR_BAD_PAGE = 4, 5, 6, 7
 DSA_FP32, DSA_BF16 = 0, 1
 
 
@@ -85,6 +88,7 @@ def _load():
             "dsa_set_attn_fwd_route": ([i32], ctypes.c_int),
             "dsa_selftest_bounded_wait": ([u32, P], ctypes.c_int),
             "dsa_probe_traffic": ([D, P, P, P, P, P, P], ctypes.c_int),
+            **_decode_signatures(D),
         }
         for name, (args, res) in sig.items():
             f = getattr(lib, name)
@@ -306,3 +310,9 @@ def alloc_forward_buffers(dims: Dims, device="cuda", o_acc: bool = False) -> Lay
         ws=torch.empty((ws_bytes,), dtype=torch.uint8, device=device),
         o_acc=torch.empty((dims.L, dims.Hq, dims.d), dtype=torch.float32, device=device) if o_acc else None,
     )
+
+
+from .decode import (PagedCache, Rotation, alloc_decode_workspace, alloc_paged_cache,  # noqa: E402
+                     cache_append, decode_attn, decode_indexer_topk, decode_step, decode_workspace_bytes,
+                     make_rotation, validate_decode_dims)
+from .decode import _signatures as _decode_signatures  # noqa: E402

@@ -215,6 +215,7 @@ const char* dsa_status_string(dsa_status st) {
     case DSA_ERR_CUDA: return "CUDA error";
     case DSA_ERR_TIMEOUT: return "device-side wait timed out";
     case DSA_ERR_BAD_INDEX: return "idx named a pool outside the query's causal range";
+    case DSA_ERR_BAD_PAGE: return "a page, length or offset outside the paged cache";
   }
   return "unknown status";
 }
@@ -420,6 +421,8 @@ dsa_status dsa_check_device_error(dsa_stream_t stream) {
   if (e != cudaSuccess) return cuda_status(e, "reading the device error word");
   if (word & dsa::DSA_DEV_ERR_TIMEOUT) return fail(DSA_ERR_TIMEOUT, "a bounded device wait gave up (word 0x%x)", word);
   if (word & dsa::DSA_DEV_ERR_BAD_INDEX) return fail(DSA_ERR_BAD_INDEX, "idx held a pool outside elig(t) (word 0x%x)", word);
+  if (word & dsa::DSA_DEV_ERR_BAD_PAGE)
+    return fail(DSA_ERR_BAD_PAGE, "a page, length or offset lay outside the paged cache (word 0x%x)", word);
   return DSA_OK;
 }
 

@@ -18,6 +18,7 @@ namespace dsa {
 // Device error word bits (read and cleared by dsa_check_device_error).
 constexpr unsigned DSA_DEV_ERR_TIMEOUT = 1u;
 constexpr unsigned DSA_DEV_ERR_BAD_INDEX = 2u;
+constexpr unsigned DSA_DEV_ERR_BAD_PAGE = 4u;
 
 extern __device__ unsigned int g_dev_error;
 extern __constant__ unsigned int c_wait_limit;

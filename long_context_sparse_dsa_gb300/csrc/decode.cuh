@@ -1,0 +1,43 @@
+// decode.cuh -- what the paged decode kernels share (include/dsa_decode.h).
+//
+// A cache page holds page_size tokens = ppp pools, so the physical pool of a
+// row's pool p is  table[p / ppp] * ppp + p % ppp.  ppp is any number >= 1
+// known at launch: the division is a multiplication by a precomputed
+// reciprocal (Granlund and Montgomery, "Division by invariant integers using
+// multiplication"): with s = ceil(log2 ppp) and m = floor(2^(29+s) / ppp) + 1,
+// p / ppp = (p * m) >> (29 + s) for every p < 2^29, since 2^(29+s) < m * ppp
+// <= 2^(29+s) + 2^s.  Capacities are below 2^31 tokens, so p < 2^29 holds and
+// the product stays below 2^60.
+#pragma once
+
+#include "common.cuh"
+#include "decode.h"
+
+namespace dsa {
+
+__device__ __forceinline__ int page_of_pool(const PagedView& pv, int p) {
+  return (int)(((uint64_t)(uint32_t)p * pv.div_mul) >> pv.div_shift);
+}
+
+// Length of row b, 0 (idle) when it lies outside 0..capacity.
+__device__ __forceinline__ int row_length(const PagedView& pv, int64_t b, bool& bad) {
+  const int n = __ldg(pv.lens + b);
+  if (n < 0 || n > pv.capacity) {
+    bad = true;
+    return 0;
+  }
+  return n;
+}
+
+// Physical pool of pool p of the row whose block-table row is `trow`, given
+// its page entry (trow[page_of_pool(p)], loaded earlier by the caller); -1
+// for a page outside the cache.
+__device__ __forceinline__ int phys_pool(const PagedView& pv, int p, int col, int page, bool& bad) {
+  if ((uint32_t)page >= (uint32_t)pv.num_pages) {
+    bad = true;
+    return -1;
+  }
+  return page * pv.ppp + (p - col * pv.ppp);
+}
+
+}  // namespace dsa

@@ -1,0 +1,80 @@
+// decode.h -- host side of the paged decode kernels (internal to the
+// library).  Arguments are validated in decode_api.cu before any of these is
+// called.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+#include <cuda_runtime.h>
+
+namespace dsa {
+
+// A batch of rows over the paged cache, as the kernels take it.
+struct PagedView {
+  const int32_t* lens;    // [batch]
+  const int32_t* table;   // [batch, cols]
+  int64_t num_pages;
+  int capacity;           // longest row, tokens
+  int cols;               // block-table columns
+  int ppp;                // pools per page
+  uint32_t div_mul;       // page_of_pool's multiplier and shift
+  int div_shift;
+};
+
+inline PagedView make_paged_view(const int32_t* lens, const int32_t* table, int64_t num_pages, int page_size,
+                                 int64_t capacity) {
+  PagedView v;
+  v.lens = lens;
+  v.table = table;
+  v.num_pages = num_pages;
+  v.capacity = (int)capacity;
+  v.cols = (int)((capacity + page_size - 1) / page_size);
+  v.ppp = page_size / 4;
+  int s = 0;
+  while ((1 << s) < v.ppp) ++s;
+  v.div_mul = (uint32_t)(((uint64_t)1 << (29 + s)) / (uint64_t)v.ppp + 1);
+  v.div_shift = 29 + s;
+  return v;
+}
+
+struct RotationArgs {
+  const uint64_t* turns;   // nullptr: no rotation
+  int dim;
+  int interleaved;
+};
+
+struct AppendArgs {
+  PagedView pv;
+  int64_t batch, n_tokens;
+  const int32_t* offsets;   // nullptr: token b belongs to row b
+  int Hq, d, di;
+  const void *k, *v, *k_idx, *q;
+  void *q_out, *k_out;
+  void *ck, *cv, *ckpool, *cktail;   // the cache
+  RotationArgs rot;
+};
+cudaError_t launch_cache_append(bool bf16, const AppendArgs& a, cudaStream_t s);
+
+// Scores of one query per row over the paged pool keys: scores [batch, P].
+cudaError_t launch_decode_scores(bool bf16, const PagedView& pv, int64_t batch, int Hi, int di, const void* q_idx,
+                                 const float* w, const void* kpool, float* scores, int64_t P, cudaStream_t s);
+// Top-k of each score row's first lens[b]/4 entries.
+cudaError_t launch_decode_topk(const PagedView& pv, int64_t batch, int k, const float* scores, int64_t P, int32_t* idx,
+                               cudaStream_t s);
+size_t decode_scores_bytes(int64_t batch, int64_t P);
+
+struct DecodeAttnArgs {
+  PagedView pv;
+  int64_t batch;
+  int Hq, d, k;
+  float scale;
+  const void *q, *ck, *cv;
+  const int32_t* idx;   // nullptr: every token of the row
+  void* o;
+  float* lse;
+  float* ws;            // partial results: decode_attn_ws_bytes
+};
+size_t decode_attn_ws_bytes(int64_t batch, int Hq, int d);
+cudaError_t launch_decode_attn(bool bf16, const DecodeAttnArgs& a, cudaStream_t s);
+
+}  // namespace dsa

@@ -1,0 +1,184 @@
+// decode_scores.cu -- indexer scores of one query per row over the paged pool
+// keys: s[b,p] = sum_h w[b,h] * max(0, q_idx[b,h,:] . kpool[p,:]), p < lens[b]/4.
+//
+// Bound: HBM, each pool key is read once (di * 2 bytes for 2 * Hi * di flops:
+// at most 8 flops a byte).  bf16: m16n8k16 MMAs with 16 pools on M and the
+// heads (padded to 8 with zeros) on N.  A dot product may take its terms in
+// any order as long as both operands agree, so a lane feeds the MMAs straight
+// from its 16-byte global loads: lane (g, qi) holds the 16-byte chunks qi,
+// qi + 4, .. of pool rows g and g + 8, and the same chunks of head g, and its
+// words are the MMA's k positions in that order.  No shared memory.
+// fp32: a pool row is spread over di/8 lanes, each holding its 8 channels of
+// all heads; the heads' partial dot products are reduced across the lanes.
+#include "decode.cuh"
+#include "decode.h"
+
+namespace dsa {
+
+constexpr int kScoreWarps = 4;
+constexpr int kScorePoolsPerWarp = 64;
+constexpr int kScorePools = kScoreWarps * kScorePoolsPerWarp;   // pools per CTA
+
+template <int DI>
+__global__ void __launch_bounds__(kScoreWarps * 32)
+    decode_scores_bf16_kernel(PagedView pv, int Hi, const uint4* __restrict__ q_idx, const float* __restrict__ w,
+                              const uint4* __restrict__ kpool, float* __restrict__ scores, int64_t P) {
+  constexpr int CH = DI / 8;     // 16-byte chunks per row
+  constexpr int CL = CH / 4;     // chunks per lane and row
+  const int64_t b = blockIdx.y;
+  bool bad = false;
+  const int n = row_length(pv, b, bad) >> 2;
+  const int lane = threadIdx.x & 31;
+  const int p0 = blockIdx.x * kScorePools + (threadIdx.x >> 5) * kScorePoolsPerWarp;
+  if (p0 >= n) return;   // bad lengths are recorded by the selection
+  const int g = lane >> 2, qi = lane & 3;
+  uint4 qf[CL];
+  float w0 = 0.f, w1 = 0.f;
+#pragma unroll
+  for (int c = 0; c < CL; ++c) qf[c] = make_uint4(0u, 0u, 0u, 0u);
+  if (g < Hi) {
+    const uint4* q = q_idx + (b * Hi + g) * CH;
+#pragma unroll
+    for (int c = 0; c < CL; ++c) qf[c] = __ldg(q + qi + 4 * c);
+  }
+  if (2 * qi < Hi) w0 = __ldg(w + b * Hi + 2 * qi);
+  if (2 * qi + 1 < Hi) w1 = __ldg(w + b * Hi + 2 * qi + 1);
+  const int32_t* trow = pv.table + b * pv.cols;
+  float* srow = scores + b * P;
+#pragma unroll
+  for (int i = 0; i < kScorePoolsPerWarp / 16; ++i) {
+    uint4 kf[2][CL];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int p = p0 + i * 16 + r * 8 + g;
+#pragma unroll
+      for (int c = 0; c < CL; ++c) kf[r][c] = make_uint4(0u, 0u, 0u, 0u);
+      if (p < n) {
+        const int col = page_of_pool(pv, p);
+        const int pp = phys_pool(pv, p, col, __ldg(trow + col), bad);
+        if (pp >= 0) {
+          const uint4* src = kpool + (int64_t)pp * CH + qi;
+#pragma unroll
+          for (int c = 0; c < CL; ++c) kf[r][c] = __ldg(src + 4 * c);
+        }
+      }
+    }
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int c = 0; c < CL; ++c) {
+      mma_bf16_16816(acc, kf[0][c].x, kf[1][c].x, kf[0][c].y, kf[1][c].y, qf[c].x, qf[c].y);
+      mma_bf16_16816(acc, kf[0][c].z, kf[1][c].z, kf[0][c].w, kf[1][c].w, qf[c].z, qf[c].w);
+    }
+    float s0 = fmaf(w1, fmaxf(acc[1], 0.f), w0 * fmaxf(acc[0], 0.f));
+    float s1 = fmaf(w1, fmaxf(acc[3], 0.f), w0 * fmaxf(acc[2], 0.f));
+    s0 += __shfl_xor_sync(0xffffffffu, s0, 1);
+    s1 += __shfl_xor_sync(0xffffffffu, s1, 1);
+    s0 += __shfl_xor_sync(0xffffffffu, s0, 2);
+    s1 += __shfl_xor_sync(0xffffffffu, s1, 2);
+    const int p = p0 + i * 16 + g;
+    if (qi == 0) {
+      if (p < n) srow[p] = s0;
+      if (p + 8 < n) srow[p + 8] = s1;
+    }
+  }
+  if (bad) record_error(DSA_DEV_ERR_BAD_PAGE);
+}
+
+template <int DI>
+__global__ void __launch_bounds__(kScoreWarps * 32)
+    decode_scores_f32_kernel(PagedView pv, int Hi, const float4* __restrict__ q_idx, const float* __restrict__ w,
+                             const float4* __restrict__ kpool, float* __restrict__ scores, int64_t P) {
+  constexpr int LPR = DI / 8;          // lanes per pool row, 8 channels each
+  constexpr int RPW = 32 / LPR;        // pool rows per warp and pass
+  const int64_t b = blockIdx.y;
+  bool bad = false;
+  const int n = row_length(pv, b, bad) >> 2;
+  const int lane = threadIdx.x & 31;
+  const int p0 = blockIdx.x * kScorePools + (threadIdx.x >> 5) * kScorePoolsPerWarp;
+  if (p0 >= n) return;
+  const int sub = lane / LPR, li = lane % LPR;
+  // channels li*4 .. +3 and DI/2 + li*4 .. +3: consecutive lanes read consecutive 16 bytes
+  float4 qf[8][2];
+#pragma unroll
+  for (int h = 0; h < 8; ++h) {
+    qf[h][0] = qf[h][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (h < Hi) {
+      qf[h][0] = __ldg(q_idx + (b * Hi + h) * (DI / 4) + li);
+      qf[h][1] = __ldg(q_idx + (b * Hi + h) * (DI / 4) + LPR + li);
+    }
+  }
+  // after the reduction below lane li holds head li & 7
+  const float wh = (li & 7) < Hi ? __ldg(w + b * Hi + (li & 7)) : 0.f;
+  const int32_t* trow = pv.table + b * pv.cols;
+  for (int i = 0; i < kScorePoolsPerWarp; i += RPW) {
+    const int p = p0 + i + sub;
+    float4 k0 = make_float4(0.f, 0.f, 0.f, 0.f), k1 = k0;
+    if (p < n) {
+      const int col = page_of_pool(pv, p);
+      const int pp = phys_pool(pv, p, col, __ldg(trow + col), bad);
+      if (pp >= 0) {
+        k0 = __ldg(kpool + (int64_t)pp * (DI / 4) + li);
+        k1 = __ldg(kpool + (int64_t)pp * (DI / 4) + LPR + li);
+      }
+    }
+    float dot[8];
+#pragma unroll
+    for (int h = 0; h < 8; ++h) {
+      float s = qf[h][0].x * k0.x;
+      s = fmaf(qf[h][0].y, k0.y, s);
+      s = fmaf(qf[h][0].z, k0.z, s);
+      s = fmaf(qf[h][0].w, k0.w, s);
+      s = fmaf(qf[h][1].x, k1.x, s);
+      s = fmaf(qf[h][1].y, k1.y, s);
+      s = fmaf(qf[h][1].z, k1.z, s);
+      dot[h] = fmaf(qf[h][1].w, k1.w, s);
+    }
+    // halve the heads a lane holds at each step: lane li ends with head li & 7
+#pragma unroll
+    for (int m = 4; m >= 1; m >>= 1) {
+      const bool up = (li & m) != 0;
+#pragma unroll
+      for (int h = 0; h < m; ++h) {
+        const float send = up ? dot[h] : dot[h + m];
+        const float keep = up ? dot[h + m] : dot[h];
+        dot[h] = keep + __shfl_xor_sync(0xffffffffu, send, m);
+      }
+    }
+    float s = dot[0];
+    if (LPR == 16) s += __shfl_xor_sync(0xffffffffu, s, 8);
+    s = wh * fmaxf(s, 0.f);
+    s += __shfl_xor_sync(0xffffffffu, s, 1);
+    s += __shfl_xor_sync(0xffffffffu, s, 2);
+    s += __shfl_xor_sync(0xffffffffu, s, 4);
+    if (li == 0 && p < n) scores[b * P + p] = s;
+  }
+  if (bad) record_error(DSA_DEV_ERR_BAD_PAGE);
+}
+
+size_t decode_scores_bytes(int64_t batch, int64_t P) {
+  return ((size_t)batch * (size_t)P * sizeof(float) + 255) & ~(size_t)255;
+}
+
+cudaError_t launch_decode_scores(bool bf16, const PagedView& pv, int64_t batch, int Hi, int di, const void* q_idx,
+                                 const float* w, const void* kpool, float* scores, int64_t P, cudaStream_t s) {
+  const dim3 grid((unsigned)((P + kScorePools - 1) / kScorePools), (unsigned)batch);
+  const int threads = kScoreWarps * 32;
+  if (bf16) {
+    auto q = static_cast<const uint4*>(q_idx);
+    auto kp = static_cast<const uint4*>(kpool);
+    if (di == 64)
+      decode_scores_bf16_kernel<64><<<grid, threads, 0, s>>>(pv, Hi, q, w, kp, scores, P);
+    else
+      decode_scores_bf16_kernel<128><<<grid, threads, 0, s>>>(pv, Hi, q, w, kp, scores, P);
+  } else {
+    auto q = static_cast<const float4*>(q_idx);
+    auto kp = static_cast<const float4*>(kpool);
+    if (di == 64)
+      decode_scores_f32_kernel<64><<<grid, threads, 0, s>>>(pv, Hi, q, w, kp, scores, P);
+    else
+      decode_scores_f32_kernel<128><<<grid, threads, 0, s>>>(pv, Hi, q, w, kp, scores, P);
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace dsa

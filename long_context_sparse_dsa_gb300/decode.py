@@ -1,0 +1,242 @@
+"""Decoding with the DSA layer from a paged cache: binding of ``include/dsa_decode.h``.
+
+Like the package's other entry points these calls only check and marshal their arguments; the caller owns
+every tensor.  Unlike them they also check types and shapes, since a decoder's integer arguments (lengths,
+block tables) are easily of another type.
+
+A decoder keeps a ``PagedCache``, a workspace (``alloc_decode_workspace``) and, if its model rotates keys and
+queries, a ``Rotation``; per step it advances ``lens`` and calls ``decode_step``, or the three calls it is made
+of: ``cache_append``, ``decode_indexer_topk``, ``decode_attn``.  All of them can be captured into a CUDA graph.
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+from dataclasses import dataclass, field
+
+import long_context_sparse_dsa_gb300 as _dsa
+
+
+class _CCache(ctypes.Structure):
+    """Mirror of ``dsa_paged_cache``."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("kpool", ctypes.c_void_p),
+                ("ktail", ctypes.c_void_p), ("num_pages", ctypes.c_int64), ("page_size", ctypes.c_int32)]
+
+
+class _CRotation(ctypes.Structure):
+    """Mirror of ``dsa_rotation``."""
+    _fields_ = [("turns", ctypes.c_void_p), ("dim", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
+
+
+@dataclass(frozen=True)
+class PagedCache:
+    """k, v [pages, page_size, d], kpool [pages, page_size / 4, di], ktail [pages, 3, di], in the layer dtype.
+
+    An array that no call uses may be None (``decode_attn`` reads k and v, ``decode_indexer_topk`` kpool,
+    ``cache_append`` writes all four)."""
+    k: object = None
+    v: object = None
+    kpool: object = None
+    ktail: object = None
+    pages: int = field(init=False)
+    page_size: int = field(init=False)
+    _c: object = field(init=False, repr=False)
+
+    def __post_init__(self):
+        given = [t for t in (self.k, self.v, self.kpool, self.ktail) if t is not None]
+        if not given or (self.k is None and self.kpool is None):
+            raise ValueError("a paged cache has k and v, or kpool, or all of k, v, kpool and ktail")
+        first = given[0]
+        for t in given:
+            _dsa._ptr(t)    # CUDA, contiguous
+            if t.dim() != 3 or t.shape[0] != first.shape[0] or t.dtype != first.dtype or t.device != first.device:
+                raise ValueError("the cache's arrays are 3-dimensional, with the same pages, dtype and device")
+        page = self.k.shape[1] if self.k is not None else 4 * self.kpool.shape[1]
+        if page < 4 or page % 4:
+            raise ValueError(f"page_size must be a positive multiple of 4 (got {page})")
+        if (self.k is None) != (self.v is None) or (self.k is not None and self.k.shape != self.v.shape):
+            raise ValueError("k and v have one shape")
+        if self.kpool is not None and self.kpool.shape[1] != page // 4:
+            raise ValueError("kpool has page_size / 4 rows per page")
+        if self.ktail is not None and (self.ktail.shape[1] != 3 or self.kpool is None or
+                                       self.ktail.shape[2] != self.kpool.shape[2]):
+            raise ValueError("ktail is [pages, 3, di], beside a kpool of the same di")
+        put = object.__setattr__
+        put(self, "pages", int(first.shape[0]))
+        put(self, "page_size", int(page))
+        put(self, "_c", _CCache(_dsa._ptr(self.k), _dsa._ptr(self.v), _dsa._ptr(self.kpool), _dsa._ptr(self.ktail),
+                                self.pages, self.page_size))
+
+
+def alloc_paged_cache(dims, pages: int, page_size: int = 64, device="cuda") -> PagedCache:
+    """Uninitialised arrays of a cache of `pages` pages for the layer `dims` (nothing in them needs a value)."""
+    import torch
+    _dsa._check(validate_decode_dims(dims), "dsa_validate_decode_dims")
+    dt = _dtype(dims)
+    e = lambda *shape: torch.empty(shape, dtype=dt, device=device)
+    return PagedCache(k=e(pages, page_size, dims.d), v=e(pages, page_size, dims.d),
+                      kpool=e(pages, page_size // 4, dims.di), ktail=e(pages, 3, dims.di))
+
+
+class Rotation:
+    """Position rotation of the first 2 * len(freq) channels: see ``make_rotation``."""
+
+    def __init__(self, turns, interleaved: bool):
+        self.turns = turns
+        self.dim = 2 * turns.numel()
+        self._c = _CRotation(turns.data_ptr(), self.dim, int(bool(interleaved)))
+
+
+def make_rotation(freq, interleaved: bool = False, device="cuda") -> Rotation:
+    """freq: the pairs' frequencies in radians per position, e.g. ``base ** (-arange(0, dim, 2) / dim)``, as a float64
+    tensor or a sequence of numbers.  Pair i is channels (i, i + dim/2), or (2i, 2i+1) when interleaved."""
+    import torch
+    values = [float(f) for f in (freq.tolist() if hasattr(freq, "tolist") else freq)]
+    if not values or len(values) % 8 or not all(math.isfinite(f) for f in values):
+        raise ValueError("a rotation has a multiple of 8 finite frequencies")
+    # turns per position in units of 2^-64, modulo a whole turn, as the int64 of the same bits
+    turns = [int(round((f / (2.0 * math.pi)) % 1.0 * 2.0 ** 64)) % 2 ** 64 for f in values]
+    turns = [t - 2 ** 64 if t >= 2 ** 63 else t for t in turns]
+    return Rotation(torch.tensor(turns, dtype=torch.int64, device=device), interleaved)
+
+
+def _dtype(dims):
+    import torch
+    return torch.bfloat16 if dims.dtype == _dsa.DSA_BF16 else torch.float32
+
+
+class _Args:
+    """Checks of one call's tensors: on the cache's device, which has to be the current one."""
+
+    def __init__(self, func, dims, cache):
+        import torch
+        self.func, self.dims, self.torch = func, dims, torch
+        self.dt = _dtype(dims)
+        self.device = (cache.k if cache.k is not None else cache.kpool).device
+        if self.device.index != torch.cuda.current_device():
+            raise ValueError(f"{func}: the cache is on {self.device}, not on the current device")
+        if (cache.k if cache.k is not None else cache.kpool).dtype != self.dt:
+            raise ValueError(f"{func}: the cache is not of the layer's dtype")
+        if cache.k is not None and cache.k.shape[2] != dims.d:
+            raise ValueError(f"{func}: the cache's k and v have {cache.k.shape[2]} channels, not d = {dims.d}")
+        if cache.kpool is not None and cache.kpool.shape[2] != dims.di:
+            raise ValueError(f"{func}: the cache's kpool has {cache.kpool.shape[2]} channels, not di = {dims.di}")
+
+    def ptr(self, name, t, dtype, *shape):
+        if t.dtype != dtype or t.shape != shape or t.device != self.device or not t.is_contiguous():
+            raise ValueError(f"{self.func}: {name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on "
+                             f"{self.device} (got {t.dtype}, {tuple(t.shape)}, {t.device})")
+        return t.data_ptr()
+
+    def rows(self, cache, lens, block_table):
+        """(batch, lens, block table)"""
+        i32, batch = self.torch.int32, lens.numel()
+        return (batch, self.ptr("lens", lens, i32, batch),
+                self.ptr("block_table", block_table, i32, batch, -(-self.dims.L // cache.page_size)))
+
+    def workspace(self, ws):
+        if ws is None:
+            return None, 0
+        if ws.device != self.device or not ws.is_contiguous():
+            raise ValueError(f"{self.func}: ws must be a contiguous tensor on {self.device}")
+        return ws.data_ptr(), ws.numel() * ws.element_size()
+
+    def rotation(self, rotation):
+        if rotation is None:
+            return None
+        if rotation.turns.device != self.device:
+            raise ValueError(f"{self.func}: the rotation is on {rotation.turns.device}, not on {self.device}")
+        return ctypes.byref(rotation._c)
+
+
+def validate_decode_dims(dims) -> int:
+    return _dsa._load().dsa_validate_decode_dims(ctypes.byref(dims))
+
+
+def decode_workspace_bytes(dims, batch: int) -> int:
+    return int(_dsa._load().dsa_decode_workspace_bytes(ctypes.byref(dims), int(batch)))
+
+
+def alloc_decode_workspace(dims, batch: int, device="cuda"):
+    """Scratch of the decode calls for up to `batch` rows; calls that may overlap on the GPU need one each."""
+    import torch
+    n = decode_workspace_bytes(dims, batch)
+    if n == 0:
+        _dsa._check(validate_decode_dims(dims), "dsa_decode_workspace_bytes")
+        raise _dsa.DSAError(_dsa.DSA_ERR_INVALID_ARG, "dsa_decode_workspace_bytes", f"batch {batch}")
+    return torch.empty((n,), dtype=torch.uint8, device=device)
+
+
+def cache_append(dims, cache, lens, block_table, k, v, k_idx, offsets=None, rotation=None, q=None, q_out=None,
+                 k_out=None, stream=None):
+    """New tokens into the cache; lens [batch] int32 count them.  Without offsets one token per row, with offsets
+    [batch + 1] int32 rows offsets[b] .. offsets[b+1]-1 of k, v, k_idx (q) are row b's.  With a rotation, k enters the
+    cache rotated to its position (and goes to k_out), and q goes to q_out rotated."""
+    a = _Args("cache_append", dims, cache)
+    batch, pl, pt = a.rows(cache, lens, block_table)
+    n, dt = k.shape[0], a.dt
+    pq = pqo = pko = po = None
+    if offsets is not None:
+        po = a.ptr("offsets", offsets, a.torch.int32, batch + 1)
+    if q is not None:
+        pq = a.ptr("q", q, dt, n, dims.Hq, dims.d)
+    if q_out is not None:
+        pqo = a.ptr("q_out", q_out, dt, n, dims.Hq, dims.d)
+    if k_out is not None:
+        pko = a.ptr("k_out", k_out, dt, n, dims.d)
+    _dsa._check(_dsa._load().dsa_cache_append(
+        ctypes.byref(dims), ctypes.byref(cache._c), batch, pl, pt, n, po, a.ptr("k", k, dt, n, dims.d),
+        a.ptr("v", v, dt, n, dims.d), a.ptr("k_idx", k_idx, dt, n, dims.di), a.rotation(rotation), pq, pqo, pko,
+        _dsa._stream(stream)), "dsa_cache_append")
+
+
+def decode_indexer_topk(dims, cache, lens, block_table, q_idx, w, idx, ws, stream=None):
+    """The min(k, lens[b] // 4) best complete pools of every row, ascending, then -1, into idx [batch, k] int32."""
+    a = _Args("decode_indexer_topk", dims, cache)
+    batch, pl, pt = a.rows(cache, lens, block_table)
+    pw, nw = a.workspace(ws)
+    _dsa._check(_dsa._load().dsa_decode_indexer_topk(
+        ctypes.byref(dims), ctypes.byref(cache._c), batch, pl, pt, a.ptr("q_idx", q_idx, a.dt, batch, dims.Hi, dims.di),
+        a.ptr("w", w, a.torch.float32, batch, dims.Hi), a.ptr("idx", idx, a.torch.int32, batch, dims.k), pw, nw,
+        _dsa._stream(stream)), "dsa_decode_indexer_topk")
+
+
+def decode_attn(dims, cache, lens, block_table, q, o, lse, ws, idx=None, stream=None):
+    """Attention of one query per row: over the pools of idx [batch, k] and the row's partial pool, or, without idx, over
+    all of the row's tokens.  o [batch, Hq, d], lse [batch, Hq] fp32."""
+    a = _Args("decode_attn", dims, cache)
+    batch, pl, pt = a.rows(cache, lens, block_table)
+    pw, nw = a.workspace(ws)
+    _dsa._check(_dsa._load().dsa_decode_attn(
+        ctypes.byref(dims), ctypes.byref(cache._c), batch, pl, pt,
+        None if idx is None else a.ptr("idx", idx, a.torch.int32, batch, dims.k),
+        a.ptr("q", q, a.dt, batch, dims.Hq, dims.d), a.ptr("o", o, a.dt, batch, dims.Hq, dims.d),
+        a.ptr("lse", lse, a.torch.float32, batch, dims.Hq), pw, nw, _dsa._stream(stream)), "dsa_decode_attn")
+
+
+def decode_step(dims, cache, lens, block_table, q, k, v, q_idx, k_idx, w, o, lse, idx, ws, rotation=None, stream=None):
+    """One decode step: append one token per row, select its pools (idx), attend to them (o, lse)."""
+    a = _Args("decode_step", dims, cache)
+    batch, pl, pt = a.rows(cache, lens, block_table)
+    pw, nw = a.workspace(ws)
+    dt, f32 = a.dt, a.torch.float32
+    _dsa._check(_dsa._load().dsa_decode_step(
+        ctypes.byref(dims), ctypes.byref(cache._c), batch, pl, pt, a.ptr("q", q, dt, batch, dims.Hq, dims.d),
+        a.ptr("k", k, dt, batch, dims.d), a.ptr("v", v, dt, batch, dims.d),
+        a.ptr("q_idx", q_idx, dt, batch, dims.Hi, dims.di), a.ptr("k_idx", k_idx, dt, batch, dims.di),
+        a.ptr("w", w, f32, batch, dims.Hi), a.rotation(rotation), a.ptr("o", o, dt, batch, dims.Hq, dims.d),
+        a.ptr("lse", lse, f32, batch, dims.Hq), a.ptr("idx", idx, a.torch.int32, batch, dims.k), pw, nw,
+        _dsa._stream(stream)), "dsa_decode_step")
+
+
+def _signatures(D):
+    P, i64, size = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t
+    C, R = ctypes.POINTER(_CCache), ctypes.POINTER(_CRotation)
+    return {
+        "dsa_validate_decode_dims": ([D], ctypes.c_int),
+        "dsa_decode_workspace_bytes": ([D, i64], size),
+        "dsa_cache_append": ([D, C, i64, P, P, i64, P, P, P, P, R, P, P, P, P], ctypes.c_int),
+        "dsa_decode_indexer_topk": ([D, C, i64, P, P, P, P, P, P, size, P], ctypes.c_int),
+        "dsa_decode_attn": ([D, C, i64, P, P, P, P, P, P, P, size, P], ctypes.c_int),
+        "dsa_decode_step": ([D, C, i64, P, P, P, P, P, P, P, P, R, P, P, P, P, size, P], ctypes.c_int),
+    }
