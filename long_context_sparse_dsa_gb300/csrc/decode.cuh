@@ -40,4 +40,35 @@ __device__ __forceinline__ int phys_pool(const PagedView& pv, int p, int col, in
   return page * pv.ppp + (p - col * pv.ppp);
 }
 
+// Programmatic dependent launch: a kernel launched by launch_chained
+// (decode.h) may become resident while its predecessor on the stream still
+// runs.  chain_wait() returns when the predecessor has finished and its writes
+// are visible; nothing is read or written before it.  chain_release(), by
+// every CTA (or its end), lets the successor become resident.
+__device__ __forceinline__ void chain_wait() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
+__device__ __forceinline__ void chain_release() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
+
+// Thread-block clusters: barrier over all threads of the cluster (release /
+// acquire of shared memory), and loads from another CTA's shared memory.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_map(uint32_t saddr, uint32_t rank) {
+  uint32_t a;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(a) : "r"(saddr), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ float4 cluster_ld4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];\n"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ float2 cluster_ld2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];\n" : "=f"(v.x), "=f"(v.y) : "r"(addr));
+  return v;
+}
+
 }  // namespace dsa

@@ -37,6 +37,34 @@ inline PagedView make_paged_view(const int32_t* lens, const int32_t* table, int6
   return v;
 }
 
+// Launches `kern` so that it may become resident before its predecessor on
+// the stream has finished (it calls chain_wait() before it touches memory):
+// its launch latency overlaps the predecessor's end.  cluster: CTAs per
+// cluster along x.
+template <typename... P, typename... A>
+inline cudaError_t launch_chained_cluster(unsigned cluster, void (*kern)(P...), dim3 grid, dim3 block, size_t smem,
+                                          cudaStream_t s, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = cluster;
+  at[1].val.clusterDim.y = 1;
+  at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
+}
+template <typename... P, typename... A>
+inline cudaError_t launch_chained(void (*kern)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, A... args) {
+  return launch_chained_cluster(1, kern, grid, block, smem, s, args...);
+}
+
 struct RotationArgs {
   const uint64_t* turns;   // nullptr: no rotation
   int dim;

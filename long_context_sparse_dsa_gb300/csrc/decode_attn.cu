@@ -6,29 +6,62 @@
 // slot k the partial pool, or, without idx, slot i is pool i.  A pool's 4 K
 // rows (and 4 V rows) are contiguous in its page.
 //
-// The slots of a row are split evenly over `splits` CTAs; a CTA's warps take
-// every 4th step of 4 slots (16 keys), gathered with cp.async into a ring of
-// their own, with heads on the M side of m16n8k16 MMAs as in attn_fwd.cu.
-// Warps join in shared memory, CTAs through partial results (o, base, sum)
-// in the workspace and a second kernel.  P enters P V as two bf16 terms (hi +
-// lo, about 2^-17 relative).
+// Bound: HBM (4*d bytes of K and V per key for 4*Hq*d flops: Hq flops a byte
+// in bf16), or, for few rows, the chain of dependent loads (length, idx entry,
+// page, rows) and the joins.
+//
+// Selected pools: every row has the same number of steps (of 4 slots, 16
+// keys), cut evenly over the CTAs of a cluster, which join through distributed
+// shared memory: one launch, no workspace traffic.
+// Whole cache: rows differ, so the rows' steps form one list, cut into equal
+// contiguous ranges, one per CTA: a CTA takes the end of one row, whole rows,
+// the start of another.  Every CTA derives the cut from the lengths itself.
+// A row that lies in one CTA is written out; the pieces of a row that
+// straddles CTAs (at most two per CTA) go to the workspace as (o, base, sum)
+// and a second kernel joins them.  (Cutting selected rows that way cost a
+// second piece, with its whole load chain, in a fifth of the CTAs: 42 us
+// against 24 for 96 rows of 2051 keys.)
+//
+// bf16: steps go round-robin to a CTA's warps, each with a ring of its own
+// filled by cp.async, heads on the M side of m16n8k16 MMAs as in attn_fwd.cu;
+// with more than 16 heads two warps share a ring, one loads K rows, the other
+// V rows.  P enters P V as two bf16 terms (hi + lo, about 2^-17 relative): the
+// MMAs are not what bounds the kernel.
+// fp32: tiles of 32 keys in shared memory, plain FFMA; for S a lane owns a key
+// and a warp a quarter of the heads, for P V a thread owns a channel.
 #include "decode.cuh"
 #include "gather.cuh"
 
 namespace dsa {
 
-constexpr int kAttnCtas = 456;   // CTAs a launch aims for: 3 per SM of 152
+constexpr int kAttnCtas = 456;   // 3 per SM of 152
+constexpr int kAttnThreads = 128;
+constexpr int kJoinThreads = 512;
+constexpr float kDecLazyLog2 = 8.f;   // the softmax base lags the running max by at most this (log2 units)
+constexpr float kLn2 = 0.6931471805599453f;
 
-static int attn_splits(int64_t batch, int64_t max_slots) {
-  int64_t s = (kAttnCtas + batch - 1) / batch;
-  const int64_t steps = (max_slots + 15) / 16;   // at least one step for each of 4 warps
-  if (s > steps) s = steps;
-  return s < 1 ? 1 : (int)s;
+// Workspace: two pieces per CTA, each Hq * d fp32 of o and Hq (base, sum)
+// pairs, then one JoinItem per row (or per CTA, when the rows are more).
+struct JoinItem {
+  int row, first, last, skip;   // row -1: nothing to join; pieces of CTAs first..last; skip: first's piece is its second
+};
+static size_t piece_floats(int Hq, int d) { return (size_t)Hq * (d + 2); }
+size_t decode_attn_ws_bytes(int64_t, int Hq, int d) {
+  const size_t n = 2 * kAttnCtas * piece_floats(Hq, d) * sizeof(float) + kAttnCtas * sizeof(JoinItem);
+  return (n + 255) & ~(size_t)255;
 }
 
-size_t decode_attn_ws_bytes(int64_t batch, int Hq, int d) {
-  const int64_t parts = batch > kAttnCtas ? batch : batch * ((kAttnCtas + batch - 1) / batch);
-  return ((size_t)parts * Hq * (size_t)(d + 2) * sizeof(float) + 255) & ~(size_t)255;
+struct Pieces {
+  float* o;       // [2 * CTAs][Hq][d]
+  float* ml;      // [2 * CTAs][Hq][2]
+  JoinItem* items;
+};
+static Pieces pieces_of(float* ws, int Hq, int d) {
+  Pieces p;
+  p.o = ws;
+  p.ml = ws + 2 * (size_t)kAttnCtas * Hq * d;
+  p.items = reinterpret_cast<JoinItem*>(p.ml + 2 * (size_t)kAttnCtas * Hq * 2);
+  return p;
 }
 
 // x = hi + lo for two fp32 values: hi their bf16 rounding, lo that of the rest.
@@ -37,85 +70,237 @@ __device__ __forceinline__ void split_hi_lo(float x0, float x1, uint32_t& hi, ui
   lo = pack_bf16(x0 - __uint_as_float(hi << 16), x1 - __uint_as_float(hi & 0xFFFF0000u));
 }
 
+// ------------------------------------------------------------------- slots
 // A row's slot list.
 struct SlotRow {
   const int32_t* idx;    // nullptr: slot i is pool i
   const int32_t* trow;   // block-table row
   int k;
   int len;
-  int n_slots;
 };
-__device__ __forceinline__ SlotRow slot_row(const PagedView& pv, const int32_t* idx, int k, int64_t b, bool& bad) {
-  SlotRow r;
-  r.idx = idx ? idx + b * k : nullptr;
-  r.trow = pv.table + b * pv.cols;
-  r.k = k;
-  r.len = row_length(pv, b, bad);
-  r.n_slots = r.len == 0 ? 0 : (idx ? k + 1 : (r.len + 3) >> 2);
-  return r;
+// Steps of a row of `len` tokens; an idle row has one, without keys, so that
+// some CTA writes its outputs.
+__device__ __forceinline__ int row_steps(int len, bool selected, int k) {
+  if (len == 0) return 1;
+  return selected ? (k + 4) >> 2 : (len + 15) >> 4;
 }
 // Slot `i` in three stages, so that its two dependent loads can be issued
 // ahead: the idx entry, the pool and its visible rows, the physical pool.
 __device__ __forceinline__ int slot_idx(const SlotRow& r, int i) {
-  return (r.idx && i < r.k) ? __ldg(r.idx + i) : i;
+  return (r.idx && i < r.k) ? __ldg(r.idx + i) : -1;
 }
-__device__ __forceinline__ void slot_pool_rows(const SlotRow& r, int i, int end, int raw, int& pool, int& rows,
-                                               bool& bad) {
+__device__ __forceinline__ void slot_pool_rows(const SlotRow& r, int i, int raw, int& pool, int& rows, bool& bad) {
   pool = 0;
   rows = 0;
-  if (i >= end) return;
   if (r.idx) {
     if (i < r.k) {
-      if (raw < 0) return;
-      if (raw >= (r.len >> 2)) {
-        bad = true;
-        return;
+      const bool out = raw >= (r.len >> 2);
+      bad |= out && r.len > 0;
+      if (raw >= 0 && !out) {
+        pool = raw;
+        rows = 4;
       }
-      pool = raw;
-      rows = 4;
-    } else {
+    } else if (i == r.k && (r.len & 3)) {
       pool = r.len >> 2;
       rows = r.len & 3;
-      if (rows == 0) pool = 0;
     }
-  } else {
+  } else if (4 * (int64_t)i < r.len) {
     pool = i;
     rows = min(4, r.len - 4 * i);
   }
 }
 
-template <int D, int NST>
-struct DecCfg {
-  static constexpr int WARPS = 4;
-  static constexpr int RING = NST * GatherCfg<D>::STAGE_BYTES;   // per warp; also holds the warp's 16 x D fp32 result
-  static constexpr int SMEM = WARPS * RING;
-  static_assert(RING >= 16 * D * 4, "the ring doubles as the join buffer");
+// ------------------------------------------------------------------- the cut
+// Where the CTA's range of steps begins.
+struct Cut {
+  int64_t rest;    // steps of the range
+  int64_t per;     // steps per CTA
+  int64_t begin;   // first step of the range, in the list
+  int64_t row;     // its row
+  int step;        // and its step in that row
 };
 
-template <int D, int HG>
-__global__ void __launch_bounds__(128, 3)
-    decode_attn_bf16_kernel(PagedView pv, int64_t batch, const __nv_bfloat16* __restrict__ Q,
-                            const __nv_bfloat16* __restrict__ K, const __nv_bfloat16* __restrict__ V,
-                            const int32_t* __restrict__ idx, __nv_bfloat16* __restrict__ O, float* __restrict__ LSE,
-                            float* __restrict__ part, int Hq, int k, float scale_log2, int splits) {
-  constexpr int NST = 2;
+// Shared scratch of the attention kernels, behind the tiles.  It lies in
+// dynamic shared memory: with relocatable device code the linker adds up the
+// static arrays of a file's kernels, which cost this kernel its third CTA per
+// SM.
+struct alignas(16) AttnScratch {
+  float2 ml[32];        // a head's base (log2 units) and sum, joined over the CTA's warps
+  float m[4][16], l[4][16];   // bf16: the warps' own; m becomes their weights
+  int64_t warp_sum[kAttnThreads / 32];
+  int64_t row;
+  int64_t step;
+};
+
+// Called by all threads of the CTA.  Sums the rows' steps, kAttnThreads rows at
+// a time: one pass when that is all rows, else one for the total and one up
+// to the range's first row.
+__device__ __forceinline__ Cut make_cut(const PagedView& pv, int64_t batch, int min_per, AttnScratch& sc) {
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  auto steps_of = [&](int64_t b) {
+    bool bad = false;
+    if (b >= batch) return 0;
+    const int n = row_steps(row_length(pv, b, bad), false, 0);
+    if (bad && blockIdx.x == 0) record_error(DSA_DEV_ERR_BAD_PAGE);
+    return n;
+  };
+  int64_t total = 0;
+  int mine = 0;
+  if (batch > kAttnThreads) {
+    int64_t part = 0;
+    for (int64_t b = threadIdx.x; b < batch; b += kAttnThreads) part += steps_of(b);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
+    if (lane == 0) sc.warp_sum[wid] = part;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kAttnThreads / 32; ++w) total += sc.warp_sum[w];
+    __syncthreads();
+  }
+  Cut c;
+  int64_t base = 0;
+  for (int64_t b0 = 0; b0 < batch; b0 += kAttnThreads) {
+    mine = steps_of(b0 + threadIdx.x);
+    int64_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    if (lane == 31) sc.warp_sum[wid] = incl;
+    __syncthreads();
+    int64_t before = base, chunk = 0;
+#pragma unroll
+    for (int w = 0; w < kAttnThreads / 32; ++w) {
+      if (w < wid) before += sc.warp_sum[w];
+      chunk += sc.warp_sum[w];
+    }
+    if (batch <= kAttnThreads) total = chunk;
+    c.per = (total + gridDim.x - 1) / gridDim.x;
+    if (c.per < min_per) c.per = min_per;
+    c.begin = c.per * blockIdx.x;
+    const int64_t excl = before + incl - mine;
+    if (excl <= c.begin && c.begin < excl + mine) {
+      sc.row = b0 + threadIdx.x;
+      sc.step = c.begin - excl;
+    }
+    base += chunk;
+    __syncthreads();
+    if (c.begin < base) break;
+  }
+  c.rest = total - c.begin < c.per ? total - c.begin : c.per;
+  c.row = sc.row;
+  c.step = (int)sc.step;
+  return c;
+}
+
+// Records how the row that begins in this CTA (at its `pos`-th step of the
+// list) is to be joined.  One item per row, or, when the rows are more than
+// the CTAs, one per CTA: that of its last row (`last_here`).
+__device__ __forceinline__ void put_join_item(const Pieces& ps, int64_t batch, const Cut& c, int64_t row, int64_t pos,
+                                              int steps, bool last_here) {
+  const int64_t last = (pos + steps - 1) / c.per;
+  const bool joined = last > blockIdx.x;
+  const bool by_row = batch <= gridDim.x;
+  if (threadIdx.x == 0 && (by_row || last_here)) {
+    JoinItem it;
+    it.row = joined ? (int)row : -1;
+    it.first = blockIdx.x;
+    it.last = (int)last;
+    it.skip = pos != c.begin;
+    ps.items[by_row ? row : blockIdx.x] = it;
+  }
+}
+__device__ __forceinline__ void put_no_item(const Pieces& ps, int64_t batch) {
+  if (batch > gridDim.x && threadIdx.x == 0) ps.items[blockIdx.x].row = -1;
+}
+
+// ------------------------------------------------------------------- bf16
+// One tensor's half of gather_step16 (gather.cuh): rows of K or of V.
+template <int D>
+__device__ __forceinline__ void gather_half16(uint32_t tile, const __nv_bfloat16* __restrict__ T,
+                                              const uint32_t (&slots)[4], const GatherLane<D>& gl) {
   using C = GatherCfg<D>;
-  using G = DecCfg<D, NST>;
-  constexpr int NSUB = 4 / HG;   // warps that share a head group
-  extern __shared__ __align__(128) unsigned char dec_smem[];
-  __shared__ float sm_m[4][16], sm_l[4][16];
+  constexpr int NRB = GatherLane<D>::NRB;
+  constexpr int POOL_BYTES = 4 * C::ROW_BYTES;
+#pragma unroll
+  for (int sig = 0; sig < 4; ++sig) {
+    const int nrows = slot_nrows(slots[sig]);
+    const char* src =
+        reinterpret_cast<const char*>(T) + (int64_t)(slots[sig] >> 3) * POOL_BYTES + gl.src_off;
+#pragma unroll
+    for (int rb = 0; rb < NRB; ++rb) {
+      const uint32_t bytes = rb * C::ROWS_PER_COPY + gl.row_lo < nrows ? 16u : 0u;
+      cp_async16(tile + sig * POOL_BYTES + gl.dst_off[sig & 1][rb], src + rb * C::ROWS_PER_COPY * C::ROW_BYTES, bytes);
+    }
+  }
+}
+
+template <int D, int HG>
+struct DecCfg {
+  static constexpr int WARPS = kAttnThreads / 32;
+  static constexpr int RINGS = WARPS / HG;           // a ring per warp, or per pair
+  static constexpr int NSUB = RINGS;                 // steps in progress at once
+  static constexpr int NST = (D == 128 ? 2 : 4) * HG;
+  static constexpr int RING = NST * GatherCfg<D>::STAGE_BYTES;
+  static constexpr int TILES = RINGS * RING;
+  static constexpr int SMEM = TILES + (int)sizeof(AttnScratch);
+  static_assert(TILES >= WARPS * 16 * D * 4, "the rings double as the join buffer");
+};
+
+// Steps [w0, steps) of row b.  Leaves o [Hq][D] at the start of the tiles and
+// the heads' bases and sums in sc.ml; ends with a __syncthreads().
+template <int D, int HG>
+__device__ __forceinline__ void attn_piece_bf16(const PagedView& pv, const __nv_bfloat16* __restrict__ Q,
+                                                const __nv_bfloat16* __restrict__ K,
+                                                const __nv_bfloat16* __restrict__ V, const SlotRow& sr, int64_t b,
+                                                int w0, int steps, int Hq, float scale_log2, unsigned char* tiles,
+                                                AttnScratch& sc, bool& bad_page, bool& bad_idx) {
+  using C = GatherCfg<D>;
+  using G = DecCfg<D, HG>;
+  constexpr int NST = G::NST;
+  constexpr int NSUB = G::NSUB;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int hg = warp % HG, sub = warp / HG;
-  const int64_t b = blockIdx.y;
-  const int split = blockIdx.x;
   const int g = lane >> 2, qi = lane & 3;
-  bool bad_page = false, bad_idx = false;
-  const SlotRow sr = slot_row(pv, idx, k, b, bad_page);
-  const int per = ((sr.n_slots + splits - 1) / splits + 3) & ~3;   // slots per CTA, whole steps
-  const int s_begin = min(sr.n_slots, split * per), s_end = min(sr.n_slots, s_begin + per);
-  const int steps = (s_end - s_begin + 3) >> 2;
-  const uint32_t wbase = smem_u32(dec_smem) + warp * G::RING;
+  const uint32_t ring = smem_u32(tiles) + sub * G::RING;
   const GatherLane<D> gl = gather_lane<D>(lane);
+  auto ring_sync = [&]() {
+    if (HG == 1)
+      __syncwarp();
+    else
+      asm volatile("bar.sync %0, 64;\n" ::"r"(1 + sub) : "memory");
+  };
+  // Slot pipeline: this lane decides slot (lane & 3) of every step of its warp.
+  int raw = -1, pool = 0, rows = 0, page = 0;
+  auto load_raw = [&](int st) { raw = st < steps ? slot_idx(sr, st * 4 + (lane & 3)) : -1; };
+  auto load_page = [&](int st) {
+    slot_pool_rows(sr, st * 4 + (lane & 3), raw, pool, rows, bad_idx);
+    if (st >= steps) rows = 0;
+    page = rows ? __ldg(sr.trow + page_of_pool(pv, pool)) : 0;
+  };
+  uint32_t vis[NST];   // visible rows of the ring's steps: 4 bits per slot
+  auto fetch = [&](int st, int stage, uint32_t& v) {
+    v = 0u;
+    if (st < steps) {
+      uint32_t mine = 0u, slots[4];
+      if (rows) {
+        const int pp = phys_pool(pv, pool, page_of_pool(pv, pool), page, bad_page);
+        if (pp >= 0) mine = ((uint32_t)pp << 3) | (uint32_t)rows;
+      }
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        slots[s] = __shfl_sync(0xffffffffu, mine, s);
+        v |= (slots[s] & 7u) << (4 * s);
+      }
+      const uint32_t base = ring + stage * C::STAGE_BYTES;
+      if (HG == 1)
+        gather_step16<D>(base, K, V, slots, gl);
+      else
+        gather_half16<D>(base + hg * C::TILE_BYTES, hg ? V : K, slots, gl);
+    }
+    cp_async_commit();
+  };
 
   uint32_t qa[D / 16][4];
   {
@@ -130,61 +315,59 @@ __global__ void __launch_bounds__(128, 3)
       qa[ks][3] = h1 < Hq ? __ldg(q32 + c1 + 4) : 0u;
     }
   }
+  // fill the ring: all idx entries, then all pages, then the rows
+  int st = w0 + sub;
+  {
+    int raws[NST], pools[NST], rws[NST], pgs[NST];
+#pragma unroll
+    for (int i = 0; i < NST; ++i) {
+      load_raw(st + i * NSUB);
+      raws[i] = raw;
+    }
+    load_raw(st + NST * NSUB);
+    const int raw_next = raw;
+#pragma unroll
+    for (int i = 0; i < NST; ++i) {
+      raw = raws[i];
+      load_page(st + i * NSUB);
+      pools[i] = pool;
+      rws[i] = rows;
+      pgs[i] = page;
+    }
+#pragma unroll
+    for (int i = 0; i < NST; ++i) {
+      pool = pools[i];
+      rows = rws[i];
+      page = pgs[i];
+      if (i < NST - 1) fetch(st + i * NSUB, i, vis[i]);
+    }
+    raw = raw_next;
+  }
   float o[D / 8][4];
 #pragma unroll
   for (int n = 0; n < D / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
   float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
 
-  // Slot pipeline: this lane decides slot (lane & 3) of every step of its warp.
-  int raw = 0, pool = 0, rows = 0, page = 0;
-  auto slot_of = [&](int step) { return s_begin + step * 4 + (lane & 3); };
-  auto load_raw = [&](int step) { raw = slot_of(step) < s_end ? slot_idx(sr, slot_of(step)) : -1; };
-  auto load_page = [&](int step) {
-    slot_pool_rows(sr, slot_of(step), s_end, raw, pool, rows, bad_idx);
-    page = rows ? __ldg(sr.trow + page_of_pool(pv, pool)) : 0;
-  };
-  auto resolve = [&](uint32_t (&slots)[4]) {
-    uint32_t mine = 0u;
-    if (rows) {
-      const int pp = phys_pool(pv, pool, page_of_pool(pv, pool), page, bad_page);
-      if (pp >= 0) mine = ((uint32_t)pp << 3) | (uint32_t)rows;
-    }
-#pragma unroll
-    for (int s = 0; s < 4; ++s) slots[s] = __shfl_sync(0xffffffffu, mine, s);
-  };
-
-  uint32_t pc[4] = {0u, 0u, 0u, 0u};
-  load_raw(sub);
-  load_page(sub);
-  load_raw(sub + NSUB);
-  if (sub < steps) {
-    resolve(pc);
-    gather_step16<D>(wbase, K, V, pc, gl);
-  }
-  cp_async_commit();
-  load_page(sub + NSUB);
-  load_raw(sub + 2 * NSUB);
   int stage = 0;
-  for (int st = sub; st < steps; st += NSUB) {
-    uint32_t pf[4] = {0u, 0u, 0u, 0u};
-    if (st + NSUB < steps) {
-      resolve(pf);
-      gather_step16<D>(wbase + (stage ^ 1) * C::STAGE_BYTES, K, V, pf, gl);
+  for (; st < steps; st += NSUB) {
+    {
+      const int nx = stage == 0 ? NST - 1 : stage - 1;   // the stage consumed last
+      fetch(st + (NST - 1) * NSUB, nx, vis[NST - 1]);
+      load_page(st + NST * NSUB);
+      load_raw(st + (NST + 1) * NSUB);
     }
-    cp_async_commit();
-    load_page(st + 2 * NSUB);
-    load_raw(st + 3 * NSUB);
     bool kv[2][2];
 #pragma unroll
     for (int nt = 0; nt < 2; ++nt) {
-      const int nrows = slot_nrows((qi >> 1) ? pc[nt * 2 + 1] : pc[nt * 2]);
+      const int nrows = (int)(vis[0] >> (8 * nt + 4 * (qi >> 1))) & 7;
 #pragma unroll
       for (int e = 0; e < 2; ++e) kv[nt][e] = 2 * (qi & 1) + e < nrows;
     }
-    cp_async_wait<1>();
-    __syncwarp();
-    const uint32_t ks_base = wbase + stage * C::STAGE_BYTES;
+    cp_async_wait<NST - 1>();
+    ring_sync();
+    const uint32_t ks_base = ring + stage * C::STAGE_BYTES;
     const uint32_t vs_base = ks_base + C::TILE_BYTES;
+    // S = Q K^T as four independent accumulation chains
     float s[2][4], s2[2][4];
 #pragma unroll
     for (int nt = 0; nt < 2; ++nt)
@@ -206,18 +389,15 @@ __global__ void __launch_bounds__(128, 3)
           mma_bf16_16816(s[1], qa[ks][0], qa[ks][1], qa[ks][2], qa[ks][3], b2, b3);
         }
       }
-#pragma unroll
-      for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[nt][e] += s2[nt][e];
     }
+    // online softmax in log2 units with a lazily moved base (attn_fwd.cu)
     float mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll
     for (int nt = 0; nt < 2; ++nt) {
-      s[nt][0] = kv[nt][0] ? s[nt][0] : -INFINITY;
-      s[nt][1] = kv[nt][1] ? s[nt][1] : -INFINITY;
-      s[nt][2] = kv[nt][0] ? s[nt][2] : -INFINITY;
-      s[nt][3] = kv[nt][1] ? s[nt][3] : -INFINITY;
+      s[nt][0] = kv[nt][0] ? s[nt][0] + s2[nt][0] : -INFINITY;
+      s[nt][1] = kv[nt][1] ? s[nt][1] + s2[nt][1] : -INFINITY;
+      s[nt][2] = kv[nt][0] ? s[nt][2] + s2[nt][2] : -INFINITY;
+      s[nt][3] = kv[nt][1] ? s[nt][3] + s2[nt][3] : -INFINITY;
       mx0 = fmaxf(mx0, fmaxf(s[nt][0], s[nt][1]));
       mx1 = fmaxf(mx1, fmaxf(s[nt][2], s[nt][3]));
     }
@@ -227,9 +407,10 @@ __global__ void __launch_bounds__(128, 3)
     mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 2));
     mx0 *= scale_log2;
     mx1 *= scale_log2;
-    const float mn0 = fmaxf(m0, mx0), mn1 = fmaxf(m1, mx1);
+    const bool up0 = mx0 > m0 + kDecLazyLog2, up1 = mx1 > m1 + kDecLazyLog2;
+    const float mn0 = up0 ? mx0 : m0, mn1 = up1 ? mx1 : m1;
     const float base0 = mn0 == -INFINITY ? 0.f : mn0, base1 = mn1 == -INFINITY ? 0.f : mn1;
-    const float a0 = ex2_approx(m0 - base0), a1 = ex2_approx(m1 - base1);
+    const float a0 = up0 ? ex2_approx(m0 - base0) : 1.f, a1 = up1 ? ex2_approx(m1 - base1) : 1.f;
     m0 = mn0;
     m1 = mn1;
     float rs0 = 0.f, rs1 = 0.f;
@@ -277,235 +458,559 @@ __global__ void __launch_bounds__(128, 3)
         mma_bf16_16816(o[2 * j + 3], pl0, pl1, pl2, pl3, c2, c3);
       }
     }
-    __syncwarp();
+    ring_sync();
 #pragma unroll
-    for (int s4 = 0; s4 < 4; ++s4) pc[s4] = pf[s4];
-    stage ^= 1;
+    for (int i = 0; i + 1 < NST; ++i) vis[i] = vis[i + 1];
+    stage = stage == NST - 1 ? 0 : stage + 1;
   }
   cp_async_wait<0>();
-  if (bad_idx) record_error(DSA_DEV_ERR_BAD_INDEX);
-  if (bad_page) record_error(DSA_DEV_ERR_BAD_PAGE);
 
-  // ---- join the warps of a head group ------------------------------------------
+  // ---- join the CTA's warps ----------------------------------------------------
   l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
   l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
   l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
   l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
-  float* my = reinterpret_cast<float*>(dec_smem + warp * G::RING);   // [16][D], this warp's own ring
-  __syncwarp();
-#pragma unroll
-  for (int n = 0; n < D / 8; ++n) {
-    *reinterpret_cast<float2*>(my + g * D + n * 8 + 2 * qi) = make_float2(o[n][0], o[n][1]);
-    *reinterpret_cast<float2*>(my + (g + 8) * D + n * 8 + 2 * qi) = make_float2(o[n][2], o[n][3]);
-  }
   if (qi == 0) {
-    sm_m[warp][g] = m0;
-    sm_m[warp][g + 8] = m1;
-    sm_l[warp][g] = l0;
-    sm_l[warp][g + 8] = l1;
+    sc.m[warp][g] = m0;
+    sc.m[warp][g + 8] = m1;
+    sc.l[warp][g] = l0;
+    sc.l[warp][g + 8] = l1;
   }
-  __syncthreads();
-  const int64_t p = b * splits + split;
-  float* po = part + p * Hq * D;
-  float* pml = part + (int64_t)batch * splits * Hq * D + p * Hq * 2;
-  for (int i = threadIdx.x; i < Hq * D; i += 128) {
-    const int h = i / D, c = i % D;
-    float mm = -INFINITY;
+  __syncthreads();   // every ring is idle: the tiles are the join buffer, [warp][16][D]
+  {
+    float* my = reinterpret_cast<float*>(tiles) + warp * 16 * D;
 #pragma unroll
-    for (int s = 0; s < NSUB; ++s) mm = fmaxf(mm, sm_m[s * HG + h / 16][h % 16]);
+    for (int n = 0; n < D / 8; ++n) {
+      *reinterpret_cast<float2*>(my + g * D + n * 8 + 2 * qi) = make_float2(o[n][0], o[n][1]);
+      *reinterpret_cast<float2*>(my + (g + 8) * D + n * 8 + 2 * qi) = make_float2(o[n][2], o[n][3]);
+    }
+  }
+  if (threadIdx.x < HG * 16) {   // warps h/16, h/16 + HG, .. hold head h's parts
+    const int h = threadIdx.x, r = h & 15;
+    float mm = -INFINITY, l = 0.f;
+#pragma unroll
+    for (int s = 0; s < NSUB; ++s) mm = fmaxf(mm, sc.m[s * HG + (h >> 4)][r]);
     const float base = mm == -INFINITY ? 0.f : mm;
-    float acc = 0.f, l = 0.f;
 #pragma unroll
     for (int s = 0; s < NSUB; ++s) {
-      const int w = s * HG + h / 16;
-      const float f = ex2_approx(sm_m[w][h % 16] - base);
-      acc += f * reinterpret_cast<const float*>(dec_smem + w * G::RING)[(h % 16) * D + c];
-      l += f * sm_l[w][h % 16];
+      const float f = ex2_approx(sc.m[s * HG + (h >> 4)][r] - base);
+      sc.m[s * HG + (h >> 4)][r] = f;
+      l += f * sc.l[s * HG + (h >> 4)][r];
     }
-    if (splits == 1) {
-      O[(b * Hq + h) * D + c] = __float2bfloat16(l == 0.f ? 0.f : acc / l);
-      if (c == 0) LSE[b * Hq + h] = l == 0.f ? -INFINITY : (mm + log2f(l)) * 0.6931471805599453f;
-    } else {
-      po[i] = acc;
-      if (c == 0) {
-        pml[2 * h] = mm;
-        pml[2 * h + 1] = l;
-      }
-    }
+    sc.ml[h] = make_float2(mm, l);
   }
+  __syncthreads();
+  float4* o4 = reinterpret_cast<float4*>(tiles);
+#pragma unroll
+  for (int i = threadIdx.x; i < HG * 16 * D / 4; i += kAttnThreads) {
+    const int h = i / (D / 4);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int s = 0; s < NSUB; ++s) {
+      const float f = sc.m[s * HG + (h >> 4)][h & 15];
+      const float4 x = o4[s * HG * 16 * (D / 4) + i];
+      acc.x += f * x.x;
+      acc.y += f * x.y;
+      acc.z += f * x.z;
+      acc.w += f * x.w;
+    }
+    o4[i] = acc;   // in place: warp group 0's part, this thread's own element
+  }
+  __syncthreads();
 }
 
-// ------------------------------------------------------------ fp32 (FFMA)
-// One CTA of 128 threads per (row, split); key tiles of 32 in shared memory.
-constexpr int kDecF32Tile = 32;
+// ------------------------------------------------------------------- fp32 (FFMA)
+constexpr int kF32Keys = 32;        // keys per tile (8 slots, two steps)
 
-__global__ void __launch_bounds__(128)
-    decode_attn_f32_kernel(PagedView pv, int64_t batch, const float* __restrict__ Q, const float* __restrict__ K,
-                           const float* __restrict__ V, const int32_t* __restrict__ idx, float* __restrict__ O,
-                           float* __restrict__ LSE, float* __restrict__ part, int Hq, int d, int k, float scale_log2,
-                           int splits) {
-  extern __shared__ float f32_smem[];
-  float* qs = f32_smem;                     // [Hq][d]
-  float* ks = qs + Hq * d;                  // [32][d]
-  float* vs = ks + kDecF32Tile * d;         // [32][d]
-  float* os = vs + kDecF32Tile * d;         // [Hq][d]
-  float* ss = os + Hq * d;                  // [Hq][32]
-  float* ms = ss + Hq * kDecF32Tile;        // [Hq]
-  float* ls = ms + Hq;                      // [Hq]
-  float* as = ls + Hq;                      // [Hq]
-  __shared__ int64_t keys[kDecF32Tile];
+template <int D>
+struct F32Cfg {
+  static constexpr int PITCH = D + 4;                       // floats per row: 16-byte rows, conflict-free columns
+  static constexpr int STAGE = 2 * kF32Keys * PITCH;        // K and V of a tile, floats
+  static constexpr int TILES = 2 * STAGE * 4;               // two stages, bytes
+  static int smem(int Hq) {                                 // + q [Hq][D], p [Hq][36], alpha [Hq], vis [2][8]
+    return TILES + 4 * Hq * (D + 36 + 1) + 64 + 16 + (int)sizeof(AttnScratch);
+  }
+  static_assert(TILES >= 32 * D * 4, "the tiles double as the result buffer");
+};
+
+// MAXH: heads, rounded up to 8, 16 or 32.  As attn_piece_bf16.
+template <int D, int MAXH>
+__device__ __forceinline__ void attn_piece_f32(const PagedView& pv, const float* __restrict__ Q,
+                                               const float* __restrict__ K, const float* __restrict__ V,
+                                               const SlotRow& sr, int64_t b, int w0, int steps, int Hq,
+                                               float scale_log2, unsigned char* tiles, AttnScratch& sc,
+                                               bool& bad_page, bool& bad_idx) {
+  using F = F32Cfg<D>;
+  constexpr int HPW = MAXH / 4;                 // heads a warp scores
+  constexpr int GROUPS = kAttnThreads / D;      // thread groups over the heads in P V
+  constexpr int HPT = MAXH / GROUPS;            // heads a thread accumulates
+  constexpr int CH = D / 4;                     // 16-byte chunks per row
+  constexpr int RPI = 32 / CH;                  // rows a warp copies at once (1 or 2)
+  float* kv = reinterpret_cast<float*>(tiles);
+  float* qs = kv + 2 * F::STAGE;                // [Hq][D]
+  float* pt = qs + Hq * D;                      // [Hq][36]
+  int* vis = reinterpret_cast<int*>(pt + Hq * 36);   // [2][8]
+  float* alpha = reinterpret_cast<float*>(vis + 16); // [Hq]
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int c = threadIdx.x % D, grp = threadIdx.x / D;
+  for (int i = threadIdx.x; i < Hq * D / 4; i += kAttnThreads)
+    reinterpret_cast<float4*>(qs)[i] = __ldg(reinterpret_cast<const float4*>(Q + b * Hq * D) + i);
+
+  // Slot pipeline: a warp copies slots 2*warp and 2*warp + 1 of every tile; lane
+  // (lane & 1) decides one of them, two tiles ahead for the idx entry, one for the page.
+  const int s_end = 4 * steps;
+  int raw = -1, pool = 0, rows = 0, page = 0;
+  auto slot_of = [&](int t) { return 4 * w0 + 8 * t + 2 * warp + (lane & 1); };
+  auto load_raw = [&](int t) { raw = slot_of(t) < s_end ? slot_idx(sr, slot_of(t)) : -1; };
+  auto load_page = [&](int t) {
+    slot_pool_rows(sr, slot_of(t), raw, pool, rows, bad_idx);
+    if (slot_of(t) >= s_end) rows = 0;
+    page = rows ? __ldg(sr.trow + page_of_pool(pv, pool)) : 0;
+  };
+  const int n_tiles = (steps - w0 + 1) >> 1;
+  auto fetch = [&](int t, int stage) {
+    if (t < n_tiles) {
+      uint32_t mine = 0u;
+      if (rows) {
+        const int pp = phys_pool(pv, pool, page_of_pool(pv, pool), page, bad_page);
+        if (pp >= 0) mine = ((uint32_t)pp << 3) | (uint32_t)rows;
+      }
+      if (lane < 2) vis[stage * 8 + 2 * warp + lane] = (int)(mine & 7u);
+      float* dst0 = kv + stage * F::STAGE + 8 * warp * F::PITCH;
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const uint32_t slot = __shfl_sync(0xffffffffu, mine, s);
+        const int64_t row0 = (int64_t)(slot >> 3) * 4;
+#pragma unroll
+        for (int r = 0; r < 4; r += RPI) {
+          const int rr = r + lane / CH;
+          const uint32_t bytes = rr < (int)(slot & 7u) ? 16u : 0u;
+          const int64_t src = (row0 + rr) * D + 4 * (lane % CH);
+          const uint32_t dst = smem_u32(dst0 + (4 * s + rr) * F::PITCH + 4 * (lane % CH));
+          cp_async16(dst, K + src, bytes);
+          cp_async16(dst + kF32Keys * F::PITCH * 4, V + src, bytes);
+        }
+      }
+    }
+    cp_async_commit();
+  };
+  load_raw(0);
+  load_page(0);
+  load_raw(1);
+  fetch(0, 0);
+  load_page(1);
+  load_raw(2);
+
+  float m[HPW], l[HPW];
+#pragma unroll
+  for (int i = 0; i < HPW; ++i) {
+    m[i] = -INFINITY;
+    l[i] = 0.f;
+  }
+  float o[HPT];
+#pragma unroll
+  for (int i = 0; i < HPT; ++i) o[i] = 0.f;
+  for (int t = 0; t < n_tiles; ++t) {
+    const int stage = t & 1;
+    fetch(t + 1, stage ^ 1);
+    load_page(t + 2);
+    load_raw(t + 3);
+    cp_async_wait<1>();
+    __syncthreads();
+    const float* ks = kv + stage * F::STAGE;
+    const float* vs = ks + kF32Keys * F::PITCH;
+    // scores: this lane's key, this warp's heads warp, warp + 4, ..
+    {
+      float s[HPW];
+#pragma unroll
+      for (int i = 0; i < HPW; ++i) s[i] = 0.f;
+      const float4* kr = reinterpret_cast<const float4*>(ks + lane * F::PITCH);
+#pragma unroll 4
+      for (int x = 0; x < D / 4; ++x) {
+        const float4 kk = kr[x];
+#pragma unroll
+        for (int i = 0; i < HPW; ++i) {
+          const int h = warp + 4 * i;
+          if (h < Hq) {
+            const float4 qq = reinterpret_cast<const float4*>(qs + h * D)[x];
+            s[i] = fmaf(qq.x, kk.x, s[i]);
+            s[i] = fmaf(qq.y, kk.y, s[i]);
+            s[i] = fmaf(qq.z, kk.z, s[i]);
+            s[i] = fmaf(qq.w, kk.w, s[i]);
+          }
+        }
+      }
+      const bool seen = (lane & 3) < vis[stage * 8 + (lane >> 2)];
+#pragma unroll
+      for (int i = 0; i < HPW; ++i) {
+        const int h = warp + 4 * i;
+        if (h < Hq) {
+          const float z = seen ? s[i] * scale_log2 : -INFINITY;
+          float mx = z;
+#pragma unroll
+          for (int w = 16; w; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
+          const bool up = mx > m[i] + kDecLazyLog2;
+          const float mn = up ? mx : m[i];
+          const float base = mn == -INFINITY ? 0.f : mn;
+          const float a = up ? exp2f(m[i] - base) : 1.f;
+          m[i] = mn;
+          const float p = exp2f(z - base);
+          l[i] = l[i] * a + p;   // this lane's share of the sum
+          pt[h * 36 + lane] = p;
+          if (lane == 0) alpha[h] = a;
+        }
+      }
+    }
+    __syncthreads();
+    // P V: this thread's channel, heads grp, grp + GROUPS, ..
+#pragma unroll
+    for (int i = 0; i < HPT; ++i) {
+      const int h = grp + GROUPS * i;
+      if (h < Hq) o[i] *= alpha[h];
+    }
+#pragma unroll 2
+    for (int j = 0; j < kF32Keys; j += 4) {
+      float v[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = vs[(j + e) * F::PITCH + c];
+#pragma unroll
+      for (int i = 0; i < HPT; ++i) {
+        const int h = grp + GROUPS * i;
+        if (h < Hq) {
+          const float4 p = *reinterpret_cast<const float4*>(pt + h * 36 + j);
+          o[i] = fmaf(p.x, v[0], o[i]);
+          o[i] = fmaf(p.y, v[1], o[i]);
+          o[i] = fmaf(p.z, v[2], o[i]);
+          o[i] = fmaf(p.w, v[3], o[i]);
+        }
+      }
+    }
+    __syncthreads();   // the stage, p and alpha are free again
+  }
+  cp_async_wait<0>();
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < HPT; ++i) {
+    const int h = grp + GROUPS * i;
+    if (h < Hq) kv[h * D + c] = o[i];
+  }
+#pragma unroll
+  for (int i = 0; i < HPW; ++i) {
+    const int h = warp + 4 * i;
+    float sum = l[i];
+#pragma unroll
+    for (int w = 16; w; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
+    if (h < Hq && lane == 0) sc.ml[h] = make_float2(m[i], sum);
+  }
+  __syncthreads();
+}
+
+// ------------------------------------------------------------------- kernels
+template <typename T>
+struct AttnArgs {
+  PagedView pv;
+  int64_t batch;
+  const T *Q, *K, *V;
+  const int32_t* idx;
+  T* O;
+  float* LSE;
+  Pieces ps;
+  int Hq, k;
+  float scale_log2;
+};
+
+// The type's piece function, its shared memory and its steps in progress.
+template <typename T, int D, int MAXH>
+struct Piece;
+template <int D, int MAXH>
+struct Piece<__nv_bfloat16, D, MAXH> {
+  static constexpr int HG = MAXH > 16 ? 2 : 1;
+  static constexpr int MIN_STEPS = DecCfg<D, HG>::NSUB;
+  static constexpr int MIN_CTAS = 3;
+  static int smem(int) { return DecCfg<D, HG>::SMEM; }
+  static __device__ __forceinline__ AttnScratch& scratch(unsigned char* smem, int) {
+    return *reinterpret_cast<AttnScratch*>(smem + DecCfg<D, HG>::TILES);
+  }
+  static __device__ __forceinline__ void run(const AttnArgs<__nv_bfloat16>& a, const SlotRow& sr, int64_t b, int w0,
+                                             int steps, unsigned char* smem, AttnScratch& sc, bool& bad_page,
+                                             bool& bad_idx) {
+    attn_piece_bf16<D, HG>(a.pv, a.Q, a.K, a.V, sr, b, w0, steps, a.Hq, a.scale_log2, smem, sc, bad_page, bad_idx);
+  }
+};
+template <int D, int MAXH>
+struct Piece<float, D, MAXH> {
+  static constexpr int MIN_STEPS = 2;
+  static constexpr int MIN_CTAS = 2;
+  static int smem(int Hq) { return F32Cfg<D>::smem(Hq); }
+  static __device__ __forceinline__ AttnScratch& scratch(unsigned char* smem, int Hq) {
+    return *reinterpret_cast<AttnScratch*>(smem + ((F32Cfg<D>::TILES + 4 * Hq * (D + 36 + 1) + 64 + 15) & ~15));
+  }
+  static __device__ __forceinline__ void run(const AttnArgs<float>& a, const SlotRow& sr, int64_t b, int w0, int steps,
+                                             unsigned char* smem, AttnScratch& sc, bool& bad_page, bool& bad_idx) {
+    attn_piece_f32<D, MAXH>(a.pv, a.Q, a.K, a.V, sr, b, w0, steps, a.Hq, a.scale_log2, smem, sc, bad_page, bad_idx);
+  }
+};
+
+// Four consecutive outputs of head h from their sum x and the head's (base,
+// sum).  A sum of 0 means no key (o = 0, lse = -infinity); a NaN sum stays NaN.
+__device__ __forceinline__ void store_out4(__nv_bfloat16* o, float4 x, float inv) {
+  *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16(x.x * inv, x.y * inv), pack_bf16(x.z * inv, x.w * inv));
+}
+__device__ __forceinline__ void store_out4(float* o, float4 x, float inv) {
+  *reinterpret_cast<float4*>(o) = make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
+}
+__device__ __forceinline__ float inv_sum(float l) { return l == 0.f ? 0.f : 1.f / l; }
+__device__ __forceinline__ float lse_of(float m, float l) { return l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2; }
+
+template <typename T>
+__device__ __forceinline__ SlotRow slot_row(const AttnArgs<T>& a, int64_t b, bool& bad) {
+  SlotRow sr;
+  sr.idx = a.idx ? a.idx + b * a.k : nullptr;
+  sr.trow = a.pv.table + b * a.pv.cols;
+  sr.k = a.k;
+  sr.len = row_length(a.pv, b, bad);
+  return sr;
+}
+
+// Selected pools: grid (splits, batch), the splits of a row are one cluster.
+template <typename T, int D, int MAXH>
+__global__ void __launch_bounds__(kAttnThreads, (Piece<T, D, MAXH>::MIN_CTAS))
+    decode_attn_selected_kernel(const __grid_constant__ AttnArgs<T> a) {
+  using P = Piece<T, D, MAXH>;
+  extern __shared__ __align__(128) unsigned char dec_smem[];
+  AttnScratch& sc = P::scratch(dec_smem, a.Hq);
+  chain_wait();
+  chain_release();
   const int64_t b = blockIdx.y;
-  const int split = blockIdx.x, tid = threadIdx.x;
+  const int splits = gridDim.x, rank = blockIdx.x;
   bool bad_page = false, bad_idx = false;
-  const SlotRow sr = slot_row(pv, idx, k, b, bad_page);
-  const int per = (sr.n_slots + splits - 1) / splits;
-  const int s_begin = min(sr.n_slots, split * per), s_end = min(sr.n_slots, s_begin + per);
-  for (int i = tid; i < Hq * d; i += 128) {
-    qs[i] = Q[b * Hq * d + i];
-    os[i] = 0.f;
-  }
-  for (int h = tid; h < Hq; h += 128) {
-    ms[h] = -INFINITY;
-    ls[h] = 0.f;
-  }
-  for (int sb = s_begin; sb < s_end; sb += kDecF32Tile / 4) {
-    __syncthreads();
-    if (tid < kDecF32Tile) {
-      const int i = sb + (tid >> 2);
-      int pool, rows;
-      slot_pool_rows(sr, i, s_end, i < s_end ? slot_idx(sr, i) : -1, pool, rows, bad_idx);
-      int64_t key = -1;
-      if ((tid & 3) < rows) {
-        const int col = page_of_pool(pv, pool);
-        const int pp = phys_pool(pv, pool, col, __ldg(sr.trow + col), bad_page);
-        if (pp >= 0) key = (int64_t)pp * 4 + (tid & 3);
+  const SlotRow sr = slot_row(a, b, bad_page);
+  const int n_steps = sr.len == 0 ? 0 : row_steps(sr.len, true, a.k);
+  const int w0 = (int)((int64_t)n_steps * rank / splits), w1 = (int)((int64_t)n_steps * (rank + 1) / splits);
+  P::run(a, sr, b, w0, w1, dec_smem, sc, bad_page, bad_idx);
+  const float4* o4 = reinterpret_cast<const float4*>(dec_smem);
+  const int n4 = a.Hq * (D / 4);
+  T* out = a.O + b * a.Hq * D;
+  float* lse = a.LSE + b * a.Hq;
+  if (splits == 1) {
+    for (int i = threadIdx.x; i < n4; i += kAttnThreads) {
+      const float2 ml = sc.ml[i / (D / 4)];
+      store_out4(out + 4 * i, o4[i], inv_sum(ml.y));
+    }
+    if (threadIdx.x < a.Hq) lse[threadIdx.x] = lse_of(sc.ml[threadIdx.x].x, sc.ml[threadIdx.x].y);
+  } else {
+    cluster_sync();
+    // each CTA writes its share of the outputs from all CTAs' parts
+    const uint32_t o_s = smem_u32(o4), ml_s = smem_u32(sc.ml);
+    const int per = (n4 + splits - 1) / splits;
+    const int end = min(n4, (rank + 1) * per);
+    for (int i = rank * per + threadIdx.x; i < end; i += kAttnThreads) {
+      const int h = i / (D / 4);
+      float mm = -INFINITY;
+      for (int s = 0; s < splits; ++s) mm = fmaxf(mm, cluster_ld2(cluster_map(ml_s + 8 * h, s)).x);
+      const float base = mm == -INFINITY ? 0.f : mm;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      float l = 0.f;
+#pragma unroll 4
+      for (int s = 0; s < splits; ++s) {
+        const float2 ml = cluster_ld2(cluster_map(ml_s + 8 * h, s));
+        const float4 x = cluster_ld4(cluster_map(o_s + 16 * i, s));
+        const float f = exp2f(ml.x - base);
+        l += f * ml.y;
+        acc.x += f * x.x;
+        acc.y += f * x.y;
+        acc.z += f * x.z;
+        acc.w += f * x.w;
       }
-      keys[tid] = key;
+      store_out4(out + 4 * i, acc, inv_sum(l));
+      if (i % (D / 4) == 0) lse[h] = lse_of(mm, l);
     }
-    __syncthreads();
-    for (int i = tid; i < kDecF32Tile * d; i += 128) {
-      const int64_t key = keys[i / d];
-      ks[i] = key >= 0 ? K[key * d + i % d] : 0.f;
-      vs[i] = key >= 0 ? V[key * d + i % d] : 0.f;
-    }
-    __syncthreads();
-    for (int i = tid; i < Hq * kDecF32Tile; i += 128) {
-      const int h = i / kDecF32Tile, j = i % kDecF32Tile;
-      float acc = 0.f;
-      for (int c = 0; c < d; ++c) acc = fmaf(qs[h * d + c], ks[j * d + c], acc);
-      ss[i] = keys[j] >= 0 ? acc * scale_log2 : -INFINITY;
-    }
-    __syncthreads();
-    for (int h = tid; h < Hq; h += 128) {
-      float mx = ms[h];
-      for (int j = 0; j < kDecF32Tile; ++j) mx = fmaxf(mx, ss[h * kDecF32Tile + j]);
-      const float base = mx == -INFINITY ? 0.f : mx;
-      const float a = exp2f(ms[h] - base);
-      float sum = ls[h] * a;
-      for (int j = 0; j < kDecF32Tile; ++j) {
-        const float pj = exp2f(ss[h * kDecF32Tile + j] - base);
-        ss[h * kDecF32Tile + j] = pj;
-        sum += pj;
-      }
-      ms[h] = mx;
-      ls[h] = sum;
-      as[h] = a;
-    }
-    __syncthreads();
-    for (int i = tid; i < Hq * d; i += 128) {
-      const int h = i / d, c = i % d;
-      float acc = os[i] * as[h];
-      for (int j = 0; j < kDecF32Tile; ++j) acc = fmaf(ss[h * kDecF32Tile + j], vs[j * d + c], acc);
-      os[i] = acc;
-    }
+    cluster_sync();   // no CTA leaves while its shared memory is being read
   }
   if (bad_idx) record_error(DSA_DEV_ERR_BAD_INDEX);
   if (bad_page) record_error(DSA_DEV_ERR_BAD_PAGE);
-  __syncthreads();
-  const int64_t p = b * splits + split;
-  float* po = part + p * Hq * d;
-  float* pml = part + (int64_t)batch * splits * Hq * d + p * Hq * 2;
-  for (int i = tid; i < Hq * d; i += 128) {
-    const int h = i / d;
-    if (splits == 1) {
-      O[b * Hq * d + i] = ls[h] == 0.f ? 0.f : os[i] / ls[h];
-      if (i % d == 0) LSE[b * Hq + h] = ls[h] == 0.f ? -INFINITY : (ms[h] + log2f(ls[h])) * 0.6931471805599453f;
-    } else {
-      po[i] = os[i];
-      if (i % d == 0) {
-        pml[2 * h] = ms[h];
-        pml[2 * h + 1] = ls[h];
+}
+
+// Whole cache: one CTA per range of the list of steps.
+template <typename T, int D, int MAXH>
+__global__ void __launch_bounds__(kAttnThreads, (Piece<T, D, MAXH>::MIN_CTAS))
+    decode_attn_all_kernel(const __grid_constant__ AttnArgs<T> a) {
+  using P = Piece<T, D, MAXH>;
+  extern __shared__ __align__(128) unsigned char dec_smem[];
+  AttnScratch& sc = P::scratch(dec_smem, a.Hq);
+  chain_wait();
+  chain_release();
+  const Cut cut = make_cut(a.pv, a.batch, P::MIN_STEPS, sc);
+  if (cut.rest <= 0) {
+    put_no_item(a.ps, a.batch);
+    return;
+  }
+  bool bad_page = false, bad_idx = false;
+  int64_t b = cut.row, pos = cut.begin, rest = cut.rest;
+  int w0 = cut.step;
+  const float4* o4 = reinterpret_cast<const float4*>(dec_smem);
+  const int n4 = a.Hq * (D / 4);
+  while (true) {
+    bool bad_len = false;   // recorded by make_cut
+    const SlotRow sr = slot_row(a, b, bad_len);
+    const int n_steps = row_steps(sr.len, false, 0);
+    const int take = (int)min(rest, (int64_t)(n_steps - w0));
+    P::run(a, sr, b, w0, w0 + take, dec_smem, sc, bad_page, bad_idx);
+    if (w0 == 0)
+      put_join_item(a.ps, a.batch, cut, b, pos, n_steps, take == rest);
+    else if (take == rest)
+      put_no_item(a.ps, a.batch);
+    if (w0 == 0 && take == n_steps) {
+      for (int i = threadIdx.x; i < n4; i += kAttnThreads) {
+        const float2 ml = sc.ml[i / (D / 4)];
+        store_out4(a.O + b * a.Hq * D + 4 * i, o4[i], inv_sum(ml.y));
       }
+      if (threadIdx.x < a.Hq)
+        a.LSE[b * a.Hq + threadIdx.x] = lse_of(sc.ml[threadIdx.x].x, sc.ml[threadIdx.x].y);
+    } else {
+      const int64_t piece = 2 * (int64_t)blockIdx.x + (pos != cut.begin);
+      for (int i = threadIdx.x; i < n4; i += kAttnThreads)
+        reinterpret_cast<float4*>(a.ps.o)[piece * n4 + i] = o4[i];
+      if (threadIdx.x < a.Hq) reinterpret_cast<float2*>(a.ps.ml)[piece * a.Hq + threadIdx.x] = sc.ml[threadIdx.x];
     }
+    rest -= take;
+    if (rest <= 0) break;
+    pos += take;
+    w0 = 0;
+    ++b;
+    __syncthreads();   // the results become tiles again
   }
+  if (bad_page) record_error(DSA_DEV_ERR_BAD_PAGE);
 }
 
-// A sum of 0 means no key (o = 0, lse = -infinity); a NaN sum stays NaN.
-// Joins the splits of one (row, head): o = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s.
-template <typename T>
-__global__ void __launch_bounds__(128) decode_join_kernel(const float* __restrict__ part, T* __restrict__ O,
-                                                          float* __restrict__ LSE, int64_t batch, int Hq, int d,
-                                                          int splits) {
-  const int64_t b = blockIdx.x;
+// ------------------------------------------------------------------- the join
+// One CTA per join item and head: o = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s
+// over the row's pieces s.  The weights go to shared memory, then each warp
+// sums every 16th piece (512 B a load) and the warps' sums are added in order.
+template <typename T, int D>
+__global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(Pieces ps, T* __restrict__ O,
+                                                                   float* __restrict__ LSE, int Hq) {
+  constexpr int LPP = D / 4;            // lanes per piece row
+  constexpr int PPW = 32 / LPP;         // pieces a warp reads at once
+  extern __shared__ __align__(16) float join_smem[];
+  float* sums = join_smem;                                 // [warps * PPW][D]: 128 floats a warp
+  float* red = sums + 128 * (kJoinThreads / 32);           // [2][warps]
+  float* wt = red + 2 * (kJoinThreads / 32);               // [kAttnCtas]
+  chain_wait();
+  chain_release();
+  const JoinItem it = ps.items[blockIdx.x];
+  if (it.row < 0) return;
   const int h = blockIdx.y;
-  const float* pml = part + batch * splits * Hq * d + b * splits * Hq * 2 + 2 * h;
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const int n = it.last - it.first + 1;   // <= kAttnCtas
+  auto piece = [&](int s) { return 2 * (int64_t)(it.first + s) + (s == 0 ? it.skip : 0); };
+  auto ml_of = [&](int s) { return __ldcg(reinterpret_cast<const float2*>(ps.ml) + piece(s) * Hq + h); };
   float mm = -INFINITY;
-  for (int s = 0; s < splits; ++s) mm = fmaxf(mm, __ldg(pml + (int64_t)s * Hq * 2));
-  const float base = mm == -INFINITY ? 0.f : mm;
-  for (int c = threadIdx.x; c < d; c += blockDim.x) {
-    float acc = 0.f, l = 0.f;
-    for (int s = 0; s < splits; ++s) {
-      const float f = exp2f(__ldg(pml + (int64_t)s * Hq * 2) - base);
-      acc += f * __ldg(part + ((b * splits + s) * Hq + h) * (int64_t)d + c);
-      l += f * __ldg(pml + (int64_t)s * Hq * 2 + 1);
-    }
-    O[(b * Hq + h) * (int64_t)d + c] = (T)(l == 0.f ? 0.f : acc / l);
-    if (c == 0) LSE[b * Hq + h] = l == 0.f ? -INFINITY : (mm + log2f(l)) * 0.6931471805599453f;
+  for (int s = threadIdx.x; s < n; s += blockDim.x) mm = fmaxf(mm, ml_of(s).x);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
+  if (lane == 0) red[wid] = mm;
+  __syncthreads();
+  mm = -INFINITY;
+  for (int w = 0; w < warps; ++w) mm = fmaxf(mm, red[w]);
+  float l = 0.f;
+  for (int s = threadIdx.x; s < n; s += blockDim.x) {
+    const float2 ml = ml_of(s);
+    const float f = exp2f(ml.x - (mm == -INFINITY ? 0.f : mm));
+    wt[s] = f;
+    l += f * ml.y;
   }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  if (lane == 0) red[kJoinThreads / 32 + wid] = l;
+  __syncthreads();
+  l = 0.f;
+  for (int w = 0; w < warps; ++w) l += red[kJoinThreads / 32 + w];
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  const int c4 = lane % LPP;
+#pragma unroll 4
+  for (int s = wid * PPW + lane / LPP; s < n; s += warps * PPW) {
+    const float4 x = __ldcg(reinterpret_cast<const float4*>(ps.o) + (piece(s) * Hq + h) * LPP + c4);
+    const float w = wt[s];
+    acc.x += w * x.x;
+    acc.y += w * x.y;
+    acc.z += w * x.z;
+    acc.w += w * x.w;
+  }
+  reinterpret_cast<float4*>(sums)[threadIdx.x] = acc;
+  __syncthreads();
+  const float inv = inv_sum(l);
+  for (int c = threadIdx.x; c < D; c += blockDim.x) {
+    float x = 0.f;
+    for (int i = 0; i < warps * PPW; ++i) x += sums[i * D + c];
+    O[((int64_t)it.row * Hq + h) * D + c] = (T)(x * inv);
+  }
+  if (threadIdx.x == 0) LSE[(int64_t)it.row * Hq + h] = lse_of(mm, l);
 }
 
-template <int D, int HG>
-static cudaError_t launch_bf16(const DecodeAttnArgs& a, int splits, float scale_log2, cudaStream_t s) {
-  constexpr int smem = DecCfg<D, 2>::SMEM;
-  auto kern = decode_attn_bf16_kernel<D, HG>;
+// CTAs per row of selected pools: the most (1, 2, 4, 8 or 16, a cluster) that
+// keep all rows resident at once and give a CTA work for its warps.
+static unsigned selected_splits(int64_t batch, int n_steps, int min_steps) {
+  unsigned s = 1;
+  while (s < 16 && batch * s * 2 <= kAttnCtas && (int)s * min_steps < n_steps) s *= 2;
+  return s;
+}
+
+template <typename T, int D, int MAXH>
+static cudaError_t launch_all(const DecodeAttnArgs& g, const AttnArgs<T>& a, cudaStream_t s) {
+  using P = Piece<T, D, MAXH>;
+  const int smem = P::smem(a.Hq);
+  if (a.idx) {
+    auto kern = decode_attn_selected_kernel<T, D, MAXH>;
+    const unsigned splits = selected_splits(a.batch, (a.k + 4) >> 2, P::MIN_STEPS);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess && splits > 8) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    return launch_chained_cluster(splits, kern, dim3(splits, (unsigned)a.batch), dim3(kAttnThreads), smem, s, a);
+  }
+  auto kern = decode_attn_all_kernel<T, D, MAXH>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  kern<<<dim3(splits, (unsigned)a.batch), 128, smem, s>>>(
-      a.pv, a.batch, static_cast<const __nv_bfloat16*>(a.q), static_cast<const __nv_bfloat16*>(a.ck),
-      static_cast<const __nv_bfloat16*>(a.cv), a.idx, static_cast<__nv_bfloat16*>(a.o), a.lse, a.ws, a.Hq, a.k,
-      scale_log2, splits);
-  return cudaGetLastError();
+  // as many CTAs as can have work
+  const int64_t row_max = ((int64_t)a.pv.capacity + 15) >> 4;
+  const int64_t want = (a.batch * row_max + P::MIN_STEPS - 1) / P::MIN_STEPS;
+  const unsigned ctas = (unsigned)(want < kAttnCtas ? want : kAttnCtas);
+  e = launch_chained(kern, dim3(ctas), dim3(kAttnThreads), smem, s, a);
+  if (e != cudaSuccess || ctas == 1) return e;
+  // few rows: many pieces each, more warps per join
+  const unsigned items = a.batch < ctas ? (unsigned)a.batch : ctas;
+  const unsigned threads = items <= 16 ? kJoinThreads : 128;
+  const size_t jsmem = sizeof(float) * (kJoinThreads / 32 * 130 + kAttnCtas);
+  return launch_chained(decode_join_kernel<T, D>, dim3(items, a.Hq), dim3(threads), jsmem, s, a.ps, a.O, a.LSE, a.Hq);
+}
+
+template <typename T>
+static cudaError_t launch_typed(const DecodeAttnArgs& g, cudaStream_t s) {
+  AttnArgs<T> a;
+  a.pv = g.pv;
+  a.batch = g.batch;
+  a.Q = static_cast<const T*>(g.q);
+  a.K = static_cast<const T*>(g.ck);
+  a.V = static_cast<const T*>(g.cv);
+  a.idx = g.idx;
+  a.O = static_cast<T*>(g.o);
+  a.LSE = g.lse;
+  a.ps = pieces_of(g.ws, g.Hq, g.d);
+  a.Hq = g.Hq;
+  a.k = g.k;
+  a.scale_log2 = g.scale * 1.4426950408889634f;
+  if (g.d == 128) {
+    if (g.Hq > 16) return launch_all<T, 128, 32>(g, a, s);
+    if (sizeof(T) == 2 || g.Hq > 8) return launch_all<T, 128, 16>(g, a, s);
+    return launch_all<T, 128, sizeof(T) == 2 ? 16 : 8>(g, a, s);
+  }
+  if (g.Hq > 16) return launch_all<T, 64, 32>(g, a, s);
+  if (sizeof(T) == 2 || g.Hq > 8) return launch_all<T, 64, 16>(g, a, s);
+  return launch_all<T, 64, sizeof(T) == 2 ? 16 : 8>(g, a, s);
 }
 
 cudaError_t launch_decode_attn(bool bf16, const DecodeAttnArgs& a, cudaStream_t s) {
-  const float scale_log2 = a.scale * 1.4426950408889634f;
-  const int64_t max_slots = a.idx ? (int64_t)a.k + 1 : ((int64_t)a.pv.capacity + 3) / 4;
-  const int splits = attn_splits(a.batch, max_slots);
-  cudaError_t e;
-  if (bf16) {
-    if (a.d == 128)
-      e = a.Hq > 16 ? launch_bf16<128, 2>(a, splits, scale_log2, s) : launch_bf16<128, 1>(a, splits, scale_log2, s);
-    else
-      e = a.Hq > 16 ? launch_bf16<64, 2>(a, splits, scale_log2, s) : launch_bf16<64, 1>(a, splits, scale_log2, s);
-  } else {
-    const size_t smem =
-        sizeof(float) * ((size_t)a.Hq * a.d * 2 + 2 * kDecF32Tile * a.d + a.Hq * kDecF32Tile + 3 * a.Hq);
-    e = cudaFuncSetAttribute(decode_attn_f32_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-    decode_attn_f32_kernel<<<dim3(splits, (unsigned)a.batch), 128, smem, s>>>(
-        a.pv, a.batch, static_cast<const float*>(a.q), static_cast<const float*>(a.ck),
-        static_cast<const float*>(a.cv), a.idx, static_cast<float*>(a.o), a.lse, a.ws, a.Hq, a.d, a.k, scale_log2,
-        splits);
-    e = cudaGetLastError();
-  }
-  if (e != cudaSuccess || splits == 1) return e;
-  const dim3 grid((unsigned)a.batch, a.Hq);
-  if (bf16)
-    decode_join_kernel<__nv_bfloat16><<<grid, 128, 0, s>>>(a.ws, static_cast<__nv_bfloat16*>(a.o), a.lse, a.batch,
-                                                           a.Hq, a.d, splits);
-  else
-    decode_join_kernel<float><<<grid, 128, 0, s>>>(a.ws, static_cast<float*>(a.o), a.lse, a.batch, a.Hq, a.d, splits);
-  return cudaGetLastError();
+  return bf16 ? launch_typed<__nv_bfloat16>(a, s) : launch_typed<float>(a, s);
 }
 
 }  // namespace dsa
