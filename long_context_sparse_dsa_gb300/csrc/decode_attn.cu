@@ -24,8 +24,7 @@
 //
 // bf16: steps go round-robin to a CTA's warps, each with a ring of its own
 // filled by cp.async, heads on the M side of m16n8k16 MMAs as in attn_fwd.cu;
-// with more than 16 heads two warps share a ring, one loads K rows, the other
-// V rows.  P enters P V as two bf16 terms (hi + lo, about 2^-17 relative): the
+// up to two groups of 16.  P enters P V as two bf16 terms (hi + lo, about 2^-17 relative): the
 // MMAs are not what bounds the kernel.
 // fp32: tiles of 32 keys in shared memory, plain FFMA; for S a lane owns a key
 // and a warp a quarter of the heads, for P V a thread owns a channel.
@@ -34,9 +33,10 @@
 
 namespace dsa {
 
-constexpr int kAttnCtas = 456;   // 3 per SM of 152
+constexpr int kSms = 152;
+constexpr int kAttnCtas = 3 * kSms;   // most CTAs of a launch over the whole cache
 constexpr int kAttnThreads = 128;
-constexpr int kJoinThreads = 512;
+constexpr int kJoinThreads = 256;
 constexpr float kDecLazyLog2 = 8.f;   // the softmax base lags the running max by at most this (log2 units)
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -86,13 +86,15 @@ __device__ __forceinline__ int row_steps(int len, bool selected, int k) {
 }
 // Slot `i` in three stages, so that its two dependent loads can be issued
 // ahead: the idx entry, the pool and its visible rows, the physical pool.
+template <bool SEL>
 __device__ __forceinline__ int slot_idx(const SlotRow& r, int i) {
-  return (r.idx && i < r.k) ? __ldg(r.idx + i) : -1;
+  return (SEL && i < r.k) ? __ldg(r.idx + i) : -1;
 }
+template <bool SEL>
 __device__ __forceinline__ void slot_pool_rows(const SlotRow& r, int i, int raw, int& pool, int& rows, bool& bad) {
   pool = 0;
   rows = 0;
-  if (r.idx) {
+  if (SEL) {
     if (i < r.k) {
       const bool out = raw >= (r.len >> 2);
       bad |= out && r.len > 0;
@@ -126,7 +128,7 @@ struct Cut {
 // SM.
 struct alignas(16) AttnScratch {
   float2 ml[32];        // a head's base (log2 units) and sum, joined over the CTA's warps
-  float m[4][16], l[4][16];   // bf16: the warps' own; m becomes their weights
+  float m[4][32], l[4][32];   // bf16: the warps' own; m becomes their weights
   int64_t warp_sum[kAttnThreads / 32];
   int64_t row;
   int64_t step;
@@ -216,66 +218,44 @@ __device__ __forceinline__ void put_no_item(const Pieces& ps, int64_t batch) {
 }
 
 // ------------------------------------------------------------------- bf16
-// One tensor's half of gather_step16 (gather.cuh): rows of K or of V.
-template <int D>
-__device__ __forceinline__ void gather_half16(uint32_t tile, const __nv_bfloat16* __restrict__ T,
-                                              const uint32_t (&slots)[4], const GatherLane<D>& gl) {
-  using C = GatherCfg<D>;
-  constexpr int NRB = GatherLane<D>::NRB;
-  constexpr int POOL_BYTES = 4 * C::ROW_BYTES;
-#pragma unroll
-  for (int sig = 0; sig < 4; ++sig) {
-    const int nrows = slot_nrows(slots[sig]);
-    const char* src =
-        reinterpret_cast<const char*>(T) + (int64_t)(slots[sig] >> 3) * POOL_BYTES + gl.src_off;
-#pragma unroll
-    for (int rb = 0; rb < NRB; ++rb) {
-      const uint32_t bytes = rb * C::ROWS_PER_COPY + gl.row_lo < nrows ? 16u : 0u;
-      cp_async16(tile + sig * POOL_BYTES + gl.dst_off[sig & 1][rb], src + rb * C::ROWS_PER_COPY * C::ROW_BYTES, bytes);
-    }
-  }
-}
-
-template <int D, int HG>
+// A CTA's warps each take every 4th step, with a ring of their own.  NG: groups
+// of 16 heads; a warp computes all of them from each gathered tile (two warps
+// sharing a ring, each with one group, ran 94 us against 82 for 40 ragged rows
+// of 32 heads: twice the ldmatrix traffic and barriers).
+template <int D, int NG>
 struct DecCfg {
   static constexpr int WARPS = kAttnThreads / 32;
-  static constexpr int RINGS = WARPS / HG;           // a ring per warp, or per pair
-  static constexpr int NSUB = RINGS;                 // steps in progress at once
-  static constexpr int NST = (D == 128 ? 2 : 4) * HG;
+  static constexpr int CTAS = D == 128 && NG == 2 ? 2 : 3;   // per SM: 255 or 168 registers a thread
+  static constexpr int NST = D == 128 ? (NG == 2 ? 3 : 2) : 4;
   static constexpr int RING = NST * GatherCfg<D>::STAGE_BYTES;
-  static constexpr int TILES = RINGS * RING;
+  static constexpr int TILES = WARPS * RING;
   static constexpr int SMEM = TILES + (int)sizeof(AttnScratch);
-  static_assert(TILES >= WARPS * 16 * D * 4, "the rings double as the join buffer");
+  static_assert(TILES >= WARPS * NG * 16 * D * 4, "the rings double as the join buffer");
 };
 
 // Steps [w0, steps) of row b.  Leaves o [Hq][D] at the start of the tiles and
 // the heads' bases and sums in sc.ml; ends with a __syncthreads().
-template <int D, int HG>
+// SEL: the slots are selected pools; else all pools.
+template <int D, int NG, bool SEL>
 __device__ __forceinline__ void attn_piece_bf16(const PagedView& pv, const __nv_bfloat16* __restrict__ Q,
                                                 const __nv_bfloat16* __restrict__ K,
                                                 const __nv_bfloat16* __restrict__ V, const SlotRow& sr, int64_t b,
                                                 int w0, int steps, int Hq, float scale_log2, unsigned char* tiles,
                                                 AttnScratch& sc, bool& bad_page, bool& bad_idx) {
   using C = GatherCfg<D>;
-  using G = DecCfg<D, HG>;
+  using G = DecCfg<D, NG>;
   constexpr int NST = G::NST;
-  constexpr int NSUB = G::NSUB;
+  constexpr int WARPS = G::WARPS;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int hg = warp % HG, sub = warp / HG;
   const int g = lane >> 2, qi = lane & 3;
-  const uint32_t ring = smem_u32(tiles) + sub * G::RING;
+  const uint32_t ring = smem_u32(tiles) + warp * G::RING;
   const GatherLane<D> gl = gather_lane<D>(lane);
-  auto ring_sync = [&]() {
-    if (HG == 1)
-      __syncwarp();
-    else
-      asm volatile("bar.sync %0, 64;\n" ::"r"(1 + sub) : "memory");
-  };
+
   // Slot pipeline: this lane decides slot (lane & 3) of every step of its warp.
   int raw = -1, pool = 0, rows = 0, page = 0;
-  auto load_raw = [&](int st) { raw = st < steps ? slot_idx(sr, st * 4 + (lane & 3)) : -1; };
+  auto load_raw = [&](int st) { raw = st < steps ? slot_idx<SEL>(sr, st * 4 + (lane & 3)) : -1; };
   auto load_page = [&](int st) {
-    slot_pool_rows(sr, st * 4 + (lane & 3), raw, pool, rows, bad_idx);
+    slot_pool_rows<SEL>(sr, st * 4 + (lane & 3), raw, pool, rows, bad_idx);
     if (st >= steps) rows = 0;
     page = rows ? __ldg(sr.trow + page_of_pool(pv, pool)) : 0;
   };
@@ -293,43 +273,42 @@ __device__ __forceinline__ void attn_piece_bf16(const PagedView& pv, const __nv_
         slots[s] = __shfl_sync(0xffffffffu, mine, s);
         v |= (slots[s] & 7u) << (4 * s);
       }
-      const uint32_t base = ring + stage * C::STAGE_BYTES;
-      if (HG == 1)
-        gather_step16<D>(base, K, V, slots, gl);
-      else
-        gather_half16<D>(base + hg * C::TILE_BYTES, hg ? V : K, slots, gl);
+      gather_step16<D>(ring + stage * C::STAGE_BYTES, K, V, slots, gl);
     }
     cp_async_commit();
   };
 
-  uint32_t qa[D / 16][4];
+  uint32_t qa[NG][D / 16][4];
   {
-    const int h0 = hg * 16 + g, h1 = h0 + 8;
     const uint32_t* q32 = reinterpret_cast<const uint32_t*>(Q + b * Hq * D);
 #pragma unroll
-    for (int ks = 0; ks < D / 16; ++ks) {
-      const int c0 = (h0 * D + ks * 16 + 2 * qi) / 2, c1 = (h1 * D + ks * 16 + 2 * qi) / 2;
-      qa[ks][0] = h0 < Hq ? __ldg(q32 + c0) : 0u;
-      qa[ks][1] = h1 < Hq ? __ldg(q32 + c1) : 0u;
-      qa[ks][2] = h0 < Hq ? __ldg(q32 + c0 + 4) : 0u;
-      qa[ks][3] = h1 < Hq ? __ldg(q32 + c1 + 4) : 0u;
+    for (int n = 0; n < NG; ++n) {
+      const int h0 = n * 16 + g, h1 = h0 + 8;
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks) {
+        const int c0 = (h0 * D + ks * 16 + 2 * qi) / 2, c1 = (h1 * D + ks * 16 + 2 * qi) / 2;
+        qa[n][ks][0] = h0 < Hq ? __ldg(q32 + c0) : 0u;
+        qa[n][ks][1] = h1 < Hq ? __ldg(q32 + c1) : 0u;
+        qa[n][ks][2] = h0 < Hq ? __ldg(q32 + c0 + 4) : 0u;
+        qa[n][ks][3] = h1 < Hq ? __ldg(q32 + c1 + 4) : 0u;
+      }
     }
   }
   // fill the ring: all idx entries, then all pages, then the rows
-  int st = w0 + sub;
+  int st = w0 + warp;
   {
     int raws[NST], pools[NST], rws[NST], pgs[NST];
 #pragma unroll
     for (int i = 0; i < NST; ++i) {
-      load_raw(st + i * NSUB);
+      load_raw(st + i * WARPS);
       raws[i] = raw;
     }
-    load_raw(st + NST * NSUB);
+    load_raw(st + NST * WARPS);
     const int raw_next = raw;
 #pragma unroll
     for (int i = 0; i < NST; ++i) {
       raw = raws[i];
-      load_page(st + i * NSUB);
+      load_page(st + i * WARPS);
       pools[i] = pool;
       rws[i] = rows;
       pgs[i] = page;
@@ -339,23 +318,25 @@ __device__ __forceinline__ void attn_piece_bf16(const PagedView& pv, const __nv_
       pool = pools[i];
       rows = rws[i];
       page = pgs[i];
-      if (i < NST - 1) fetch(st + i * NSUB, i, vis[i]);
+      if (i < NST - 1) fetch(st + i * WARPS, i, vis[i]);
     }
     raw = raw_next;
   }
-  float o[D / 8][4];
+  float o[NG][D / 8][4];
+  float m[NG][2], l[NG][2];   // heads g and g + 8 of each group
 #pragma unroll
-  for (int n = 0; n < D / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
-  float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+  for (int n = 0; n < NG; ++n) {
+#pragma unroll
+    for (int c = 0; c < D / 8; ++c) o[n][c][0] = o[n][c][1] = o[n][c][2] = o[n][c][3] = 0.f;
+    m[n][0] = m[n][1] = -INFINITY;
+    l[n][0] = l[n][1] = 0.f;
+  }
 
   int stage = 0;
-  for (; st < steps; st += NSUB) {
-    {
-      const int nx = stage == 0 ? NST - 1 : stage - 1;   // the stage consumed last
-      fetch(st + (NST - 1) * NSUB, nx, vis[NST - 1]);
-      load_page(st + NST * NSUB);
-      load_raw(st + (NST + 1) * NSUB);
-    }
+  for (; st < steps; st += WARPS) {
+    fetch(st + (NST - 1) * WARPS, stage == 0 ? NST - 1 : stage - 1, vis[NST - 1]);   // the stage consumed last
+    load_page(st + NST * WARPS);
+    load_raw(st + (NST + 1) * WARPS);
     bool kv[2][2];
 #pragma unroll
     for (int nt = 0; nt < 2; ++nt) {
@@ -364,15 +345,18 @@ __device__ __forceinline__ void attn_piece_bf16(const PagedView& pv, const __nv_
       for (int e = 0; e < 2; ++e) kv[nt][e] = 2 * (qi & 1) + e < nrows;
     }
     cp_async_wait<NST - 1>();
-    ring_sync();
+    __syncwarp();
     const uint32_t ks_base = ring + stage * C::STAGE_BYTES;
     const uint32_t vs_base = ks_base + C::TILE_BYTES;
     // S = Q K^T as four independent accumulation chains
-    float s[2][4], s2[2][4];
+    constexpr int CHAINS = NG == 1 ? 2 : 1;
+    float s[NG][CHAINS][2][4];
 #pragma unroll
-    for (int nt = 0; nt < 2; ++nt)
+    for (int n = 0; n < NG; ++n)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[nt][e] = s2[nt][e] = 0.f;
+      for (int c = 0; c < CHAINS; ++c)
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) s[n][c][nt][0] = s[n][c][nt][1] = s[n][c][nt][2] = s[n][c][nt][3] = 0.f;
     {
       const int mtx = lane >> 3, r = lane & 7;
       const int key = (mtx >> 1) * 8 + r;
@@ -381,64 +365,68 @@ __device__ __forceinline__ void attn_piece_bf16(const PagedView& pv, const __nv_
         const int ch = 2 * ks + (mtx & 1);
         uint32_t b0, b1, b2, b3;
         ldsm_x4(ks_base + key * C::ROW_BYTES + ((ch ^ (key & 7)) << 4), b0, b1, b2, b3);
-        if (ks & 1) {
-          mma_bf16_16816(s2[0], qa[ks][0], qa[ks][1], qa[ks][2], qa[ks][3], b0, b1);
-          mma_bf16_16816(s2[1], qa[ks][0], qa[ks][1], qa[ks][2], qa[ks][3], b2, b3);
-        } else {
-          mma_bf16_16816(s[0], qa[ks][0], qa[ks][1], qa[ks][2], qa[ks][3], b0, b1);
-          mma_bf16_16816(s[1], qa[ks][0], qa[ks][1], qa[ks][2], qa[ks][3], b2, b3);
+#pragma unroll
+        for (int n = 0; n < NG; ++n) {
+          float(&sc2)[2][4] = s[n][ks % CHAINS];
+          mma_bf16_16816(sc2[0], qa[n][ks][0], qa[n][ks][1], qa[n][ks][2], qa[n][ks][3], b0, b1);
+          mma_bf16_16816(sc2[1], qa[n][ks][0], qa[n][ks][1], qa[n][ks][2], qa[n][ks][3], b2, b3);
         }
       }
     }
     // online softmax in log2 units with a lazily moved base (attn_fwd.cu)
-    float mx0 = -INFINITY, mx1 = -INFINITY;
+    uint32_t ph[NG][4], pl[NG][4];
+    bool moved = false;
+    float al[NG][2];
 #pragma unroll
-    for (int nt = 0; nt < 2; ++nt) {
-      s[nt][0] = kv[nt][0] ? s[nt][0] + s2[nt][0] : -INFINITY;
-      s[nt][1] = kv[nt][1] ? s[nt][1] + s2[nt][1] : -INFINITY;
-      s[nt][2] = kv[nt][0] ? s[nt][2] + s2[nt][2] : -INFINITY;
-      s[nt][3] = kv[nt][1] ? s[nt][3] + s2[nt][3] : -INFINITY;
-      mx0 = fmaxf(mx0, fmaxf(s[nt][0], s[nt][1]));
-      mx1 = fmaxf(mx1, fmaxf(s[nt][2], s[nt][3]));
-    }
-    mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 1));
-    mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 2));
-    mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 1));
-    mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 2));
-    mx0 *= scale_log2;
-    mx1 *= scale_log2;
-    const bool up0 = mx0 > m0 + kDecLazyLog2, up1 = mx1 > m1 + kDecLazyLog2;
-    const float mn0 = up0 ? mx0 : m0, mn1 = up1 ? mx1 : m1;
-    const float base0 = mn0 == -INFINITY ? 0.f : mn0, base1 = mn1 == -INFINITY ? 0.f : mn1;
-    const float a0 = up0 ? ex2_approx(m0 - base0) : 1.f, a1 = up1 ? ex2_approx(m1 - base1) : 1.f;
-    m0 = mn0;
-    m1 = mn1;
-    float rs0 = 0.f, rs1 = 0.f;
+    for (int n = 0; n < NG; ++n) {
+      float(&z)[2][4] = s[n][0];
+      float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-    for (int nt = 0; nt < 2; ++nt) {
-      s[nt][0] = ex2_approx(fmaf(s[nt][0], scale_log2, -base0));
-      s[nt][1] = ex2_approx(fmaf(s[nt][1], scale_log2, -base0));
-      s[nt][2] = ex2_approx(fmaf(s[nt][2], scale_log2, -base1));
-      s[nt][3] = ex2_approx(fmaf(s[nt][3], scale_log2, -base1));
-      rs0 += s[nt][0] + s[nt][1];
-      rs1 += s[nt][2] + s[nt][3];
-    }
-    l0 = l0 * a0 + rs0;
-    l1 = l1 * a1 + rs1;
-    if (__any_sync(0xffffffffu, a0 != 1.f || a1 != 1.f)) {
+      for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
-      for (int n = 0; n < D / 8; ++n) {
-        o[n][0] *= a0;
-        o[n][1] *= a0;
-        o[n][2] *= a1;
-        o[n][3] *= a1;
+        for (int e = 0; e < 4; ++e) {
+          if (CHAINS == 2) z[nt][e] += s[n][CHAINS - 1][nt][e];
+          z[nt][e] = kv[nt][e & 1] ? z[nt][e] : -INFINITY;
+          mx[e >> 1] = fmaxf(mx[e >> 1], z[nt][e]);
+        }
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
+        mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
+        mx[r] *= scale_log2;
+        const bool up = mx[r] > m[n][r] + kDecLazyLog2;
+        const float mn = up ? mx[r] : m[n][r];
+        const float base = mn == -INFINITY ? 0.f : mn;
+        al[n][r] = up ? ex2_approx(m[n][r] - base) : 1.f;
+        moved |= up;
+        m[n][r] = mn;
+        float sum = 0.f;
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+          for (int e = 2 * r; e < 2 * r + 2; ++e) {
+            z[nt][e] = ex2_approx(fmaf(z[nt][e], scale_log2, -base));
+            sum += z[nt][e];
+          }
+        l[n][r] = l[n][r] * al[n][r] + sum;
+      }
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt) {
+        split_hi_lo(z[nt][0], z[nt][1], ph[n][2 * nt], pl[n][2 * nt]);
+        split_hi_lo(z[nt][2], z[nt][3], ph[n][2 * nt + 1], pl[n][2 * nt + 1]);
       }
     }
-    uint32_t pa0, pa1, pa2, pa3, pl0, pl1, pl2, pl3;
-    split_hi_lo(s[0][0], s[0][1], pa0, pl0);
-    split_hi_lo(s[0][2], s[0][3], pa1, pl1);
-    split_hi_lo(s[1][0], s[1][1], pa2, pl2);
-    split_hi_lo(s[1][2], s[1][3], pa3, pl3);
+    if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+      for (int n = 0; n < NG; ++n)
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+          o[n][c][0] *= al[n][0];
+          o[n][c][1] *= al[n][0];
+          o[n][c][2] *= al[n][1];
+          o[n][c][3] *= al[n][1];
+        }
+    }
     {
       const int mtx = lane >> 3, r = lane & 7;
       const int key = (mtx & 1) * 8 + r;
@@ -448,17 +436,23 @@ __device__ __forceinline__ void attn_piece_bf16(const PagedView& pv, const __nv_
         uint32_t b0, b1, b2, b3, c0, c1, c2, c3;
         ldsm_x4_t(vs_base + key * C::ROW_BYTES + ((ch ^ (key & 7)) << 4), b0, b1, b2, b3);
         ldsm_x4_t(vs_base + key * C::ROW_BYTES + (((ch + 2) ^ (key & 7)) << 4), c0, c1, c2, c3);
-        mma_bf16_16816(o[2 * j], pa0, pa1, pa2, pa3, b0, b1);
-        mma_bf16_16816(o[2 * j + 1], pa0, pa1, pa2, pa3, b2, b3);
-        mma_bf16_16816(o[2 * j + 2], pa0, pa1, pa2, pa3, c0, c1);
-        mma_bf16_16816(o[2 * j + 3], pa0, pa1, pa2, pa3, c2, c3);
-        mma_bf16_16816(o[2 * j], pl0, pl1, pl2, pl3, b0, b1);
-        mma_bf16_16816(o[2 * j + 1], pl0, pl1, pl2, pl3, b2, b3);
-        mma_bf16_16816(o[2 * j + 2], pl0, pl1, pl2, pl3, c0, c1);
-        mma_bf16_16816(o[2 * j + 3], pl0, pl1, pl2, pl3, c2, c3);
+#pragma unroll
+        for (int n = 0; n < NG; ++n) {
+          mma_bf16_16816(o[n][2 * j], ph[n][0], ph[n][1], ph[n][2], ph[n][3], b0, b1);
+          mma_bf16_16816(o[n][2 * j + 1], ph[n][0], ph[n][1], ph[n][2], ph[n][3], b2, b3);
+          mma_bf16_16816(o[n][2 * j + 2], ph[n][0], ph[n][1], ph[n][2], ph[n][3], c0, c1);
+          mma_bf16_16816(o[n][2 * j + 3], ph[n][0], ph[n][1], ph[n][2], ph[n][3], c2, c3);
+        }
+#pragma unroll
+        for (int n = 0; n < NG; ++n) {
+          mma_bf16_16816(o[n][2 * j], pl[n][0], pl[n][1], pl[n][2], pl[n][3], b0, b1);
+          mma_bf16_16816(o[n][2 * j + 1], pl[n][0], pl[n][1], pl[n][2], pl[n][3], b2, b3);
+          mma_bf16_16816(o[n][2 * j + 2], pl[n][0], pl[n][1], pl[n][2], pl[n][3], c0, c1);
+          mma_bf16_16816(o[n][2 * j + 3], pl[n][0], pl[n][1], pl[n][2], pl[n][3], c2, c3);
+        }
       }
     }
-    ring_sync();
+    __syncwarp();
 #pragma unroll
     for (int i = 0; i + 1 < NST; ++i) vis[i] = vis[i + 1];
     stage = stage == NST - 1 ? 0 : stage + 1;
@@ -466,55 +460,57 @@ __device__ __forceinline__ void attn_piece_bf16(const PagedView& pv, const __nv_
   cp_async_wait<0>();
 
   // ---- join the CTA's warps ----------------------------------------------------
-  l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
-  l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
-  l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
-  l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
-  if (qi == 0) {
-    sc.m[warp][g] = m0;
-    sc.m[warp][g + 8] = m1;
-    sc.l[warp][g] = l0;
-    sc.l[warp][g + 8] = l1;
-  }
-  __syncthreads();   // every ring is idle: the tiles are the join buffer, [warp][16][D]
-  {
-    float* my = reinterpret_cast<float*>(tiles) + warp * 16 * D;
 #pragma unroll
-    for (int n = 0; n < D / 8; ++n) {
-      *reinterpret_cast<float2*>(my + g * D + n * 8 + 2 * qi) = make_float2(o[n][0], o[n][1]);
-      *reinterpret_cast<float2*>(my + (g + 8) * D + n * 8 + 2 * qi) = make_float2(o[n][2], o[n][3]);
+  for (int n = 0; n < NG; ++n)
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      l[n][r] += __shfl_xor_sync(0xffffffffu, l[n][r], 1);
+      l[n][r] += __shfl_xor_sync(0xffffffffu, l[n][r], 2);
+      if (qi == 0) {
+        sc.m[warp][n * 16 + g + 8 * r] = m[n][r];
+        sc.l[warp][n * 16 + g + 8 * r] = l[n][r];
+      }
+    }
+  __syncthreads();   // every ring is idle: the tiles are the join buffer, [warp][NG * 16][D]
+#pragma unroll
+  for (int n = 0; n < NG; ++n) {
+    float* my = reinterpret_cast<float*>(tiles) + (warp * NG + n) * 16 * D;
+#pragma unroll
+    for (int c = 0; c < D / 8; ++c) {
+      *reinterpret_cast<float2*>(my + g * D + c * 8 + 2 * qi) = make_float2(o[n][c][0], o[n][c][1]);
+      *reinterpret_cast<float2*>(my + (g + 8) * D + c * 8 + 2 * qi) = make_float2(o[n][c][2], o[n][c][3]);
     }
   }
-  if (threadIdx.x < HG * 16) {   // warps h/16, h/16 + HG, .. hold head h's parts
-    const int h = threadIdx.x, r = h & 15;
-    float mm = -INFINITY, l = 0.f;
+  if (threadIdx.x < NG * 16) {
+    const int h = threadIdx.x;
+    float mm = -INFINITY, sum = 0.f;
 #pragma unroll
-    for (int s = 0; s < NSUB; ++s) mm = fmaxf(mm, sc.m[s * HG + (h >> 4)][r]);
+    for (int w = 0; w < WARPS; ++w) mm = fmaxf(mm, sc.m[w][h]);
     const float base = mm == -INFINITY ? 0.f : mm;
 #pragma unroll
-    for (int s = 0; s < NSUB; ++s) {
-      const float f = ex2_approx(sc.m[s * HG + (h >> 4)][r] - base);
-      sc.m[s * HG + (h >> 4)][r] = f;
-      l += f * sc.l[s * HG + (h >> 4)][r];
+    for (int w = 0; w < WARPS; ++w) {
+      const float f = ex2_approx(sc.m[w][h] - base);
+      sc.m[w][h] = f;
+      sum += f * sc.l[w][h];
     }
-    sc.ml[h] = make_float2(mm, l);
+    sc.ml[h] = make_float2(mm, sum);
   }
   __syncthreads();
   float4* o4 = reinterpret_cast<float4*>(tiles);
 #pragma unroll
-  for (int i = threadIdx.x; i < HG * 16 * D / 4; i += kAttnThreads) {
+  for (int i = threadIdx.x; i < NG * 16 * D / 4; i += kAttnThreads) {
     const int h = i / (D / 4);
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int s = 0; s < NSUB; ++s) {
-      const float f = sc.m[s * HG + (h >> 4)][h & 15];
-      const float4 x = o4[s * HG * 16 * (D / 4) + i];
+    for (int w = 0; w < WARPS; ++w) {
+      const float f = sc.m[w][h];
+      const float4 x = o4[w * NG * 16 * (D / 4) + i];
       acc.x += f * x.x;
       acc.y += f * x.y;
       acc.z += f * x.z;
       acc.w += f * x.w;
     }
-    o4[i] = acc;   // in place: warp group 0's part, this thread's own element
+    o4[i] = acc;   // in place: warp 0's part, this thread's own element
   }
   __syncthreads();
 }
@@ -534,7 +530,7 @@ struct F32Cfg {
 };
 
 // MAXH: heads, rounded up to 8, 16 or 32.  As attn_piece_bf16.
-template <int D, int MAXH>
+template <int D, int MAXH, bool SEL>
 __device__ __forceinline__ void attn_piece_f32(const PagedView& pv, const float* __restrict__ Q,
                                                const float* __restrict__ K, const float* __restrict__ V,
                                                const SlotRow& sr, int64_t b, int w0, int steps, int Hq,
@@ -561,9 +557,9 @@ __device__ __forceinline__ void attn_piece_f32(const PagedView& pv, const float*
   const int s_end = 4 * steps;
   int raw = -1, pool = 0, rows = 0, page = 0;
   auto slot_of = [&](int t) { return 4 * w0 + 8 * t + 2 * warp + (lane & 1); };
-  auto load_raw = [&](int t) { raw = slot_of(t) < s_end ? slot_idx(sr, slot_of(t)) : -1; };
+  auto load_raw = [&](int t) { raw = slot_of(t) < s_end ? slot_idx<SEL>(sr, slot_of(t)) : -1; };
   auto load_page = [&](int t) {
-    slot_pool_rows(sr, slot_of(t), raw, pool, rows, bad_idx);
+    slot_pool_rows<SEL>(sr, slot_of(t), raw, pool, rows, bad_idx);
     if (slot_of(t) >= s_end) rows = 0;
     page = rows ? __ldg(sr.trow + page_of_pool(pv, pool)) : 0;
   };
@@ -724,30 +720,33 @@ template <typename T, int D, int MAXH>
 struct Piece;
 template <int D, int MAXH>
 struct Piece<__nv_bfloat16, D, MAXH> {
-  static constexpr int HG = MAXH > 16 ? 2 : 1;
-  static constexpr int MIN_STEPS = DecCfg<D, HG>::NSUB;
-  static constexpr int MIN_CTAS = 3;
-  static int smem(int) { return DecCfg<D, HG>::SMEM; }
+  using G = DecCfg<D, MAXH / 16>;
+  static constexpr int MIN_STEPS = G::WARPS;
+  static constexpr int CTAS = G::CTAS;
+  static int smem(int) { return G::SMEM; }
   static __device__ __forceinline__ AttnScratch& scratch(unsigned char* smem, int) {
-    return *reinterpret_cast<AttnScratch*>(smem + DecCfg<D, HG>::TILES);
+    return *reinterpret_cast<AttnScratch*>(smem + G::TILES);
   }
+  template <bool SEL>
   static __device__ __forceinline__ void run(const AttnArgs<__nv_bfloat16>& a, const SlotRow& sr, int64_t b, int w0,
                                              int steps, unsigned char* smem, AttnScratch& sc, bool& bad_page,
                                              bool& bad_idx) {
-    attn_piece_bf16<D, HG>(a.pv, a.Q, a.K, a.V, sr, b, w0, steps, a.Hq, a.scale_log2, smem, sc, bad_page, bad_idx);
+    attn_piece_bf16<D, MAXH / 16, SEL>(a.pv, a.Q, a.K, a.V, sr, b, w0, steps, a.Hq, a.scale_log2, smem, sc, bad_page,
+                                       bad_idx);
   }
 };
 template <int D, int MAXH>
 struct Piece<float, D, MAXH> {
   static constexpr int MIN_STEPS = 2;
-  static constexpr int MIN_CTAS = 2;
+  static constexpr int CTAS = 2;
   static int smem(int Hq) { return F32Cfg<D>::smem(Hq); }
   static __device__ __forceinline__ AttnScratch& scratch(unsigned char* smem, int Hq) {
     return *reinterpret_cast<AttnScratch*>(smem + ((F32Cfg<D>::TILES + 4 * Hq * (D + 36 + 1) + 64 + 15) & ~15));
   }
+  template <bool SEL>
   static __device__ __forceinline__ void run(const AttnArgs<float>& a, const SlotRow& sr, int64_t b, int w0, int steps,
                                              unsigned char* smem, AttnScratch& sc, bool& bad_page, bool& bad_idx) {
-    attn_piece_f32<D, MAXH>(a.pv, a.Q, a.K, a.V, sr, b, w0, steps, a.Hq, a.scale_log2, smem, sc, bad_page, bad_idx);
+    attn_piece_f32<D, MAXH, SEL>(a.pv, a.Q, a.K, a.V, sr, b, w0, steps, a.Hq, a.scale_log2, smem, sc, bad_page, bad_idx);
   }
 };
 
@@ -774,7 +773,7 @@ __device__ __forceinline__ SlotRow slot_row(const AttnArgs<T>& a, int64_t b, boo
 
 // Selected pools: grid (splits, batch), the splits of a row are one cluster.
 template <typename T, int D, int MAXH>
-__global__ void __launch_bounds__(kAttnThreads, (Piece<T, D, MAXH>::MIN_CTAS))
+__global__ void __launch_bounds__(kAttnThreads, (Piece<T, D, MAXH>::CTAS))
     decode_attn_selected_kernel(const __grid_constant__ AttnArgs<T> a) {
   using P = Piece<T, D, MAXH>;
   extern __shared__ __align__(128) unsigned char dec_smem[];
@@ -787,7 +786,7 @@ __global__ void __launch_bounds__(kAttnThreads, (Piece<T, D, MAXH>::MIN_CTAS))
   const SlotRow sr = slot_row(a, b, bad_page);
   const int n_steps = sr.len == 0 ? 0 : row_steps(sr.len, true, a.k);
   const int w0 = (int)((int64_t)n_steps * rank / splits), w1 = (int)((int64_t)n_steps * (rank + 1) / splits);
-  P::run(a, sr, b, w0, w1, dec_smem, sc, bad_page, bad_idx);
+  P::template run<true>(a, sr, b, w0, w1, dec_smem, sc, bad_page, bad_idx);
   const float4* o4 = reinterpret_cast<const float4*>(dec_smem);
   const int n4 = a.Hq * (D / 4);
   T* out = a.O + b * a.Hq * D;
@@ -833,13 +832,12 @@ __global__ void __launch_bounds__(kAttnThreads, (Piece<T, D, MAXH>::MIN_CTAS))
 
 // Whole cache: one CTA per range of the list of steps.
 template <typename T, int D, int MAXH>
-__global__ void __launch_bounds__(kAttnThreads, (Piece<T, D, MAXH>::MIN_CTAS))
+__global__ void __launch_bounds__(kAttnThreads, (Piece<T, D, MAXH>::CTAS))
     decode_attn_all_kernel(const __grid_constant__ AttnArgs<T> a) {
   using P = Piece<T, D, MAXH>;
   extern __shared__ __align__(128) unsigned char dec_smem[];
   AttnScratch& sc = P::scratch(dec_smem, a.Hq);
   chain_wait();
-  chain_release();
   const Cut cut = make_cut(a.pv, a.batch, P::MIN_STEPS, sc);
   if (cut.rest <= 0) {
     put_no_item(a.ps, a.batch);
@@ -855,7 +853,7 @@ __global__ void __launch_bounds__(kAttnThreads, (Piece<T, D, MAXH>::MIN_CTAS))
     const SlotRow sr = slot_row(a, b, bad_len);
     const int n_steps = row_steps(sr.len, false, 0);
     const int take = (int)min(rest, (int64_t)(n_steps - w0));
-    P::run(a, sr, b, w0, w0 + take, dec_smem, sc, bad_page, bad_idx);
+    P::template run<false>(a, sr, b, w0, w0 + take, dec_smem, sc, bad_page, bad_idx);
     if (w0 == 0)
       put_join_item(a.ps, a.batch, cut, b, pos, n_steps, take == rest);
     else if (take == rest)
@@ -884,75 +882,101 @@ __global__ void __launch_bounds__(kAttnThreads, (Piece<T, D, MAXH>::MIN_CTAS))
 }
 
 // ------------------------------------------------------------------- the join
-// One CTA per join item and head: o = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s
-// over the row's pieces s.  The weights go to shared memory, then each warp
-// sums every 16th piece (512 B a load) and the warps' sums are added in order.
-template <typename T, int D>
+// One CTA per join item, head and column slice of CW channels:
+// o = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s over the row's pieces s.  A
+// lane reads 16 bytes of a piece, CW/4 lanes a piece; the first pieces' loads
+// are issued before their weights are known.  Sums are added in a fixed order.
+template <typename T, int D, int CW>
 __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(Pieces ps, T* __restrict__ O,
                                                                    float* __restrict__ LSE, int Hq) {
-  constexpr int LPP = D / 4;            // lanes per piece row
-  constexpr int PPW = 32 / LPP;         // pieces a warp reads at once
+  constexpr int LPP = CW / 4;                    // lanes per piece
+  constexpr int PAR = kJoinThreads / LPP;        // pieces read at once
+  constexpr int AHEAD = 4;                       // loads a thread has in flight
+  constexpr int WARPS = kJoinThreads / 32;
   extern __shared__ __align__(16) float join_smem[];
-  float* sums = join_smem;                                 // [warps * PPW][D]: 128 floats a warp
-  float* red = sums + 128 * (kJoinThreads / 32);           // [2][warps]
-  float* wt = red + 2 * (kJoinThreads / 32);               // [kAttnCtas]
+  float4* sums = reinterpret_cast<float4*>(join_smem);   // [kJoinThreads]
+  float* red = join_smem + 4 * kJoinThreads;             // [2][WARPS]
+  float* wt = red + 2 * WARPS;                           // [kAttnCtas]
   chain_wait();
   chain_release();
   const JoinItem it = ps.items[blockIdx.x];
   if (it.row < 0) return;
   const int h = blockIdx.y;
-  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  const int n = it.last - it.first + 1;   // <= kAttnCtas
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  const int n = it.last - it.first + 1;   // 2 .. kAttnCtas
   auto piece = [&](int s) { return 2 * (int64_t)(it.first + s) + (s == 0 ? it.skip : 0); };
-  auto ml_of = [&](int s) { return __ldcg(reinterpret_cast<const float2*>(ps.ml) + piece(s) * Hq + h); };
+  const float4* col = reinterpret_cast<const float4*>(ps.o) + h * (D / 4) + blockIdx.z * LPP + threadIdx.x % LPP;
+  auto load = [&](int s) {
+    return s < n ? __ldcg(col + piece(s) * Hq * (D / 4)) : make_float4(0.f, 0.f, 0.f, 0.f);
+  };
+  const int s0 = threadIdx.x / LPP;
+  float4 x[AHEAD];
+#pragma unroll
+  for (int i = 0; i < AHEAD; ++i) x[i] = load(s0 + i * PAR);
+  constexpr int MLN = (kAttnCtas + kJoinThreads - 1) / kJoinThreads;
+  float2 ml[MLN];
   float mm = -INFINITY;
-  for (int s = threadIdx.x; s < n; s += blockDim.x) mm = fmaxf(mm, ml_of(s).x);
+#pragma unroll
+  for (int i = 0; i < MLN; ++i) {
+    const int s = threadIdx.x + i * kJoinThreads;
+    ml[i] = s < n ? __ldcg(reinterpret_cast<const float2*>(ps.ml) + piece(s) * Hq + h) : make_float2(-INFINITY, 0.f);
+    mm = fmaxf(mm, ml[i].x);
+  }
 #pragma unroll
   for (int o = 16; o; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
   if (lane == 0) red[wid] = mm;
   __syncthreads();
-  mm = -INFINITY;
-  for (int w = 0; w < warps; ++w) mm = fmaxf(mm, red[w]);
+  mm = red[0];
+#pragma unroll
+  for (int w = 1; w < WARPS; ++w) mm = fmaxf(mm, red[w]);
   float l = 0.f;
-  for (int s = threadIdx.x; s < n; s += blockDim.x) {
-    const float2 ml = ml_of(s);
-    const float f = exp2f(ml.x - (mm == -INFINITY ? 0.f : mm));
-    wt[s] = f;
-    l += f * ml.y;
+#pragma unroll
+  for (int i = 0; i < MLN; ++i) {
+    const int s = threadIdx.x + i * kJoinThreads;
+    const float f = exp2f(ml[i].x - (mm == -INFINITY ? 0.f : mm));
+    if (s < n) wt[s] = f;
+    l += f * ml[i].y;
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-  if (lane == 0) red[kJoinThreads / 32 + wid] = l;
+  if (lane == 0) red[WARPS + wid] = l;
   __syncthreads();
   l = 0.f;
-  for (int w = 0; w < warps; ++w) l += red[kJoinThreads / 32 + w];
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) l += red[WARPS + w];
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  const int c4 = lane % LPP;
-#pragma unroll 4
-  for (int s = wid * PPW + lane / LPP; s < n; s += warps * PPW) {
-    const float4 x = __ldcg(reinterpret_cast<const float4*>(ps.o) + (piece(s) * Hq + h) * LPP + c4);
-    const float w = wt[s];
-    acc.x += w * x.x;
-    acc.y += w * x.y;
-    acc.z += w * x.z;
-    acc.w += w * x.w;
+  for (int s = s0; s < n; s += AHEAD * PAR) {
+    float4 y[AHEAD];
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      y[i] = x[i];
+      x[i] = load(s + (AHEAD + i) * PAR);
+    }
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      const float w = s + i * PAR < n ? wt[s + i * PAR] : 0.f;
+      acc.x += w * y[i].x;
+      acc.y += w * y[i].y;
+      acc.z += w * y[i].z;
+      acc.w += w * y[i].w;
+    }
   }
-  reinterpret_cast<float4*>(sums)[threadIdx.x] = acc;
+  sums[threadIdx.x] = acc;
   __syncthreads();
-  const float inv = inv_sum(l);
-  for (int c = threadIdx.x; c < D; c += blockDim.x) {
-    float x = 0.f;
-    for (int i = 0; i < warps * PPW; ++i) x += sums[i * D + c];
-    O[((int64_t)it.row * Hq + h) * D + c] = (T)(x * inv);
+  const int parts = n < PAR ? n : PAR;
+  if (threadIdx.x < CW) {
+    float sum = 0.f;
+    for (int i = 0; i < parts; ++i) sum += join_smem[i * CW + threadIdx.x];
+    O[((int64_t)it.row * Hq + h) * D + blockIdx.z * CW + threadIdx.x] = (T)(sum * inv_sum(l));
   }
-  if (threadIdx.x == 0) LSE[(int64_t)it.row * Hq + h] = lse_of(mm, l);
+  if (threadIdx.x == 0 && blockIdx.z == 0) LSE[(int64_t)it.row * Hq + h] = lse_of(mm, l);
 }
 
 // CTAs per row of selected pools: the most (1, 2, 4, 8 or 16, a cluster) that
 // keep all rows resident at once and give a CTA work for its warps.
-static unsigned selected_splits(int64_t batch, int n_steps, int min_steps) {
+static unsigned selected_splits(int64_t batch, int n_steps, int min_steps, int resident) {
   unsigned s = 1;
-  while (s < 16 && batch * s * 2 <= kAttnCtas && (int)s * min_steps < n_steps) s *= 2;
+  while (s < 16 && batch * s * 2 <= resident && (int)s * min_steps < n_steps) s *= 2;
   return s;
 }
 
@@ -962,7 +986,7 @@ static cudaError_t launch_all(const DecodeAttnArgs& g, const AttnArgs<T>& a, cud
   const int smem = P::smem(a.Hq);
   if (a.idx) {
     auto kern = decode_attn_selected_kernel<T, D, MAXH>;
-    const unsigned splits = selected_splits(a.batch, (a.k + 4) >> 2, P::MIN_STEPS);
+    const unsigned splits = selected_splits(a.batch, (a.k + 4) >> 2, P::MIN_STEPS, kSms * P::CTAS);
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e == cudaSuccess && splits > 8) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
@@ -974,14 +998,16 @@ static cudaError_t launch_all(const DecodeAttnArgs& g, const AttnArgs<T>& a, cud
   // as many CTAs as can have work
   const int64_t row_max = ((int64_t)a.pv.capacity + 15) >> 4;
   const int64_t want = (a.batch * row_max + P::MIN_STEPS - 1) / P::MIN_STEPS;
-  const unsigned ctas = (unsigned)(want < kAttnCtas ? want : kAttnCtas);
+  const unsigned ctas = (unsigned)(want < kSms * P::CTAS ? want : kSms * P::CTAS);
   e = launch_chained(kern, dim3(ctas), dim3(kAttnThreads), smem, s, a);
   if (e != cudaSuccess || ctas == 1) return e;
-  // few rows: many pieces each, more warps per join
+  // few rows, so many pieces of each: the columns of a head are split too
   const unsigned items = a.batch < ctas ? (unsigned)a.batch : ctas;
-  const unsigned threads = items <= 16 ? kJoinThreads : 128;
-  const size_t jsmem = sizeof(float) * (kJoinThreads / 32 * 130 + kAttnCtas);
-  return launch_chained(decode_join_kernel<T, D>, dim3(items, a.Hq), dim3(threads), jsmem, s, a.ps, a.O, a.LSE, a.Hq);
+  const size_t jsmem = sizeof(float) * (4 * kJoinThreads + 2 * (kJoinThreads / 32) + kAttnCtas);
+  const dim3 jt(kJoinThreads);
+  if (items * a.Hq * (D / 32) <= 1024)
+    return launch_chained(decode_join_kernel<T, D, 32>, dim3(items, a.Hq, D / 32), jt, jsmem, s, a.ps, a.O, a.LSE, a.Hq);
+  return launch_chained(decode_join_kernel<T, D, D>, dim3(items, a.Hq), jt, jsmem, s, a.ps, a.O, a.LSE, a.Hq);
 }
 
 template <typename T>
