@@ -106,20 +106,25 @@ __device__ __forceinline__ void slot_pool_rows(const SlotRow& r, int i, int raw,
       pool = r.len >> 2;
       rows = r.len & 3;
     }
-  } else if (4 * (int64_t)i < r.len) {
+  } else if (i <= (r.len - 1) >> 2) {
     pool = i;
     rows = min(4, r.len - 4 * i);
   }
 }
 
 // ------------------------------------------------------------------- the cut
-// Where the CTA's range of steps begins.
+// Beginning a row costs a CTA a chain of loads and a join, about as long as
+// kRowPad of its steps take, so each row counts kRowPad more than its steps
+// (without it, the CTAs that get parts of two rows finish last: 98 us against
+// 88 for 40 ragged rows of 32 heads).
+constexpr int kRowPad = 8;
+
+// The CTA's range of the weighted list.
 struct Cut {
-  int64_t rest;    // steps of the range
-  int64_t per;     // steps per CTA
-  int64_t begin;   // first step of the range, in the list
-  int64_t row;     // its row
-  int step;        // and its step in that row
+  int64_t begin, rest;   // where it begins, what it covers
+  int64_t per;           // what a CTA covers
+  int64_t row;           // the row it begins in
+  int64_t off;           // and where in that row
 };
 
 // Shared scratch of the attention kernels, behind the tiles.  It lies in
@@ -131,18 +136,18 @@ struct alignas(16) AttnScratch {
   float m[4][32], l[4][32];   // bf16: the warps' own; m becomes their weights
   int64_t warp_sum[kAttnThreads / 32];
   int64_t row;
-  int64_t step;
+  int64_t off;
 };
 
-// Called by all threads of the CTA.  Sums the rows' steps, kAttnThreads rows at
-// a time: one pass when that is all rows, else one for the total and one up
+// Called by all threads of the CTA.  Sums the rows' weights, kAttnThreads rows
+// at a time: one pass when that is all rows, else one for the total and one up
 // to the range's first row.
 __device__ __forceinline__ Cut make_cut(const PagedView& pv, int64_t batch, int min_per, AttnScratch& sc) {
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-  auto steps_of = [&](int64_t b) {
+  auto weight_of = [&](int64_t b) {
     bool bad = false;
     if (b >= batch) return 0;
-    const int n = row_steps(row_length(pv, b, bad), false, 0);
+    const int n = kRowPad + row_steps(row_length(pv, b, bad), false, 0);
     if (bad && blockIdx.x == 0) record_error(DSA_DEV_ERR_BAD_PAGE);
     return n;
   };
@@ -150,7 +155,7 @@ __device__ __forceinline__ Cut make_cut(const PagedView& pv, int64_t batch, int 
   int mine = 0;
   if (batch > kAttnThreads) {
     int64_t part = 0;
-    for (int64_t b = threadIdx.x; b < batch; b += kAttnThreads) part += steps_of(b);
+    for (int64_t b = threadIdx.x; b < batch; b += kAttnThreads) part += weight_of(b);
 #pragma unroll
     for (int o = 16; o; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
     if (lane == 0) sc.warp_sum[wid] = part;
@@ -162,7 +167,7 @@ __device__ __forceinline__ Cut make_cut(const PagedView& pv, int64_t batch, int 
   Cut c;
   int64_t base = 0;
   for (int64_t b0 = 0; b0 < batch; b0 += kAttnThreads) {
-    mine = steps_of(b0 + threadIdx.x);
+    mine = weight_of(b0 + threadIdx.x);
     int64_t incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -184,7 +189,7 @@ __device__ __forceinline__ Cut make_cut(const PagedView& pv, int64_t batch, int 
     const int64_t excl = before + incl - mine;
     if (excl <= c.begin && c.begin < excl + mine) {
       sc.row = b0 + threadIdx.x;
-      sc.step = c.begin - excl;
+      sc.off = c.begin - excl;
     }
     base += chunk;
     __syncthreads();
@@ -192,32 +197,46 @@ __device__ __forceinline__ Cut make_cut(const PagedView& pv, int64_t batch, int 
   }
   c.rest = total - c.begin < c.per ? total - c.begin : c.per;
   c.row = sc.row;
-  c.step = (int)sc.step;
+  c.off = sc.off;
   return c;
 }
 
-// Records how the row that begins in this CTA (at its `pos`-th step of the
-// list) is to be joined.  One item per row, or, when the rows are more than
-// the CTAs, one per CTA: that of its last row (`last_here`).
-__device__ __forceinline__ void put_join_item(const Pieces& ps, int64_t batch, const Cut& c, int64_t row, int64_t pos,
-                                              int steps, bool last_here) {
-  const int64_t last = (pos + steps - 1) / c.per;
-  const bool joined = last > blockIdx.x;
-  const bool by_row = batch <= gridDim.x;
-  if (threadIdx.x == 0 && (by_row || last_here)) {
+// Join items: one per row, or, when the rows are more than the CTAs, one per
+// CTA (at most one row begins in a CTA and goes on in the next).
+__device__ __forceinline__ void put_join_item(const Pieces& ps, int64_t at, int row, int64_t last, int skip) {
+  if (threadIdx.x == 0) {
     JoinItem it;
-    it.row = joined ? (int)row : -1;
+    it.row = row;
     it.first = blockIdx.x;
     it.last = (int)last;
-    it.skip = pos != c.begin;
-    ps.items[by_row ? row : blockIdx.x] = it;
+    it.skip = skip;
+    ps.items[at] = it;
   }
-}
-__device__ __forceinline__ void put_no_item(const Pieces& ps, int64_t batch) {
-  if (batch > gridDim.x && threadIdx.x == 0) ps.items[blockIdx.x].row = -1;
 }
 
 // ------------------------------------------------------------------- bf16
+// gather_step16 (gather.cuh) for a step whose 16 keys are all visible.
+template <int D>
+__device__ __forceinline__ void gather_full16(uint32_t stage, const __nv_bfloat16* __restrict__ K,
+                                              const __nv_bfloat16* __restrict__ V, const uint32_t (&slots)[4],
+                                              const GatherLane<D>& gl) {
+  using C = GatherCfg<D>;
+  constexpr int NRB = GatherLane<D>::NRB;
+  constexpr uint32_t POOL_BYTES = 4 * C::ROW_BYTES;
+  const char* k0 = reinterpret_cast<const char*>(K) + gl.src_off;
+  const char* v0 = reinterpret_cast<const char*>(V) + gl.src_off;
+#pragma unroll
+  for (int sig = 0; sig < 4; ++sig) {
+    const uint64_t off = (uint64_t)(slots[sig] >> 3) * POOL_BYTES;
+#pragma unroll
+    for (int rb = 0; rb < NRB; ++rb) {
+      const uint32_t dst = stage + gl.dst_off[sig & 1][rb] + sig * POOL_BYTES;
+      cp_async16_full(dst, k0 + off + rb * C::ROWS_PER_COPY * C::ROW_BYTES);
+      cp_async16_full(dst + C::TILE_BYTES, v0 + off + rb * C::ROWS_PER_COPY * C::ROW_BYTES);
+    }
+  }
+}
+
 // A CTA's warps each take every 4th step, with a ring of their own.  NG: groups
 // of 16 heads; a warp computes all of them from each gathered tile (two warps
 // sharing a ring, each with one group, ran 94 us against 82 for 40 ragged rows
@@ -252,12 +271,13 @@ __device__ __forceinline__ void attn_piece_bf16(const PagedView& pv, const __nv_
   const GatherLane<D> gl = gather_lane<D>(lane);
 
   // Slot pipeline: this lane decides slot (lane & 3) of every step of its warp.
-  int raw = -1, pool = 0, rows = 0, page = 0;
+  int raw = -1, pool = 0, rows = 0, col = 0, page = 0;
   auto load_raw = [&](int st) { raw = st < steps ? slot_idx<SEL>(sr, st * 4 + (lane & 3)) : -1; };
   auto load_page = [&](int st) {
     slot_pool_rows<SEL>(sr, st * 4 + (lane & 3), raw, pool, rows, bad_idx);
     if (st >= steps) rows = 0;
-    page = rows ? __ldg(sr.trow + page_of_pool(pv, pool)) : 0;
+    col = page_of_pool(pv, pool);
+    page = rows ? __ldg(sr.trow + col) : 0;
   };
   uint32_t vis[NST];   // visible rows of the ring's steps: 4 bits per slot
   auto fetch = [&](int st, int stage, uint32_t& v) {
@@ -265,7 +285,7 @@ __device__ __forceinline__ void attn_piece_bf16(const PagedView& pv, const __nv_
     if (st < steps) {
       uint32_t mine = 0u, slots[4];
       if (rows) {
-        const int pp = phys_pool(pv, pool, page_of_pool(pv, pool), page, bad_page);
+        const int pp = phys_pool(pv, pool, col, page, bad_page);
         if (pp >= 0) mine = ((uint32_t)pp << 3) | (uint32_t)rows;
       }
 #pragma unroll
@@ -273,7 +293,10 @@ __device__ __forceinline__ void attn_piece_bf16(const PagedView& pv, const __nv_
         slots[s] = __shfl_sync(0xffffffffu, mine, s);
         v |= (slots[s] & 7u) << (4 * s);
       }
-      gather_step16<D>(ring + stage * C::STAGE_BYTES, K, V, slots, gl);
+      if (v == 0x4444u)
+        gather_full16<D>(ring + stage * C::STAGE_BYTES, K, V, slots, gl);
+      else
+        gather_step16<D>(ring + stage * C::STAGE_BYTES, K, V, slots, gl);
     }
     cp_async_commit();
   };
@@ -297,7 +320,7 @@ __device__ __forceinline__ void attn_piece_bf16(const PagedView& pv, const __nv_
   // fill the ring: all idx entries, then all pages, then the rows
   int st = w0 + warp;
   {
-    int raws[NST], pools[NST], rws[NST], pgs[NST];
+    int raws[NST], pools[NST], rws[NST], cols[NST], pgs[NST];
 #pragma unroll
     for (int i = 0; i < NST; ++i) {
       load_raw(st + i * WARPS);
@@ -311,24 +334,26 @@ __device__ __forceinline__ void attn_piece_bf16(const PagedView& pv, const __nv_
       load_page(st + i * WARPS);
       pools[i] = pool;
       rws[i] = rows;
+      cols[i] = col;
       pgs[i] = page;
     }
 #pragma unroll
     for (int i = 0; i < NST; ++i) {
       pool = pools[i];
       rows = rws[i];
+      col = cols[i];
       page = pgs[i];
       if (i < NST - 1) fetch(st + i * WARPS, i, vis[i]);
     }
     raw = raw_next;
   }
   float o[NG][D / 8][4];
-  float m[NG][2], l[NG][2];   // heads g and g + 8 of each group
+  float m[NG][2], l[NG][2], top[NG][2];   // heads g and g + 8 of each group
 #pragma unroll
   for (int n = 0; n < NG; ++n) {
 #pragma unroll
     for (int c = 0; c < D / 8; ++c) o[n][c][0] = o[n][c][1] = o[n][c][2] = o[n][c][3] = 0.f;
-    m[n][0] = m[n][1] = -INFINITY;
+    m[n][0] = m[n][1] = top[n][0] = top[n][1] = -INFINITY;
     l[n][0] = l[n][1] = 0.f;
   }
 
@@ -337,13 +362,6 @@ __device__ __forceinline__ void attn_piece_bf16(const PagedView& pv, const __nv_
     fetch(st + (NST - 1) * WARPS, stage == 0 ? NST - 1 : stage - 1, vis[NST - 1]);   // the stage consumed last
     load_page(st + NST * WARPS);
     load_raw(st + (NST + 1) * WARPS);
-    bool kv[2][2];
-#pragma unroll
-    for (int nt = 0; nt < 2; ++nt) {
-      const int nrows = (int)(vis[0] >> (8 * nt + 4 * (qi >> 1))) & 7;
-#pragma unroll
-      for (int e = 0; e < 2; ++e) kv[nt][e] = 2 * (qi & 1) + e < nrows;
-    }
     cp_async_wait<NST - 1>();
     __syncwarp();
     const uint32_t ks_base = ring + stage * C::STAGE_BYTES;
@@ -373,59 +391,81 @@ __device__ __forceinline__ void attn_piece_bf16(const PagedView& pv, const __nv_
         }
       }
     }
-    // online softmax in log2 units with a lazily moved base (attn_fwd.cu)
-    uint32_t ph[NG][4], pl[NG][4];
-    bool moved = false;
-    float al[NG][2];
+    // Online softmax in log2 units with a lazily moved base (attn_fwd.cu): while
+    // no score of the step exceeds a row's base by more than kDecLazyLog2, no
+    // row maximum is needed at all, only a vote.  `top` is that limit in the
+    // units of the raw scores.
 #pragma unroll
-    for (int n = 0; n < NG; ++n) {
-      float(&z)[2][4] = s[n][0];
-      float mx[2] = {-INFINITY, -INFINITY};
+    for (int n = 0; n < NG; ++n)
 #pragma unroll
       for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if (CHAINS == 2) z[nt][e] += s[n][CHAINS - 1][nt][e];
-          z[nt][e] = kv[nt][e & 1] ? z[nt][e] : -INFINITY;
-          mx[e >> 1] = fmaxf(mx[e >> 1], z[nt][e]);
-        }
+        for (int e = 0; e < 4; ++e)
+          if (CHAINS == 2) s[n][0][nt][e] += s[n][CHAINS - 1][nt][e];
+    if (vis[0] != 0x4444u) {
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt) {
+        const int nrows = (int)(vis[0] >> (8 * nt + 4 * (qi >> 1))) & 7;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (2 * (qi & 1) + (e & 1) >= nrows) {
+#pragma unroll
+            for (int n = 0; n < NG; ++n) s[n][0][nt][e] = -INFINITY;
+          }
+      }
+    }
+    float mx[NG][2];
+    bool over = false;
+#pragma unroll
+    for (int n = 0; n < NG; ++n)
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
-        mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
-        mx[r] *= scale_log2;
-        const bool up = mx[r] > m[n][r] + kDecLazyLog2;
-        const float mn = up ? mx[r] : m[n][r];
-        const float base = mn == -INFINITY ? 0.f : mn;
-        al[n][r] = up ? ex2_approx(m[n][r] - base) : 1.f;
-        moved |= up;
-        m[n][r] = mn;
-        float sum = 0.f;
+        float(&z)[2][4] = s[n][0];
+        mx[n][r] = fmaxf(fmaxf(z[0][2 * r], z[0][2 * r + 1]), fmaxf(z[1][2 * r], z[1][2 * r + 1]));
+        over |= mx[n][r] > top[n][r];
+      }
+    if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+      for (int n = 0; n < NG; ++n) {
+        float al[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          float x = mx[n][r];
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+          const float mn = x > top[n][r] ? x * scale_log2 : m[n][r];
+          al[r] = mn == m[n][r] ? 1.f : ex2_approx(m[n][r] - mn);
+          m[n][r] = mn;
+          if (x > top[n][r]) top[n][r] = x + kDecLazyLog2 / scale_log2;
+          l[n][r] *= al[r];
+        }
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+          o[n][c][0] *= al[0];
+          o[n][c][1] *= al[0];
+          o[n][c][2] *= al[1];
+          o[n][c][3] *= al[1];
+        }
+      }
+    }
+    uint32_t ph[NG][4], pl[NG][4];
+#pragma unroll
+    for (int n = 0; n < NG; ++n) {
+      float(&z)[2][4] = s[n][0];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const float base = m[n][r] == -INFINITY ? 0.f : m[n][r];
 #pragma unroll
         for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
-          for (int e = 2 * r; e < 2 * r + 2; ++e) {
-            z[nt][e] = ex2_approx(fmaf(z[nt][e], scale_log2, -base));
-            sum += z[nt][e];
-          }
-        l[n][r] = l[n][r] * al[n][r] + sum;
+          for (int e = 2 * r; e < 2 * r + 2; ++e) z[nt][e] = ex2_approx(fmaf(z[nt][e], scale_log2, -base));
+        l[n][r] += (z[0][2 * r] + z[0][2 * r + 1]) + (z[1][2 * r] + z[1][2 * r + 1]);
       }
 #pragma unroll
       for (int nt = 0; nt < 2; ++nt) {
         split_hi_lo(z[nt][0], z[nt][1], ph[n][2 * nt], pl[n][2 * nt]);
         split_hi_lo(z[nt][2], z[nt][3], ph[n][2 * nt + 1], pl[n][2 * nt + 1]);
       }
-    }
-    if (__any_sync(0xffffffffu, moved)) {
-#pragma unroll
-      for (int n = 0; n < NG; ++n)
-#pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-          o[n][c][0] *= al[n][0];
-          o[n][c][1] *= al[n][0];
-          o[n][c][2] *= al[n][1];
-          o[n][c][3] *= al[n][1];
-        }
     }
     {
       const int mtx = lane >> 3, r = lane & 7;
@@ -839,45 +879,49 @@ __global__ void __launch_bounds__(kAttnThreads, (Piece<T, D, MAXH>::CTAS))
   AttnScratch& sc = P::scratch(dec_smem, a.Hq);
   chain_wait();
   const Cut cut = make_cut(a.pv, a.batch, P::MIN_STEPS, sc);
-  if (cut.rest <= 0) {
-    put_no_item(a.ps, a.batch);
-    return;
-  }
-  bool bad_page = false, bad_idx = false;
-  int64_t b = cut.row, pos = cut.begin, rest = cut.rest;
-  int w0 = cut.step;
+  const bool by_row = a.batch <= gridDim.x;
+  bool bad_page = false, bad_idx = false, item = by_row;
   const float4* o4 = reinterpret_cast<const float4*>(dec_smem);
   const int n4 = a.Hq * (D / 4);
-  while (true) {
+  int64_t rest = cut.rest, off = cut.off, row_pos = cut.begin - cut.off;
+  int pieces = 0;
+  for (int64_t b = cut.row; rest > 0; ++b) {
     bool bad_len = false;   // recorded by make_cut
     const SlotRow sr = slot_row(a, b, bad_len);
     const int n_steps = row_steps(sr.len, false, 0);
-    const int take = (int)min(rest, (int64_t)(n_steps - w0));
-    P::template run<false>(a, sr, b, w0, w0 + take, dec_smem, sc, bad_page, bad_idx);
-    if (w0 == 0)
-      put_join_item(a.ps, a.batch, cut, b, pos, n_steps, take == rest);
-    else if (take == rest)
-      put_no_item(a.ps, a.batch);
-    if (w0 == 0 && take == n_steps) {
-      for (int i = threadIdx.x; i < n4; i += kAttnThreads) {
-        const float2 ml = sc.ml[i / (D / 4)];
-        store_out4(a.O + b * a.Hq * D + 4 * i, o4[i], inv_sum(ml.y));
+    const int64_t end = min(off + rest, (int64_t)kRowPad + n_steps);
+    const int w0 = (int)max(off - kRowPad, (int64_t)0), w1 = (int)max(end - kRowPad, (int64_t)0);
+    if (w1 > w0) {
+      if (pieces) __syncthreads();   // the previous results become tiles again
+      P::template run<false>(a, sr, b, w0, w1, dec_smem, sc, bad_page, bad_idx);
+      if (w0 == 0) {
+        const int64_t last = (row_pos + kRowPad + n_steps - 1) / cut.per;
+        const bool joined = last > blockIdx.x;
+        if (by_row || joined) {
+          put_join_item(a.ps, by_row ? b : blockIdx.x, joined ? (int)b : -1, last, pieces > 0);
+          item = true;
+        }
       }
-      if (threadIdx.x < a.Hq)
-        a.LSE[b * a.Hq + threadIdx.x] = lse_of(sc.ml[threadIdx.x].x, sc.ml[threadIdx.x].y);
-    } else {
-      const int64_t piece = 2 * (int64_t)blockIdx.x + (pos != cut.begin);
-      for (int i = threadIdx.x; i < n4; i += kAttnThreads)
-        reinterpret_cast<float4*>(a.ps.o)[piece * n4 + i] = o4[i];
-      if (threadIdx.x < a.Hq) reinterpret_cast<float2*>(a.ps.ml)[piece * a.Hq + threadIdx.x] = sc.ml[threadIdx.x];
+      if (w0 == 0 && w1 == n_steps) {
+        for (int i = threadIdx.x; i < n4; i += kAttnThreads) {
+          const float2 ml = sc.ml[i / (D / 4)];
+          store_out4(a.O + b * a.Hq * D + 4 * i, o4[i], inv_sum(ml.y));
+        }
+        if (threadIdx.x < a.Hq)
+          a.LSE[b * a.Hq + threadIdx.x] = lse_of(sc.ml[threadIdx.x].x, sc.ml[threadIdx.x].y);
+      } else {
+        const int64_t piece = 2 * (int64_t)blockIdx.x + (pieces > 0);
+        for (int i = threadIdx.x; i < n4; i += kAttnThreads)
+          reinterpret_cast<float4*>(a.ps.o)[piece * n4 + i] = o4[i];
+        if (threadIdx.x < a.Hq) reinterpret_cast<float2*>(a.ps.ml)[piece * a.Hq + threadIdx.x] = sc.ml[threadIdx.x];
+      }
+      ++pieces;
     }
-    rest -= take;
-    if (rest <= 0) break;
-    pos += take;
-    w0 = 0;
-    ++b;
-    __syncthreads();   // the results become tiles again
+    rest -= end - off;
+    row_pos += kRowPad + n_steps;
+    off = 0;
   }
+  if (!item) put_join_item(a.ps, blockIdx.x, -1, 0, 0);
   if (bad_page) record_error(DSA_DEV_ERR_BAD_PAGE);
 }
 
@@ -997,7 +1041,7 @@ static cudaError_t launch_all(const DecodeAttnArgs& g, const AttnArgs<T>& a, cud
   if (e != cudaSuccess) return e;
   // as many CTAs as can have work
   const int64_t row_max = ((int64_t)a.pv.capacity + 15) >> 4;
-  const int64_t want = (a.batch * row_max + P::MIN_STEPS - 1) / P::MIN_STEPS;
+  const int64_t want = a.batch * ((row_max + kRowPad + P::MIN_STEPS - 1) / P::MIN_STEPS);
   const unsigned ctas = (unsigned)(want < kSms * P::CTAS ? want : kSms * P::CTAS);
   e = launch_chained(kern, dim3(ctas), dim3(kAttnThreads), smem, s, a);
   if (e != cudaSuccess || ctas == 1) return e;
