@@ -249,11 +249,12 @@ struct DecCfg {
   static constexpr int RING = NST * GatherCfg<D>::STAGE_BYTES;
   static constexpr int TILES = WARPS * RING;
   static constexpr int SMEM = TILES + (int)sizeof(AttnScratch);
-  static_assert(TILES >= WARPS * NG * 16 * D * 4, "the rings double as the join buffer");
+  static constexpr int PITCH = D + 8;   // floats per head in the join buffer: fragment stores without bank conflicts
+  static_assert(TILES >= WARPS * NG * 16 * PITCH * 4, "the rings double as the join buffer");
 };
 
-// Steps [w0, steps) of row b.  Leaves o [Hq][D] at the start of the tiles and
-// the heads' bases and sums in sc.ml; ends with a __syncthreads().
+// Steps [w0, steps) of row b.  Leaves o [Hq][PITCH] at the start of the tiles
+// and the heads' bases and sums in sc.ml; ends with a __syncthreads().
 // SEL: the slots are selected pools; else all pools.
 template <int D, int NG, bool SEL>
 __device__ __forceinline__ void attn_piece_bf16(const PagedView& pv, const __nv_bfloat16* __restrict__ Q,
@@ -328,6 +329,7 @@ __device__ __forceinline__ void attn_piece_bf16(const PagedView& pv, const __nv_
     }
     load_raw(st + NST * WARPS);
     const int raw_next = raw;
+    if (SEL && sr.len == 0) steps = w0;   // an idle row
 #pragma unroll
     for (int i = 0; i < NST; ++i) {
       raw = raws[i];
@@ -511,14 +513,14 @@ __device__ __forceinline__ void attn_piece_bf16(const PagedView& pv, const __nv_
         sc.l[warp][n * 16 + g + 8 * r] = l[n][r];
       }
     }
-  __syncthreads();   // every ring is idle: the tiles are the join buffer, [warp][NG * 16][D]
+  __syncthreads();   // every ring is idle: the tiles are the join buffer, [warp][NG * 16][PITCH]
 #pragma unroll
   for (int n = 0; n < NG; ++n) {
-    float* my = reinterpret_cast<float*>(tiles) + (warp * NG + n) * 16 * D;
+    float* my = reinterpret_cast<float*>(tiles) + (warp * NG + n) * 16 * G::PITCH;
 #pragma unroll
     for (int c = 0; c < D / 8; ++c) {
-      *reinterpret_cast<float2*>(my + g * D + c * 8 + 2 * qi) = make_float2(o[n][c][0], o[n][c][1]);
-      *reinterpret_cast<float2*>(my + (g + 8) * D + c * 8 + 2 * qi) = make_float2(o[n][c][2], o[n][c][3]);
+      *reinterpret_cast<float2*>(my + g * G::PITCH + c * 8 + 2 * qi) = make_float2(o[n][c][0], o[n][c][1]);
+      *reinterpret_cast<float2*>(my + (g + 8) * G::PITCH + c * 8 + 2 * qi) = make_float2(o[n][c][2], o[n][c][3]);
     }
   }
   if (threadIdx.x < NG * 16) {
@@ -539,18 +541,18 @@ __device__ __forceinline__ void attn_piece_bf16(const PagedView& pv, const __nv_
   float4* o4 = reinterpret_cast<float4*>(tiles);
 #pragma unroll
   for (int i = threadIdx.x; i < NG * 16 * D / 4; i += kAttnThreads) {
-    const int h = i / (D / 4);
+    const int h = i / (D / 4), at = h * (G::PITCH / 4) + i % (D / 4);
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < WARPS; ++w) {
       const float f = sc.m[w][h];
-      const float4 x = o4[w * NG * 16 * (D / 4) + i];
+      const float4 x = o4[w * NG * 16 * (G::PITCH / 4) + at];
       acc.x += f * x.x;
       acc.y += f * x.y;
       acc.z += f * x.z;
       acc.w += f * x.w;
     }
-    o4[i] = acc;   // in place: warp 0's part, this thread's own element
+    o4[at] = acc;   // in place: warp 0's part, this thread's own element
   }
   __syncthreads();
 }
@@ -763,6 +765,7 @@ struct Piece<__nv_bfloat16, D, MAXH> {
   using G = DecCfg<D, MAXH / 16>;
   static constexpr int MIN_STEPS = G::WARPS;
   static constexpr int CTAS = G::CTAS;
+  static constexpr int PITCH = G::PITCH;   // floats per head of the result
   static int smem(int) { return G::SMEM; }
   static __device__ __forceinline__ AttnScratch& scratch(unsigned char* smem, int) {
     return *reinterpret_cast<AttnScratch*>(smem + G::TILES);
@@ -779,6 +782,7 @@ template <int D, int MAXH>
 struct Piece<float, D, MAXH> {
   static constexpr int MIN_STEPS = 2;
   static constexpr int CTAS = 2;
+  static constexpr int PITCH = D;
   static int smem(int Hq) { return F32Cfg<D>::smem(Hq); }
   static __device__ __forceinline__ AttnScratch& scratch(unsigned char* smem, int Hq) {
     return *reinterpret_cast<AttnScratch*>(smem + ((F32Cfg<D>::TILES + 4 * Hq * (D + 36 + 1) + 64 + 15) & ~15));
@@ -800,6 +804,12 @@ __device__ __forceinline__ void store_out4(float* o, float4 x, float inv) {
 }
 __device__ __forceinline__ float inv_sum(float l) { return l == 0.f ? 0.f : 1.f / l; }
 __device__ __forceinline__ float lse_of(float m, float l) { return l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2; }
+
+// Where element group i of [Hq][D/4] lies in a piece's result.
+template <typename P, int D>
+__device__ __forceinline__ int result_at(int i) {
+  return i / (D / 4) * (P::PITCH / 4) + i % (D / 4);
+}
 
 template <typename T>
 __device__ __forceinline__ SlotRow slot_row(const AttnArgs<T>& a, int64_t b, bool& bad) {
@@ -824,7 +834,7 @@ __global__ void __launch_bounds__(kAttnThreads, (Piece<T, D, MAXH>::CTAS))
   const int splits = gridDim.x, rank = blockIdx.x;
   bool bad_page = false, bad_idx = false;
   const SlotRow sr = slot_row(a, b, bad_page);
-  const int n_steps = sr.len == 0 ? 0 : row_steps(sr.len, true, a.k);
+  const int n_steps = (a.k + 4) >> 2;   // whatever the length: the idx loads need not wait for it
   const int w0 = (int)((int64_t)n_steps * rank / splits), w1 = (int)((int64_t)n_steps * (rank + 1) / splits);
   P::template run<true>(a, sr, b, w0, w1, dec_smem, sc, bad_page, bad_idx);
   const float4* o4 = reinterpret_cast<const float4*>(dec_smem);
@@ -834,35 +844,49 @@ __global__ void __launch_bounds__(kAttnThreads, (Piece<T, D, MAXH>::CTAS))
   if (splits == 1) {
     for (int i = threadIdx.x; i < n4; i += kAttnThreads) {
       const float2 ml = sc.ml[i / (D / 4)];
-      store_out4(out + 4 * i, o4[i], inv_sum(ml.y));
+      store_out4(out + 4 * i, o4[result_at<P, D>(i)], inv_sum(ml.y));
     }
     if (threadIdx.x < a.Hq) lse[threadIdx.x] = lse_of(sc.ml[threadIdx.x].x, sc.ml[threadIdx.x].y);
   } else {
     cluster_sync();
-    // each CTA writes its share of the outputs from all CTAs' parts
+    // Each CTA writes its share of the outputs from all CTAs' parts.  Lane s of
+    // every 16 lanes holds CTA s's base and sum of the lanes' head (16 lanes
+    // never cross a head: D/4 is a multiple of 16), so that all remote loads
+    // are in flight at once.
     const uint32_t o_s = smem_u32(o4), ml_s = smem_u32(sc.ml);
-    const int per = (n4 + splits - 1) / splits;
+    const int per = ((n4 + splits - 1) / splits + 15) & ~15;
     const int end = min(n4, (rank + 1) * per);
-    for (int i = rank * per + threadIdx.x; i < end; i += kAttnThreads) {
-      const int h = i / (D / 4);
-      float mm = -INFINITY;
-      for (int s = 0; s < splits; ++s) mm = fmaxf(mm, cluster_ld2(cluster_map(ml_s + 8 * h, s)).x);
-      const float base = mm == -INFINITY ? 0.f : mm;
+    for (int i0 = rank * per; i0 < end; i0 += kAttnThreads) {   // end and i0 are multiples of 16
+      const int i = min(i0 + (int)threadIdx.x, end - 1);
+      const int h = i / (D / 4), lane16 = threadIdx.x & 15;
+      float2 ml = make_float2(-INFINITY, 0.f);
+      if (lane16 < splits) ml = cluster_ld2(cluster_map(ml_s + 8 * h, lane16));
+      float4 x[16];
+#pragma unroll
+      for (int s = 0; s < 16; ++s)
+        if (s < splits) x[s] = cluster_ld4(cluster_map(o_s + 16 * result_at<P, D>(i), s));
+      float mm = ml.x;
+#pragma unroll
+      for (int w = 8; w; w >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, w));
+      const float f = exp2f(ml.x - (mm == -INFINITY ? 0.f : mm));
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
       float l = 0.f;
-#pragma unroll 4
-      for (int s = 0; s < splits; ++s) {
-        const float2 ml = cluster_ld2(cluster_map(ml_s + 8 * h, s));
-        const float4 x = cluster_ld4(cluster_map(o_s + 16 * i, s));
-        const float f = exp2f(ml.x - base);
-        l += f * ml.y;
-        acc.x += f * x.x;
-        acc.y += f * x.y;
-        acc.z += f * x.z;
-        acc.w += f * x.w;
+      const float fl = f * ml.y;
+#pragma unroll
+      for (int s = 0; s < 16; ++s) {
+        if (s < splits) {
+          const float w = __shfl_sync(0xffffffffu, f, s, 16);
+          l += __shfl_sync(0xffffffffu, fl, s, 16);
+          acc.x += w * x[s].x;
+          acc.y += w * x[s].y;
+          acc.z += w * x[s].z;
+          acc.w += w * x[s].w;
+        }
       }
-      store_out4(out + 4 * i, acc, inv_sum(l));
-      if (i % (D / 4) == 0) lse[h] = lse_of(mm, l);
+      if (i0 + (int)threadIdx.x < end) {
+        store_out4(out + 4 * i, acc, inv_sum(l));
+        if (i % (D / 4) == 0) lse[h] = lse_of(mm, l);
+      }
     }
     cluster_sync();   // no CTA leaves while its shared memory is being read
   }
@@ -905,14 +929,14 @@ __global__ void __launch_bounds__(kAttnThreads, (Piece<T, D, MAXH>::CTAS))
       if (w0 == 0 && w1 == n_steps) {
         for (int i = threadIdx.x; i < n4; i += kAttnThreads) {
           const float2 ml = sc.ml[i / (D / 4)];
-          store_out4(a.O + b * a.Hq * D + 4 * i, o4[i], inv_sum(ml.y));
+          store_out4(a.O + b * a.Hq * D + 4 * i, o4[result_at<P, D>(i)], inv_sum(ml.y));
         }
         if (threadIdx.x < a.Hq)
           a.LSE[b * a.Hq + threadIdx.x] = lse_of(sc.ml[threadIdx.x].x, sc.ml[threadIdx.x].y);
       } else {
         const int64_t piece = 2 * (int64_t)blockIdx.x + (pieces > 0);
         for (int i = threadIdx.x; i < n4; i += kAttnThreads)
-          reinterpret_cast<float4*>(a.ps.o)[piece * n4 + i] = o4[i];
+          reinterpret_cast<float4*>(a.ps.o)[piece * n4 + i] = o4[result_at<P, D>(i)];
         if (threadIdx.x < a.Hq) reinterpret_cast<float2*>(a.ps.ml)[piece * a.Hq + threadIdx.x] = sc.ml[threadIdx.x];
       }
       ++pieces;
@@ -1016,12 +1040,14 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(Pieces ps, T*
   if (threadIdx.x == 0 && blockIdx.z == 0) LSE[(int64_t)it.row * Hq + h] = lse_of(mm, l);
 }
 
-// CTAs per row of selected pools: the most (1, 2, 4, 8 or 16, a cluster) that
-// keep all rows resident at once and give a CTA work for its warps.
+// CTAs per row of selected pools (a cluster: 1 .. 8, or 16): the most that keep
+// all rows resident at once and give every warp a step.
 static unsigned selected_splits(int64_t batch, int n_steps, int min_steps, int resident) {
-  unsigned s = 1;
-  while (s < 16 && batch * s * 2 <= resident && (int)s * min_steps < n_steps) s *= 2;
-  return s;
+  int64_t s = resident / batch;
+  const int64_t most = (n_steps + min_steps - 1) / min_steps;
+  if (s > most) s = most;
+  if (s >= 16) return 16;
+  return s > 8 ? 8 : s < 1 ? 1 : (unsigned)s;
 }
 
 template <typename T, int D, int MAXH>
