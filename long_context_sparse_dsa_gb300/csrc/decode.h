@@ -83,13 +83,14 @@ struct AppendArgs {
 };
 cudaError_t launch_cache_append(bool bf16, const AppendArgs& a, cudaStream_t s);
 
-// Scores of one query per row over the paged pool keys: scores [batch, P].
+// Scores of one query per row over the paged pool keys: scores [batch, pitch].
 cudaError_t launch_decode_scores(bool bf16, const PagedView& pv, int64_t batch, int Hi, int di, const void* q_idx,
-                                 const float* w, const void* kpool, float* scores, int64_t P, cudaStream_t s);
+                                 const float* w, const void* kpool, float* scores, int64_t pitch, cudaStream_t s);
 // Top-k of each score row's first lens[b]/4 entries.
-cudaError_t launch_decode_topk(const PagedView& pv, int64_t batch, int k, const float* scores, int64_t P, int32_t* idx,
-                               cudaStream_t s);
-size_t decode_scores_bytes(int64_t batch, int64_t P);
+cudaError_t launch_decode_topk(const PagedView& pv, int64_t batch, int k, const float* scores, int64_t pitch,
+                               int32_t* idx, cudaStream_t s);
+// Row pitch of the score block: whole 16-byte pieces.
+inline int64_t decode_scores_pitch(int64_t pools) { return (pools + 3) & ~(int64_t)3; }
 
 struct DecodeAttnArgs {
   PagedView pv;

@@ -139,13 +139,13 @@ dsa_status do_indexer_topk(const dsa_dims* dims, const dsa_paged_cache* c, int64
                            const int32_t* table, const void* q_idx, const float* w, int32_t* idx, void* ws,
                            cudaStream_t s) {
   const dsa::PagedView pv = view(dims, c, lens, table);
-  const int64_t P = dims->L / 4;
+  const int64_t pitch = dsa::decode_scores_pitch(dims->L / 4);
   float* scores = reinterpret_cast<float*>(static_cast<char*>(ws) + q_bytes(dims, batch));
   dsa_status st = launched(dsa::launch_decode_scores(is_bf16(dims), pv, batch, dims->Hi, dims->di, q_idx, w, c->kpool,
-                                                     scores, P, s),
+                                                     scores, pitch, s),
                            "decode scores launch");
   if (st) return st;
-  return launched(dsa::launch_decode_topk(pv, batch, dims->k, scores, P, idx, s), "decode top-k launch");
+  return launched(dsa::launch_decode_topk(pv, batch, dims->k, scores, pitch, idx, s), "decode top-k launch");
 }
 
 dsa_status do_attn(const dsa_dims* dims, const dsa_paged_cache* c, int64_t batch, const int32_t* lens,
@@ -179,7 +179,7 @@ dsa_status dsa_validate_decode_dims(const dsa_dims* dims) {
 
 size_t dsa_decode_workspace_bytes(const dsa_dims* dims, int64_t batch) {
   if (check_dims(dims) != DSA_OK || check_batch(batch) != DSA_OK) return 0;
-  const size_t sc = dsa::decode_scores_bytes(batch, dims->L / 4);
+  const size_t sc = ((size_t)batch * dsa::decode_scores_pitch(dims->L / 4) * sizeof(float) + 255) & ~(size_t)255;
   const size_t at = dsa::decode_attn_ws_bytes(batch, dims->Hq, dims->d);
   return q_bytes(dims, batch) + (sc > at ? sc : at);
 }

@@ -22,9 +22,11 @@ constexpr int kScorePools = kScoreWarps * kScorePoolsPerWarp;   // pools per CTA
 template <int DI>
 __global__ void __launch_bounds__(kScoreWarps * 32)
     decode_scores_bf16_kernel(PagedView pv, int Hi, const uint4* __restrict__ q_idx, const float* __restrict__ w,
-                              const uint4* __restrict__ kpool, float* __restrict__ scores, int64_t P) {
+                              const uint4* __restrict__ kpool, float* __restrict__ scores, int64_t pitch) {
   constexpr int CH = DI / 8;     // 16-byte chunks per row
   constexpr int CL = CH / 4;     // chunks per lane and row
+  chain_wait();
+  chain_release();
   const int64_t b = blockIdx.y;
   bool bad = false;
   const int n = row_length(pv, b, bad) >> 2;
@@ -44,7 +46,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32)
   if (2 * qi < Hi) w0 = __ldg(w + b * Hi + 2 * qi);
   if (2 * qi + 1 < Hi) w1 = __ldg(w + b * Hi + 2 * qi + 1);
   const int32_t* trow = pv.table + b * pv.cols;
-  float* srow = scores + b * P;
+  float* srow = scores + b * pitch;
 #pragma unroll
   for (int i = 0; i < kScorePoolsPerWarp / 16; ++i) {
     uint4 kf[2][CL];
@@ -87,9 +89,11 @@ __global__ void __launch_bounds__(kScoreWarps * 32)
 template <int DI>
 __global__ void __launch_bounds__(kScoreWarps * 32)
     decode_scores_f32_kernel(PagedView pv, int Hi, const float4* __restrict__ q_idx, const float* __restrict__ w,
-                             const float4* __restrict__ kpool, float* __restrict__ scores, int64_t P) {
+                             const float4* __restrict__ kpool, float* __restrict__ scores, int64_t pitch) {
   constexpr int LPR = DI / 8;          // lanes per pool row, 8 channels each
   constexpr int RPW = 32 / LPR;        // pool rows per warp and pass
+  chain_wait();
+  chain_release();
   const int64_t b = blockIdx.y;
   bool bad = false;
   const int n = row_length(pv, b, bad) >> 2;
@@ -150,35 +154,31 @@ __global__ void __launch_bounds__(kScoreWarps * 32)
     s += __shfl_xor_sync(0xffffffffu, s, 1);
     s += __shfl_xor_sync(0xffffffffu, s, 2);
     s += __shfl_xor_sync(0xffffffffu, s, 4);
-    if (li == 0 && p < n) scores[b * P + p] = s;
+    if (li == 0 && p < n) scores[b * pitch + p] = s;
   }
   if (bad) record_error(DSA_DEV_ERR_BAD_PAGE);
 }
 
-size_t decode_scores_bytes(int64_t batch, int64_t P) {
-  return ((size_t)batch * (size_t)P * sizeof(float) + 255) & ~(size_t)255;
-}
-
 cudaError_t launch_decode_scores(bool bf16, const PagedView& pv, int64_t batch, int Hi, int di, const void* q_idx,
-                                 const float* w, const void* kpool, float* scores, int64_t P, cudaStream_t s) {
+                                 const float* w, const void* kpool, float* scores, int64_t pitch, cudaStream_t s) {
+  const int64_t P = pv.capacity / 4;
   const dim3 grid((unsigned)((P + kScorePools - 1) / kScorePools), (unsigned)batch);
   const int threads = kScoreWarps * 32;
   if (bf16) {
     auto q = static_cast<const uint4*>(q_idx);
     auto kp = static_cast<const uint4*>(kpool);
     if (di == 64)
-      decode_scores_bf16_kernel<64><<<grid, threads, 0, s>>>(pv, Hi, q, w, kp, scores, P);
+      return launch_chained(decode_scores_bf16_kernel<64>, grid, dim3(threads), 0, s, pv, Hi, q, w, kp, scores, pitch);
     else
-      decode_scores_bf16_kernel<128><<<grid, threads, 0, s>>>(pv, Hi, q, w, kp, scores, P);
+      return launch_chained(decode_scores_bf16_kernel<128>, grid, dim3(threads), 0, s, pv, Hi, q, w, kp, scores, pitch);
   } else {
     auto q = static_cast<const float4*>(q_idx);
     auto kp = static_cast<const float4*>(kpool);
     if (di == 64)
-      decode_scores_f32_kernel<64><<<grid, threads, 0, s>>>(pv, Hi, q, w, kp, scores, P);
+      return launch_chained(decode_scores_f32_kernel<64>, grid, dim3(threads), 0, s, pv, Hi, q, w, kp, scores, pitch);
     else
-      decode_scores_f32_kernel<128><<<grid, threads, 0, s>>>(pv, Hi, q, w, kp, scores, P);
+      return launch_chained(decode_scores_f32_kernel<128>, grid, dim3(threads), 0, s, pv, Hi, q, w, kp, scores, pitch);
   }
-  return cudaGetLastError();
 }
 
 }  // namespace dsa

@@ -41,7 +41,6 @@
 // above, or -- when even that overflows -- rounds and selection over the
 // whole row.
 #include "common.cuh"
-#include "decode.cuh"
 #include "launch.h"
 
 namespace dsa {
@@ -247,10 +246,10 @@ __device__ __forceinline__ void select_from_candidates(const uint32_t* cand_key,
   }
 }
 
-// The selection of one row: the k best of row[0 .. n64) into out[0 .. k), done
-// by the whole CTA.  vec4: the row may be read in 16-byte pieces.
-__device__ __forceinline__ void topk_select_row(const float* __restrict__ row, int64_t n64, int k, bool vec4,
-                                                int32_t* __restrict__ out) {
+// The selection of one row (row r of the score block, query q_begin + r),
+// done by the whole CTA.
+__device__ __forceinline__ void topk_row(const float* __restrict__ scores, int64_t P, int k, int64_t q_begin,
+                                         int64_t r, int32_t* __restrict__ idx) {
   __shared__ __align__(16) int hist[2048];
   __shared__ int warp_buf[32];
   __shared__ int sel[4];
@@ -262,11 +261,16 @@ __device__ __forceinline__ void topk_select_row(const float* __restrict__ row, i
   __shared__ uint32_t samples[kSamples];
 
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  const int64_t t = q_begin + r;
+  const int64_t n64 = elig(t);
+  int32_t* out = idx + t * (int64_t)k;
   if (n64 <= k) {
     for (int i = threadIdx.x; i < k; i += kTopkThreads) out[i] = i < n64 ? i : -1;
     return;
   }
   const int n = (int)n64;
+  const float* row = scores + r * P;
+  const bool vec4 = ((P & 3) == 0) && ((reinterpret_cast<uintptr_t>(scores) & 15) == 0);
 
   // ---- 1. threshold from evenly spaced samples ------------------------------
   uint32_t tau = 0u;   // every key is >= 0
@@ -555,14 +559,6 @@ __device__ __forceinline__ void topk_select_row(const float* __restrict__ row, i
   }
 }
 
-// Row r of the score block, query q_begin + r.
-__device__ __forceinline__ void topk_row(const float* __restrict__ scores, int64_t P, int k, int64_t q_begin,
-                                         int64_t r, int32_t* __restrict__ idx) {
-  const bool vec4 = ((P & 3) == 0) && ((reinterpret_cast<uintptr_t>(scores) & 15) == 0);
-  const int64_t t = q_begin + r;
-  topk_select_row(scores + r * P, elig(t), k, vec4, idx + t * (int64_t)k);
-}
-
 // Four CTAs per SM (64 registers a thread).  Five fit in shared memory
 // (about 45 KB each), but the 48-register cap that five need spills, and four
 // measured faster on long rows (1M tokens: -20%) and no slower at 128k.
@@ -586,23 +582,6 @@ __global__ void __launch_bounds__(kTopkThreads, 4) topk_list_kernel(const float*
     topk_row(scores, P, k, q_begin, rlist[b], idx);
     __syncthreads();   // the shared arrays are reused by the next row
   }
-}
-
-// One query per row of a decode batch: row b selects from its first lens[b]/4
-// scores (a length outside the capacity counts as 0).
-__global__ void __launch_bounds__(kTopkThreads, 4) decode_topk_kernel(PagedView pv, const float* __restrict__ scores,
-                                                                   int64_t P, int k, int32_t* __restrict__ idx) {
-  const int64_t b = blockIdx.x;
-  bool bad = false;
-  const int len = row_length(pv, b, bad);
-  if (bad && threadIdx.x == 0) record_error(DSA_DEV_ERR_BAD_PAGE);
-  topk_select_row(scores + b * P, len >> 2, k, (P & 3) == 0, idx + b * (int64_t)k);
-}
-
-cudaError_t launch_decode_topk(const PagedView& pv, int64_t batch, int k, const float* scores, int64_t P, int32_t* idx,
-                               cudaStream_t s) {
-  decode_topk_kernel<<<(unsigned)batch, kTopkThreads, 0, s>>>(pv, scores, P, k, idx);
-  return cudaGetLastError();
 }
 
 cudaError_t launch_topk(int64_t L, int k, const float* scores, int64_t q_begin, int64_t q_count, int32_t* idx,
