@@ -49,9 +49,14 @@ __device__ __forceinline__ void chain_wait() { asm volatile("griddepcontrol.wait
 __device__ __forceinline__ void chain_release() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
 
 // Thread-block clusters: barrier over all threads of the cluster (release /
-// acquire of shared memory), and loads from another CTA's shared memory.
+// acquire of shared memory), and accesses to another CTA's shared memory (only
+// between two barriers: after one the CTA is known to run, until the next it
+// does not leave).
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;\n" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+  cluster_arrive();
+  cluster_wait();
 }
 __device__ __forceinline__ uint32_t cluster_map(uint32_t saddr, uint32_t rank) {
   uint32_t a;
@@ -65,10 +70,8 @@ __device__ __forceinline__ float4 cluster_ld4(uint32_t addr) {
                : "r"(addr));
   return v;
 }
-__device__ __forceinline__ uint32_t cluster_ld_u32(uint32_t addr) {
-  uint32_t v;
-  asm volatile("ld.shared::cluster.u32 %0, [%1];\n" : "=r"(v) : "r"(addr));
-  return v;
+__device__ __forceinline__ void cluster_st_u32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;\n" ::"r"(addr), "r"(v) : "memory");
 }
 __device__ __forceinline__ float2 cluster_ld2(uint32_t addr) {
   float2 v;

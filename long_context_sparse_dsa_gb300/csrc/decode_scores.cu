@@ -16,10 +16,32 @@
 namespace dsa {
 
 constexpr int kScoreWarps = 4;
-constexpr int kScorePoolsPerWarp = 64;
-constexpr int kScorePools = kScoreWarps * kScorePoolsPerWarp;   // pools per CTA
 
-template <int DI>
+// Physical pools of a warp's PPW pools from p0: lane i resolves pools p0 + i and
+// p0 + 32 + i, so that all block-table loads are in flight at once.  -1: past
+// the row's end, or outside the cache.
+template <int PPW>
+struct PoolBlock {
+  static constexpr int N = (PPW + 31) / 32;
+  int pp[N];
+  __device__ __forceinline__ void load(const PagedView& pv, const int32_t* trow, int p0, int n, bool& bad) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int p = p0 + 32 * i + lane;
+      pp[i] = -1;
+      if (p < n && 32 * i + lane < PPW) {
+        const int col = page_of_pool(pv, p);
+        pp[i] = phys_pool(pv, p, col, __ldg(trow + col), bad);
+      }
+    }
+  }
+  __device__ __forceinline__ int get(int i, int j) const {   // pool p0 + 32 i + j
+    return __shfl_sync(0xffffffffu, pp[i], j);
+  }
+};
+
+template <int DI, int PPW>
 __global__ void __launch_bounds__(kScoreWarps * 32)
     decode_scores_bf16_kernel(PagedView pv, int Hi, const uint4* __restrict__ q_idx, const float* __restrict__ w,
                               const uint4* __restrict__ kpool, float* __restrict__ scores, int64_t pitch) {
@@ -31,9 +53,11 @@ __global__ void __launch_bounds__(kScoreWarps * 32)
   bool bad = false;
   const int n = row_length(pv, b, bad) >> 2;
   const int lane = threadIdx.x & 31;
-  const int p0 = blockIdx.x * kScorePools + (threadIdx.x >> 5) * kScorePoolsPerWarp;
+  const int p0 = (blockIdx.x * kScoreWarps + (threadIdx.x >> 5)) * PPW;
   if (p0 >= n) return;   // bad lengths are recorded by the selection
   const int g = lane >> 2, qi = lane & 3;
+  PoolBlock<PPW> pools;
+  pools.load(pv, pv.table + b * pv.cols, p0, n, bad);
   uint4 qf[CL];
   float w0 = 0.f, w1 = 0.f;
 #pragma unroll
@@ -45,25 +69,16 @@ __global__ void __launch_bounds__(kScoreWarps * 32)
   }
   if (2 * qi < Hi) w0 = __ldg(w + b * Hi + 2 * qi);
   if (2 * qi + 1 < Hi) w1 = __ldg(w + b * Hi + 2 * qi + 1);
-  const int32_t* trow = pv.table + b * pv.cols;
   float* srow = scores + b * pitch;
 #pragma unroll
-  for (int i = 0; i < kScorePoolsPerWarp / 16; ++i) {
+  for (int i = 0; i < PPW / 16; ++i) {
     uint4 kf[2][CL];
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      const int p = p0 + i * 16 + r * 8 + g;
+      const int pp = pools.get(i / 2, (i & 1) * 16 + r * 8 + g);
 #pragma unroll
-      for (int c = 0; c < CL; ++c) kf[r][c] = make_uint4(0u, 0u, 0u, 0u);
-      if (p < n) {
-        const int col = page_of_pool(pv, p);
-        const int pp = phys_pool(pv, p, col, __ldg(trow + col), bad);
-        if (pp >= 0) {
-          const uint4* src = kpool + (int64_t)pp * CH + qi;
-#pragma unroll
-          for (int c = 0; c < CL; ++c) kf[r][c] = __ldg(src + 4 * c);
-        }
-      }
+      for (int c = 0; c < CL; ++c)
+        kf[r][c] = pp >= 0 ? __ldg(kpool + (int64_t)pp * CH + qi + 4 * c) : make_uint4(0u, 0u, 0u, 0u);
     }
     float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -86,7 +101,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32)
   if (bad) record_error(DSA_DEV_ERR_BAD_PAGE);
 }
 
-template <int DI>
+template <int DI, int PPW>
 __global__ void __launch_bounds__(kScoreWarps * 32)
     decode_scores_f32_kernel(PagedView pv, int Hi, const float4* __restrict__ q_idx, const float* __restrict__ w,
                              const float4* __restrict__ kpool, float* __restrict__ scores, int64_t pitch) {
@@ -98,9 +113,11 @@ __global__ void __launch_bounds__(kScoreWarps * 32)
   bool bad = false;
   const int n = row_length(pv, b, bad) >> 2;
   const int lane = threadIdx.x & 31;
-  const int p0 = blockIdx.x * kScorePools + (threadIdx.x >> 5) * kScorePoolsPerWarp;
+  const int p0 = (blockIdx.x * kScoreWarps + (threadIdx.x >> 5)) * PPW;
   if (p0 >= n) return;
   const int sub = lane / LPR, li = lane % LPR;
+  PoolBlock<PPW> pools;
+  pools.load(pv, pv.table + b * pv.cols, p0, n, bad);
   // channels li*4 .. +3 and DI/2 + li*4 .. +3: consecutive lanes read consecutive 16 bytes
   float4 qf[8][2];
 #pragma unroll
@@ -113,17 +130,14 @@ __global__ void __launch_bounds__(kScoreWarps * 32)
   }
   // after the reduction below lane li holds head li & 7
   const float wh = (li & 7) < Hi ? __ldg(w + b * Hi + (li & 7)) : 0.f;
-  const int32_t* trow = pv.table + b * pv.cols;
-  for (int i = 0; i < kScorePoolsPerWarp; i += RPW) {
+#pragma unroll 4
+  for (int i = 0; i < PPW; i += RPW) {
     const int p = p0 + i + sub;
+    const int pp = pools.get(PPW > 32 && i >= 32 ? 1 : 0, (i & 31) + sub);
     float4 k0 = make_float4(0.f, 0.f, 0.f, 0.f), k1 = k0;
-    if (p < n) {
-      const int col = page_of_pool(pv, p);
-      const int pp = phys_pool(pv, p, col, __ldg(trow + col), bad);
-      if (pp >= 0) {
-        k0 = __ldg(kpool + (int64_t)pp * (DI / 4) + li);
-        k1 = __ldg(kpool + (int64_t)pp * (DI / 4) + LPR + li);
-      }
+    if (pp >= 0) {
+      k0 = __ldg(kpool + (int64_t)pp * (DI / 4) + li);
+      k1 = __ldg(kpool + (int64_t)pp * (DI / 4) + LPR + li);
     }
     float dot[8];
 #pragma unroll
@@ -159,26 +173,28 @@ __global__ void __launch_bounds__(kScoreWarps * 32)
   if (bad) record_error(DSA_DEV_ERR_BAD_PAGE);
 }
 
+template <int DI, int PPW>
+static cudaError_t launch_scores(bool bf16, const PagedView& pv, int64_t batch, int Hi, const void* q_idx,
+                                 const float* w, const void* kpool, float* scores, int64_t pitch, cudaStream_t s) {
+  const int64_t P = pv.capacity / 4, per = kScoreWarps * PPW;
+  const dim3 grid((unsigned)((P + per - 1) / per), (unsigned)batch), threads(kScoreWarps * 32);
+  if (bf16)
+    return launch_chained(decode_scores_bf16_kernel<DI, PPW>, grid, threads, 0, s, pv, Hi,
+                          static_cast<const uint4*>(q_idx), w, static_cast<const uint4*>(kpool), scores, pitch);
+  return launch_chained(decode_scores_f32_kernel<DI, PPW>, grid, threads, 0, s, pv, Hi,
+                        static_cast<const float4*>(q_idx), w, static_cast<const float4*>(kpool), scores, pitch);
+}
+
 cudaError_t launch_decode_scores(bool bf16, const PagedView& pv, int64_t batch, int Hi, int di, const void* q_idx,
                                  const float* w, const void* kpool, float* scores, int64_t pitch, cudaStream_t s) {
-  const int64_t P = pv.capacity / 4;
-  const dim3 grid((unsigned)((P + kScorePools - 1) / kScorePools), (unsigned)batch);
-  const int threads = kScoreWarps * 32;
-  if (bf16) {
-    auto q = static_cast<const uint4*>(q_idx);
-    auto kp = static_cast<const uint4*>(kpool);
-    if (di == 64)
-      return launch_chained(decode_scores_bf16_kernel<64>, grid, dim3(threads), 0, s, pv, Hi, q, w, kp, scores, pitch);
-    else
-      return launch_chained(decode_scores_bf16_kernel<128>, grid, dim3(threads), 0, s, pv, Hi, q, w, kp, scores, pitch);
-  } else {
-    auto q = static_cast<const float4*>(q_idx);
-    auto kp = static_cast<const float4*>(kpool);
-    if (di == 64)
-      return launch_chained(decode_scores_f32_kernel<64>, grid, dim3(threads), 0, s, pv, Hi, q, w, kp, scores, pitch);
-    else
-      return launch_chained(decode_scores_f32_kernel<128>, grid, dim3(threads), 0, s, pv, Hi, q, w, kp, scores, pitch);
-  }
+  // 64 pools a warp (16 KB in flight at di = 128) once that gives every SM 8
+  // warps, else 16, for latency
+  const bool many = batch * (pv.capacity / 4) >= (int64_t)152 * 8 * 64;
+  if (di == 64)
+    return many ? launch_scores<64, 64>(bf16, pv, batch, Hi, q_idx, w, kpool, scores, pitch, s)
+                : launch_scores<64, 16>(bf16, pv, batch, Hi, q_idx, w, kpool, scores, pitch, s);
+  return many ? launch_scores<128, 64>(bf16, pv, batch, Hi, q_idx, w, kpool, scores, pitch, s)
+              : launch_scores<128, 16>(bf16, pv, batch, Hi, q_idx, w, kpool, scores, pitch, s);
 }
 
 }  // namespace dsa

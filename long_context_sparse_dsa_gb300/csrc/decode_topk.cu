@@ -5,18 +5,21 @@
 // topk.cu, for few long rows instead of thousands.  A row is one cluster of up
 // to 16 CTAs, each with a contiguous slice of the row, so that one row of a
 // million tokens is read by 16 SMs.  For n > kCap:
-//   1. every CTA finds the same threshold tau from evenly spaced samples of
-//      the whole row: the r-th largest, r = mu + 4 sqrt(mu) + 2 with mu =
-//      k * samples / n, below the k-th score with high probability;
+//   1. every CTA finds the same threshold tau from samples, g evenly spaced
+//      scores for each of its 512 threads, of which a thread keeps the best:
+//      the r-th largest of those, r = mu + 4 sqrt(mu) + 2 with mu = k * 512 g /
+//      n the number of samples expected above the k-th score, lies below the
+//      k-th score with high probability (g grows with n so that r stays far
+//      below 512 and keeping one sample of g loses little);
 //   2. one pass over its slice keeps the scores > tau with their pools, in
 //      order, and counts the scores == tau;
 //   3. the counts are exchanged.  Usually the scores > tau number at least k and
-//      at most kCap: the first CTA fetches them and selects exactly (three
-//      radix rounds over order-preserving keys).  If they are fewer than k but
+//      at most kCap: the first CTA gets them and selects exactly (histogram
+//      rounds over order-preserving keys).  If they are fewer than k but
 //      the ties at tau make up the rest, tau is the k-th score: each CTA
 //      writes its own part of the result in a second pass over its slice.
 //      Otherwise (the samples missed) the first CTA selects from the whole row
-//      by radix rounds over it; the result never depends on tau.
+//      by histogram rounds over it; the result never depends on tau.
 // Rows of at most kCap scores skip 1 and keep every score.
 // A NaN score has no defined rank.
 //
@@ -31,174 +34,297 @@ namespace dsa {
 constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kCap = 4096;                           // scores selected from exactly
-constexpr int kPerLane = 16;                         // scores a lane holds per chunk (float4 x 4)
+constexpr int kPerLane = 16;                         // scores a thread holds per chunk
 constexpr int kChunk = kSelThreads * kPerLane;       // scores of a CTA's pass
 constexpr uint32_t kFullMask = 0xffffffffu;
+
+// order_key, without the key 0 (which only a NaN has).
+__device__ __forceinline__ uint32_t own_key(float x) { return max(order_key(x), 1u); }
 
 struct SelShared {
   alignas(16) int hist[2048];
   alignas(16) uint32_t key[kCap];    // this CTA's candidates
   int32_t pool[kCap];
-  alignas(16) uint32_t gkey[kCap];   // the first CTA: all candidates; before that, the samples
+  alignas(16) uint32_t gkey[kCap];   // the first CTA: all CTAs' candidates
   int32_t gpool[kCap];
-  int64_t wsum[kSelWarps];
-  int sel[2];
-  alignas(8) int count[2];           // candidates and ties of this CTA, for the cluster
+  alignas(16) int wsum[2][kSelWarps];
+  uint32_t lo, hi;
+  int sel[3];
+  int listed;
+  uint32_t list[32];
+  int n_gt[16], n_eq[16];            // candidates and ties of every CTA of the cluster
 };
 
-// Exclusive prefix over the CTA's threads of a pair of counts, (hi << 32) +
-// lo; *total gets the sum.  Ends with a __syncthreads().
-__device__ __forceinline__ int64_t block_prefix(int64_t v, SelShared& sh, int64_t* total) {
+// Exclusive prefix of v over the CTA's threads, and its sum; one barrier
+// inside, none after: the caller has one before sh.wsum[0] is used again.
+__device__ __forceinline__ int block_prefix(int v, SelShared& sh, int* total) {
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-  int64_t incl = v;
+  int incl = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t y = __shfl_up_sync(kFullMask, incl, o);
+    const int y = __shfl_up_sync(kFullMask, incl, o);
     if (lane >= o) incl += y;
   }
-  if (lane == 31) sh.wsum[wid] = incl;
+  if (lane == 31) sh.wsum[0][wid] = incl;
   __syncthreads();
-  int64_t before = 0, all = 0;
+  // lane w of every warp sums up to warp w
+  int ws = lane < kSelWarps ? sh.wsum[0][lane] : 0;
 #pragma unroll
-  for (int w = 0; w < kSelWarps; ++w) {
-    const int64_t x = sh.wsum[w];
-    if (w < wid) before += x;
-    all += x;
+  for (int o = 1; o < kSelWarps; o <<= 1) {
+    const int y = __shfl_up_sync(kFullMask, ws, o);
+    if (lane >= o) ws += y;
   }
-  *total = all;
-  __syncthreads();
-  return before + incl - v;
+  *total = __shfl_sync(kFullMask, ws, kSelWarps - 1);
+  const int before = __shfl_sync(kFullMask, ws, wid ? wid - 1 : 0);
+  return (wid ? before : 0) + incl - v;
 }
 
-// The `need`-th largest of n keys (1 <= need <= n), key(i) by index; *above
-// gets how many are larger.  Radix rounds of 11, 11 and 10 bits.
+// The range of n keys, key(i) by index.  Ends with a barrier.
 template <typename F>
-__device__ __forceinline__ uint32_t kth_largest(F key, int64_t n, int64_t need, SelShared& sh, int64_t* above) {
-  uint32_t prefix = 0;
-  int64_t got = 0;
+__device__ __forceinline__ void key_range(F key, int n, SelShared& sh, uint32_t& lo, uint32_t& hi) {
+  if (threadIdx.x == 0) {
+    sh.lo = 0xffffffffu;
+    sh.hi = 0u;
+  }
+  __syncthreads();
+  uint32_t l = 0xffffffffu, h = 0u;
+  for (int i = threadIdx.x; i < n; i += kSelThreads) {
+    const uint32_t x = key(i);
+    l = min(l, x);
+    h = max(h, x);
+  }
+  l = __reduce_min_sync(kFullMask, l);
+  h = __reduce_max_sync(kFullMask, h);
+  if ((threadIdx.x & 31) == 0) {
+    atomicMin(&sh.lo, l);
+    atomicMax(&sh.hi, h);
+  }
+  __syncthreads();
+  lo = sh.lo;
+  hi = sh.hi;
+}
+
+// One histogram round over the keys in [lo, lo + span], bins of 2^shift: finds,
+// from the top, the bin where the count reaches `need`.  bin gets the bin's
+// lowest key, above the keys of higher bins, in_bin the bin's keys.
+template <typename F>
+__device__ __forceinline__ void hist_round(F key, int n, uint32_t lo, uint32_t span, int shift, int need,
+                                           SelShared& sh, uint32_t& bin, int& above, int& in_bin) {
+  static_assert(kSelThreads * 4 == 2048, "a thread owns 4 bins");
+  reinterpret_cast<int4*>(sh.hist)[threadIdx.x] = make_int4(0, 0, 0, 0);
+  __syncthreads();
+  for (int i = threadIdx.x; i < n; i += kSelThreads) {
+    const uint32_t x = key(i), d = x - lo;
+    if (x >= lo && d <= span) atomicAdd(&sh.hist[d >> shift], 1);
+  }
+  __syncthreads();
+  const int first = 2044 - 4 * (int)threadIdx.x;   // thread 0 owns the top bins
+  const int4 h4 = reinterpret_cast<const int4*>(sh.hist)[first / 4];
+  const int h[4] = {h4.w, h4.z, h4.y, h4.x};
+  int total;
+  int cum = block_prefix(h[0] + h[1] + h[2] + h[3], sh, &total);
 #pragma unroll
-  for (int round = 0; round < 3; ++round) {
-    constexpr int widths[3] = {11, 11, 10}, shifts[3] = {21, 10, 0};
-    const int shift = shifts[round], top = shift + widths[round];
-    reinterpret_cast<int4*>(sh.hist)[threadIdx.x] = make_int4(0, 0, 0, 0);   // 2048 bins
-    __syncthreads();
-    for (int64_t i = threadIdx.x; i < n; i += kSelThreads) {
-      const uint32_t x = key(i);
-      if (round == 0 || (x >> (top & 31)) == prefix) atomicAdd(&sh.hist[(x >> shift) & ((1 << widths[round]) - 1)], 1);
+  for (int j = 0; j < 4; ++j) {
+    if (cum < need && cum + h[j] >= need) {
+      sh.sel[0] = first + 3 - j;
+      sh.sel[1] = cum;
+      sh.sel[2] = h[j];
     }
+    cum += h[j];
+  }
+  __syncthreads();
+  bin = lo + ((uint32_t)sh.sel[0] << shift);
+  above = sh.sel[1];
+  in_bin = sh.sel[2];
+}
+
+// The `need` largest of n keys (1 <= need <= n) in memory: returns T and a
+// number of ties such that they are those > T and the first `ties` of those ==
+// T.  Histogram rounds of 2048 bins over the keys' own range; a round whose bin
+// is wanted whole is the last (T then lies just below the bin).
+template <typename F>
+__device__ __forceinline__ uint32_t kth_largest(F key, int n, int need, SelShared& sh, int* ties) {
+  uint32_t lo, hi;
+  key_range(key, n, sh, lo, hi);
+  uint32_t span = hi - lo;
+  int shift = span >> 11 ? 21 - __clz(span) : 0;   // span >> shift < 2048
+  while (true) {
+    uint32_t bin;
+    int above, in_bin;
+    hist_round(key, n, lo, span, shift, need, sh, bin, above, in_bin);
+    need -= above;
+    if (need == in_bin && bin > 0u) {
+      *ties = 0;
+      return bin - 1u;
+    }
+    if (shift == 0) {
+      *ties = need;
+      return bin;
+    }
+    lo = bin;
+    span = (1u << shift) - 1u;
+    shift = shift > 11 ? shift - 11 : 0;
+  }
+}
+
+// The same for keys in registers, J a thread, 0 where there is none (own_key()
+// gives no score key 0).  Once a bin holds at most 32 keys, every warp ranks them.
+template <int J>
+__device__ __forceinline__ uint32_t kth_largest_own(const uint32_t (&x)[J], int need, SelShared& sh, int* ties) {
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  int4* hist4 = reinterpret_cast<int4*>(sh.hist);
+  const int first = 2044 - 4 * (int)threadIdx.x;   // thread 0 owns the top bins
+  uint32_t l = 0xffffffffu, h = 0u;
+#pragma unroll
+  for (int i = 0; i < J; ++i) {
+    l = x[i] ? min(l, x[i]) : l;
+    h = max(h, x[i]);
+  }
+  l = __reduce_min_sync(kFullMask, l);
+  h = __reduce_max_sync(kFullMask, h);
+  if (lane == 0) {
+    sh.wsum[0][wid] = (int)l;
+    sh.wsum[1][wid] = (int)h;
+  }
+  hist4[threadIdx.x] = make_int4(0, 0, 0, 0);
+  if (threadIdx.x == 0) sh.listed = 0;
+  __syncthreads();
+  uint32_t lo = __reduce_min_sync(kFullMask, lane < kSelWarps ? (uint32_t)sh.wsum[0][lane] : 0xffffffffu);
+  uint32_t span = __reduce_max_sync(kFullMask, lane < kSelWarps ? (uint32_t)sh.wsum[1][lane] : 0u) - lo;
+  int shift = span >> 11 ? 21 - __clz(span) : 0;   // span >> shift < 2048
+  while (true) {
+#pragma unroll
+    for (int i = 0; i < J; ++i)
+      if (x[i] >= lo && x[i] - lo <= span) atomicAdd(&sh.hist[(x[i] - lo) >> shift], 1);
     __syncthreads();
-    // thread t owns the bins 2047 - 4 t .. 2044 - 4 t, from the top
-    const int lo = 2044 - 4 * (int)threadIdx.x;
-    const int4 h4 = reinterpret_cast<const int4*>(sh.hist)[lo / 4];
-    const int h[4] = {h4.w, h4.z, h4.y, h4.x};
-    int64_t all;
-    int64_t cum = got + block_prefix((int64_t)h[0] + h[1] + h[2] + h[3], sh, &all);
+    const int4 h4 = hist4[first / 4];
+    hist4[first / 4] = make_int4(0, 0, 0, 0);   // for the next round
+    const int c[4] = {h4.w, h4.z, h4.y, h4.x};
+    int total;
+    int cum = block_prefix(c[0] + c[1] + c[2] + c[3], sh, &total);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      if (cum < need && cum + h[j] >= need) {
-        sh.sel[0] = lo + 3 - j;
-        sh.wsum[0] = cum;
+      if (cum < need && cum + c[j] >= need) {
+        sh.sel[0] = first + 3 - j;
+        sh.sel[1] = cum;
+        sh.sel[2] = c[j];
       }
-      cum += h[j];
+      cum += c[j];
     }
     __syncthreads();
-    prefix = (prefix << widths[round]) | (uint32_t)sh.sel[0];
-    got = sh.wsum[0];
-    __syncthreads();
+    lo += (uint32_t)sh.sel[0] << shift;
+    need -= sh.sel[1];
+    const int in_bin = sh.sel[2];
+    if (shift == 0) {
+      *ties = need;
+      return lo;
+    }
+    span = (1u << shift) - 1u;
+    if (in_bin <= 32) {
+#pragma unroll
+      for (int i = 0; i < J; ++i)
+        if (x[i] >= lo && x[i] - lo <= span) sh.list[atomicAdd(&sh.listed, 1)] = x[i];
+      __syncthreads();
+      const uint32_t y = lane < in_bin ? sh.list[lane] : 0u;
+      int larger = 0;
+      for (int j = 0; j < in_bin; ++j) larger += __shfl_sync(kFullMask, y, j) > y;
+      // the need-th largest is the smallest key with fewer than need larger ones
+      const uint32_t v = __reduce_min_sync(kFullMask, lane < in_bin && larger < need ? y : 0xffffffffu);
+      *ties = need - (int)__reduce_max_sync(kFullMask, lane < in_bin && y == v ? (unsigned)larger : 0u);
+      return v;
+    }
+    shift = shift > 11 ? shift - 11 : 0;
   }
-  *above = got;
-  return prefix;
 }
 
-// Writes, in order, the keys > T and the first need_eq keys == T of n keys.
+// Writes, in order, the keys > T and the first `ties` keys == T of n keys.  A
+// thread takes up to 8 consecutive keys at a time.
 template <typename F, typename G>
-__device__ __forceinline__ void write_selected(F key, G pool, int64_t n, uint32_t T, int64_t need_eq, SelShared& sh,
+__device__ __forceinline__ void write_selected(F key, G pool, int n, uint32_t T, int ties, SelShared& sh,
                                                int32_t* __restrict__ out) {
-  int64_t base = 0;   // (ties << 32) + larger ones
-  for (int64_t i0 = 0; i0 < n; i0 += kSelThreads) {
-    const int64_t i = i0 + threadIdx.x;
-    const uint32_t x = i < n ? key(i) : 0u;
-    const bool gt = i < n && x > T, eq = i < n && x == T;
-    int64_t total;
-    const int64_t p = base + block_prefix((int64_t)gt + ((int64_t)eq << 32), sh, &total);
-    const int64_t eq_before = p >> 32, gt_before = p & 0xffffffff;
-    if (gt || (eq && eq_before < need_eq))
-      out[gt_before + (eq_before < need_eq ? eq_before : need_eq)] = (int32_t)pool(i);
-    base += total;
+  constexpr int J = 8;
+  int gt_base = 0, eq_base = 0;
+  const int per = n < J * kSelThreads ? (n + kSelThreads - 1) / kSelThreads : J;
+  for (int64_t i0 = 0; i0 < n; i0 += per * kSelThreads) {
+    uint32_t gt = 0, eq = 0;
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const int64_t i = i0 + threadIdx.x * per + j;
+      if (j < per && i < n) {
+        const uint32_t x = key((int)i);
+        gt |= (uint32_t)(x > T) << j;
+        eq |= (uint32_t)(x == T) << j;
+      }
+    }
+    int total;
+    const int p = block_prefix(__popc(gt) + (__popc(eq) << 16), sh, &total);   // at most 4096 of each
+    int g = gt_base + (p & 0xffff), e = eq_base + (p >> 16);
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const bool is_gt = (gt >> j) & 1u, is_eq = (eq >> j) & 1u;
+      if (is_gt || (is_eq && e < ties)) out[g + min(e, ties)] = (int32_t)pool((int)(i0 + threadIdx.x * per + j));
+      g += is_gt;
+      e += is_eq;
+    }
+    gt_base += total & 0xffff;
+    eq_base += total >> 16;
+    __syncthreads();   // wsum is free again
   }
 }
 
-// One pass over scores [begin, end) of a row, kChunk at a time, in order: put(pool, gt, gt_before, eq_before) for
-// every score > tau (or any, if keep_all) or == tau, with the numbers of both before it in the slice.  Returns the
-// slice's numbers, (eq << 32) + gt.
+// One pass over scores [begin, end) of a row, kChunk at a time, in order:
+// put(pool, score, gt, gt_before, eq_before) for every score > tau (or any, if
+// keep_all) or == tau, with the numbers of both before it in the slice.
 template <typename F>
-__device__ __forceinline__ int64_t scan_slice(const float* __restrict__ row, int64_t begin, int64_t end, bool keep_all,
-                                              float tau, SelShared& sh, F put) {
-  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-  int64_t base = 0;
+__device__ __forceinline__ void scan_slice(const float* __restrict__ row, int64_t begin, int64_t end, bool keep_all,
+                                           float tau, SelShared& sh, int& n_gt, int& n_eq, F put) {
+  n_gt = n_eq = 0;
   for (int64_t c0 = begin; c0 < end; c0 += kChunk) {
-    // a warp's 512 scores of the chunk: 4 groups of 128, a lane's 4 consecutive in each
-    const int64_t w0 = c0 + (int64_t)wid * 32 * kPerLane;
+    // a lane's kPerLane consecutive scores
+    const int64_t e0 = c0 + (int64_t)threadIdx.x * kPerLane;
     float x[kPerLane];
 #pragma unroll
-    for (int u = 0; u < kPerLane / 4; ++u) {
-      const int64_t e = w0 + u * 128 + 4 * lane;
+    for (int u = 0; u < kPerLane; u += 4) {
       float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (e + 3 < end)
-        f = __ldcg(reinterpret_cast<const float4*>(row + e));   // begin is a multiple of 4
-      else {
-        if (e < end) f.x = __ldcg(row + e);
-        if (e + 1 < end) f.y = __ldcg(row + e + 1);
-        if (e + 2 < end) f.z = __ldcg(row + e + 2);
+      if (e0 + u + 3 < end) {
+        f = *reinterpret_cast<const float4*>(row + e0 + u);   // begin is a multiple of 4
+      } else {
+        if (e0 + u < end) f.x = row[e0 + u];
+        if (e0 + u + 1 < end) f.y = row[e0 + u + 1];
+        if (e0 + u + 2 < end) f.z = row[e0 + u + 2];
       }
-      x[4 * u] = f.x;
-      x[4 * u + 1] = f.y;
-      x[4 * u + 2] = f.z;
-      x[4 * u + 3] = f.w;
+      x[u] = f.x;
+      x[u + 1] = f.y;
+      x[u + 2] = f.z;
+      x[u + 3] = f.w;
     }
-    // flags: 4 bits per group
+    const int left = (int)max((int64_t)0, min((int64_t)kPerLane, end - e0));
+    const uint32_t valid = (1u << left) - 1u;
     uint32_t gt = 0, eq = 0;
 #pragma unroll
     for (int i = 0; i < kPerLane; ++i) {
-      const bool in = w0 + (i >> 2) * 128 + 4 * lane + (i & 3) < end;
-      gt |= (uint32_t)(in && (keep_all || x[i] > tau)) << i;
-      eq |= (uint32_t)(in && !keep_all && x[i] == tau) << i;
+      gt |= (uint32_t)(keep_all || x[i] > tau) << i;
+      eq |= (uint32_t)(x[i] == tau) << i;
     }
-    const int n_gt = __reduce_add_sync(kFullMask, __popc(gt)), n_eq = __reduce_add_sync(kFullMask, __popc(eq));
-    if (lane == 0) sh.wsum[wid] = (int64_t)n_gt + ((int64_t)n_eq << 32);
-    __syncthreads();
-    int64_t before = base;
+    gt &= valid;
+    eq = keep_all ? 0u : eq & valid;
+    // numbers before this lane: both in one word (a chunk holds 8192 scores)
+    int total;
+    const int p = block_prefix(__popc(gt) | __popc(eq) << 16, sh, &total);
+    if (__any_sync(kFullMask, gt | eq)) {
+      int g = n_gt + (p & 0xffff), q = n_eq + (p >> 16);
 #pragma unroll
-    for (int w = 0; w < kSelWarps; ++w) {
-      const int64_t s = sh.wsum[w];
-      if (w < wid) before += s;
-      base += s;
-    }
-    if (n_gt + n_eq) {
-#pragma unroll
-      for (int u = 0; u < kPerLane / 4; ++u) {
-        const uint32_t fg = (gt >> (4 * u)) & 15u, fe = (eq >> (4 * u)) & 15u;
-        if (__any_sync(kFullMask, fg | fe)) {
-          int64_t v = (int64_t)__popc(fg) + ((int64_t)__popc(fe) << 32), incl = v;
-#pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const int64_t y = __shfl_up_sync(kFullMask, incl, o);
-            if (lane >= o) incl += y;
-          }
-          int64_t p = before + incl - v;
-          before += __shfl_sync(kFullMask, incl, 31);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const bool g = (fg >> e) & 1u, q = (fe >> e) & 1u;
-            if (g || q) put(w0 + u * 128 + 4 * lane + e, x[4 * u + e], g, p & 0xffffffff, p >> 32);
-            p += (int64_t)g + ((int64_t)q << 32);
-          }
-        }
+      for (int i = 0; i < kPerLane; ++i) {
+        const bool is_gt = (gt >> i) & 1u, is_eq = (eq >> i) & 1u;
+        if (is_gt || is_eq) put(e0 + i, x[i], is_gt, g, q);
+        g += is_gt;
+        q += is_eq;
       }
     }
+    n_gt += total & 0xffff;
+    n_eq += total >> 16;
     __syncthreads();   // wsum is free again
   }
-  return base;
 }
 
 __global__ void __launch_bounds__(kSelThreads, 2)
@@ -219,84 +345,92 @@ __global__ void __launch_bounds__(kSelThreads, 2)
       for (int i = tid; i < k; i += kSelThreads) out[i] = i < n ? i : -1;
     return;
   }
+  if (ctas > 1) cluster_arrive();
   const float* row = scores + b * pitch;
   const bool keep_all = n <= kCap;
   float tau = 0.f;
   if (!keep_all) {
-    const int samples = n > 65536 ? 4096 : 1024;
-    for (int i = tid; i < samples; i += kSelThreads)
-      sh.gkey[i] = order_key(__ldcg(row + (int)((int64_t)i * n / samples)));
-    const float mu = (float)k * (float)samples / (float)n;
-    int rank_s = (int)(mu + 4.f * sqrtf(mu)) + 2;
-    if (rank_s > samples) rank_s = samples;
-    __syncthreads();
-    int64_t above;
-    tau = key_value(kth_largest([&](int64_t i) { return sh.gkey[i]; }, samples, rank_s, sh, &above));
+    int g = 1;
+    while (g < 64 && n / g > 65536) g *= 2;
+    const uint64_t step = ((uint64_t)n << 20) / (uint32_t)(kSelThreads * g);   // between samples, in 2^-20 scores
+    float best = -INFINITY;
+    for (int j0 = 0; j0 < g; j0 += 8) {
+      float x[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j0 + j < g) x[j] = __ldcg(row + (int)(((uint64_t)(tid + (j0 + j) * kSelThreads) * step) >> 20));
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j0 + j < g) best = fmaxf(best, x[j]);
+    }
+    const float mu = (float)k * (float)(kSelThreads * g) / (float)n;
+    int r = (int)(mu + 4.f * sqrtf(mu)) + 2;
+    if (r > kSelThreads) r = kSelThreads;
+    const uint32_t own[1] = {own_key(best)};
+    int unused;
+    tau = key_value(kth_largest_own(own, r, sh, &unused));
+    __syncthreads();   // sh.list and wsum are free again
   }
   const int64_t slice = ((((int64_t)n + ctas - 1) / ctas) + 3) & ~(int64_t)3;
   const int64_t begin = min((int64_t)n, rank * slice), end = min((int64_t)n, begin + slice);
-  const int64_t mine =
-      scan_slice(row, begin, end, keep_all, tau, sh, [&](int64_t pool, float x, bool gt, int64_t at, int64_t) {
-        if (gt && at < kCap) {
-          sh.key[at] = order_key(x);
-          sh.pool[at] = (int32_t)pool;
-        }
-      });
-  if (tid == 0) {
-    sh.count[0] = (int)(mine & 0xffffffff);
-    sh.count[1] = (int)(mine >> 32);
+  int n_gt, n_eq;
+  scan_slice(row, begin, end, keep_all, tau, sh, n_gt, n_eq, [&](int64_t pool, float x, bool gt, int at, int) {
+    if (gt && at < kCap) {
+      sh.key[at] = own_key(x);
+      sh.pool[at] = (int32_t)pool;
+    }
+  });
+  // the counts go to every CTA of the cluster
+  if (ctas > 1) cluster_wait();   // all of them run by now
+  if (tid < ctas) {
+    cluster_st_u32(cluster_map(smem_u32(&sh.n_gt[rank]), tid), (uint32_t)n_gt);
+    cluster_st_u32(cluster_map(smem_u32(&sh.n_eq[rank]), tid), (uint32_t)n_eq);
   }
   if (ctas > 1)
     cluster_sync();
   else
-    __syncthreads();
-  // everyone's counts: lane c (of every warp) holds CTA c's
-  const int lane = tid & 31, wid = tid >> 5;
-  int gt_c = 0, eq_c = 0;
-  if (lane < ctas) {
-    const float2 f = cluster_ld2(cluster_map(smem_u32(sh.count), lane));
-    gt_c = __float_as_int(f.x);
-    eq_c = __float_as_int(f.y);
-  }
+    __syncthreads();   // also: sh.key is complete
+  const int lane = tid & 31;
+  const int gt_c = lane < ctas ? sh.n_gt[lane] : 0, eq_c = lane < ctas ? sh.n_eq[lane] : 0;
   const int m = __reduce_add_sync(kFullMask, gt_c), ties = __reduce_add_sync(kFullMask, eq_c);
   const int gt_before = __reduce_add_sync(kFullMask, lane < rank ? gt_c : 0);
   const int eq_before = __reduce_add_sync(kFullMask, lane < rank ? eq_c : 0);
   if (m >= k && m <= kCap) {
-    if (rank == 0 && ctas > 1) {
-      // warp c fetches CTA c's candidates
-      const int from = __reduce_add_sync(kFullMask, lane < wid ? gt_c : 0);
-      const int cnt = __shfl_sync(kFullMask, gt_c, wid < ctas ? wid : 0);
-      if (wid < ctas) {
-        const uint32_t ks = cluster_map(smem_u32(sh.key), wid), ps = cluster_map(smem_u32(sh.pool), wid);
-        for (int i = lane; i < cnt; i += 32) {
-          sh.gkey[from + i] = cluster_ld_u32(ks + 4 * i);
-          sh.gpool[from + i] = (int32_t)cluster_ld_u32(ps + 4 * i);
-        }
+    if (ctas > 1) {
+      // the candidates go to the first CTA
+      const uint32_t ks = cluster_map(smem_u32(sh.gkey + gt_before), 0);
+      const uint32_t ps = cluster_map(smem_u32(sh.gpool + gt_before), 0);
+      for (int i = tid; i < n_gt; i += kSelThreads) {
+        cluster_st_u32(ks + 4 * i, sh.key[i]);
+        cluster_st_u32(ps + 4 * i, (uint32_t)sh.pool[i]);
       }
+      cluster_sync();
     }
-    if (ctas > 1) cluster_sync();   // the others may leave
     if (rank != 0) return;
     const uint32_t* gk = ctas > 1 ? sh.gkey : sh.key;
     const int32_t* gp = ctas > 1 ? sh.gpool : sh.pool;
-    int64_t above;
-    const uint32_t T = kth_largest([&](int64_t i) { return gk[i]; }, m, k, sh, &above);
-    write_selected([&](int64_t i) { return gk[i]; }, [&](int64_t i) { return gp[i]; }, m, T, k - above, sh, out);
+    constexpr int kOwn = kCap / kSelThreads;
+    uint32_t own[kOwn];
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) own[i] = tid + i * kSelThreads < m ? gk[tid + i * kSelThreads] : 0u;
+    int eq;
+    const uint32_t T = kth_largest_own(own, k, sh, &eq);
+    write_selected([&](int i) { return gk[i]; }, [&](int i) { return gp[i]; }, m, T, eq, sh, out);
     return;
   }
-  if (ctas > 1) cluster_sync();   // nobody's counts are read any more
   if (m < k && (int64_t)m + ties >= k) {
-    const int64_t need_eq = k - m;
-    scan_slice(row, begin, end, false, tau, sh, [&](int64_t pool, float, bool gt, int64_t g, int64_t e) {
-      const int64_t eq = eq_before + e;
-      if (gt || eq < need_eq) out[gt_before + g + (eq < need_eq ? eq : need_eq)] = (int32_t)pool;
+    const int need_eq = k - m;
+    scan_slice(row, begin, end, false, tau, sh, n_gt, n_eq, [&](int64_t pool, float, bool gt, int g, int e) {
+      const int eq = eq_before + e;
+      if (gt || eq < need_eq) out[gt_before + g + min(eq, need_eq)] = (int32_t)pool;
     });
     return;
   }
   if (rank != 0) return;
-  auto key = [&](int64_t i) { return order_key(__ldcg(row + i)); };
-  int64_t above;
-  const uint32_t T = kth_largest(key, n, k, sh, &above);
-  write_selected(key, [](int64_t i) { return i; }, n, T, k - above, sh, out);
+  auto key = [&](int i) { return order_key(__ldcg(row + i)); };
+  int eq;
+  const uint32_t T = kth_largest(key, n, k, sh, &eq);
+  write_selected(key, [](int i) { return i; }, n, T, eq, sh, out);
 }
 
 cudaError_t launch_decode_topk(const PagedView& pv, int64_t batch, int k, const float* scores, int64_t pitch,
