@@ -16,6 +16,17 @@ from dataclasses import dataclass, field
 
 import long_context_sparse_dsa_gb300 as _dsa
 
+torch = _DTYPES = None   # set by _need_torch(): importing the package (to build it, say) does not need torch
+
+
+def _need_torch():
+    """Every call of this module needs an object made by one of the functions that call this."""
+    global torch, _DTYPES
+    if torch is None:
+        import torch as t
+        _DTYPES = {_dsa.DSA_FP32: t.float32, _dsa.DSA_BF16: t.bfloat16}
+        torch = t
+
 
 class _CCache(ctypes.Structure):
     """Mirror of ``dsa_paged_cache``."""
@@ -43,6 +54,7 @@ class PagedCache:
     _c: object = field(init=False, repr=False)
 
     def __post_init__(self):
+        _need_torch()
         given = [t for t in (self.k, self.v, self.kpool, self.ktail) if t is not None]
         if not given or (self.k is None and self.kpool is None):
             raise ValueError("a paged cache has k and v, or kpool, or all of k, v, kpool and ktail")
@@ -64,15 +76,20 @@ class PagedCache:
         put = object.__setattr__
         put(self, "pages", int(first.shape[0]))
         put(self, "page_size", int(page))
+        put(self, "_device", first.get_device())
+        put(self, "_dtype", first.dtype)
+        put(self, "_d", None if self.k is None else int(self.k.shape[2]))
+        put(self, "_di", None if self.kpool is None else int(self.kpool.shape[2]))
         put(self, "_c", _CCache(_dsa._ptr(self.k), _dsa._ptr(self.v), _dsa._ptr(self.kpool), _dsa._ptr(self.ktail),
                                 self.pages, self.page_size))
+        put(self, "_ref", ctypes.byref(self._c))
 
 
 def alloc_paged_cache(dims, pages: int, page_size: int = 64, device="cuda") -> PagedCache:
     """Uninitialised arrays of a cache of `pages` pages for the layer `dims` (nothing in them needs a value)."""
-    import torch
+    _need_torch()
     _dsa._check(validate_decode_dims(dims), "dsa_validate_decode_dims")
-    dt = _dtype(dims)
+    dt = _DTYPES[dims.dtype]
     e = lambda *shape: torch.empty(shape, dtype=dt, device=device)
     return PagedCache(k=e(pages, page_size, dims.d), v=e(pages, page_size, dims.d),
                       kpool=e(pages, page_size // 4, dims.di), ktail=e(pages, 3, dims.di))
@@ -85,12 +102,13 @@ class Rotation:
         self.turns = turns
         self.dim = 2 * turns.numel()
         self._c = _CRotation(turns.data_ptr(), self.dim, int(bool(interleaved)))
+        self._ref = ctypes.byref(self._c)
 
 
 def make_rotation(freq, interleaved: bool = False, device="cuda") -> Rotation:
     """freq: the pairs' frequencies in radians per position, e.g. ``base ** (-arange(0, dim, 2) / dim)``, as a float64
     tensor or a sequence of numbers.  Pair i is channels (i, i + dim/2), or (2i, 2i+1) when interleaved."""
-    import torch
+    _need_torch()
     values = [float(f) for f in (freq.tolist() if hasattr(freq, "tolist") else freq)]
     if not values or len(values) % 8 or not all(math.isfinite(f) for f in values):
         raise ValueError("a rotation has a multiple of 8 finite frequencies")
@@ -100,53 +118,58 @@ def make_rotation(freq, interleaved: bool = False, device="cuda") -> Rotation:
     return Rotation(torch.tensor(turns, dtype=torch.int64, device=device), interleaved)
 
 
-def _dtype(dims):
-    import torch
-    return torch.bfloat16 if dims.dtype == _dsa.DSA_BF16 else torch.float32
+def _shape_error(func, name, t, dtype, shape, device):
+    return ValueError(f"{func}: {name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{device} "
+                      f"(got {t.dtype}, {tuple(t.shape)}, {t.device}, {'' if t.is_contiguous() else 'not '}contiguous)")
 
 
 class _Args:
-    """Checks of one call's tensors: on the cache's device, which has to be the current one."""
+    """Checks of one call's tensors: on the cache's device, which has to be the current one.  A decode step makes these
+    calls for every token, so the checks are kept to a few attribute reads per tensor."""
+    __slots__ = ("func", "dims", "dt", "device", "batch")
 
     def __init__(self, func, dims, cache):
-        import torch
-        self.func, self.dims, self.torch = func, dims, torch
-        self.dt = _dtype(dims)
-        self.device = (cache.k if cache.k is not None else cache.kpool).device
-        if self.device.index != torch.cuda.current_device():
-            raise ValueError(f"{func}: the cache is on {self.device}, not on the current device")
-        if (cache.k if cache.k is not None else cache.kpool).dtype != self.dt:
+        self.func, self.dims = func, dims
+        self.dt = _DTYPES[dims.dtype]
+        self.device = cache._device
+        if self.device != torch.cuda.current_device():
+            raise ValueError(f"{func}: the cache is on cuda:{self.device}, not on the current device")
+        if cache._dtype is not self.dt:
             raise ValueError(f"{func}: the cache is not of the layer's dtype")
-        if cache.k is not None and cache.k.shape[2] != dims.d:
-            raise ValueError(f"{func}: the cache's k and v have {cache.k.shape[2]} channels, not d = {dims.d}")
-        if cache.kpool is not None and cache.kpool.shape[2] != dims.di:
-            raise ValueError(f"{func}: the cache's kpool has {cache.kpool.shape[2]} channels, not di = {dims.di}")
+        if cache._d is not None and cache._d != dims.d:
+            raise ValueError(f"{func}: the cache's k and v have {cache._d} channels, not d = {dims.d}")
+        if cache._di is not None and cache._di != dims.di:
+            raise ValueError(f"{func}: the cache's kpool has {cache._di} channels, not di = {dims.di}")
 
-    def ptr(self, name, t, dtype, *shape):
-        if t.dtype != dtype or t.shape != shape or t.device != self.device or not t.is_contiguous():
-            raise ValueError(f"{self.func}: {name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on "
-                             f"{self.device} (got {t.dtype}, {tuple(t.shape)}, {t.device})")
-        return t.data_ptr()
+    def ptr(self, name, t, dtype, shape):
+        if t.dtype is dtype and t.shape == shape and t.get_device() == self.device and t.is_contiguous():
+            return t.data_ptr()
+        raise _shape_error(self.func, name, t, dtype, shape, self.device)
 
     def rows(self, cache, lens, block_table):
-        """(batch, lens, block table)"""
-        i32, batch = self.torch.int32, lens.numel()
-        return (batch, self.ptr("lens", lens, i32, batch),
-                self.ptr("block_table", block_table, i32, batch, -(-self.dims.L // cache.page_size)))
+        """(lens, block table)"""
+        self.batch = batch = lens.numel()
+        return (self.ptr("lens", lens, torch.int32, (batch,)),
+                self.ptr("block_table", block_table, torch.int32, (batch, -(-self.dims.L // cache.page_size))))
 
     def workspace(self, ws):
         if ws is None:
             return None, 0
-        if ws.device != self.device or not ws.is_contiguous():
-            raise ValueError(f"{self.func}: ws must be a contiguous tensor on {self.device}")
+        if ws.get_device() != self.device or not ws.is_contiguous():
+            raise ValueError(f"{self.func}: ws must be a contiguous tensor on cuda:{self.device}")
         return ws.data_ptr(), ws.numel() * ws.element_size()
 
     def rotation(self, rotation):
         if rotation is None:
             return None
-        if rotation.turns.device != self.device:
-            raise ValueError(f"{self.func}: the rotation is on {rotation.turns.device}, not on {self.device}")
-        return ctypes.byref(rotation._c)
+        if rotation.turns.get_device() != self.device:
+            raise ValueError(f"{self.func}: the rotation is on {rotation.turns.device}, not on cuda:{self.device}")
+        return rotation._ref
+
+    def stream(self, stream):
+        if stream is None:   # what torch.cuda.current_stream().cuda_stream gives, without a Stream object per call
+            return torch._C._cuda_getCurrentRawStream(self.device)
+        return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
 
 
 def validate_decode_dims(dims) -> int:
@@ -159,7 +182,7 @@ def decode_workspace_bytes(dims, batch: int) -> int:
 
 def alloc_decode_workspace(dims, batch: int, device="cuda"):
     """Scratch of the decode calls for up to `batch` rows; calls that may overlap on the GPU need one each."""
-    import torch
+    _need_torch()
     n = decode_workspace_bytes(dims, batch)
     if n == 0:
         _dsa._check(validate_decode_dims(dims), "dsa_decode_workspace_bytes")
@@ -173,60 +196,68 @@ def cache_append(dims, cache, lens, block_table, k, v, k_idx, offsets=None, rota
     [batch + 1] int32 rows offsets[b] .. offsets[b+1]-1 of k, v, k_idx (q) are row b's.  With a rotation, k enters the
     cache rotated to its position (and goes to k_out), and q goes to q_out rotated."""
     a = _Args("cache_append", dims, cache)
-    batch, pl, pt = a.rows(cache, lens, block_table)
-    n, dt = k.shape[0], a.dt
+    pl, pt = a.rows(cache, lens, block_table)
+    n, dt, ptr = k.shape[0], a.dt, a.ptr
     pq = pqo = pko = po = None
     if offsets is not None:
-        po = a.ptr("offsets", offsets, a.torch.int32, batch + 1)
+        po = ptr("offsets", offsets, torch.int32, (a.batch + 1,))
     if q is not None:
-        pq = a.ptr("q", q, dt, n, dims.Hq, dims.d)
+        pq = ptr("q", q, dt, (n, dims.Hq, dims.d))
     if q_out is not None:
-        pqo = a.ptr("q_out", q_out, dt, n, dims.Hq, dims.d)
+        pqo = ptr("q_out", q_out, dt, (n, dims.Hq, dims.d))
     if k_out is not None:
-        pko = a.ptr("k_out", k_out, dt, n, dims.d)
-    _dsa._check(_dsa._load().dsa_cache_append(
-        ctypes.byref(dims), ctypes.byref(cache._c), batch, pl, pt, n, po, a.ptr("k", k, dt, n, dims.d),
-        a.ptr("v", v, dt, n, dims.d), a.ptr("k_idx", k_idx, dt, n, dims.di), a.rotation(rotation), pq, pqo, pko,
-        _dsa._stream(stream)), "dsa_cache_append")
+        pko = ptr("k_out", k_out, dt, (n, dims.d))
+    st = _dsa._load().dsa_cache_append(
+        ctypes.byref(dims), cache._ref, a.batch, pl, pt, n, po, ptr("k", k, dt, (n, dims.d)), ptr("v", v, dt, (n, dims.d)),
+        ptr("k_idx", k_idx, dt, (n, dims.di)), a.rotation(rotation), pq, pqo, pko, a.stream(stream))
+    if st:
+        _dsa._check(st, "dsa_cache_append")
 
 
 def decode_indexer_topk(dims, cache, lens, block_table, q_idx, w, idx, ws, stream=None):
     """The min(k, lens[b] // 4) best complete pools of every row, ascending, then -1, into idx [batch, k] int32."""
     a = _Args("decode_indexer_topk", dims, cache)
-    batch, pl, pt = a.rows(cache, lens, block_table)
+    pl, pt = a.rows(cache, lens, block_table)
     pw, nw = a.workspace(ws)
-    _dsa._check(_dsa._load().dsa_decode_indexer_topk(
-        ctypes.byref(dims), ctypes.byref(cache._c), batch, pl, pt, a.ptr("q_idx", q_idx, a.dt, batch, dims.Hi, dims.di),
-        a.ptr("w", w, a.torch.float32, batch, dims.Hi), a.ptr("idx", idx, a.torch.int32, batch, dims.k), pw, nw,
-        _dsa._stream(stream)), "dsa_decode_indexer_topk")
+    batch, ptr = a.batch, a.ptr
+    st = _dsa._load().dsa_decode_indexer_topk(
+        ctypes.byref(dims), cache._ref, batch, pl, pt, ptr("q_idx", q_idx, a.dt, (batch, dims.Hi, dims.di)),
+        ptr("w", w, torch.float32, (batch, dims.Hi)), ptr("idx", idx, torch.int32, (batch, dims.k)), pw, nw,
+        a.stream(stream))
+    if st:
+        _dsa._check(st, "dsa_decode_indexer_topk")
 
 
 def decode_attn(dims, cache, lens, block_table, q, o, lse, ws, idx=None, stream=None):
     """Attention of one query per row: over the pools of idx [batch, k] and the row's partial pool, or, without idx, over
     all of the row's tokens.  o [batch, Hq, d], lse [batch, Hq] fp32."""
     a = _Args("decode_attn", dims, cache)
-    batch, pl, pt = a.rows(cache, lens, block_table)
+    pl, pt = a.rows(cache, lens, block_table)
     pw, nw = a.workspace(ws)
-    _dsa._check(_dsa._load().dsa_decode_attn(
-        ctypes.byref(dims), ctypes.byref(cache._c), batch, pl, pt,
-        None if idx is None else a.ptr("idx", idx, a.torch.int32, batch, dims.k),
-        a.ptr("q", q, a.dt, batch, dims.Hq, dims.d), a.ptr("o", o, a.dt, batch, dims.Hq, dims.d),
-        a.ptr("lse", lse, a.torch.float32, batch, dims.Hq), pw, nw, _dsa._stream(stream)), "dsa_decode_attn")
+    batch, ptr, heads = a.batch, a.ptr, (a.batch, dims.Hq, dims.d)
+    st = _dsa._load().dsa_decode_attn(
+        ctypes.byref(dims), cache._ref, batch, pl, pt,
+        None if idx is None else ptr("idx", idx, torch.int32, (batch, dims.k)), ptr("q", q, a.dt, heads),
+        ptr("o", o, a.dt, heads), ptr("lse", lse, torch.float32, (batch, dims.Hq)), pw, nw, a.stream(stream))
+    if st:
+        _dsa._check(st, "dsa_decode_attn")
 
 
 def decode_step(dims, cache, lens, block_table, q, k, v, q_idx, k_idx, w, o, lse, idx, ws, rotation=None, stream=None):
     """One decode step: append one token per row, select its pools (idx), attend to them (o, lse)."""
     a = _Args("decode_step", dims, cache)
-    batch, pl, pt = a.rows(cache, lens, block_table)
+    pl, pt = a.rows(cache, lens, block_table)
     pw, nw = a.workspace(ws)
-    dt, f32 = a.dt, a.torch.float32
-    _dsa._check(_dsa._load().dsa_decode_step(
-        ctypes.byref(dims), ctypes.byref(cache._c), batch, pl, pt, a.ptr("q", q, dt, batch, dims.Hq, dims.d),
-        a.ptr("k", k, dt, batch, dims.d), a.ptr("v", v, dt, batch, dims.d),
-        a.ptr("q_idx", q_idx, dt, batch, dims.Hi, dims.di), a.ptr("k_idx", k_idx, dt, batch, dims.di),
-        a.ptr("w", w, f32, batch, dims.Hi), a.rotation(rotation), a.ptr("o", o, dt, batch, dims.Hq, dims.d),
-        a.ptr("lse", lse, f32, batch, dims.Hq), a.ptr("idx", idx, a.torch.int32, batch, dims.k), pw, nw,
-        _dsa._stream(stream)), "dsa_decode_step")
+    batch, ptr, dt, f32 = a.batch, a.ptr, a.dt, torch.float32
+    heads, token = (batch, dims.Hq, dims.d), (batch, dims.d)
+    st = _dsa._load().dsa_decode_step(
+        ctypes.byref(dims), cache._ref, batch, pl, pt, ptr("q", q, dt, heads), ptr("k", k, dt, token),
+        ptr("v", v, dt, token), ptr("q_idx", q_idx, dt, (batch, dims.Hi, dims.di)),
+        ptr("k_idx", k_idx, dt, (batch, dims.di)), ptr("w", w, f32, (batch, dims.Hi)), a.rotation(rotation),
+        ptr("o", o, dt, heads), ptr("lse", lse, f32, (batch, dims.Hq)), ptr("idx", idx, torch.int32, (batch, dims.k)),
+        pw, nw, a.stream(stream))
+    if st:
+        _dsa._check(st, "dsa_decode_step")
 
 
 def _signatures(D):
