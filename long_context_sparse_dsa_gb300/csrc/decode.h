@@ -3,6 +3,7 @@
 // called.
 #pragma once
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <cuda_runtime.h>
@@ -35,6 +36,23 @@ inline PagedView make_paged_view(const int32_t* lens, const int32_t* table, int6
   v.div_mul = (uint32_t)(((uint64_t)1 << (29 + s)) / (uint64_t)v.ppp + 1);
   v.div_shift = 29 + s;
   return v;
+}
+
+// Sets a kernel's dynamic shared memory limit (and, for clusters above 8, the
+// permission) the first time it is launched on a device: each such call costs
+// a launch about half a microsecond of host time.  `done` is the kernel's own
+// flag word, one bit per device.
+template <typename K>
+inline cudaError_t prepare_kernel(K* kern, int smem, bool big_clusters, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? (uint64_t)1 << dev : 0;
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess && big_clusters) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
 }
 
 // Launches `kern` so that it may become resident before its predecessor on

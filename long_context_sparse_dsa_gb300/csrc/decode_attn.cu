@@ -1057,13 +1057,14 @@ static cudaError_t launch_all(const DecodeAttnArgs& g, const AttnArgs<T>& a, cud
   if (a.idx) {
     auto kern = decode_attn_selected_kernel<T, D, MAXH>;
     const unsigned splits = selected_splits(a.batch, (a.k + 4) >> 2, P::MIN_STEPS, kSms * P::CTAS);
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e == cudaSuccess && splits > 8) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = prepare_kernel(kern, P::smem(MAXH), true, done);
     if (e != cudaSuccess) return e;
     return launch_chained_cluster(splits, kern, dim3(splits, (unsigned)a.batch), dim3(kAttnThreads), smem, s, a);
   }
   auto kern = decode_attn_all_kernel<T, D, MAXH>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = prepare_kernel(kern, P::smem(MAXH), false, done);
   if (e != cudaSuccess) return e;
   // as many CTAs as can have work
   const int64_t row_max = ((int64_t)a.pv.capacity + 15) >> 4;

@@ -440,10 +440,8 @@ cudaError_t launch_decode_topk(const PagedView& pv, int64_t batch, int k, const 
   const int64_t most = ((int64_t)pv.capacity / 4 + 2047) / 2048;
   if (c > most) c = most;
   const unsigned ctas = c >= 16 ? 16 : c > 8 ? 8 : c < 1 ? 1 : (unsigned)c;
-  cudaError_t e = cudaFuncSetAttribute(decode_topk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)sizeof(SelShared));
-  if (e == cudaSuccess && ctas > 8)
-    e = cudaFuncSetAttribute(decode_topk_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = prepare_kernel(decode_topk_kernel, (int)sizeof(SelShared), true, done);
   if (e != cudaSuccess) return e;
   return launch_chained_cluster(ctas, decode_topk_kernel, dim3(ctas, (unsigned)batch), dim3(kSelThreads),
                                 sizeof(SelShared), s, pv, scores, pitch, k, idx);

@@ -118,58 +118,36 @@ def make_rotation(freq, interleaved: bool = False, device="cuda") -> Rotation:
     return Rotation(torch.tensor(turns, dtype=torch.int64, device=device), interleaved)
 
 
-def _shape_error(func, name, t, dtype, shape, device):
-    return ValueError(f"{func}: {name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{device} "
-                      f"(got {t.dtype}, {tuple(t.shape)}, {t.device}, {'' if t.is_contiguous() else 'not '}contiguous)")
+# A decoder makes these calls for every token, so each checks its tensors in one plain condition (a few attribute
+# reads per tensor) and only looks for what is wrong when it fails.
 
 
-class _Args:
-    """Checks of one call's tensors: on the cache's device, which has to be the current one.  A decode step makes these
-    calls for every token, so the checks are kept to a few attribute reads per tensor."""
-    __slots__ = ("func", "dims", "dt", "device", "batch")
+def _refuse(func, dims, cache, *specs):
+    """Raise for the first of `specs` (name, tensor, dtype, shape) that is not what the call takes."""
+    device = cache._device
+    if device != torch.cuda.current_device():
+        raise ValueError(f"{func}: the cache is on cuda:{device}, not on the current device")
+    if cache._dtype is not _DTYPES[dims.dtype]:
+        raise ValueError(f"{func}: the cache is not of the layer's dtype")
+    if cache._d not in (None, dims.d) or cache._di not in (None, dims.di):
+        raise ValueError(f"{func}: the cache is of d = {cache._d}, di = {cache._di}, the layer of {dims.d}, {dims.di}")
+    for name, t, dtype, shape in specs:
+        if t is not None and (t.get_device() != device or not t.is_contiguous() or
+                              dtype is not None and (t.dtype is not dtype or t.shape != shape)):
+            raise ValueError(f"{func}: {name} must be a contiguous {dtype or 'tensor'} of shape {shape} on cuda:{device} "
+                             f"(got {t.dtype}, {tuple(t.shape)}, strides {t.stride()}, {t.device})")
+    raise ValueError(f"{func}: unusable arguments")
 
-    def __init__(self, func, dims, cache):
-        self.func, self.dims = func, dims
-        self.dt = _DTYPES[dims.dtype]
-        self.device = cache._device
-        if self.device != torch.cuda.current_device():
-            raise ValueError(f"{func}: the cache is on cuda:{self.device}, not on the current device")
-        if cache._dtype is not self.dt:
-            raise ValueError(f"{func}: the cache is not of the layer's dtype")
-        if cache._d is not None and cache._d != dims.d:
-            raise ValueError(f"{func}: the cache's k and v have {cache._d} channels, not d = {dims.d}")
-        if cache._di is not None and cache._di != dims.di:
-            raise ValueError(f"{func}: the cache's kpool has {cache._di} channels, not di = {dims.di}")
 
-    def ptr(self, name, t, dtype, shape):
-        if t.dtype is dtype and t.shape == shape and t.get_device() == self.device and t.is_contiguous():
-            return t.data_ptr()
-        raise _shape_error(self.func, name, t, dtype, shape, self.device)
+def _cache_ok(dims, cache, dt):
+    return (cache._device == torch.cuda.current_device() and cache._dtype is dt and
+            (cache._d is None or cache._d == dims.d) and (cache._di is None or cache._di == dims.di))
 
-    def rows(self, cache, lens, block_table):
-        """(lens, block table)"""
-        self.batch = batch = lens.numel()
-        return (self.ptr("lens", lens, torch.int32, (batch,)),
-                self.ptr("block_table", block_table, torch.int32, (batch, -(-self.dims.L // cache.page_size))))
 
-    def workspace(self, ws):
-        if ws is None:
-            return None, 0
-        if ws.get_device() != self.device or not ws.is_contiguous():
-            raise ValueError(f"{self.func}: ws must be a contiguous tensor on cuda:{self.device}")
-        return ws.data_ptr(), ws.numel() * ws.element_size()
-
-    def rotation(self, rotation):
-        if rotation is None:
-            return None
-        if rotation.turns.get_device() != self.device:
-            raise ValueError(f"{self.func}: the rotation is on {rotation.turns.device}, not on cuda:{self.device}")
-        return rotation._ref
-
-    def stream(self, stream):
-        if stream is None:   # what torch.cuda.current_stream().cuda_stream gives, without a Stream object per call
-            return torch._C._cuda_getCurrentRawStream(self.device)
-        return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
+def _raw_stream(stream, device):
+    if stream is None:   # what torch.cuda.current_stream().cuda_stream gives, without a Stream object per call
+        return torch._C._cuda_getCurrentRawStream(device)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
 
 
 def validate_decode_dims(dims) -> int:
@@ -195,35 +173,69 @@ def cache_append(dims, cache, lens, block_table, k, v, k_idx, offsets=None, rota
     """New tokens into the cache; lens [batch] int32 count them.  Without offsets one token per row, with offsets
     [batch + 1] int32 rows offsets[b] .. offsets[b+1]-1 of k, v, k_idx (q) are row b's.  With a rotation, k enters the
     cache rotated to its position (and goes to k_out), and q goes to q_out rotated."""
-    a = _Args("cache_append", dims, cache)
-    pl, pt = a.rows(cache, lens, block_table)
-    n, dt, ptr = k.shape[0], a.dt, a.ptr
-    pq = pqo = pko = po = None
+    dt, i32, dev = _DTYPES[dims.dtype], torch.int32, cache._device
+    batch, n, d = lens.numel(), k.shape[0], dims.d
+    cols = -(-dims.L // cache.page_size)
+    row, index = (n, d), (n, dims.di)
+    ok = (_cache_ok(dims, cache, dt) and
+          lens.dtype is i32 and lens.shape == (batch,) and lens.get_device() == dev and lens.is_contiguous() and
+          block_table.dtype is i32 and block_table.shape == (batch, cols) and block_table.get_device() == dev and
+          block_table.is_contiguous() and
+          k.dtype is dt and k.shape == row and k.get_device() == dev and k.is_contiguous() and
+          v.dtype is dt and v.shape == row and v.get_device() == dev and v.is_contiguous() and
+          k_idx.dtype is dt and k_idx.shape == index and k_idx.get_device() == dev and k_idx.is_contiguous())
+    po = pr = pq = pqo = pko = None
     if offsets is not None:
-        po = ptr("offsets", offsets, torch.int32, (a.batch + 1,))
+        ok = (ok and offsets.dtype is i32 and offsets.shape == (batch + 1,) and offsets.get_device() == dev and
+              offsets.is_contiguous())
+        po = offsets.data_ptr()
+    if rotation is not None:
+        ok = ok and rotation.turns.get_device() == dev
+        pr = rotation._ref
     if q is not None:
-        pq = ptr("q", q, dt, (n, dims.Hq, dims.d))
+        heads = (n, dims.Hq, d)
+        ok = ok and q.dtype is dt and q.shape == heads and q.get_device() == dev and q.is_contiguous()
+        pq = q.data_ptr()
     if q_out is not None:
-        pqo = ptr("q_out", q_out, dt, (n, dims.Hq, dims.d))
+        heads = (n, dims.Hq, d)
+        ok = ok and q_out.dtype is dt and q_out.shape == heads and q_out.get_device() == dev and q_out.is_contiguous()
+        pqo = q_out.data_ptr()
     if k_out is not None:
-        pko = ptr("k_out", k_out, dt, (n, dims.d))
+        ok = ok and k_out.dtype is dt and k_out.shape == row and k_out.get_device() == dev and k_out.is_contiguous()
+        pko = k_out.data_ptr()
+    if not ok:
+        heads = (n, dims.Hq, d)
+        _refuse("cache_append", dims, cache, ("lens", lens, i32, (batch,)), ("block_table", block_table, i32, (batch, cols)),
+                ("k", k, dt, row), ("v", v, dt, row), ("k_idx", k_idx, dt, index), ("offsets", offsets, i32, (batch + 1,)),
+                ("q", q, dt, heads), ("q_out", q_out, dt, heads), ("k_out", k_out, dt, row),
+                ("the rotation", None if rotation is None else rotation.turns, None, None))
     st = _dsa._load().dsa_cache_append(
-        ctypes.byref(dims), cache._ref, a.batch, pl, pt, n, po, ptr("k", k, dt, (n, dims.d)), ptr("v", v, dt, (n, dims.d)),
-        ptr("k_idx", k_idx, dt, (n, dims.di)), a.rotation(rotation), pq, pqo, pko, a.stream(stream))
+        ctypes.byref(dims), cache._ref, batch, lens.data_ptr(), block_table.data_ptr(), n, po, k.data_ptr(), v.data_ptr(),
+        k_idx.data_ptr(), pr, pq, pqo, pko, _raw_stream(stream, dev))
     if st:
         _dsa._check(st, "dsa_cache_append")
 
 
 def decode_indexer_topk(dims, cache, lens, block_table, q_idx, w, idx, ws, stream=None):
     """The min(k, lens[b] // 4) best complete pools of every row, ascending, then -1, into idx [batch, k] int32."""
-    a = _Args("decode_indexer_topk", dims, cache)
-    pl, pt = a.rows(cache, lens, block_table)
-    pw, nw = a.workspace(ws)
-    batch, ptr = a.batch, a.ptr
+    dt, i32, f32, dev, batch = _DTYPES[dims.dtype], torch.int32, torch.float32, cache._device, lens.numel()
+    cols = -(-dims.L // cache.page_size)
+    queries, weights, chosen = (batch, dims.Hi, dims.di), (batch, dims.Hi), (batch, dims.k)
+    if not (_cache_ok(dims, cache, dt) and
+            lens.dtype is i32 and lens.shape == (batch,) and lens.get_device() == dev and lens.is_contiguous() and
+            block_table.dtype is i32 and block_table.shape == (batch, cols) and block_table.get_device() == dev and
+            block_table.is_contiguous() and
+            q_idx.dtype is dt and q_idx.shape == queries and q_idx.get_device() == dev and q_idx.is_contiguous() and
+            w.dtype is f32 and w.shape == weights and w.get_device() == dev and w.is_contiguous() and
+            idx.dtype is i32 and idx.shape == chosen and idx.get_device() == dev and idx.is_contiguous() and
+            (ws is None or ws.get_device() == dev and ws.is_contiguous())):
+        _refuse("decode_indexer_topk", dims, cache, ("lens", lens, i32, (batch,)),
+                ("block_table", block_table, i32, (batch, cols)), ("q_idx", q_idx, dt, queries), ("w", w, f32, weights),
+                ("idx", idx, i32, chosen), ("ws", ws, None, None))
+    pw, nw = (None, 0) if ws is None else (ws.data_ptr(), ws.nbytes)
     st = _dsa._load().dsa_decode_indexer_topk(
-        ctypes.byref(dims), cache._ref, batch, pl, pt, ptr("q_idx", q_idx, a.dt, (batch, dims.Hi, dims.di)),
-        ptr("w", w, torch.float32, (batch, dims.Hi)), ptr("idx", idx, torch.int32, (batch, dims.k)), pw, nw,
-        a.stream(stream))
+        ctypes.byref(dims), cache._ref, batch, lens.data_ptr(), block_table.data_ptr(), q_idx.data_ptr(), w.data_ptr(),
+        idx.data_ptr(), pw, nw, _raw_stream(stream, dev))
     if st:
         _dsa._check(st, "dsa_decode_indexer_topk")
 
@@ -231,31 +243,53 @@ def decode_indexer_topk(dims, cache, lens, block_table, q_idx, w, idx, ws, strea
 def decode_attn(dims, cache, lens, block_table, q, o, lse, ws, idx=None, stream=None):
     """Attention of one query per row: over the pools of idx [batch, k] and the row's partial pool, or, without idx, over
     all of the row's tokens.  o [batch, Hq, d], lse [batch, Hq] fp32."""
-    a = _Args("decode_attn", dims, cache)
-    pl, pt = a.rows(cache, lens, block_table)
-    pw, nw = a.workspace(ws)
-    batch, ptr, heads = a.batch, a.ptr, (a.batch, dims.Hq, dims.d)
+    dt, i32, f32, dev, batch = _DTYPES[dims.dtype], torch.int32, torch.float32, cache._device, lens.numel()
+    cols, heads = -(-dims.L // cache.page_size), (batch, dims.Hq, dims.d)
+    if not (_cache_ok(dims, cache, dt) and
+            lens.dtype is i32 and lens.shape == (batch,) and lens.get_device() == dev and lens.is_contiguous() and
+            block_table.dtype is i32 and block_table.shape == (batch, cols) and block_table.get_device() == dev and
+            block_table.is_contiguous() and
+            (idx is None or idx.dtype is i32 and idx.shape == (batch, dims.k) and idx.get_device() == dev and
+             idx.is_contiguous()) and
+            q.dtype is dt and q.shape == heads and q.get_device() == dev and q.is_contiguous() and
+            o.dtype is dt and o.shape == heads and o.get_device() == dev and o.is_contiguous() and
+            lse.dtype is f32 and lse.shape == heads[:2] and lse.get_device() == dev and lse.is_contiguous() and
+            (ws is None or ws.get_device() == dev and ws.is_contiguous())):
+        _refuse("decode_attn", dims, cache, ("lens", lens, i32, (batch,)), ("block_table", block_table, i32, (batch, cols)),
+                ("idx", idx, i32, (batch, dims.k)), ("q", q, dt, heads), ("o", o, dt, heads), ("lse", lse, f32, heads[:2]),
+                ("ws", ws, None, None))
+    pw, nw = (None, 0) if ws is None else (ws.data_ptr(), ws.nbytes)
     st = _dsa._load().dsa_decode_attn(
-        ctypes.byref(dims), cache._ref, batch, pl, pt,
-        None if idx is None else ptr("idx", idx, torch.int32, (batch, dims.k)), ptr("q", q, a.dt, heads),
-        ptr("o", o, a.dt, heads), ptr("lse", lse, torch.float32, (batch, dims.Hq)), pw, nw, a.stream(stream))
+        ctypes.byref(dims), cache._ref, batch, lens.data_ptr(), block_table.data_ptr(),
+        None if idx is None else idx.data_ptr(), q.data_ptr(), o.data_ptr(), lse.data_ptr(), pw, nw,
+        _raw_stream(stream, dev))
     if st:
         _dsa._check(st, "dsa_decode_attn")
 
 
 def decode_step(dims, cache, lens, block_table, q, k, v, q_idx, k_idx, w, o, lse, idx, ws, rotation=None, stream=None):
     """One decode step: append one token per row, select its pools (idx), attend to them (o, lse)."""
-    a = _Args("decode_step", dims, cache)
-    pl, pt = a.rows(cache, lens, block_table)
-    pw, nw = a.workspace(ws)
-    batch, ptr, dt, f32 = a.batch, a.ptr, a.dt, torch.float32
-    heads, token = (batch, dims.Hq, dims.d), (batch, dims.d)
+    dt, i32, f32, dev, batch = _DTYPES[dims.dtype], torch.int32, torch.float32, cache._device, lens.numel()
+    specs = (("lens", lens, i32, (batch,)), ("block_table", block_table, i32, (batch, -(-dims.L // cache.page_size))),
+             ("q", q, dt, (batch, dims.Hq, dims.d)), ("k", k, dt, (batch, dims.d)), ("v", v, dt, (batch, dims.d)),
+             ("q_idx", q_idx, dt, (batch, dims.Hi, dims.di)), ("k_idx", k_idx, dt, (batch, dims.di)),
+             ("w", w, f32, (batch, dims.Hi)), ("o", o, dt, (batch, dims.Hq, dims.d)), ("lse", lse, f32, (batch, dims.Hq)),
+             ("idx", idx, i32, (batch, dims.k)))
+    ok = _cache_ok(dims, cache, dt)
+    for _, t, dtype, shape in specs:
+        ok = ok and t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous()
+    pr = None
+    if rotation is not None:
+        ok = ok and rotation.turns.get_device() == dev
+        pr = rotation._ref
+    if not ok or ws is not None and not (ws.get_device() == dev and ws.is_contiguous()):
+        _refuse("decode_step", dims, cache, *specs, ("ws", ws, None, None),
+                ("the rotation", None if rotation is None else rotation.turns, None, None))
+    pw, nw = (None, 0) if ws is None else (ws.data_ptr(), ws.nbytes)
     st = _dsa._load().dsa_decode_step(
-        ctypes.byref(dims), cache._ref, batch, pl, pt, ptr("q", q, dt, heads), ptr("k", k, dt, token),
-        ptr("v", v, dt, token), ptr("q_idx", q_idx, dt, (batch, dims.Hi, dims.di)),
-        ptr("k_idx", k_idx, dt, (batch, dims.di)), ptr("w", w, f32, (batch, dims.Hi)), a.rotation(rotation),
-        ptr("o", o, dt, heads), ptr("lse", lse, f32, (batch, dims.Hq)), ptr("idx", idx, torch.int32, (batch, dims.k)),
-        pw, nw, a.stream(stream))
+        ctypes.byref(dims), cache._ref, batch, lens.data_ptr(), block_table.data_ptr(), q.data_ptr(), k.data_ptr(),
+        v.data_ptr(), q_idx.data_ptr(), k_idx.data_ptr(), w.data_ptr(), pr, o.data_ptr(), lse.data_ptr(),
+        idx.data_ptr(), pw, nw, _raw_stream(stream, dev))
     if st:
         _dsa._check(st, "dsa_decode_step")
 
