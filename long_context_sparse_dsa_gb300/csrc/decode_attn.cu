@@ -117,7 +117,7 @@ __device__ __forceinline__ void slot_pool_rows(const SlotRow& r, int i, int raw,
 // kRowPad of its steps take, so each row counts kRowPad more than its steps
 // (without it, the CTAs that get parts of two rows finish last: 98 us against
 // 88 for 40 ragged rows of 32 heads).
-constexpr int kRowPad = 8;
+constexpr int kRowPad = 24;
 
 // The CTA's range of the weighted list.
 struct Cut {
@@ -182,10 +182,10 @@ __device__ __forceinline__ Cut make_cut(const PagedView& pv, int64_t batch, int 
       if (w < wid) before += sc.warp_sum[w];
       chunk += sc.warp_sum[w];
     }
-    if (batch <= kAttnThreads) total = chunk;
+    if (b0 == 0) total = (batch <= kAttnThreads ? chunk : total) - kRowPad;   // the list's first row has no pad
     c.per = (total + gridDim.x - 1) / gridDim.x;
     if (c.per < min_per) c.per = min_per;
-    c.begin = c.per * blockIdx.x;
+    c.begin = kRowPad + c.per * blockIdx.x;
     const int64_t excl = before + incl - mine;
     if (excl <= c.begin && c.begin < excl + mine) {
       sc.row = b0 + threadIdx.x;
@@ -195,7 +195,8 @@ __device__ __forceinline__ Cut make_cut(const PagedView& pv, int64_t batch, int 
     __syncthreads();
     if (c.begin < base) break;
   }
-  c.rest = total - c.begin < c.per ? total - c.begin : c.per;
+  const int64_t end = kRowPad + total;
+  c.rest = end - c.begin < c.per ? end - c.begin : c.per;
   c.row = sc.row;
   c.off = sc.off;
   return c;
@@ -241,11 +242,14 @@ __device__ __forceinline__ void gather_full16(uint32_t stage, const __nv_bfloat1
 // of 16 heads; a warp computes all of them from each gathered tile (two warps
 // sharing a ring, each with one group, ran 94 us against 82 for 40 ragged rows
 // of 32 heads: twice the ldmatrix traffic and barriers).
-template <int D, int NG>
+template <int D, int NG, bool SEL>
 struct DecCfg {
   static constexpr int WARPS = kAttnThreads / 32;
-  static constexpr int CTAS = D == 128 && NG == 2 ? 2 : 3;   // per SM: 255 or 168 registers a thread
-  static constexpr int NST = D == 128 ? (NG == 2 ? 3 : 2) : 4;
+  // CTAs per SM: 255 or 168 registers a thread.  Three of 16 heads at d = 128
+  // start selected rows faster (22.0 against 22.7 us for 96 rows), two with a
+  // deeper ring stream a whole cache faster (85.7 against 89.3 us for 1M keys).
+  static constexpr int CTAS = D == 128 && (NG == 2 || !SEL) ? 2 : 3;
+  static constexpr int NST = D == 128 ? (CTAS == 2 ? 3 : 2) : 4;
   static constexpr int RING = NST * GatherCfg<D>::STAGE_BYTES;
   static constexpr int TILES = WARPS * RING;
   static constexpr int SMEM = TILES + (int)sizeof(AttnScratch);
@@ -263,7 +267,7 @@ __device__ __forceinline__ void attn_piece_bf16(const PagedView& pv, const __nv_
                                                 int w0, int steps, int Hq, float scale_log2, unsigned char* tiles,
                                                 AttnScratch& sc, bool& bad_page, bool& bad_idx) {
   using C = GatherCfg<D>;
-  using G = DecCfg<D, NG>;
+  using G = DecCfg<D, NG, SEL>;
   constexpr int NST = G::NST;
   constexpr int WARPS = G::WARPS;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -302,34 +306,31 @@ __device__ __forceinline__ void attn_piece_bf16(const PagedView& pv, const __nv_
     cp_async_commit();
   };
 
-  uint32_t qa[NG][D / 16][4];
-  {
-    const uint32_t* q32 = reinterpret_cast<const uint32_t*>(Q + b * Hq * D);
-#pragma unroll
-    for (int n = 0; n < NG; ++n) {
-      const int h0 = n * 16 + g, h1 = h0 + 8;
-#pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks) {
-        const int c0 = (h0 * D + ks * 16 + 2 * qi) / 2, c1 = (h1 * D + ks * 16 + 2 * qi) / 2;
-        qa[n][ks][0] = h0 < Hq ? __ldg(q32 + c0) : 0u;
-        qa[n][ks][1] = h1 < Hq ? __ldg(q32 + c1) : 0u;
-        qa[n][ks][2] = h0 < Hq ? __ldg(q32 + c0 + 4) : 0u;
-        qa[n][ks][3] = h1 < Hq ? __ldg(q32 + c1 + 4) : 0u;
-      }
-    }
-  }
-  // fill the ring: all idx entries, then all pages, then the rows
+  // Start-up, ordered by its chains of dependent loads: the ring's idx entries;
+  // Q, by 16-byte copies into the last stage of the first warp's ring (free
+  // until that warp's first step; fragment-shaped loads of Q from global memory
+  // took the load units 1 us); the pages; the rows; then Q's fragments.
   int st = w0 + warp;
-  {
-    int raws[NST], pools[NST], rws[NST], cols[NST], pgs[NST];
+  int raws[NST], raw_next;
 #pragma unroll
-    for (int i = 0; i < NST; ++i) {
-      load_raw(st + i * WARPS);
-      raws[i] = raw;
-    }
-    load_raw(st + NST * WARPS);
-    const int raw_next = raw;
-    if (SEL && sr.len == 0) steps = w0;   // an idle row
+  for (int i = 0; i < NST; ++i) {
+    load_raw(st + i * WARPS);
+    raws[i] = raw;
+  }
+  load_raw(st + NST * WARPS);
+  raw_next = raw;
+  const uint32_t q_s = smem_u32(tiles) + (NST - 1) * C::STAGE_BYTES;   // [NG * 16][D], swizzled as the tiles
+  static_assert(NG * 16 * C::ROW_BYTES <= C::STAGE_BYTES, "Q fits a stage");
+#pragma unroll
+  for (int i = threadIdx.x; i < NG * 16 * C::CHUNKS; i += kAttnThreads) {
+    const int h = i / C::CHUNKS, ch = i % C::CHUNKS;
+    cp_async16(q_s + h * C::ROW_BYTES + ((ch ^ (h & 7)) << 4), Q + (b * Hq + (h < Hq ? h : 0)) * D + ch * 8,
+               h < Hq ? 16u : 0u);
+  }
+  cp_async_commit();
+  if (SEL && sr.len == 0) steps = w0;   // an idle row
+  {
+    int pools[NST], rws[NST], cols[NST], pgs[NST];
 #pragma unroll
     for (int i = 0; i < NST; ++i) {
       raw = raws[i];
@@ -349,6 +350,17 @@ __device__ __forceinline__ void attn_piece_bf16(const PagedView& pv, const __nv_
     }
     raw = raw_next;
   }
+  uint32_t qa[NG][D / 16][4];
+  cp_async_wait<NST - 1>();   // all but the rows: Q
+  __syncthreads();
+#pragma unroll
+  for (int n = 0; n < NG; ++n)
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks) {
+      const int h = n * 16 + (lane & 15), ch = 2 * ks + (lane >> 4);
+      ldsm_x4(q_s + h * C::ROW_BYTES + ((ch ^ (h & 7)) << 4), qa[n][ks][0], qa[n][ks][1], qa[n][ks][2], qa[n][ks][3]);
+    }
+  __syncthreads();   // the stage is the first warp's again
   float o[NG][D / 8][4];
   float m[NG][2], l[NG][2], top[NG][2];   // heads g and g + 8 of each group
 #pragma unroll
@@ -758,11 +770,11 @@ struct AttnArgs {
 };
 
 // The type's piece function, its shared memory and its steps in progress.
-template <typename T, int D, int MAXH>
+template <typename T, int D, int MAXH, bool SEL>
 struct Piece;
-template <int D, int MAXH>
-struct Piece<__nv_bfloat16, D, MAXH> {
-  using G = DecCfg<D, MAXH / 16>;
+template <int D, int MAXH, bool SEL>
+struct Piece<__nv_bfloat16, D, MAXH, SEL> {
+  using G = DecCfg<D, MAXH / 16, SEL>;
   static constexpr int MIN_STEPS = G::WARPS;
   static constexpr int CTAS = G::CTAS;
   static constexpr int PITCH = G::PITCH;   // floats per head of the result
@@ -770,7 +782,6 @@ struct Piece<__nv_bfloat16, D, MAXH> {
   static __device__ __forceinline__ AttnScratch& scratch(unsigned char* smem, int) {
     return *reinterpret_cast<AttnScratch*>(smem + G::TILES);
   }
-  template <bool SEL>
   static __device__ __forceinline__ void run(const AttnArgs<__nv_bfloat16>& a, const SlotRow& sr, int64_t b, int w0,
                                              int steps, unsigned char* smem, AttnScratch& sc, bool& bad_page,
                                              bool& bad_idx) {
@@ -778,8 +789,8 @@ struct Piece<__nv_bfloat16, D, MAXH> {
                                        bad_idx);
   }
 };
-template <int D, int MAXH>
-struct Piece<float, D, MAXH> {
+template <int D, int MAXH, bool SEL>
+struct Piece<float, D, MAXH, SEL> {
   static constexpr int MIN_STEPS = 2;
   static constexpr int CTAS = 2;
   static constexpr int PITCH = D;
@@ -787,7 +798,6 @@ struct Piece<float, D, MAXH> {
   static __device__ __forceinline__ AttnScratch& scratch(unsigned char* smem, int Hq) {
     return *reinterpret_cast<AttnScratch*>(smem + ((F32Cfg<D>::TILES + 4 * Hq * (D + 36 + 1) + 64 + 15) & ~15));
   }
-  template <bool SEL>
   static __device__ __forceinline__ void run(const AttnArgs<float>& a, const SlotRow& sr, int64_t b, int w0, int steps,
                                              unsigned char* smem, AttnScratch& sc, bool& bad_page, bool& bad_idx) {
     attn_piece_f32<D, MAXH, SEL>(a.pv, a.Q, a.K, a.V, sr, b, w0, steps, a.Hq, a.scale_log2, smem, sc, bad_page, bad_idx);
@@ -823,9 +833,9 @@ __device__ __forceinline__ SlotRow slot_row(const AttnArgs<T>& a, int64_t b, boo
 
 // Selected pools: grid (splits, batch), the splits of a row are one cluster.
 template <typename T, int D, int MAXH>
-__global__ void __launch_bounds__(kAttnThreads, (Piece<T, D, MAXH>::CTAS))
+__global__ void __launch_bounds__(kAttnThreads, (Piece<T, D, MAXH, true>::CTAS))
     decode_attn_selected_kernel(const __grid_constant__ AttnArgs<T> a) {
-  using P = Piece<T, D, MAXH>;
+  using P = Piece<T, D, MAXH, true>;
   extern __shared__ __align__(128) unsigned char dec_smem[];
   AttnScratch& sc = P::scratch(dec_smem, a.Hq);
   chain_wait();
@@ -836,7 +846,7 @@ __global__ void __launch_bounds__(kAttnThreads, (Piece<T, D, MAXH>::CTAS))
   const SlotRow sr = slot_row(a, b, bad_page);
   const int n_steps = (a.k + 4) >> 2;   // whatever the length: the idx loads need not wait for it
   const int w0 = (int)((int64_t)n_steps * rank / splits), w1 = (int)((int64_t)n_steps * (rank + 1) / splits);
-  P::template run<true>(a, sr, b, w0, w1, dec_smem, sc, bad_page, bad_idx);
+  P::run(a, sr, b, w0, w1, dec_smem, sc, bad_page, bad_idx);
   const float4* o4 = reinterpret_cast<const float4*>(dec_smem);
   const int n4 = a.Hq * (D / 4);
   T* out = a.O + b * a.Hq * D;
@@ -896,9 +906,9 @@ __global__ void __launch_bounds__(kAttnThreads, (Piece<T, D, MAXH>::CTAS))
 
 // Whole cache: one CTA per range of the list of steps.
 template <typename T, int D, int MAXH>
-__global__ void __launch_bounds__(kAttnThreads, (Piece<T, D, MAXH>::CTAS))
+__global__ void __launch_bounds__(kAttnThreads, (Piece<T, D, MAXH, false>::CTAS))
     decode_attn_all_kernel(const __grid_constant__ AttnArgs<T> a) {
-  using P = Piece<T, D, MAXH>;
+  using P = Piece<T, D, MAXH, false>;
   extern __shared__ __align__(128) unsigned char dec_smem[];
   AttnScratch& sc = P::scratch(dec_smem, a.Hq);
   chain_wait();
@@ -917,9 +927,9 @@ __global__ void __launch_bounds__(kAttnThreads, (Piece<T, D, MAXH>::CTAS))
     const int w0 = (int)max(off - kRowPad, (int64_t)0), w1 = (int)max(end - kRowPad, (int64_t)0);
     if (w1 > w0) {
       if (pieces) __syncthreads();   // the previous results become tiles again
-      P::template run<false>(a, sr, b, w0, w1, dec_smem, sc, bad_page, bad_idx);
+      P::run(a, sr, b, w0, w1, dec_smem, sc, bad_page, bad_idx);
       if (w0 == 0) {
-        const int64_t last = (row_pos + kRowPad + n_steps - 1) / cut.per;
+        const int64_t last = (row_pos + n_steps - 1) / cut.per;
         const bool joined = last > blockIdx.x;
         if (by_row || joined) {
           put_join_item(a.ps, by_row ? b : blockIdx.x, joined ? (int)b : -1, last, pieces > 0);
@@ -1052,16 +1062,17 @@ static unsigned selected_splits(int64_t batch, int n_steps, int min_steps, int r
 
 template <typename T, int D, int MAXH>
 static cudaError_t launch_all(const DecodeAttnArgs& g, const AttnArgs<T>& a, cudaStream_t s) {
-  using P = Piece<T, D, MAXH>;
-  const int smem = P::smem(a.Hq);
   if (a.idx) {
+    using P = Piece<T, D, MAXH, true>;
     auto kern = decode_attn_selected_kernel<T, D, MAXH>;
     const unsigned splits = selected_splits(a.batch, (a.k + 4) >> 2, P::MIN_STEPS, kSms * P::CTAS);
     static std::atomic<uint64_t> done{0};
     cudaError_t e = prepare_kernel(kern, P::smem(MAXH), true, done);
     if (e != cudaSuccess) return e;
-    return launch_chained_cluster(splits, kern, dim3(splits, (unsigned)a.batch), dim3(kAttnThreads), smem, s, a);
+    return launch_chained_cluster(splits, kern, dim3(splits, (unsigned)a.batch), dim3(kAttnThreads), P::smem(a.Hq),
+                                  s, a);
   }
+  using P = Piece<T, D, MAXH, false>;
   auto kern = decode_attn_all_kernel<T, D, MAXH>;
   static std::atomic<uint64_t> done{0};
   cudaError_t e = prepare_kernel(kern, P::smem(MAXH), false, done);
@@ -1070,7 +1081,7 @@ static cudaError_t launch_all(const DecodeAttnArgs& g, const AttnArgs<T>& a, cud
   const int64_t row_max = ((int64_t)a.pv.capacity + 15) >> 4;
   const int64_t want = a.batch * ((row_max + kRowPad + P::MIN_STEPS - 1) / P::MIN_STEPS);
   const unsigned ctas = (unsigned)(want < kSms * P::CTAS ? want : kSms * P::CTAS);
-  e = launch_chained(kern, dim3(ctas), dim3(kAttnThreads), smem, s, a);
+  e = launch_chained(kern, dim3(ctas), dim3(kAttnThreads), P::smem(a.Hq), s, a);
   if (e != cudaSuccess || ctas == 1) return e;
   // few rows, so many pieces of each: the columns of a head are split too
   const unsigned items = a.batch < ctas ? (unsigned)a.batch : ctas;
