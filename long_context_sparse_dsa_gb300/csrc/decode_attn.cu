@@ -254,18 +254,21 @@ struct DecCfg {
   static constexpr int TILES = WARPS * RING;
   static constexpr int SMEM = TILES + (int)sizeof(AttnScratch);
   static constexpr int PITCH = D + 8;   // floats per head in the join buffer: fragment stores without bank conflicts
-  static_assert(TILES >= WARPS * NG * 16 * PITCH * 4, "the rings double as the join buffer");
+  static constexpr int JOIN = WARPS * NG * 16 * PITCH * 4;
+  static_assert(TILES >= JOIN, "the rings double as the join buffer");
 };
 
 // Steps [w0, steps) of row b.  Leaves o [Hq][PITCH] at the start of the tiles
 // and the heads' bases and sums in sc.ml; ends with a __syncthreads().
+// arrive: arrives at the cluster's barrier as soon as the tiles behind the
+// join buffer are no longer used.
 // SEL: the slots are selected pools; else all pools.
 template <int D, int NG, bool SEL>
 __device__ __forceinline__ void attn_piece_bf16(const PagedView& pv, const __nv_bfloat16* __restrict__ Q,
                                                 const __nv_bfloat16* __restrict__ K,
                                                 const __nv_bfloat16* __restrict__ V, const SlotRow& sr, int64_t b,
                                                 int w0, int steps, int Hq, float scale_log2, unsigned char* tiles,
-                                                AttnScratch& sc, bool& bad_page, bool& bad_idx) {
+                                                AttnScratch& sc, bool arrive, bool& bad_page, bool& bad_idx) {
   using C = GatherCfg<D>;
   using G = DecCfg<D, NG, SEL>;
   constexpr int NST = G::NST;
@@ -526,6 +529,7 @@ __device__ __forceinline__ void attn_piece_bf16(const PagedView& pv, const __nv_
       }
     }
   __syncthreads();   // every ring is idle: the tiles are the join buffer, [warp][NG * 16][PITCH]
+  if (arrive) cluster_arrive();
 #pragma unroll
   for (int n = 0; n < NG; ++n) {
     float* my = reinterpret_cast<float*>(tiles) + (warp * NG + n) * 16 * G::PITCH;
@@ -588,7 +592,7 @@ template <int D, int MAXH, bool SEL>
 __device__ __forceinline__ void attn_piece_f32(const PagedView& pv, const float* __restrict__ Q,
                                                const float* __restrict__ K, const float* __restrict__ V,
                                                const SlotRow& sr, int64_t b, int w0, int steps, int Hq,
-                                               float scale_log2, unsigned char* tiles, AttnScratch& sc,
+                                               float scale_log2, unsigned char* tiles, AttnScratch& sc, bool arrive,
                                                bool& bad_page, bool& bad_idx) {
   using F = F32Cfg<D>;
   constexpr int HPW = MAXH / 4;                 // heads a warp scores
@@ -739,6 +743,7 @@ __device__ __forceinline__ void attn_piece_f32(const PagedView& pv, const float*
   }
   cp_async_wait<0>();
   __syncthreads();
+  if (arrive) cluster_arrive();
 #pragma unroll
   for (int i = 0; i < HPT; ++i) {
     const int h = grp + GROUPS * i;
@@ -778,15 +783,17 @@ struct Piece<__nv_bfloat16, D, MAXH, SEL> {
   static constexpr int MIN_STEPS = G::WARPS;
   static constexpr int CTAS = G::CTAS;
   static constexpr int PITCH = G::PITCH;   // floats per head of the result
+  static constexpr int INBOX = G::JOIN;    // where the tiles are free behind the join
+  static constexpr int TILES = G::TILES;
   static int smem(int) { return G::SMEM; }
   static __device__ __forceinline__ AttnScratch& scratch(unsigned char* smem, int) {
     return *reinterpret_cast<AttnScratch*>(smem + G::TILES);
   }
   static __device__ __forceinline__ void run(const AttnArgs<__nv_bfloat16>& a, const SlotRow& sr, int64_t b, int w0,
-                                             int steps, unsigned char* smem, AttnScratch& sc, bool& bad_page,
-                                             bool& bad_idx) {
-    attn_piece_bf16<D, MAXH / 16, SEL>(a.pv, a.Q, a.K, a.V, sr, b, w0, steps, a.Hq, a.scale_log2, smem, sc, bad_page,
-                                       bad_idx);
+                                             int steps, unsigned char* smem, AttnScratch& sc, bool arrive,
+                                             bool& bad_page, bool& bad_idx) {
+    attn_piece_bf16<D, MAXH / 16, SEL>(a.pv, a.Q, a.K, a.V, sr, b, w0, steps, a.Hq, a.scale_log2, smem, sc, arrive,
+                                            bad_page, bad_idx);
   }
 };
 template <int D, int MAXH, bool SEL>
@@ -794,13 +801,16 @@ struct Piece<float, D, MAXH, SEL> {
   static constexpr int MIN_STEPS = 2;
   static constexpr int CTAS = 2;
   static constexpr int PITCH = D;
+  static constexpr int INBOX = MAXH * D * 4;
+  static constexpr int TILES = F32Cfg<D>::TILES;
   static int smem(int Hq) { return F32Cfg<D>::smem(Hq); }
   static __device__ __forceinline__ AttnScratch& scratch(unsigned char* smem, int Hq) {
     return *reinterpret_cast<AttnScratch*>(smem + ((F32Cfg<D>::TILES + 4 * Hq * (D + 36 + 1) + 64 + 15) & ~15));
   }
   static __device__ __forceinline__ void run(const AttnArgs<float>& a, const SlotRow& sr, int64_t b, int w0, int steps,
-                                             unsigned char* smem, AttnScratch& sc, bool& bad_page, bool& bad_idx) {
-    attn_piece_f32<D, MAXH, SEL>(a.pv, a.Q, a.K, a.V, sr, b, w0, steps, a.Hq, a.scale_log2, smem, sc, bad_page, bad_idx);
+                                             unsigned char* smem, AttnScratch& sc, bool arrive, bool& bad_page,
+                                             bool& bad_idx) {
+    attn_piece_f32<D, MAXH, SEL>(a.pv, a.Q, a.K, a.V, sr, b, w0, steps, a.Hq, a.scale_log2, smem, sc, arrive, bad_page, bad_idx);
   }
 };
 
@@ -846,7 +856,7 @@ __global__ void __launch_bounds__(kAttnThreads, (Piece<T, D, MAXH, true>::CTAS))
   const SlotRow sr = slot_row(a, b, bad_page);
   const int n_steps = (a.k + 4) >> 2;   // whatever the length: the idx loads need not wait for it
   const int w0 = (int)((int64_t)n_steps * rank / splits), w1 = (int)((int64_t)n_steps * (rank + 1) / splits);
-  P::run(a, sr, b, w0, w1, dec_smem, sc, bad_page, bad_idx);
+  P::run(a, sr, b, w0, w1, dec_smem, sc, splits > 1, bad_page, bad_idx);
   const float4* o4 = reinterpret_cast<const float4*>(dec_smem);
   const int n4 = a.Hq * (D / 4);
   T* out = a.O + b * a.Hq * D;
@@ -858,47 +868,51 @@ __global__ void __launch_bounds__(kAttnThreads, (Piece<T, D, MAXH, true>::CTAS))
     }
     if (threadIdx.x < a.Hq) lse[threadIdx.x] = lse_of(sc.ml[threadIdx.x].x, sc.ml[threadIdx.x].y);
   } else {
-    cluster_sync();
-    // Each CTA writes its share of the outputs from all CTAs' parts.  Lane s of
-    // every 16 lanes holds CTA s's base and sum of the lanes' head (16 lanes
-    // never cross a head: D/4 is a multiple of 16), so that all remote loads
-    // are in flight at once.
-    const uint32_t o_s = smem_u32(o4), ml_s = smem_u32(sc.ml);
+    // Each CTA writes a share of the row's outputs.  Its inbox, in the tiles
+    // behind its join buffer, takes that share of every CTA's part, and all
+    // bases and sums: the CTAs store there directly, so that nobody waits for
+    // a remote load and nobody has to stay for another's.
+    constexpr int MAX4 = MAXH * (D / 4);
+    static_assert(P::INBOX + 16 * (MAX4 + 16 * 16) + 8 * 16 * MAXH <= P::TILES, "the inbox fits behind the join buffer");
+    float4* in4 = reinterpret_cast<float4*>(dec_smem + P::INBOX);                       // [splits][per]
+    float2* in_ml = reinterpret_cast<float2*>(in4 + MAX4 + 16 * 16);                    // [splits][Hq]
     const int per = ((n4 + splits - 1) / splits + 15) & ~15;
+    cluster_wait();   // everyone's inbox is free
+    for (int i = threadIdx.x; i < n4; i += kAttnThreads) {
+      const int to = i / per;
+      cluster_st4(cluster_map(smem_u32(in4 + rank * per + i - to * per), to), o4[result_at<P, D>(i)]);
+    }
+    for (int i = threadIdx.x; i < splits * a.Hq; i += kAttnThreads)
+      cluster_st2(cluster_map(smem_u32(in_ml + rank * a.Hq + i % a.Hq), i / a.Hq), sc.ml[i % a.Hq]);
+    cluster_sync();
+    // Lane s of every 16 lanes weighs CTA s's part of the lanes' head (16 lanes
+    // never cross a head: D/4 is a multiple of 16).
     const int end = min(n4, (rank + 1) * per);
     for (int i0 = rank * per; i0 < end; i0 += kAttnThreads) {   // end and i0 are multiples of 16
       const int i = min(i0 + (int)threadIdx.x, end - 1);
       const int h = i / (D / 4), lane16 = threadIdx.x & 15;
-      float2 ml = make_float2(-INFINITY, 0.f);
-      if (lane16 < splits) ml = cluster_ld2(cluster_map(ml_s + 8 * h, lane16));
-      float4 x[16];
-#pragma unroll
-      for (int s = 0; s < 16; ++s)
-        if (s < splits) x[s] = cluster_ld4(cluster_map(o_s + 16 * result_at<P, D>(i), s));
+      const float2 ml = lane16 < splits ? in_ml[lane16 * a.Hq + h] : make_float2(-INFINITY, 0.f);
       float mm = ml.x;
 #pragma unroll
       for (int w = 8; w; w >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, w));
       const float f = exp2f(ml.x - (mm == -INFINITY ? 0.f : mm));
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      float l = 0.f;
-      const float fl = f * ml.y;
+      float l = f * ml.y;
 #pragma unroll
-      for (int s = 0; s < 16; ++s) {
-        if (s < splits) {
-          const float w = __shfl_sync(0xffffffffu, f, s, 16);
-          l += __shfl_sync(0xffffffffu, fl, s, 16);
-          acc.x += w * x[s].x;
-          acc.y += w * x[s].y;
-          acc.z += w * x[s].z;
-          acc.w += w * x[s].w;
-        }
+      for (int w = 8; w; w >>= 1) l += __shfl_xor_sync(0xffffffffu, l, w);
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int s = 0; s < splits; ++s) {
+        const float4 x = in4[s * per + i - rank * per];
+        const float w = __shfl_sync(0xffffffffu, f, s, 16);
+        acc.x += w * x.x;
+        acc.y += w * x.y;
+        acc.z += w * x.z;
+        acc.w += w * x.w;
       }
       if (i0 + (int)threadIdx.x < end) {
         store_out4(out + 4 * i, acc, inv_sum(l));
         if (i % (D / 4) == 0) lse[h] = lse_of(mm, l);
       }
     }
-    cluster_sync();   // no CTA leaves while its shared memory is being read
   }
   if (bad_idx) record_error(DSA_DEV_ERR_BAD_INDEX);
   if (bad_page) record_error(DSA_DEV_ERR_BAD_PAGE);
@@ -927,7 +941,7 @@ __global__ void __launch_bounds__(kAttnThreads, (Piece<T, D, MAXH, false>::CTAS)
     const int w0 = (int)max(off - kRowPad, (int64_t)0), w1 = (int)max(end - kRowPad, (int64_t)0);
     if (w1 > w0) {
       if (pieces) __syncthreads();   // the previous results become tiles again
-      P::run(a, sr, b, w0, w1, dec_smem, sc, bad_page, bad_idx);
+      P::run(a, sr, b, w0, w1, dec_smem, sc, false, bad_page, bad_idx);
       if (w0 == 0) {
         const int64_t last = (row_pos + n_steps - 1) / cut.per;
         const bool joined = last > blockIdx.x;
