@@ -187,13 +187,14 @@ static cudaError_t launch_scores(bool bf16, const PagedView& pv, int64_t batch, 
 
 cudaError_t launch_decode_scores(bool bf16, const PagedView& pv, int64_t batch, int Hi, int di, const void* q_idx,
                                  const float* w, const void* kpool, float* scores, int64_t pitch, cudaStream_t s) {
-  // 64 pools a warp (16 KB in flight at di = 128) once that gives every SM 8
-  // warps, else 16, for latency
-  const bool many = batch * (pv.capacity / 4) >= (int64_t)152 * 8 * 64;
+  // 8 KB of pool keys a warp once that gives every SM 8 warps (128-byte rows:
+  // 64 pools; 256-byte rows: 32, measured 34.9 us against 35.9 with 64 for 32
+  // ragged rows of 32768 pools), else 16 pools, for latency
+  const bool many = batch * (pv.capacity / 4) >= (int64_t)152 * 8 * (4096 / di);
   if (di == 64)
     return many ? launch_scores<64, 64>(bf16, pv, batch, Hi, q_idx, w, kpool, scores, pitch, s)
                 : launch_scores<64, 16>(bf16, pv, batch, Hi, q_idx, w, kpool, scores, pitch, s);
-  return many ? launch_scores<128, 64>(bf16, pv, batch, Hi, q_idx, w, kpool, scores, pitch, s)
+  return many ? launch_scores<128, 32>(bf16, pv, batch, Hi, q_idx, w, kpool, scores, pitch, s)
               : launch_scores<128, 16>(bf16, pv, batch, Hi, q_idx, w, kpool, scores, pitch, s);
 }
 

@@ -144,9 +144,11 @@ def test_dense_attention(dtype, Hq, d, page):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
-@pytest.mark.parametrize("lens", [[20011], [9001, 3, 0, 12289], [700] * 70, [1] * 600, [0] * 5])
+@pytest.mark.parametrize("lens", [[20011], [9001, 3, 0, 12289], [700] * 70, [1] * 600, [0] * 5,
+                                  [1 + 7919 * b % 613 for b in range(700)]])
 def test_dense_attention_batches(dtype, lens):
-    """One long row, very uneven rows, more rows than resident CTAs, rows of one token, only idle rows."""
+    """One long row, very uneven rows, more rows than resident CTAs (of one token each, and of uneven lengths, so that rows
+    straddle the CTAs' ranges), only idle rows."""
     pg = Paged(lens, 64, d=64, dtype=dtype, seed=3).fill()
     q, o, lse = _attn(pg, 16, 64)
     _check_attn(pg, q, o, lse, 64 ** -0.5)
@@ -201,6 +203,19 @@ def test_selected_attention(dtype, Hq, d, page, k):
     idx = _selection(pg, k)
     q, o, lse = _attn(pg, Hq, d, k, idx)
     _check_attn(pg, q, o, lse, d ** -0.5, idx)
+    dsa.check_device_error()
+
+
+@pytest.mark.parametrize("dtype,Hq", [("bf16", 16), ("bf16", 32), ("fp32", 8)])
+@pytest.mark.parametrize("batch", [1, 17, 28, 45, 60, 95, 150, 400, 700])
+def test_selected_attention_batches(dtype, Hq, batch):
+    """Every number of CTAs per row (16, 8 .. 1), and more rows than fit at once; some rows idle or too short to fill k."""
+    lens = [(b * 7919 + 61) % 800 if b % 9 else 0 for b in range(batch)]
+    lens[0] = 801
+    pg = Paged(lens, 16, d=64, dtype=dtype, seed=batch).fill()
+    idx = _selection(pg, 150)
+    q, o, lse = _attn(pg, Hq, 64, 150, idx)
+    _check_attn(pg, q, o, lse, 64 ** -0.5, idx)
     dsa.check_device_error()
 
 
@@ -318,6 +333,100 @@ def test_indexer_topk_all_scores_equal():
         dsa.decode_indexer_topk(dims, pg.cache(), lens, table, q, w, idx, _junk_ws(dims, 2))
         assert torch.equal(idx[0].cpu(), torch.arange(512, dtype=torch.int32))
         assert idx[1].tolist() == [0, 1, 2, 3] + [-1] * 508
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_indexer_topk_many_wide_rows(dtype):
+    """The wide indexer (di = 128) at a size that gives every warp a full block of pools."""
+    pg = Paged([9000 + 37 * b for b in range(30)], 64, di=128, dtype=dtype, seed=77).fill()
+    q, w, idx = _topk(pg, 8, 128, 300)
+    assert torch.equal(idx.cpu(), _ref_topk(pg, q, w, 300))
+    dsa.check_device_error()
+
+
+def _given_scores(values, k, sign=1.0):
+    """Rows of an fp32 layer whose scores are exactly sign * values [B][n] (each >= 0): one indexer head that reads one
+    channel."""
+    B = len(values)
+    lens = [4 * len(v) for v in values]
+    cap = max(lens)
+    cols = cap // 64 + 1
+    dims = dsa.make_dims(cap, 16, 128, 1, 64, k, dtype="fp32")
+    table = torch.arange(B * cols, dtype=torch.int32).view(B, cols)[:, :-(-cap // 64)].contiguous()
+    kpool = torch.zeros(B * cols, 16, 64)
+    for b, v in enumerate(values):
+        flat = torch.zeros(cols * 16)
+        flat[:len(v)] = v
+        kpool[b * cols:(b + 1) * cols, :, 0] = flat.view(cols, 16)
+    q = torch.zeros(B, 1, 64)
+    q[:, 0, 0] = 1.0
+    idx = torch.full((B, k), -9, dtype=torch.int32, device=DEV)
+    dsa.decode_indexer_topk(dims, dsa.PagedCache(kpool=kpool.to(DEV)), torch.tensor(lens, dtype=torch.int32, device=DEV),
+                            table.to(DEV), q.to(DEV), torch.full((B, 1), sign, device=DEV), idx, _junk_ws(dims, B))
+    for b, v in enumerate(values):
+        best = torch.sort(sign * v, descending=True, stable=True).indices[:k].sort().values
+        want = torch.full((k,), -1, dtype=torch.int32)
+        want[:len(best)] = best.to(torch.int32)
+        assert torch.equal(idx[b].cpu(), want), b
+    dsa.check_device_error()
+
+
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+@pytest.mark.parametrize("n,k", [(4095, 512), (4096, 512), (4097, 512), (4097, 1024), (20000, 1), (70000, 1024),
+                                 (70000, 512)])
+def test_topk_of_awkward_scores(n, k, sign):
+    """Scores that rise or fall along the row, that sit in one stretch of it or at every 61st pool only (which evenly spaced
+    samples misjudge), that tie in bulk just above or below the k-th, that span all magnitudes: always the exact selection."""
+    g = torch.Generator().manual_seed(n + k)
+    r = torch.rand(n, generator=g)
+    ramp = torch.arange(n, dtype=torch.float32)
+    stretch, comb, ties, few = r.clone(), r.clone(), torch.full((n,), 3.0), torch.full((n,), 3.0)
+    stretch[n // 3:n // 3 + 2 * k] += 5.0
+    comb[::61] += 7.0
+    ties[torch.randperm(n, generator=g)[:k // 2]] = 4.0
+    ties[torch.randperm(n, generator=g)[:n // 3]] = 1.0
+    few[torch.randperm(n, generator=g)[:min(n, 2 * k)]] = 9.0
+    wide = torch.exp(100.0 * (r - 0.5))
+    near = 1.0 + torch.randint(0, 50, (n,), generator=g).float() * 2.0 ** -23
+    _given_scores([r, ramp, ramp.flip(0), stretch, comb, ties, few, wide, near], k, sign)
+
+
+def test_topk_of_one_row_of_awkward_scores():
+    """The same kinds for one row on a cluster of 16 CTAs."""
+    g = torch.Generator().manual_seed(8)
+    n, k = 262144, 1024
+    r = torch.rand(n, generator=g)
+    comb, stretch, most = r.clone(), r.clone(), r.clone()
+    comb[5::64] += 3.0          # 4096 pools, away from every sample
+    stretch[200000:200000 + 5000] += 3.0
+    most[:200000] = 2.0
+    for v in (r, torch.arange(n, dtype=torch.float32), comb, stretch, most, torch.full((n,), 1.5)):
+        _given_scores([v], k)
+
+
+def test_topk_with_nan_and_infinite_scores_ends():
+    """A NaN score has no rank, but the call ends, with pools of the row only, each at most once; infinities rank normally."""
+    for n in (3000, 50000):
+        v = torch.rand(n, generator=torch.Generator().manual_seed(3))
+        v[7::n // 9] = math.inf
+        _given_scores([v], 64)
+        for bad in (v.clone(), torch.full((n,), math.nan)):
+            bad[::2] = math.nan
+            dims = dsa.make_dims(4 * n, 16, 128, 1, 64, 64, dtype="fp32")
+            cols = -(-4 * n // 64)
+            kpool = torch.zeros(cols, 16, 64)
+            kpool.view(-1, 64)[:n, 0] = bad
+            q = torch.zeros(1, 1, 64)
+            q[0, 0, 0] = 1.0
+            for w in (1.0, -1.0, math.nan):     # max(0, NaN) is 0 in the indexer: a NaN weight makes every score NaN
+                idx = torch.full((1, 64), -9, dtype=torch.int32, device=DEV)
+                dsa.decode_indexer_topk(dims, dsa.PagedCache(kpool=kpool.to(DEV)),
+                                        torch.tensor([4 * n], dtype=torch.int32, device=DEV),
+                                        torch.arange(cols, dtype=torch.int32, device=DEV)[None], q.to(DEV),
+                                        torch.full((1, 1), w, device=DEV), idx, _junk_ws(dims, 1))
+                got = idx[0].tolist()
+                assert len(set(got)) == 64 and min(got) >= 0 and max(got) < n and got == sorted(got)
+    dsa.check_device_error()
 
 
 def test_indexer_topk_of_real_scores():
@@ -459,6 +568,59 @@ def test_append_in_ragged_pieces(dtype, Hq, d, di, page, rot, inter, far):
         if n % 4:
             assert torch.equal(KT[pg.table[b, at + (n - 1) // page].long(), :n % 4], pg.KI[b][n // 4 * 4:])
     assert torch.isnan(K[~seen_k]).all() and torch.isnan(V[~seen_k]).all() and torch.isnan(KP[~seen_p]).all()
+
+
+@pytest.mark.parametrize("dtype,d,di,page", [("bf16", 128, 64, 64), ("bf16", 64, 128, 12), ("fp32", 128, 128, 16),
+                                             ("fp32", 64, 64, 100)])
+def test_append_long_prompts(dtype, d, di, page):
+    """Prompts of more than 20000 tokens in all, behind starts of every remainder modulo 4, in two calls."""
+    total = [9001, 1, 0, 6002, 3, 5003, 4000, 2]
+    first = [1, 0, 0, 2, 1, 1003, 8, 1]
+    pg = Paged(total, page, d=d, di=di, dtype=dtype, seed=d + di + page)
+    dims = dsa.make_dims(pg.cap, 4, d, 8, di, 8, dtype=dtype)
+    cache, table = pg.cache(), pg.table.to(DEV)
+    for a, z in (([0] * 8, first), (first, total)):
+        cat = lambda xs: torch.cat([x[i:j] for x, i, j in zip(xs, a, z)] + [torch.full((5, xs[0].shape[1]), 7.0).to(pg.dt)])
+        off = torch.tensor([0] + [j - i for i, j in zip(a, z)], dtype=torch.int32).cumsum(0).to(torch.int32)
+        dsa.cache_append(dims, cache, torch.tensor(z, dtype=torch.int32, device=DEV), table, cat(pg.K).to(DEV), cat(pg.V).to(DEV),
+                         cat(pg.KI).to(DEV), offsets=off.to(DEV))
+    dsa.check_device_error()
+    want = Paged(total, page, d=d, di=di, dtype=dtype, seed=d + di + page).fill()
+    for got, ref in ((cache.k, want.k_c), (cache.v, want.v_c), (cache.kpool, want.kp_c)):
+        got, ref = got.cpu(), ref
+        assert torch.equal(torch.isnan(got), torch.isnan(ref)) and torch.equal(got.nan_to_num(), ref.nan_to_num())
+    for b, n in enumerate(total):
+        if n % 4:
+            assert torch.equal(cache.ktail.cpu()[pg.table[b, (n - 1) // page].long(), :n % 4], pg.KI[b][n // 4 * 4:])
+
+
+def test_cache_beyond_32_bit_offsets():
+    """A cache of 20 million tokens: the rows' pages lie beyond element 2^31 of K and V (byte 2^32), and everything agrees
+    with the same rows in a small cache."""
+    page, pages = 64, 320000
+    small = Paged([900, 333], page, seed=90)
+    dims = dsa.make_dims(small.cap, 16, 128, 8, 64, 20)
+    shift = pages - small.pages
+    e = lambda *s: torch.empty(s, dtype=torch.bfloat16, device=DEV)
+    big = dsa.PagedCache(k=e(pages, page, 128), v=e(pages, page, 128), kpool=e(pages, page // 4, 64), ktail=e(pages, 3, 64))
+    lens, table = small.args()
+    cat = lambda xs: torch.cat(xs).to(DEV)
+    q = torch.randn(2, 16, 128, generator=small.g).to(torch.bfloat16).to(DEV)
+    qi = torch.randint(-3, 4, (2, 8, 64), generator=small.g).to(torch.bfloat16).to(DEV)
+    w = torch.rand(2, 8, generator=small.g).to(DEV)
+    res = []
+    for cache, t in ((small.cache(), table), (big, table + shift)):
+        dsa.cache_append(dims, cache, lens, t, cat(small.K), cat(small.V), cat(small.KI),
+                         offsets=torch.tensor([0, 900, 1233], dtype=torch.int32, device=DEV))
+        ws, idx = _junk_ws(dims, 2), torch.empty(2, 20, dtype=torch.int32, device=DEV)
+        o, lse = (torch.empty_like(q), torch.empty_like(q)), (torch.empty(2, 16, device=DEV), torch.empty(2, 16, device=DEV))
+        dsa.decode_indexer_topk(dims, cache, lens, t, qi, w, idx, ws)
+        dsa.decode_attn(dims, cache, lens, t, q, o[0], lse[0], ws, idx=idx)
+        dsa.decode_attn(dims, cache, lens, t, q, o[1], lse[1], ws)
+        res.append((idx, *o, *lse))
+    dsa.check_device_error()
+    for a, b in zip(*res):
+        assert torch.equal(a, b)
 
 
 def test_append_pool_keys_round_as_pool_keys_does():
