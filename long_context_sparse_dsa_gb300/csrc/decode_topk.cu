@@ -20,7 +20,7 @@
 //      writes its own part of the result in a second pass over its slice.
 //      Otherwise (the samples missed) the first CTA selects from the whole row
 //      by histogram rounds over it; the result never depends on tau.
-// Rows of at most kCap scores skip 1 and keep every score.
+// Rows of at most kCap scores are selected from exactly by the first CTA alone.
 // A NaN score has no defined rank.
 //
 // Bound: latency, about 12 dependent phases of half a microsecond to one.
@@ -237,6 +237,35 @@ __device__ __forceinline__ uint32_t kth_largest_own(const uint32_t (&x)[J], int 
   }
 }
 
+// The k largest of m <= kCap keys (own_key's, key(i) by index, m >= k), in
+// order: pool(i) of each goes to `out`.  A thread holds consecutive keys.
+template <typename F, typename G>
+__device__ __forceinline__ void finish_row(F key, G pool, int m, int k, SelShared& sh, int32_t* __restrict__ out) {
+  constexpr int J = kCap / kSelThreads;
+  const int per = (m + kSelThreads - 1) / kSelThreads, i0 = threadIdx.x * per;
+  uint32_t own[J];
+#pragma unroll
+  for (int j = 0; j < J; ++j) own[j] = j < per && i0 + j < m ? key(i0 + j) : 0u;
+  int ties;
+  const uint32_t T = kth_largest_own(own, k, sh, &ties);
+  int gt = 0, eq = 0;
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    gt += own[j] > T;
+    eq += own[j] == T;
+  }
+  int total;
+  const int p = block_prefix(gt + (eq << 16), sh, &total);
+  int g = p & 0xffff, e = p >> 16;
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    const bool is_gt = own[j] > T, is_eq = own[j] == T;
+    if (is_gt || (is_eq && e < ties)) out[g + min(e, ties)] = (int32_t)pool(i0 + j);
+    g += is_gt;
+    e += is_eq;
+  }
+}
+
 // Writes, in order, the keys > T and the first `ties` keys == T of n keys.  A
 // thread takes up to 8 consecutive keys at a time.
 template <typename F, typename G>
@@ -273,11 +302,11 @@ __device__ __forceinline__ void write_selected(F key, G pool, int n, uint32_t T,
 }
 
 // One pass over scores [begin, end) of a row, kChunk at a time, in order:
-// put(pool, score, gt, gt_before, eq_before) for every score > tau (or any, if
-// keep_all) or == tau, with the numbers of both before it in the slice.
+// put(pool, score, gt, gt_before, eq_before) for every score > tau or == tau,
+// with the numbers of both before it in the slice.
 template <typename F>
-__device__ __forceinline__ void scan_slice(const float* __restrict__ row, int64_t begin, int64_t end, bool keep_all,
-                                           float tau, SelShared& sh, int& n_gt, int& n_eq, F put) {
+__device__ __forceinline__ void scan_slice(const float* __restrict__ row, int64_t begin, int64_t end, float tau,
+                                           SelShared& sh, int& n_gt, int& n_eq, F put) {
   n_gt = n_eq = 0;
   for (int64_t c0 = begin; c0 < end; c0 += kChunk) {
     // a lane's kPerLane consecutive scores
@@ -303,11 +332,11 @@ __device__ __forceinline__ void scan_slice(const float* __restrict__ row, int64_
     uint32_t gt = 0, eq = 0;
 #pragma unroll
     for (int i = 0; i < kPerLane; ++i) {
-      gt |= (uint32_t)(keep_all || x[i] > tau) << i;
+      gt |= (uint32_t)(x[i] > tau) << i;
       eq |= (uint32_t)(x[i] == tau) << i;
     }
     gt &= valid;
-    eq = keep_all ? 0u : eq & valid;
+    eq &= valid;
     // numbers before this lane: both in one word (a chunk holds 8192 scores)
     int total;
     const int p = block_prefix(__popc(gt) | __popc(eq) << 16, sh, &total);
@@ -345,11 +374,15 @@ __global__ void __launch_bounds__(kSelThreads, 2)
       for (int i = tid; i < k; i += kSelThreads) out[i] = i < n ? i : -1;
     return;
   }
-  if (ctas > 1) cluster_arrive();
   const float* row = scores + b * pitch;
-  const bool keep_all = n <= kCap;
-  float tau = 0.f;
-  if (!keep_all) {
+  if (n <= kCap) {   // the first CTA holds the whole row
+    if (rank == 0)
+      finish_row([&](int i) { return own_key(__ldcg(row + i)); }, [](int i) { return i; }, n, k, sh, out);
+    return;
+  }
+  if (ctas > 1) cluster_arrive();
+  float tau;
+  {
     int g = 1;
     while (g < 64 && n / g > 65536) g *= 2;
     const uint64_t step = ((uint64_t)n << 20) / (uint32_t)(kSelThreads * g);   // between samples, in 2^-20 scores
@@ -374,7 +407,7 @@ __global__ void __launch_bounds__(kSelThreads, 2)
   const int64_t slice = ((((int64_t)n + ctas - 1) / ctas) + 3) & ~(int64_t)3;
   const int64_t begin = min((int64_t)n, rank * slice), end = min((int64_t)n, begin + slice);
   int n_gt, n_eq;
-  scan_slice(row, begin, end, keep_all, tau, sh, n_gt, n_eq, [&](int64_t pool, float x, bool gt, int at, int) {
+  scan_slice(row, begin, end, tau, sh, n_gt, n_eq, [&](int64_t pool, float x, bool gt, int at, int) {
     if (gt && at < kCap) {
       sh.key[at] = own_key(x);
       sh.pool[at] = (int32_t)pool;
@@ -409,18 +442,12 @@ __global__ void __launch_bounds__(kSelThreads, 2)
     if (rank != 0) return;
     const uint32_t* gk = ctas > 1 ? sh.gkey : sh.key;
     const int32_t* gp = ctas > 1 ? sh.gpool : sh.pool;
-    constexpr int kOwn = kCap / kSelThreads;
-    uint32_t own[kOwn];
-#pragma unroll
-    for (int i = 0; i < kOwn; ++i) own[i] = tid + i * kSelThreads < m ? gk[tid + i * kSelThreads] : 0u;
-    int eq;
-    const uint32_t T = kth_largest_own(own, k, sh, &eq);
-    write_selected([&](int i) { return gk[i]; }, [&](int i) { return gp[i]; }, m, T, eq, sh, out);
+    finish_row([&](int i) { return gk[i]; }, [&](int i) { return gp[i]; }, m, k, sh, out);
     return;
   }
   if (m < k && (int64_t)m + ties >= k) {
     const int need_eq = k - m;
-    scan_slice(row, begin, end, false, tau, sh, n_gt, n_eq, [&](int64_t pool, float, bool gt, int g, int e) {
+    scan_slice(row, begin, end, tau, sh, n_gt, n_eq, [&](int64_t pool, float, bool gt, int g, int e) {
       const int eq = eq_before + e;
       if (gt || eq < need_eq) out[gt_before + g + min(eq, need_eq)] = (int32_t)pool;
     });
