@@ -121,7 +121,7 @@ struct DecodeAttnArgs {
   float* lse;
   float* ws;            // partial results: decode_attn_ws_bytes
 };
-size_t decode_attn_ws_bytes(int64_t batch, int Hq, int d);
+size_t decode_attn_ws_bytes(int Hq, int d);
 cudaError_t launch_decode_attn(bool bf16, const DecodeAttnArgs& a, cudaStream_t s);
 
 }  // namespace dsa

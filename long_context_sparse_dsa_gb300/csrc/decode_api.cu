@@ -180,7 +180,7 @@ dsa_status dsa_validate_decode_dims(const dsa_dims* dims) {
 size_t dsa_decode_workspace_bytes(const dsa_dims* dims, int64_t batch) {
   if (check_dims(dims) != DSA_OK || check_batch(batch) != DSA_OK) return 0;
   const size_t sc = ((size_t)batch * dsa::decode_scores_pitch(dims->L / 4) * sizeof(float) + 255) & ~(size_t)255;
-  const size_t at = dsa::decode_attn_ws_bytes(batch, dims->Hq, dims->d);
+  const size_t at = dsa::decode_attn_ws_bytes(dims->Hq, dims->d);
   return q_bytes(dims, batch) + (sc > at ? sc : at);
 }
 

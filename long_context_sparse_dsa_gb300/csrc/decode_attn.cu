@@ -23,9 +23,11 @@
 // against 24 for 96 rows of 2051 keys.)
 //
 // bf16: steps go round-robin to a CTA's warps, each with a ring of its own
-// filled by cp.async, heads on the M side of m16n8k16 MMAs as in attn_fwd.cu;
-// up to two groups of 16.  P enters P V as two bf16 terms (hi + lo, about 2^-17 relative): the
-// MMAs are not what bounds the kernel.
+// filled by cp.async, heads (one or two groups of 16) on the M side of
+// m16n8k16 MMAs as in attn_fwd.cu: tcgen05 tiles would be an eighth full.  P
+// enters P V as two bf16 terms (hi + lo, about 2^-17 relative); one term alone
+// ran no faster (83 us against 80 for 40 ragged rows of 32 heads), the MMAs
+// not being what bounds the kernel.
 // fp32: tiles of 32 keys in shared memory, plain FFMA; for S a lane owns a key
 // and a warp a quarter of the heads, for P V a thread owns a channel.
 #include "decode.cuh"
@@ -46,7 +48,7 @@ struct JoinItem {
   int row, first, last, skip;   // row -1: nothing to join; pieces of CTAs first..last; skip: first's piece is its second
 };
 static size_t piece_floats(int Hq, int d) { return (size_t)Hq * (d + 2); }
-size_t decode_attn_ws_bytes(int64_t, int Hq, int d) {
+size_t decode_attn_ws_bytes(int Hq, int d) {
   const size_t n = 2 * kAttnCtas * piece_floats(Hq, d) * sizeof(float) + kAttnCtas * sizeof(JoinItem);
   return (n + 255) & ~(size_t)255;
 }
@@ -78,12 +80,9 @@ struct SlotRow {
   int k;
   int len;
 };
-// Steps of a row of `len` tokens; an idle row has one, without keys, so that
-// some CTA writes its outputs.
-__device__ __forceinline__ int row_steps(int len, bool selected, int k) {
-  if (len == 0) return 1;
-  return selected ? (k + 4) >> 2 : (len + 15) >> 4;
-}
+// Steps of a row of `len` tokens, all of them attended; an idle row has one,
+// without keys, so that some CTA writes its outputs.
+__device__ __forceinline__ int row_steps(int len) { return len == 0 ? 1 : (int)(((int64_t)len + 15) >> 4); }
 // Slot `i` in three stages, so that its two dependent loads can be issued
 // ahead: the idx entry, the pool and its visible rows, the physical pool.
 template <bool SEL>
@@ -115,8 +114,8 @@ __device__ __forceinline__ void slot_pool_rows(const SlotRow& r, int i, int raw,
 // ------------------------------------------------------------------- the cut
 // Beginning a row costs a CTA a chain of loads and a join, about as long as
 // kRowPad of its steps take, so each row counts kRowPad more than its steps
-// (without it, the CTAs that get parts of two rows finish last: 98 us against
-// 88 for 40 ragged rows of 32 heads).
+// (without it, the CTAs that get parts of two rows finish last: 81.1 us against
+// 75.6 for 40 ragged rows of 32 heads; 12 and 32 measured 76.2 and 76.0).
 constexpr int kRowPad = 24;
 
 // The CTA's range of the weighted list.
@@ -147,7 +146,7 @@ __device__ __forceinline__ Cut make_cut(const PagedView& pv, int64_t batch, int 
   auto weight_of = [&](int64_t b) {
     bool bad = false;
     if (b >= batch) return 0;
-    const int n = kRowPad + row_steps(row_length(pv, b, bad), false, 0);
+    const int n = kRowPad + row_steps(row_length(pv, b, bad));
     if (bad && blockIdx.x == 0) record_error(DSA_DEV_ERR_BAD_PAGE);
     return n;
   };
@@ -240,8 +239,8 @@ __device__ __forceinline__ void gather_full16(uint32_t stage, const __nv_bfloat1
 
 // A CTA's warps each take every 4th step, with a ring of their own.  NG: groups
 // of 16 heads; a warp computes all of them from each gathered tile (two warps
-// sharing a ring, each with one group, ran 94 us against 82 for 40 ragged rows
-// of 32 heads: twice the ldmatrix traffic and barriers).
+// sharing a ring, each with one group, took 29.6 us against 24.9 for 64 rows of
+// 2051 selected keys: twice the ldmatrix traffic, and a barrier per step).
 template <int D, int NG, bool SEL>
 struct DecCfg {
   static constexpr int WARPS = kAttnThreads / 32;
@@ -936,7 +935,7 @@ __global__ void __launch_bounds__(kAttnThreads, (Piece<T, D, MAXH, false>::CTAS)
   for (int64_t b = cut.row; rest > 0; ++b) {
     bool bad_len = false;   // recorded by make_cut
     const SlotRow sr = slot_row(a, b, bad_len);
-    const int n_steps = row_steps(sr.len, false, 0);
+    const int n_steps = row_steps(sr.len);
     const int64_t end = min(off + rest, (int64_t)kRowPad + n_steps);
     const int w0 = (int)max(off - kRowPad, (int64_t)0), w1 = (int)max(end - kRowPad, (int64_t)0);
     if (w1 > w0) {
@@ -1075,7 +1074,7 @@ static unsigned selected_splits(int64_t batch, int n_steps, int min_steps, int r
 }
 
 template <typename T, int D, int MAXH>
-static cudaError_t launch_all(const DecodeAttnArgs& g, const AttnArgs<T>& a, cudaStream_t s) {
+static cudaError_t launch_shape(const AttnArgs<T>& a, cudaStream_t s) {
   if (a.idx) {
     using P = Piece<T, D, MAXH, true>;
     auto kern = decode_attn_selected_kernel<T, D, MAXH>;
@@ -1122,13 +1121,13 @@ static cudaError_t launch_typed(const DecodeAttnArgs& g, cudaStream_t s) {
   a.k = g.k;
   a.scale_log2 = g.scale * 1.4426950408889634f;
   if (g.d == 128) {
-    if (g.Hq > 16) return launch_all<T, 128, 32>(g, a, s);
-    if (sizeof(T) == 2 || g.Hq > 8) return launch_all<T, 128, 16>(g, a, s);
-    return launch_all<T, 128, sizeof(T) == 2 ? 16 : 8>(g, a, s);
+    if (g.Hq > 16) return launch_shape<T, 128, 32>(a, s);
+    if (sizeof(T) == 2 || g.Hq > 8) return launch_shape<T, 128, 16>(a, s);
+    return launch_shape<T, 128, sizeof(T) == 2 ? 16 : 8>(a, s);
   }
-  if (g.Hq > 16) return launch_all<T, 64, 32>(g, a, s);
-  if (sizeof(T) == 2 || g.Hq > 8) return launch_all<T, 64, 16>(g, a, s);
-  return launch_all<T, 64, sizeof(T) == 2 ? 16 : 8>(g, a, s);
+  if (g.Hq > 16) return launch_shape<T, 64, 32>(a, s);
+  if (sizeof(T) == 2 || g.Hq > 8) return launch_shape<T, 64, 16>(a, s);
+  return launch_shape<T, 64, sizeof(T) == 2 ? 16 : 8>(a, s);
 }
 
 cudaError_t launch_decode_attn(bool bf16, const DecodeAttnArgs& a, cudaStream_t s) {
