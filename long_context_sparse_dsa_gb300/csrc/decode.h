@@ -102,8 +102,10 @@ struct AppendArgs {
 cudaError_t launch_cache_append(bool bf16, const AppendArgs& a, cudaStream_t s);
 
 // Scores of one query per row over the paged pool keys: scores [batch, pitch].
-cudaError_t launch_decode_scores(bool bf16, const PagedView& pv, int64_t batch, int Hi, int di, const void* q_idx,
-                                 const float* w, const void* kpool, float* scores, int64_t pitch, cudaStream_t s);
+// (rows of at most k pools are skipped: their selection needs none).
+cudaError_t launch_decode_scores(bool bf16, const PagedView& pv, int64_t batch, int Hi, int di, int k,
+                                 const void* q_idx, const float* w, const void* kpool, float* scores, int64_t pitch,
+                                 cudaStream_t s);
 // Top-k of each score row's first lens[b]/4 entries.
 cudaError_t launch_decode_topk(const PagedView& pv, int64_t batch, int k, const float* scores, int64_t pitch,
                                int32_t* idx, cudaStream_t s);

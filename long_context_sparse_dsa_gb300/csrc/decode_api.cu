@@ -141,8 +141,8 @@ dsa_status do_indexer_topk(const dsa_dims* dims, const dsa_paged_cache* c, int64
   const dsa::PagedView pv = view(dims, c, lens, table);
   const int64_t pitch = dsa::decode_scores_pitch(dims->L / 4);
   float* scores = reinterpret_cast<float*>(static_cast<char*>(ws) + q_bytes(dims, batch));
-  dsa_status st = launched(dsa::launch_decode_scores(is_bf16(dims), pv, batch, dims->Hi, dims->di, q_idx, w, c->kpool,
-                                                     scores, pitch, s),
+  dsa_status st = launched(dsa::launch_decode_scores(is_bf16(dims), pv, batch, dims->Hi, dims->di, dims->k, q_idx, w,
+                                                     c->kpool, scores, pitch, s),
                            "decode scores launch");
   if (st) return st;
   return launched(dsa::launch_decode_topk(pv, batch, dims->k, scores, pitch, idx, s), "decode top-k launch");

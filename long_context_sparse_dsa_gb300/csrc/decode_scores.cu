@@ -43,7 +43,7 @@ struct PoolBlock {
 
 template <int DI, int PPW>
 __global__ void __launch_bounds__(kScoreWarps * 32)
-    decode_scores_bf16_kernel(PagedView pv, int Hi, const uint4* __restrict__ q_idx, const float* __restrict__ w,
+    decode_scores_bf16_kernel(PagedView pv, int Hi, int k, const uint4* __restrict__ q_idx, const float* __restrict__ w,
                               const uint4* __restrict__ kpool, float* __restrict__ scores, int64_t pitch) {
   constexpr int CH = DI / 8;     // 16-byte chunks per row
   constexpr int CL = CH / 4;     // chunks per lane and row
@@ -54,7 +54,8 @@ __global__ void __launch_bounds__(kScoreWarps * 32)
   const int n = row_length(pv, b, bad) >> 2;
   const int lane = threadIdx.x & 31;
   const int p0 = (blockIdx.x * kScoreWarps + (threadIdx.x >> 5)) * PPW;
-  if (p0 >= n) return;   // bad lengths are recorded by the selection
+  // the selection of at most k pools needs no scores; it also records bad lengths
+  if (p0 >= n || n <= k) return;
   const int g = lane >> 2, qi = lane & 3;
   PoolBlock<PPW> pools;
   pools.load(pv, pv.table + b * pv.cols, p0, n, bad);
@@ -103,7 +104,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32)
 
 template <int DI, int PPW>
 __global__ void __launch_bounds__(kScoreWarps * 32)
-    decode_scores_f32_kernel(PagedView pv, int Hi, const float4* __restrict__ q_idx, const float* __restrict__ w,
+    decode_scores_f32_kernel(PagedView pv, int Hi, int k, const float4* __restrict__ q_idx, const float* __restrict__ w,
                              const float4* __restrict__ kpool, float* __restrict__ scores, int64_t pitch) {
   constexpr int LPR = DI / 8;          // lanes per pool row, 8 channels each
   constexpr int RPW = 32 / LPR;        // pool rows per warp and pass
@@ -114,7 +115,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32)
   const int n = row_length(pv, b, bad) >> 2;
   const int lane = threadIdx.x & 31;
   const int p0 = (blockIdx.x * kScoreWarps + (threadIdx.x >> 5)) * PPW;
-  if (p0 >= n) return;
+  if (p0 >= n || n <= k) return;
   const int sub = lane / LPR, li = lane % LPR;
   PoolBlock<PPW> pools;
   pools.load(pv, pv.table + b * pv.cols, p0, n, bad);
@@ -174,28 +175,29 @@ __global__ void __launch_bounds__(kScoreWarps * 32)
 }
 
 template <int DI, int PPW>
-static cudaError_t launch_scores(bool bf16, const PagedView& pv, int64_t batch, int Hi, const void* q_idx,
+static cudaError_t launch_scores(bool bf16, const PagedView& pv, int64_t batch, int Hi, int k, const void* q_idx,
                                  const float* w, const void* kpool, float* scores, int64_t pitch, cudaStream_t s) {
   const int64_t P = pv.capacity / 4, per = kScoreWarps * PPW;
   const dim3 grid((unsigned)((P + per - 1) / per), (unsigned)batch), threads(kScoreWarps * 32);
   if (bf16)
-    return launch_chained(decode_scores_bf16_kernel<DI, PPW>, grid, threads, 0, s, pv, Hi,
+    return launch_chained(decode_scores_bf16_kernel<DI, PPW>, grid, threads, 0, s, pv, Hi, k,
                           static_cast<const uint4*>(q_idx), w, static_cast<const uint4*>(kpool), scores, pitch);
-  return launch_chained(decode_scores_f32_kernel<DI, PPW>, grid, threads, 0, s, pv, Hi,
+  return launch_chained(decode_scores_f32_kernel<DI, PPW>, grid, threads, 0, s, pv, Hi, k,
                         static_cast<const float4*>(q_idx), w, static_cast<const float4*>(kpool), scores, pitch);
 }
 
-cudaError_t launch_decode_scores(bool bf16, const PagedView& pv, int64_t batch, int Hi, int di, const void* q_idx,
-                                 const float* w, const void* kpool, float* scores, int64_t pitch, cudaStream_t s) {
+cudaError_t launch_decode_scores(bool bf16, const PagedView& pv, int64_t batch, int Hi, int di, int k,
+                                 const void* q_idx, const float* w, const void* kpool, float* scores, int64_t pitch,
+                                 cudaStream_t s) {
   // 8 KB of pool keys a warp once that gives every SM 8 warps (128-byte rows:
   // 64 pools; 256-byte rows: 32, measured 34.9 us against 35.9 with 64 for 32
   // ragged rows of 32768 pools), else 16 pools, for latency
   const bool many = batch * (pv.capacity / 4) >= (int64_t)152 * 8 * (4096 / di);
   if (di == 64)
-    return many ? launch_scores<64, 64>(bf16, pv, batch, Hi, q_idx, w, kpool, scores, pitch, s)
-                : launch_scores<64, 16>(bf16, pv, batch, Hi, q_idx, w, kpool, scores, pitch, s);
-  return many ? launch_scores<128, 32>(bf16, pv, batch, Hi, q_idx, w, kpool, scores, pitch, s)
-              : launch_scores<128, 16>(bf16, pv, batch, Hi, q_idx, w, kpool, scores, pitch, s);
+    return many ? launch_scores<64, 64>(bf16, pv, batch, Hi, k, q_idx, w, kpool, scores, pitch, s)
+                : launch_scores<64, 16>(bf16, pv, batch, Hi, k, q_idx, w, kpool, scores, pitch, s);
+  return many ? launch_scores<128, 32>(bf16, pv, batch, Hi, k, q_idx, w, kpool, scores, pitch, s)
+              : launch_scores<128, 16>(bf16, pv, batch, Hi, k, q_idx, w, kpool, scores, pitch, s);
 }
 
 }  // namespace dsa

@@ -850,6 +850,98 @@ def test_graph_replay_streams_and_reproducibility():
     dsa.check_device_error()
 
 
+def test_calls_wait_for_what_comes_before_them():
+    """Kernels may become resident before their predecessors end; what they read and overwrite is still ordered: inputs that
+    a kernel just before the call writes, outputs that a kernel just after it reads, one workspace for all calls, appends
+    that the next call reads; the same with the device held up between calls gives the same bits."""
+    def run(held):
+        pg = Paged([400, 77, 1201, 9], 16, seed=51, cap=1400).fill()
+        B, Hq, d, k = 4, 16, 128, 24
+        dims = dsa.make_dims(pg.cap, Hq, d, 8, 64, k)
+        cols = -(-pg.cap // 16)
+        lens, _ = pg.args()
+        spare = torch.arange(pg.pages, pg.pages + B * cols, dtype=torch.int32).view(B, cols)
+        table = torch.where(pg.table >= 0, pg.table, spare).to(DEV)
+        grow = lambda t: torch.cat([t, torch.zeros(B * cols, *t.shape[1:], dtype=t.dtype)]).to(DEV)
+        cache = dsa.PagedCache(k=grow(pg.k_c), v=grow(pg.v_c), kpool=grow(pg.kp_c), ktail=grow(pg.kt_c))
+        g = torch.Generator(device=DEV).manual_seed(5)
+        rn = lambda *s: torch.randn(*s, generator=g, device=DEV).to(torch.bfloat16)
+        ws, rot = _junk_ws(dims, B), dsa.make_rotation(_freq(64))
+        o, o2 = rn(B, Hq, d), rn(B, Hq, d)
+        lse, idx = torch.zeros(B, Hq, device=DEV), torch.zeros(B, k, dtype=torch.int32, device=DEV)
+        q, kk, v, qi, ki, w = rn(B, Hq, d), rn(B, d), rn(B, d), rn(B, 8, 64), rn(B, 64), torch.rand(B, 8, generator=g, device=DEV)
+        seen = []
+        wait = torch.cuda.synchronize if held else lambda: None
+        for step in range(40):
+            lens.add_(1)
+            wait()
+            q.mul_(0.75).add_(o, alpha=0.25)
+            wait()
+            dsa.decode_step(dims, cache, lens, table, q, kk, v, qi, ki, w, o, lse, idx, ws, rotation=rot)
+            wait()
+            dsa.decode_attn(dims, cache, lens, table, o, o2, lse, ws)
+            wait()
+            kk.copy_(o2[:, step % Hq])
+            seen.append((o.clone(), o2.clone(), lse.clone(), idx.clone()))
+            wait()
+        dsa.check_device_error()
+        return seen
+    for a, b in zip(run(False), run(True)):
+        for x, y in zip(a, b):
+            assert torch.equal(x, y)
+
+
+def test_capture_across_streams():
+    """A graph whose calls depend on other streams' work: what one stream computes, another stream's calls read."""
+    pg = Paged([700, 33, 0, 1029], 16, seed=52).fill()
+    B, Hq, d, k = 4, 16, 128, 24
+    dims = dsa.make_dims(pg.cap, Hq, d, 8, 64, k)
+    lens, table = pg.args()
+    cache, ws, ws2 = pg.cache(), _junk_ws(dims, B), _junk_ws(dims, B)
+    src = torch.randn(B, Hq, d, generator=pg.g).to(DEV)
+    q = torch.zeros(B, Hq, d, dtype=torch.bfloat16, device=DEV)
+    qi = torch.randint(-3, 4, (B, 8, 64), generator=pg.g).to(torch.bfloat16).to(DEV)
+    w = torch.rand(B, 8, generator=pg.g).to(DEV)
+    out = [(torch.zeros_like(q), torch.zeros(B, Hq, device=DEV)) for _ in range(2)]
+    idx = torch.zeros(B, k, dtype=torch.int32, device=DEV)
+    total = torch.zeros(B, Hq, d, device=DEV)
+
+    def work(main, side):
+        q.copy_(src)
+        ready = torch.cuda.Event()
+        ready.record(main)
+        with torch.cuda.stream(side):
+            side.wait_event(ready)
+            dsa.decode_attn(dims, cache, lens, table, q, *out[1], ws2)
+            done = torch.cuda.Event()
+            done.record(side)
+        dsa.decode_indexer_topk(dims, cache, lens, table, qi, w, idx, ws)
+        dsa.decode_attn(dims, cache, lens, table, q, *out[0], ws, idx=idx)
+        main.wait_event(done)
+        total.copy_(out[0][0].float() + out[1][0].float())
+
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(main):
+        work(main, side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=main):
+        work(main, side)
+    for trial in range(3):
+        src.mul_(0.5)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = total.clone(), idx.clone(), out[1][1].clone()
+        with torch.cuda.stream(main):
+            work(main, side)
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], total) and torch.equal(got[1], idx) and torch.equal(got[2], out[1][1])
+        _check_attn(pg, q.cpu(), *out[1], d ** -0.5)
+        _check_attn(pg, q.cpu(), *out[0], d ** -0.5, idx.cpu())
+    dsa.check_device_error()
+
+
 def test_rows_may_share_pages():
     """Three rows of one sequence at growing lengths (a draft being verified), over one block-table row each."""
     pg = Paged([301], 16, seed=60).fill()
