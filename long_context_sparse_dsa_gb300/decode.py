@@ -39,7 +39,7 @@ class _CRotation(ctypes.Structure):
     _fields_ = [("turns", ctypes.c_void_p), ("dim", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
 
 
-@dataclass(frozen=True)
+@dataclass(frozen=True, eq=False)
 class PagedCache:
     """k, v [pages, page_size, d], kpool [pages, page_size / 4, di], ktail [pages, 3, di], in the layer dtype.
 
