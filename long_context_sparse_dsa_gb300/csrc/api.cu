@@ -10,6 +10,7 @@
 
 #include "../../include/dsa.h"
 #include "common.cuh"
+#include "decode.h"
 #include "launch.h"
 
 namespace dsa {

@@ -18,7 +18,6 @@ namespace dsa {
 // Device error word bits (read and cleared by dsa_check_device_error).
 constexpr unsigned DSA_DEV_ERR_TIMEOUT = 1u;
 constexpr unsigned DSA_DEV_ERR_BAD_INDEX = 2u;
-constexpr unsigned DSA_DEV_ERR_BAD_PAGE = 4u;
 
 extern __device__ unsigned int g_dev_error;
 extern __constant__ unsigned int c_wait_limit;
@@ -106,9 +105,6 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t src_bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(src_bytes)
                : "memory");
-}
-__device__ __forceinline__ void cp_async16_full(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
 template <int N>

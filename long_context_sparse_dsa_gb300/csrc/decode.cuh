@@ -40,6 +40,12 @@ __device__ __forceinline__ int phys_pool(const PagedView& pv, int p, int col, in
   return page * pv.ppp + (p - col * pv.ppp);
 }
 
+// 16-byte global->shared copy of a row that is there (cp_async16 of common.cuh
+// without the size operand).
+__device__ __forceinline__ void cp_async16_full(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst), "l"(src) : "memory");
+}
+
 // Programmatic dependent launch: a kernel launched by launch_chained
 // (decode.h) may become resident while its predecessor on the stream still
 // runs.  chain_wait() returns when the predecessor has finished and its writes

@@ -10,6 +10,9 @@
 
 namespace dsa {
 
+// Device error word bit of these kernels (the others: common.cuh).
+constexpr unsigned DSA_DEV_ERR_BAD_PAGE = 4u;
+
 // A batch of rows over the paged cache, as the kernels take it.
 struct PagedView {
   const int32_t* lens;    // [batch]
