@@ -28,8 +28,7 @@
 // enters P V as two bf16 terms (hi + lo, about 2^-17 relative); one term alone
 // ran no faster (83 us against 80 for 40 ragged rows of 32 heads), the MMAs
 // not being what bounds the kernel.
-// fp32: tiles of 32 keys in shared memory, plain FFMA; for S a lane owns a key
-// and a warp a quarter of the heads, for P V a thread owns a channel.
+// fp32: the same with plain FFMA.
 #include "decode.cuh"
 #include "gather.cuh"
 
@@ -132,7 +131,7 @@ struct Cut {
 // SM.
 struct alignas(16) AttnScratch {
   float2 ml[32];        // a head's base (log2 units) and sum, joined over the CTA's warps
-  float m[4][32], l[4][32];   // bf16: the warps' own; m becomes their weights
+  float m[4][32], l[4][32];   // the warps' own; m becomes their weights
   int64_t warp_sum[kAttnThreads / 32];
   int64_t row;
   int64_t off;
@@ -212,6 +211,46 @@ __device__ __forceinline__ void put_join_item(const Pieces& ps, int64_t at, int 
     it.skip = skip;
     ps.items[at] = it;
   }
+}
+
+// Adds up the warps' parts: o [4 warps][H][PITCH] in the tiles and the heads'
+// bases and sums in sc.m, sc.l.  Leaves o [H][PITCH] at the start of the tiles
+// and the joined bases and sums in sc.ml; a barrier on entry and at the end.
+template <int H, int D, int PITCH>
+__device__ __forceinline__ void join_warps(unsigned char* tiles, AttnScratch& sc) {
+  constexpr int WARPS = kAttnThreads / 32;
+  if (threadIdx.x < H) {
+    const int h = threadIdx.x;
+    float mm = -INFINITY, sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) mm = fmaxf(mm, sc.m[w][h]);
+    const float base = mm == -INFINITY ? 0.f : mm;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+      const float f = exp2f(sc.m[w][h] - base);
+      sc.m[w][h] = f;
+      sum += f * sc.l[w][h];
+    }
+    sc.ml[h] = make_float2(mm, sum);
+  }
+  __syncthreads();
+  float4* o4 = reinterpret_cast<float4*>(tiles);
+#pragma unroll
+  for (int i = threadIdx.x; i < H * D / 4; i += kAttnThreads) {
+    const int h = i / (D / 4), at = h * (PITCH / 4) + i % (D / 4);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+      const float f = sc.m[w][h];
+      const float4 x = o4[w * H * (PITCH / 4) + at];
+      acc.x += f * x.x;
+      acc.y += f * x.y;
+      acc.z += f * x.z;
+      acc.w += f * x.w;
+    }
+    o4[at] = acc;   // in place: warp 0's part, this thread's own element
+  }
+  __syncthreads();
 }
 
 // ------------------------------------------------------------------- bf16
@@ -538,225 +577,275 @@ __device__ __forceinline__ void attn_piece_bf16(const PagedView& pv, const __nv_
       *reinterpret_cast<float2*>(my + (g + 8) * G::PITCH + c * 8 + 2 * qi) = make_float2(o[n][c][2], o[n][c][3]);
     }
   }
-  if (threadIdx.x < NG * 16) {
-    const int h = threadIdx.x;
-    float mm = -INFINITY, sum = 0.f;
-#pragma unroll
-    for (int w = 0; w < WARPS; ++w) mm = fmaxf(mm, sc.m[w][h]);
-    const float base = mm == -INFINITY ? 0.f : mm;
-#pragma unroll
-    for (int w = 0; w < WARPS; ++w) {
-      const float f = ex2_approx(sc.m[w][h] - base);
-      sc.m[w][h] = f;
-      sum += f * sc.l[w][h];
-    }
-    sc.ml[h] = make_float2(mm, sum);
-  }
-  __syncthreads();
-  float4* o4 = reinterpret_cast<float4*>(tiles);
-#pragma unroll
-  for (int i = threadIdx.x; i < NG * 16 * D / 4; i += kAttnThreads) {
-    const int h = i / (D / 4), at = h * (G::PITCH / 4) + i % (D / 4);
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int w = 0; w < WARPS; ++w) {
-      const float f = sc.m[w][h];
-      const float4 x = o4[w * NG * 16 * (G::PITCH / 4) + at];
-      acc.x += f * x.x;
-      acc.y += f * x.y;
-      acc.z += f * x.z;
-      acc.w += f * x.w;
-    }
-    o4[at] = acc;   // in place: warp 0's part, this thread's own element
-  }
-  __syncthreads();
+  join_warps<NG * 16, D, G::PITCH>(tiles, sc);
 }
 
 // ------------------------------------------------------------------- fp32 (FFMA)
-constexpr int kF32Keys = 32;        // keys per tile (8 slots, two steps)
-
-template <int D>
+// As in bf16, a warp takes every 4th step with a ring of its own, here in halves
+// of 8 keys (2 slots).  Bound by FFMAs where there are more than about 20 heads
+// (4*Hq*d flops for 8*d bytes a key), so the tiles are chosen to keep the loads
+// from shared memory below them:
+//   S: a lane has 2 keys (one of each slot) and MAXH/8 heads; rows are padded
+//      by 16 bytes, so that the 4 key rows and the 8 head rows that a warp
+//      reads at once lie in different banks, and the other lanes' copies are
+//      broadcasts;
+//   P V: a lane has D/32 channels of all heads; p is read as broadcast float4s.
+// (One key and a quarter of the heads per lane, tiles shared by the CTA and
+// three barriers a tile: 242 us against TODO for 114 ragged rows, 32 heads.)
+template <int D, int MAXH>
 struct F32Cfg {
-  static constexpr int PITCH = D + 4;                       // floats per row: 16-byte rows, conflict-free columns
-  static constexpr int STAGE = 2 * kF32Keys * PITCH;        // K and V of a tile, floats
-  static constexpr int TILES = 2 * STAGE * 4;               // two stages, bytes
-  static int smem(int Hq) {                                 // + q [Hq][D], p [Hq][36], alpha [Hq], vis [2][8]
-    return TILES + 4 * Hq * (D + 36 + 1) + 64 + 16 + (int)sizeof(AttnScratch);
-  }
-  static_assert(TILES >= 32 * D * 4, "the tiles double as the result buffer");
+  static constexpr int WARPS = kAttnThreads / 32;
+  static constexpr int CTAS = D == 128 ? 2 : 3;             // per SM
+  static constexpr int NST = D == 128 ? 2 : 3;
+  static constexpr int KEYS = 8;
+  static constexpr int PITCH = D + 4;                       // floats per K, V or Q row
+  static constexpr int STAGE = 2 * KEYS * PITCH;            // K and V of half a step, floats
+  static constexpr int PP = MAXH == 8 ? 8 : MAXH + 8;       // floats per key of p: stores without bank conflicts
+  static constexpr int Q_AT = WARPS * NST * STAGE;          // floats: rings, Q, p, rescale factors
+  static constexpr int P_AT = Q_AT + MAXH * PITCH;
+  static constexpr int A_AT = P_AT + WARPS * KEYS * PP;
+  static constexpr int JOIN = WARPS * MAXH * D * 4;         // bytes
+  static constexpr int INBOX_BYTES = 16 * (MAXH * (D / 4) + 256) + 8 * 16 * MAXH;
+  static constexpr int USED = 4 * (A_AT + WARPS * MAXH);
+  static constexpr int TILES = (USED > JOIN + INBOX_BYTES ? USED : JOIN + INBOX_BYTES) + 15 & ~15;
+  static constexpr int SMEM = TILES + (int)sizeof(AttnScratch);
 };
 
-// MAXH: heads, rounded up to 8, 16 or 32.  As attn_piece_bf16.
+// As attn_piece_bf16; heads from Hq to MAXH are computed as zeros.
 template <int D, int MAXH, bool SEL>
 __device__ __forceinline__ void attn_piece_f32(const PagedView& pv, const float* __restrict__ Q,
                                                const float* __restrict__ K, const float* __restrict__ V,
                                                const SlotRow& sr, int64_t b, int w0, int steps, int Hq,
                                                float scale_log2, unsigned char* tiles, AttnScratch& sc, bool arrive,
                                                bool& bad_page, bool& bad_idx) {
-  using F = F32Cfg<D>;
-  constexpr int HPW = MAXH / 4;                 // heads a warp scores
-  constexpr int GROUPS = kAttnThreads / D;      // thread groups over the heads in P V
-  constexpr int HPT = MAXH / GROUPS;            // heads a thread accumulates
-  constexpr int CH = D / 4;                     // 16-byte chunks per row
-  constexpr int RPI = 32 / CH;                  // rows a warp copies at once (1 or 2)
-  float* kv = reinterpret_cast<float*>(tiles);
-  float* qs = kv + 2 * F::STAGE;                // [Hq][D]
-  float* pt = qs + Hq * D;                      // [Hq][36]
-  int* vis = reinterpret_cast<int*>(pt + Hq * 36);   // [2][8]
-  float* alpha = reinterpret_cast<float*>(vis + 16); // [Hq]
+  using F = F32Cfg<D, MAXH>;
+  constexpr int NST = F::NST, WARPS = F::WARPS;
+  constexpr int HL = MAXH / 8;          // heads a lane scores: hp, hp + 8, ..
+  constexpr int VC = D / 32;            // channels a lane accumulates
+  constexpr int CH = D / 4;             // 16-byte chunks per row
+  constexpr int RPI = 32 / CH;          // rows a warp copies at once (1 or 2)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int c = threadIdx.x % D, grp = threadIdx.x / D;
-  for (int i = threadIdx.x; i < Hq * D / 4; i += kAttnThreads)
-    reinterpret_cast<float4*>(qs)[i] = __ldg(reinterpret_cast<const float4*>(Q + b * Hq * D) + i);
+  const int kg = lane & 3, hp = lane >> 2;
+  float* base = reinterpret_cast<float*>(tiles);
+  float* ring = base + warp * NST * F::STAGE;
+  float* qs = base + F::Q_AT;                              // [MAXH][PITCH]
+  float* pt = base + F::P_AT + warp * F::KEYS * F::PP;     // [8][PP]
+  float* al = base + F::A_AT + warp * MAXH;                // [MAXH]
 
-  // Slot pipeline: a warp copies slots 2*warp and 2*warp + 1 of every tile; lane
-  // (lane & 1) decides one of them, two tiles ahead for the idx entry, one for the page.
-  const int s_end = 4 * steps;
-  int raw = -1, pool = 0, rows = 0, page = 0;
-  auto slot_of = [&](int t) { return 4 * w0 + 8 * t + 2 * warp + (lane & 1); };
-  auto load_raw = [&](int t) { raw = slot_of(t) < s_end ? slot_idx<SEL>(sr, slot_of(t)) : -1; };
-  auto load_page = [&](int t) {
-    slot_pool_rows<SEL>(sr, slot_of(t), raw, pool, rows, bad_idx);
-    if (slot_of(t) >= s_end) rows = 0;
-    page = rows ? __ldg(sr.trow + page_of_pool(pv, pool)) : 0;
+  // Slot pipeline: half step i of this warp is slots 4 * step + 2 * (i & 1) and
+  // the next; lane (lane & 1) decides one of them.
+  int raw = -1, pool = 0, rows = 0, col = 0, page = 0;
+  auto step_of = [&](int i) { return w0 + warp + (i >> 1) * WARPS; };
+  auto slot_of = [&](int i) { return 4 * step_of(i) + 2 * (i & 1) + (lane & 1); };
+  auto load_raw = [&](int i) { raw = step_of(i) < steps ? slot_idx<SEL>(sr, slot_of(i)) : -1; };
+  auto load_page = [&](int i) {
+    slot_pool_rows<SEL>(sr, slot_of(i), raw, pool, rows, bad_idx);
+    if (step_of(i) >= steps) rows = 0;
+    col = page_of_pool(pv, pool);
+    page = rows ? __ldg(sr.trow + col) : 0;
   };
-  const int n_tiles = (steps - w0 + 1) >> 1;
-  auto fetch = [&](int t, int stage) {
-    if (t < n_tiles) {
+  uint32_t vis[NST];   // visible rows of the ring's half steps: 4 bits per slot
+  auto fetch = [&](int i, int stage, uint32_t& v) {
+    v = 0u;
+    if (step_of(i) < steps) {
       uint32_t mine = 0u;
       if (rows) {
-        const int pp = phys_pool(pv, pool, page_of_pool(pv, pool), page, bad_page);
+        const int pp = phys_pool(pv, pool, col, page, bad_page);
         if (pp >= 0) mine = ((uint32_t)pp << 3) | (uint32_t)rows;
       }
-      if (lane < 2) vis[stage * 8 + 2 * warp + lane] = (int)(mine & 7u);
-      float* dst0 = kv + stage * F::STAGE + 8 * warp * F::PITCH;
+      const uint32_t dst0 = smem_u32(ring + stage * F::STAGE + (lane / CH) * F::PITCH + 4 * (lane % CH));
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         const uint32_t slot = __shfl_sync(0xffffffffu, mine, s);
-        const int64_t row0 = (int64_t)(slot >> 3) * 4;
+        v |= (slot & 7u) << (4 * s);
+        const int64_t src = (int64_t)(slot >> 3) * 4 * D + (lane / CH) * D + 4 * (lane % CH);
 #pragma unroll
         for (int r = 0; r < 4; r += RPI) {
-          const int rr = r + lane / CH;
-          const uint32_t bytes = rr < (int)(slot & 7u) ? 16u : 0u;
-          const int64_t src = (row0 + rr) * D + 4 * (lane % CH);
-          const uint32_t dst = smem_u32(dst0 + (4 * s + rr) * F::PITCH + 4 * (lane % CH));
-          cp_async16(dst, K + src, bytes);
-          cp_async16(dst + kF32Keys * F::PITCH * 4, V + src, bytes);
+          const uint32_t bytes = r + lane / CH < (int)(slot & 7u) ? 16u : 0u;
+          const uint32_t dst = dst0 + (4 * s + r) * F::PITCH * 4;
+          cp_async16(dst, K + src + r * D, bytes);
+          cp_async16(dst + F::KEYS * F::PITCH * 4, V + src + r * D, bytes);
         }
       }
     }
     cp_async_commit();
   };
-  load_raw(0);
-  load_page(0);
-  load_raw(1);
-  fetch(0, 0);
-  load_page(1);
-  load_raw(2);
 
-  float m[HPW], l[HPW];
+  // start-up: idx entries, Q, pages, rows
+  int raws[NST], raw_next;
 #pragma unroll
-  for (int i = 0; i < HPW; ++i) {
-    m[i] = -INFINITY;
+  for (int i = 0; i < NST; ++i) {
+    load_raw(i);
+    raws[i] = raw;
+  }
+  load_raw(NST);
+  raw_next = raw;
+  for (int i = threadIdx.x; i < MAXH * CH; i += kAttnThreads) {
+    const int h = i / CH, c = i % CH;
+    cp_async16(smem_u32(qs + h * F::PITCH + 4 * c), Q + (b * Hq + (h < Hq ? h : 0)) * D + 4 * c, h < Hq ? 16u : 0u);
+  }
+  cp_async_commit();
+  if (SEL && sr.len == 0) steps = w0;   // an idle row
+  {
+    int pools[NST], rws[NST], cols[NST], pgs[NST];
+#pragma unroll
+    for (int i = 0; i < NST; ++i) {
+      raw = raws[i];
+      load_page(i);
+      pools[i] = pool;
+      rws[i] = rows;
+      cols[i] = col;
+      pgs[i] = page;
+    }
+#pragma unroll
+    for (int i = 0; i < NST; ++i) {
+      pool = pools[i];
+      rows = rws[i];
+      col = cols[i];
+      page = pgs[i];
+      if (i < NST - 1) fetch(i, i, vis[i]);
+    }
+    raw = raw_next;
+  }
+  cp_async_wait<NST - 1>();   // all but the rows: Q
+  __syncthreads();
+
+  float o[MAXH][VC];
+#pragma unroll
+  for (int h = 0; h < MAXH; ++h)
+#pragma unroll
+    for (int c = 0; c < VC; ++c) o[h][c] = 0.f;
+  float m[HL], l[HL], top[HL];
+#pragma unroll
+  for (int i = 0; i < HL; ++i) {
+    m[i] = top[i] = -INFINITY;
     l[i] = 0.f;
   }
-  float o[HPT];
+  int stage = 0;
+  for (int it = 0; step_of(it) < steps; ++it) {
+    fetch(it + NST - 1, stage == 0 ? NST - 1 : stage - 1, vis[NST - 1]);   // the stage consumed last
+    load_page(it + NST);
+    load_raw(it + NST + 1);
+    cp_async_wait<NST - 1>();
+    __syncwarp();
+    const float* ks = ring + stage * F::STAGE;
+    const float* vs = ks + F::KEYS * F::PITCH;
+    // scores of keys kg and kg + 4
+    float s[2][HL];
 #pragma unroll
-  for (int i = 0; i < HPT; ++i) o[i] = 0.f;
-  for (int t = 0; t < n_tiles; ++t) {
-    const int stage = t & 1;
-    fetch(t + 1, stage ^ 1);
-    load_page(t + 2);
-    load_raw(t + 3);
-    cp_async_wait<1>();
-    __syncthreads();
-    const float* ks = kv + stage * F::STAGE;
-    const float* vs = ks + kF32Keys * F::PITCH;
-    // scores: this lane's key, this warp's heads warp, warp + 4, ..
+    for (int i = 0; i < HL; ++i) s[0][i] = s[1][i] = 0.f;
     {
-      float s[HPW];
-#pragma unroll
-      for (int i = 0; i < HPW; ++i) s[i] = 0.f;
-      const float4* kr = reinterpret_cast<const float4*>(ks + lane * F::PITCH);
+      const float4* k0 = reinterpret_cast<const float4*>(ks + kg * F::PITCH);
+      const float4* k1 = reinterpret_cast<const float4*>(ks + (kg + 4) * F::PITCH);
+      const float4* q0 = reinterpret_cast<const float4*>(qs + hp * F::PITCH);
 #pragma unroll 4
-      for (int x = 0; x < D / 4; ++x) {
-        const float4 kk = kr[x];
+      for (int x = 0; x < CH; ++x) {
+        const float4 a = k0[x], c = k1[x];
 #pragma unroll
-        for (int i = 0; i < HPW; ++i) {
-          const int h = warp + 4 * i;
-          if (h < Hq) {
-            const float4 qq = reinterpret_cast<const float4*>(qs + h * D)[x];
-            s[i] = fmaf(qq.x, kk.x, s[i]);
-            s[i] = fmaf(qq.y, kk.y, s[i]);
-            s[i] = fmaf(qq.z, kk.z, s[i]);
-            s[i] = fmaf(qq.w, kk.w, s[i]);
-          }
-        }
-      }
-      const bool seen = (lane & 3) < vis[stage * 8 + (lane >> 2)];
-#pragma unroll
-      for (int i = 0; i < HPW; ++i) {
-        const int h = warp + 4 * i;
-        if (h < Hq) {
-          const float z = seen ? s[i] * scale_log2 : -INFINITY;
-          float mx = z;
-#pragma unroll
-          for (int w = 16; w; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
-          const bool up = mx > m[i] + kDecLazyLog2;
-          const float mn = up ? mx : m[i];
-          const float base = mn == -INFINITY ? 0.f : mn;
-          const float a = up ? exp2f(m[i] - base) : 1.f;
-          m[i] = mn;
-          const float p = exp2f(z - base);
-          l[i] = l[i] * a + p;   // this lane's share of the sum
-          pt[h * 36 + lane] = p;
-          if (lane == 0) alpha[h] = a;
+        for (int i = 0; i < HL; ++i) {
+          const float4 q = q0[i * 8 * (F::PITCH / 4) + x];
+          s[0][i] = fmaf(q.x, a.x, s[0][i]);
+          s[1][i] = fmaf(q.x, c.x, s[1][i]);
+          s[0][i] = fmaf(q.y, a.y, s[0][i]);
+          s[1][i] = fmaf(q.y, c.y, s[1][i]);
+          s[0][i] = fmaf(q.z, a.z, s[0][i]);
+          s[1][i] = fmaf(q.z, c.z, s[1][i]);
+          s[0][i] = fmaf(q.w, a.w, s[0][i]);
+          s[1][i] = fmaf(q.w, c.w, s[1][i]);
         }
       }
     }
-    __syncthreads();
-    // P V: this thread's channel, heads grp, grp + GROUPS, ..
+    // softmax with a lazily moved base, as in attn_piece_bf16
+    const bool see0 = kg < (int)(vis[0] & 7u), see1 = kg < (int)(vis[0] >> 4 & 7u);
+    bool over = false;
 #pragma unroll
-    for (int i = 0; i < HPT; ++i) {
-      const int h = grp + GROUPS * i;
-      if (h < Hq) o[i] *= alpha[h];
+    for (int i = 0; i < HL; ++i) {
+      s[0][i] = see0 ? s[0][i] : -INFINITY;
+      s[1][i] = see1 ? s[1][i] : -INFINITY;
+      over |= fmaxf(s[0][i], s[1][i]) > top[i];
     }
+    if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+      for (int i = 0; i < HL; ++i) {
+        float x = fmaxf(s[0][i], s[1][i]);
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+        const float mn = x > top[i] ? x * scale_log2 : m[i];
+        const float f = mn == m[i] ? 1.f : exp2f(m[i] - mn);
+        m[i] = mn;
+        if (x > top[i]) top[i] = x + kDecLazyLog2 / scale_log2;
+        l[i] *= f;
+        if (kg == 0) al[hp + 8 * i] = f;
+      }
+      __syncwarp();
+#pragma unroll
+      for (int h = 0; h < MAXH; ++h) {
+        const float f = al[h];
+#pragma unroll
+        for (int c = 0; c < VC; ++c) o[h][c] *= f;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < HL; ++i) {
+      const float bs = m[i] == -INFINITY ? 0.f : m[i];
+      const float p0 = exp2f(fmaf(s[0][i], scale_log2, -bs)), p1 = exp2f(fmaf(s[1][i], scale_log2, -bs));
+      l[i] += p0 + p1;
+      pt[kg * F::PP + hp + 8 * i] = p0;
+      pt[(kg + 4) * F::PP + hp + 8 * i] = p1;
+    }
+    __syncwarp();
 #pragma unroll 2
-    for (int j = 0; j < kF32Keys; j += 4) {
-      float v[4];
+    for (int j = 0; j < F::KEYS; ++j) {
+      float v[VC];
+      if (VC == 4) {
+        const float4 x = *reinterpret_cast<const float4*>(vs + j * F::PITCH + 4 * lane);
+        v[0] = x.x;
+        v[1] = x.y;
+        v[VC - 2] = x.z;
+        v[VC - 1] = x.w;
+      } else {
+        const float2 x = *reinterpret_cast<const float2*>(vs + j * F::PITCH + 2 * lane);
+        v[0] = x.x;
+        v[1] = x.y;
+      }
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = vs[(j + e) * F::PITCH + c];
+      for (int h = 0; h < MAXH; h += 4) {
+        const float4 p = *reinterpret_cast<const float4*>(pt + j * F::PP + h);
 #pragma unroll
-      for (int i = 0; i < HPT; ++i) {
-        const int h = grp + GROUPS * i;
-        if (h < Hq) {
-          const float4 p = *reinterpret_cast<const float4*>(pt + h * 36 + j);
-          o[i] = fmaf(p.x, v[0], o[i]);
-          o[i] = fmaf(p.y, v[1], o[i]);
-          o[i] = fmaf(p.z, v[2], o[i]);
-          o[i] = fmaf(p.w, v[3], o[i]);
+        for (int c = 0; c < VC; ++c) {
+          o[h][c] = fmaf(p.x, v[c], o[h][c]);
+          o[h + 1][c] = fmaf(p.y, v[c], o[h + 1][c]);
+          o[h + 2][c] = fmaf(p.z, v[c], o[h + 2][c]);
+          o[h + 3][c] = fmaf(p.w, v[c], o[h + 3][c]);
         }
       }
     }
-    __syncthreads();   // the stage, p and alpha are free again
+    __syncwarp();   // the stage and p are free again
+#pragma unroll
+    for (int i = 0; i + 1 < NST; ++i) vis[i] = vis[i + 1];
+    stage = stage == NST - 1 ? 0 : stage + 1;
   }
   cp_async_wait<0>();
-  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < HL; ++i) {
+    l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+    l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+    if (kg == 0) {
+      sc.m[warp][hp + 8 * i] = m[i];
+      sc.l[warp][hp + 8 * i] = l[i];
+    }
+  }
+  __syncthreads();   // every ring is idle: the tiles are the join buffer, [warp][MAXH][D]
   if (arrive) cluster_arrive();
 #pragma unroll
-  for (int i = 0; i < HPT; ++i) {
-    const int h = grp + GROUPS * i;
-    if (h < Hq) kv[h * D + c] = o[i];
+  for (int h = 0; h < MAXH; ++h) {
+    float* my = base + (warp * MAXH + h) * D + VC * lane;
+    if (VC == 4)
+      *reinterpret_cast<float4*>(my) = make_float4(o[h][0], o[h][1], o[h][VC - 2], o[h][VC - 1]);
+    else
+      *reinterpret_cast<float2*>(my) = make_float2(o[h][0], o[h][1]);
   }
-#pragma unroll
-  for (int i = 0; i < HPW; ++i) {
-    const int h = warp + 4 * i;
-    float sum = l[i];
-#pragma unroll
-    for (int w = 16; w; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
-    if (h < Hq && lane == 0) sc.ml[h] = make_float2(m[i], sum);
-  }
-  __syncthreads();
+  join_warps<MAXH, D, D>(tiles, sc);
 }
 
 // ------------------------------------------------------------------- kernels
@@ -784,10 +873,7 @@ struct Piece<__nv_bfloat16, D, MAXH, SEL> {
   static constexpr int PITCH = G::PITCH;   // floats per head of the result
   static constexpr int INBOX = G::JOIN;    // where the tiles are free behind the join
   static constexpr int TILES = G::TILES;
-  static int smem(int) { return G::SMEM; }
-  static __device__ __forceinline__ AttnScratch& scratch(unsigned char* smem, int) {
-    return *reinterpret_cast<AttnScratch*>(smem + G::TILES);
-  }
+  static constexpr int SMEM = G::SMEM;
   static __device__ __forceinline__ void run(const AttnArgs<__nv_bfloat16>& a, const SlotRow& sr, int64_t b, int w0,
                                              int steps, unsigned char* smem, AttnScratch& sc, bool arrive,
                                              bool& bad_page, bool& bad_idx) {
@@ -797,19 +883,18 @@ struct Piece<__nv_bfloat16, D, MAXH, SEL> {
 };
 template <int D, int MAXH, bool SEL>
 struct Piece<float, D, MAXH, SEL> {
-  static constexpr int MIN_STEPS = 2;
-  static constexpr int CTAS = 2;
+  using F = F32Cfg<D, MAXH>;
+  static constexpr int MIN_STEPS = F::WARPS;
+  static constexpr int CTAS = F::CTAS;
   static constexpr int PITCH = D;
-  static constexpr int INBOX = MAXH * D * 4;
-  static constexpr int TILES = F32Cfg<D>::TILES;
-  static int smem(int Hq) { return F32Cfg<D>::smem(Hq); }
-  static __device__ __forceinline__ AttnScratch& scratch(unsigned char* smem, int Hq) {
-    return *reinterpret_cast<AttnScratch*>(smem + ((F32Cfg<D>::TILES + 4 * Hq * (D + 36 + 1) + 64 + 15) & ~15));
-  }
+  static constexpr int INBOX = F::JOIN;
+  static constexpr int TILES = F::TILES;
+  static constexpr int SMEM = F::SMEM;
   static __device__ __forceinline__ void run(const AttnArgs<float>& a, const SlotRow& sr, int64_t b, int w0, int steps,
                                              unsigned char* smem, AttnScratch& sc, bool arrive, bool& bad_page,
                                              bool& bad_idx) {
-    attn_piece_f32<D, MAXH, SEL>(a.pv, a.Q, a.K, a.V, sr, b, w0, steps, a.Hq, a.scale_log2, smem, sc, arrive, bad_page, bad_idx);
+    attn_piece_f32<D, MAXH, SEL>(a.pv, a.Q, a.K, a.V, sr, b, w0, steps, a.Hq, a.scale_log2, smem, sc, arrive, bad_page,
+                                 bad_idx);
   }
 };
 
@@ -846,7 +931,7 @@ __global__ void __launch_bounds__(kAttnThreads, (Piece<T, D, MAXH, true>::CTAS))
     decode_attn_selected_kernel(const __grid_constant__ AttnArgs<T> a) {
   using P = Piece<T, D, MAXH, true>;
   extern __shared__ __align__(128) unsigned char dec_smem[];
-  AttnScratch& sc = P::scratch(dec_smem, a.Hq);
+  AttnScratch& sc = *reinterpret_cast<AttnScratch*>(dec_smem + P::TILES);
   chain_wait();
   chain_release();
   const int64_t b = blockIdx.y;
@@ -923,7 +1008,7 @@ __global__ void __launch_bounds__(kAttnThreads, (Piece<T, D, MAXH, false>::CTAS)
     decode_attn_all_kernel(const __grid_constant__ AttnArgs<T> a) {
   using P = Piece<T, D, MAXH, false>;
   extern __shared__ __align__(128) unsigned char dec_smem[];
-  AttnScratch& sc = P::scratch(dec_smem, a.Hq);
+  AttnScratch& sc = *reinterpret_cast<AttnScratch*>(dec_smem + P::TILES);
   chain_wait();
   const Cut cut = make_cut(a.pv, a.batch, P::MIN_STEPS, sc);
   const bool by_row = a.batch <= gridDim.x;
@@ -1080,21 +1165,21 @@ static cudaError_t launch_shape(const AttnArgs<T>& a, cudaStream_t s) {
     auto kern = decode_attn_selected_kernel<T, D, MAXH>;
     const unsigned splits = selected_splits(a.batch, (a.k + 4) >> 2, P::MIN_STEPS, kSms * P::CTAS);
     static std::atomic<uint64_t> done{0};
-    cudaError_t e = prepare_kernel(kern, P::smem(MAXH), true, done);
+    cudaError_t e = prepare_kernel(kern, P::SMEM, true, done);
     if (e != cudaSuccess) return e;
-    return launch_chained_cluster(splits, kern, dim3(splits, (unsigned)a.batch), dim3(kAttnThreads), P::smem(a.Hq),
+    return launch_chained_cluster(splits, kern, dim3(splits, (unsigned)a.batch), dim3(kAttnThreads), P::SMEM,
                                   s, a);
   }
   using P = Piece<T, D, MAXH, false>;
   auto kern = decode_attn_all_kernel<T, D, MAXH>;
   static std::atomic<uint64_t> done{0};
-  cudaError_t e = prepare_kernel(kern, P::smem(MAXH), false, done);
+  cudaError_t e = prepare_kernel(kern, P::SMEM, false, done);
   if (e != cudaSuccess) return e;
   // as many CTAs as can have work
   const int64_t row_max = ((int64_t)a.pv.capacity + 15) >> 4;
   const int64_t want = a.batch * ((row_max + kRowPad + P::MIN_STEPS - 1) / P::MIN_STEPS);
   const unsigned ctas = (unsigned)(want < kSms * P::CTAS ? want : kSms * P::CTAS);
-  e = launch_chained(kern, dim3(ctas), dim3(kAttnThreads), P::smem(a.Hq), s, a);
+  e = launch_chained(kern, dim3(ctas), dim3(kAttnThreads), P::SMEM, s, a);
   if (e != cudaSuccess || ctas == 1) return e;
   // few rows, so many pieces of each: the columns of a head are split too
   const unsigned items = a.batch < ctas ? (unsigned)a.batch : ctas;
