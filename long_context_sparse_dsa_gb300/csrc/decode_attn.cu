@@ -585,13 +585,16 @@ __device__ __forceinline__ void attn_piece_bf16(const PagedView& pv, const __nv_
 // of 8 keys (2 slots).  Bound by FFMAs where there are more than about 20 heads
 // (4*Hq*d flops for 8*d bytes a key), so the tiles are chosen to keep the loads
 // from shared memory below them:
-//   S: a lane has 2 keys (one of each slot) and MAXH/8 heads; rows are padded
-//      by 16 bytes, so that the 4 key rows and the 8 head rows that a warp
-//      reads at once lie in different banks, and the other lanes' copies are
-//      broadcasts;
+//   S: a quarter of the lanes takes every 4th 16-byte chunk of d, a lane of it
+//      4 keys and MAXH/4 heads; the quarters' sums are then scattered, one key
+//      to a lane.  (With 2 keys and MAXH/8 heads over all of d, twice the
+//      shared-memory loads per FFMA: 142 us against 129 for 114 ragged rows of
+//      32 heads; one row of 100k tokens, 16 heads of 64: 25.5 against 24.4.)
+//      Rows are padded by 16 bytes, so that the key rows and the head rows a
+//      quarter reads at once lie in different banks;
 //   P V: a lane has D/32 channels of all heads; p is read as broadcast float4s.
 // (One key and a quarter of the heads per lane, tiles shared by the CTA and
-// three barriers a tile: 242 us against TODO for 114 ragged rows, 32 heads.)
+// three barriers a tile: 242 us for the same 114 rows.)
 template <int D, int MAXH>
 struct F32Cfg {
   static constexpr int WARPS = kAttnThreads / 32;
@@ -600,7 +603,7 @@ struct F32Cfg {
   static constexpr int KEYS = 8;
   static constexpr int PITCH = D + 4;                       // floats per K, V or Q row
   static constexpr int STAGE = 2 * KEYS * PITCH;            // K and V of half a step, floats
-  static constexpr int PP = MAXH == 8 ? 8 : MAXH + 8;       // floats per key of p: stores without bank conflicts
+  static constexpr int PP = MAXH + 4;                       // floats per key of p: stores without bank conflicts
   static constexpr int Q_AT = WARPS * NST * STAGE;          // floats: rings, Q, p, rescale factors
   static constexpr int P_AT = Q_AT + MAXH * PITCH;
   static constexpr int A_AT = P_AT + WARPS * KEYS * PP;
@@ -620,12 +623,13 @@ __device__ __forceinline__ void attn_piece_f32(const PagedView& pv, const float*
                                                bool& bad_page, bool& bad_idx) {
   using F = F32Cfg<D, MAXH>;
   constexpr int NST = F::NST, WARPS = F::WARPS;
-  constexpr int HL = MAXH / 8;          // heads a lane scores: hp, hp + 8, ..
+  constexpr int HL = MAXH / 4;          // heads a lane scores: hg, hg + 4, ..
   constexpr int VC = D / 32;            // channels a lane accumulates
   constexpr int CH = D / 4;             // 16-byte chunks per row
   constexpr int RPI = 32 / CH;          // rows a warp copies at once (1 or 2)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int kg = lane & 3, hp = lane >> 2;
+  const int hg = lane & 3, kg = (lane >> 2) & 1, quarter = lane >> 3;
+  const int key = kg + ((lane >> 3) & 1) * 2 + (lane >> 4) * 4;   // the key this lane ends up with
   float* base = reinterpret_cast<float*>(tiles);
   float* ring = base + warp * NST * F::STAGE;
   float* qs = base + F::Q_AT;                              // [MAXH][PITCH]
@@ -715,10 +719,10 @@ __device__ __forceinline__ void attn_piece_f32(const PagedView& pv, const float*
   for (int h = 0; h < MAXH; ++h)
 #pragma unroll
     for (int c = 0; c < VC; ++c) o[h][c] = 0.f;
-  float m[HL], l[HL], top[HL];
+  float m[HL], l[HL];   // base (log2 units) and this lane's share of the sum
 #pragma unroll
   for (int i = 0; i < HL; ++i) {
-    m[i] = top[i] = -INFINITY;
+    m[i] = -INFINITY;
     l[i] = 0.f;
   }
   int stage = 0;
@@ -730,52 +734,60 @@ __device__ __forceinline__ void attn_piece_f32(const PagedView& pv, const float*
     __syncwarp();
     const float* ks = ring + stage * F::STAGE;
     const float* vs = ks + F::KEYS * F::PITCH;
-    // scores of keys kg and kg + 4
-    float s[2][HL];
+    // scores: keys kg, kg + 2, .. over this quarter's chunks
+    float s[4][HL];
 #pragma unroll
-    for (int i = 0; i < HL; ++i) s[0][i] = s[1][i] = 0.f;
+    for (int i = 0; i < HL; ++i) s[0][i] = s[1][i] = s[2][i] = s[3][i] = 0.f;
     {
-      const float4* k0 = reinterpret_cast<const float4*>(ks + kg * F::PITCH);
-      const float4* k1 = reinterpret_cast<const float4*>(ks + (kg + 4) * F::PITCH);
-      const float4* q0 = reinterpret_cast<const float4*>(qs + hp * F::PITCH);
-#pragma unroll 4
-      for (int x = 0; x < CH; ++x) {
-        const float4 a = k0[x], c = k1[x];
+      const float4* k0 = reinterpret_cast<const float4*>(ks + kg * F::PITCH) + quarter;
+      const float4* q0 = reinterpret_cast<const float4*>(qs + hg * F::PITCH) + quarter;
+#pragma unroll
+      for (int x = 0; x < CH; x += 4) {
+        float4 kk[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) kk[j] = k0[2 * j * (F::PITCH / 4) + x];
 #pragma unroll
         for (int i = 0; i < HL; ++i) {
-          const float4 q = q0[i * 8 * (F::PITCH / 4) + x];
-          s[0][i] = fmaf(q.x, a.x, s[0][i]);
-          s[1][i] = fmaf(q.x, c.x, s[1][i]);
-          s[0][i] = fmaf(q.y, a.y, s[0][i]);
-          s[1][i] = fmaf(q.y, c.y, s[1][i]);
-          s[0][i] = fmaf(q.z, a.z, s[0][i]);
-          s[1][i] = fmaf(q.z, c.z, s[1][i]);
-          s[0][i] = fmaf(q.w, a.w, s[0][i]);
-          s[1][i] = fmaf(q.w, c.w, s[1][i]);
+          const float4 q = q0[4 * i * (F::PITCH / 4) + x];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            s[j][i] = fmaf(q.x, kk[j].x, s[j][i]);
+            s[j][i] = fmaf(q.y, kk[j].y, s[j][i]);
+            s[j][i] = fmaf(q.z, kk[j].z, s[j][i]);
+            s[j][i] = fmaf(q.w, kk[j].w, s[j][i]);
+          }
         }
       }
     }
+    // add the quarters up, halving the keys a lane holds: 4 -> 2 -> 1
+    float z[HL];
+#pragma unroll
+    for (int i = 0; i < HL; ++i) {
+      const bool up = (lane & 16) != 0, up2 = (lane & 8) != 0;
+      const float a = (up ? s[2][i] : s[0][i]) + __shfl_xor_sync(0xffffffffu, up ? s[0][i] : s[2][i], 16);
+      const float c = (up ? s[3][i] : s[1][i]) + __shfl_xor_sync(0xffffffffu, up ? s[1][i] : s[3][i], 16);
+      z[i] = (up2 ? c : a) + __shfl_xor_sync(0xffffffffu, up2 ? a : c, 8);
+    }
     // softmax with a lazily moved base, as in attn_piece_bf16
-    const bool see0 = kg < (int)(vis[0] & 7u), see1 = kg < (int)(vis[0] >> 4 & 7u);
+    const bool seen = (key & 3) < (int)(vis[0] >> (key & 4) & 7u);
     bool over = false;
 #pragma unroll
     for (int i = 0; i < HL; ++i) {
-      s[0][i] = see0 ? s[0][i] : -INFINITY;
-      s[1][i] = see1 ? s[1][i] : -INFINITY;
-      over |= fmaxf(s[0][i], s[1][i]) > top[i];
+      z[i] = seen ? z[i] * scale_log2 : -INFINITY;
+      over |= z[i] > m[i] + kDecLazyLog2;
     }
     if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
       for (int i = 0; i < HL; ++i) {
-        float x = fmaxf(s[0][i], s[1][i]);
-        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-        const float mn = x > top[i] ? x * scale_log2 : m[i];
+        float x = z[i];
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+        const float mn = x > m[i] + kDecLazyLog2 ? x : m[i];
         const float f = mn == m[i] ? 1.f : exp2f(m[i] - mn);
         m[i] = mn;
-        if (x > top[i]) top[i] = x + kDecLazyLog2 / scale_log2;
         l[i] *= f;
-        if (kg == 0) al[hp + 8 * i] = f;
+        if (key == 0) al[hg + 4 * i] = f;
       }
       __syncwarp();
 #pragma unroll
@@ -787,11 +799,9 @@ __device__ __forceinline__ void attn_piece_f32(const PagedView& pv, const float*
     }
 #pragma unroll
     for (int i = 0; i < HL; ++i) {
-      const float bs = m[i] == -INFINITY ? 0.f : m[i];
-      const float p0 = exp2f(fmaf(s[0][i], scale_log2, -bs)), p1 = exp2f(fmaf(s[1][i], scale_log2, -bs));
-      l[i] += p0 + p1;
-      pt[kg * F::PP + hp + 8 * i] = p0;
-      pt[(kg + 4) * F::PP + hp + 8 * i] = p1;
+      const float p = exp2f(z[i] - (m[i] == -INFINITY ? 0.f : m[i]));
+      l[i] += p;
+      pt[key * F::PP + hg + 4 * i] = p;
     }
     __syncwarp();
 #pragma unroll 2
@@ -828,11 +838,11 @@ __device__ __forceinline__ void attn_piece_f32(const PagedView& pv, const float*
   cp_async_wait<0>();
 #pragma unroll
   for (int i = 0; i < HL; ++i) {
-    l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-    l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-    if (kg == 0) {
-      sc.m[warp][hp + 8 * i] = m[i];
-      sc.l[warp][hp + 8 * i] = l[i];
+#pragma unroll
+    for (int w = 4; w <= 16; w *= 2) l[i] += __shfl_xor_sync(0xffffffffu, l[i], w);
+    if (key == 0) {
+      sc.m[warp][hg + 4 * i] = m[i];
+      sc.l[warp][hg + 4 * i] = l[i];
     }
   }
   __syncthreads();   // every ring is idle: the tiles are the join buffer, [warp][MAXH][D]
