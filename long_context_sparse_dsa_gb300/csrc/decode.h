@@ -41,21 +41,60 @@ inline PagedView make_paged_view(const int32_t* lens, const int32_t* table, int6
   return v;
 }
 
-// Sets a kernel's dynamic shared memory limit (and, for clusters above 8, the
-// permission) the first time it is launched on a device: each such call costs
-// a launch about half a microsecond of host time.  `done` is the kernel's own
-// flag word, one bit per device.
-template <typename K>
-inline cudaError_t prepare_kernel(K* kern, int smem, bool big_clusters, std::atomic<uint64_t>& done) {
-  int dev = 0;
+// What a kernel's launches need to know, found the first time that it is
+// launched on a device (each of these calls costs a launch half a microsecond
+// of host time and more).  One of these, static, per kernel.
+struct KernelState {
+  static constexpr int DEVICES = 64;                 // beyond: found at every launch
+  std::atomic<uint64_t> done{0};                     // one bit per device
+  std::atomic<int> fit[DEVICES][17] = {};            // [n]: clusters of n CTAs resident at once, n = 1 .. 8, 16
+};
+
+// Sets the dynamic shared memory limit and, where `threads` is given, allows
+// clusters of 16 and asks how many clusters of each size are resident at once.
+// That is fewer than the CTAs would fill: a cluster lies within one group of
+// SMs, and what is left over in a group stays empty.  With 3 CTAs an SM there
+// is room for 456 CTAs, but for 59 clusters of 7 (413) and 21 of 16 (336).
+template <typename... P>
+inline cudaError_t prepare_kernel(void (*kern)(P...), int smem, unsigned threads, KernelState& st, int& dev) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  const uint64_t bit = dev < 64 ? (uint64_t)1 << dev : 0;
-  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  const uint64_t bit = dev < KernelState::DEVICES ? (uint64_t)1 << dev : 0;
+  dev %= KernelState::DEVICES;
+  if (st.done.load(std::memory_order_acquire) & bit) return cudaSuccess;
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e == cudaSuccess && big_clusters) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
-  return e;
+  if (e != cudaSuccess) return e;
+  if (threads) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    for (unsigned n = 1; e == cudaSuccess && n <= 16; n = n == 8 ? 16 : n + 1) {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(n);
+      cfg.blockDim = dim3(threads);
+      cfg.dynamicSmemBytes = smem;
+      cudaLaunchAttribute at;
+      at.id = cudaLaunchAttributeClusterDimension;
+      at.val.clusterDim.x = n;
+      at.val.clusterDim.y = at.val.clusterDim.z = 1;
+      cfg.attrs = &at;
+      cfg.numAttrs = 1;
+      int clusters = 0;
+      e = cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg);
+      st.fit[dev][n].store(clusters, std::memory_order_relaxed);
+    }
+    if (e != cudaSuccess) return e;
+  }
+  st.done.fetch_or(bit, std::memory_order_release);
+  return cudaSuccess;
+}
+
+// CTAs per row where a row is one cluster: the most, 1 .. 8 or 16 and no more
+// than `most`, with which all rows are resident at once.
+inline unsigned cluster_per_row(const KernelState& st, int dev, int64_t batch, int64_t most) {
+  auto fits = [&](int n) { return n <= most && st.fit[dev][n].load(std::memory_order_relaxed) >= batch; };
+  if (fits(16)) return 16;
+  for (int n = 8; n > 1; --n)
+    if (fits(n)) return (unsigned)n;
+  return 1;
 }
 
 // Launches `kern` so that it may become resident before its predecessor on

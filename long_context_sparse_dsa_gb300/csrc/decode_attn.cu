@@ -598,7 +598,7 @@ __device__ __forceinline__ void attn_piece_bf16(const PagedView& pv, const __nv_
 template <int D, int MAXH>
 struct F32Cfg {
   static constexpr int WARPS = kAttnThreads / 32;
-  static constexpr int CTAS = D == 128 ? 2 : 3;             // per SM
+  static constexpr int CTAS = D == 128 && MAXH > 8 ? 2 : 3;   // per SM
   static constexpr int NST = D == 128 ? 2 : 3;
   static constexpr int KEYS = 8;
   static constexpr int PITCH = D + 4;                       // floats per K, V or Q row
@@ -1158,32 +1158,25 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(Pieces ps, T*
   if (threadIdx.x == 0 && blockIdx.z == 0) LSE[(int64_t)it.row * Hq + h] = lse_of(mm, l);
 }
 
-// CTAs per row of selected pools (a cluster: 1 .. 8, or 16): the most that keep
-// all rows resident at once and give every warp a step.
-static unsigned selected_splits(int64_t batch, int n_steps, int min_steps, int resident) {
-  int64_t s = resident / batch;
-  const int64_t most = (n_steps + min_steps - 1) / min_steps;
-  if (s > most) s = most;
-  if (s >= 16) return 16;
-  return s > 8 ? 8 : s < 1 ? 1 : (unsigned)s;
-}
-
 template <typename T, int D, int MAXH>
 static cudaError_t launch_shape(const AttnArgs<T>& a, cudaStream_t s) {
   if (a.idx) {
     using P = Piece<T, D, MAXH, true>;
     auto kern = decode_attn_selected_kernel<T, D, MAXH>;
-    const unsigned splits = selected_splits(a.batch, (a.k + 4) >> 2, P::MIN_STEPS, kSms * P::CTAS);
-    static std::atomic<uint64_t> done{0};
-    cudaError_t e = prepare_kernel(kern, P::SMEM, true, done);
+    static KernelState st;
+    int dev;
+    cudaError_t e = prepare_kernel(kern, P::SMEM, kAttnThreads, st, dev);
     if (e != cudaSuccess) return e;
+    const int64_t row_steps = (a.k + 4) >> 2;   // a step for every warp
+    const unsigned splits = cluster_per_row(st, dev, a.batch, (row_steps + P::MIN_STEPS - 1) / P::MIN_STEPS);
     return launch_chained_cluster(splits, kern, dim3(splits, (unsigned)a.batch), dim3(kAttnThreads), P::SMEM,
                                   s, a);
   }
   using P = Piece<T, D, MAXH, false>;
   auto kern = decode_attn_all_kernel<T, D, MAXH>;
-  static std::atomic<uint64_t> done{0};
-  cudaError_t e = prepare_kernel(kern, P::SMEM, false, done);
+  static KernelState st;
+  int dev;
+  cudaError_t e = prepare_kernel(kern, P::SMEM, 0, st, dev);
   if (e != cudaSuccess) return e;
   // as many CTAs as can have work
   const int64_t row_max = ((int64_t)a.pv.capacity + 15) >> 4;

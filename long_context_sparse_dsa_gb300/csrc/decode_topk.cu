@@ -462,14 +462,12 @@ __global__ void __launch_bounds__(kSelThreads, 2)
 
 cudaError_t launch_decode_topk(const PagedView& pv, int64_t batch, int k, const float* scores, int64_t pitch,
                                int32_t* idx, cudaStream_t s) {
-  // CTAs per row: up to two a SM in all, and at least 2048 scores of the longest possible row for each
-  int64_t c = 2 * 152 / batch;
-  const int64_t most = ((int64_t)pv.capacity / 4 + 2047) / 2048;
-  if (c > most) c = most;
-  const unsigned ctas = c >= 16 ? 16 : c > 8 ? 8 : c < 1 ? 1 : (unsigned)c;
-  static std::atomic<uint64_t> done{0};
-  cudaError_t e = prepare_kernel(decode_topk_kernel, (int)sizeof(SelShared), true, done);
+  static KernelState st;
+  int dev;
+  cudaError_t e = prepare_kernel(decode_topk_kernel, (int)sizeof(SelShared), kSelThreads, st, dev);
   if (e != cudaSuccess) return e;
+  // at least 2048 scores of the longest possible row for each CTA
+  const unsigned ctas = cluster_per_row(st, dev, batch, ((int64_t)pv.capacity / 4 + 2047) / 2048);
   return launch_chained_cluster(ctas, decode_topk_kernel, dim3(ctas, (unsigned)batch), dim3(kSelThreads),
                                 sizeof(SelShared), s, pv, scores, pitch, k, idx);
 }
