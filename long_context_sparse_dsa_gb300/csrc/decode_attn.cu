@@ -214,10 +214,11 @@ __device__ __forceinline__ void put_join_item(const Pieces& ps, int64_t at, int 
 }
 
 // Adds up the warps' parts: o [4 warps][H][PITCH] in the tiles and the heads'
-// bases and sums in sc.m, sc.l.  Leaves o [H][PITCH] at the start of the tiles
-// and the joined bases and sums in sc.ml; a barrier on entry and at the end.
-template <int H, int D, int PITCH>
-__device__ __forceinline__ void join_warps(unsigned char* tiles, AttnScratch& sc) {
+// bases and sums in sc.m, sc.l.  Leaves the joined bases and sums in sc.ml, and
+// hands the sums on as they are formed: put(i, h, x, at) gets element group i of
+// [Hq][D/4], of head h; its place `at` in the first warp's part is free.
+template <int H, int D, int PITCH, typename Put>
+__device__ __forceinline__ void join_warps(unsigned char* tiles, AttnScratch& sc, int Hq, const Put& put) {
   constexpr int WARPS = kAttnThreads / 32;
   if (threadIdx.x < H) {
     const int h = threadIdx.x;
@@ -238,6 +239,7 @@ __device__ __forceinline__ void join_warps(unsigned char* tiles, AttnScratch& sc
 #pragma unroll
   for (int i = threadIdx.x; i < H * D / 4; i += kAttnThreads) {
     const int h = i / (D / 4), at = h * (PITCH / 4) + i % (D / 4);
+    if (h >= Hq) break;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < WARPS; ++w) {
@@ -248,9 +250,8 @@ __device__ __forceinline__ void join_warps(unsigned char* tiles, AttnScratch& sc
       acc.z += f * x.z;
       acc.w += f * x.w;
     }
-    o4[at] = acc;   // in place: warp 0's part, this thread's own element
+    put(i, h, acc, o4 + at);
   }
-  __syncthreads();
 }
 
 // ------------------------------------------------------------------- bf16
@@ -296,17 +297,18 @@ struct DecCfg {
   static_assert(TILES >= JOIN, "the rings double as the join buffer");
 };
 
-// Steps [w0, steps) of row b.  Leaves o [Hq][PITCH] at the start of the tiles
-// and the heads' bases and sums in sc.ml; ends with a __syncthreads().
+// Steps [w0, steps) of row b; the result goes on through put and sc.ml, as in
+// join_warps.
 // arrive: arrives at the cluster's barrier as soon as the tiles behind the
 // join buffer are no longer used.
 // SEL: the slots are selected pools; else all pools.
-template <int D, int NG, bool SEL>
+template <int D, int NG, bool SEL, typename Put>
 __device__ __forceinline__ void attn_piece_bf16(const PagedView& pv, const __nv_bfloat16* __restrict__ Q,
                                                 const __nv_bfloat16* __restrict__ K,
                                                 const __nv_bfloat16* __restrict__ V, const SlotRow& sr, int64_t b,
                                                 int w0, int steps, int Hq, float scale_log2, unsigned char* tiles,
-                                                AttnScratch& sc, bool arrive, bool& bad_page, bool& bad_idx) {
+                                                AttnScratch& sc, bool arrive, const Put& put, bool& bad_page,
+                                                bool& bad_idx) {
   using C = GatherCfg<D>;
   using G = DecCfg<D, NG, SEL>;
   constexpr int NST = G::NST;
@@ -577,7 +579,7 @@ __device__ __forceinline__ void attn_piece_bf16(const PagedView& pv, const __nv_
       *reinterpret_cast<float2*>(my + (g + 8) * G::PITCH + c * 8 + 2 * qi) = make_float2(o[n][c][2], o[n][c][3]);
     }
   }
-  join_warps<NG * 16, D, G::PITCH>(tiles, sc);
+  join_warps<NG * 16, D, G::PITCH>(tiles, sc, Hq, put);
 }
 
 // ------------------------------------------------------------------- fp32 (FFMA)
@@ -615,12 +617,12 @@ struct F32Cfg {
 };
 
 // As attn_piece_bf16; heads from Hq to MAXH are computed as zeros.
-template <int D, int MAXH, bool SEL>
+template <int D, int MAXH, bool SEL, typename Put>
 __device__ __forceinline__ void attn_piece_f32(const PagedView& pv, const float* __restrict__ Q,
                                                const float* __restrict__ K, const float* __restrict__ V,
                                                const SlotRow& sr, int64_t b, int w0, int steps, int Hq,
                                                float scale_log2, unsigned char* tiles, AttnScratch& sc, bool arrive,
-                                               bool& bad_page, bool& bad_idx) {
+                                               const Put& put, bool& bad_page, bool& bad_idx) {
   using F = F32Cfg<D, MAXH>;
   constexpr int NST = F::NST, WARPS = F::WARPS;
   constexpr int HL = MAXH / 4;          // heads a lane scores: hg, hg + 4, ..
@@ -855,7 +857,7 @@ __device__ __forceinline__ void attn_piece_f32(const PagedView& pv, const float*
     else
       *reinterpret_cast<float2*>(my) = make_float2(o[h][0], o[h][1]);
   }
-  join_warps<MAXH, D, D>(tiles, sc);
+  join_warps<MAXH, D, D>(tiles, sc, Hq, put);
 }
 
 // ------------------------------------------------------------------- kernels
@@ -884,11 +886,12 @@ struct Piece<__nv_bfloat16, D, MAXH, SEL> {
   static constexpr int INBOX = G::JOIN;    // where the tiles are free behind the join
   static constexpr int TILES = G::TILES;
   static constexpr int SMEM = G::SMEM;
+  template <typename Put>
   static __device__ __forceinline__ void run(const AttnArgs<__nv_bfloat16>& a, const SlotRow& sr, int64_t b, int w0,
                                              int steps, unsigned char* smem, AttnScratch& sc, bool arrive,
-                                             bool& bad_page, bool& bad_idx) {
+                                             const Put& put, bool& bad_page, bool& bad_idx) {
     attn_piece_bf16<D, MAXH / 16, SEL>(a.pv, a.Q, a.K, a.V, sr, b, w0, steps, a.Hq, a.scale_log2, smem, sc, arrive,
-                                            bad_page, bad_idx);
+                                       put, bad_page, bad_idx);
   }
 };
 template <int D, int MAXH, bool SEL>
@@ -900,11 +903,12 @@ struct Piece<float, D, MAXH, SEL> {
   static constexpr int INBOX = F::JOIN;
   static constexpr int TILES = F::TILES;
   static constexpr int SMEM = F::SMEM;
+  template <typename Put>
   static __device__ __forceinline__ void run(const AttnArgs<float>& a, const SlotRow& sr, int64_t b, int w0, int steps,
-                                             unsigned char* smem, AttnScratch& sc, bool arrive, bool& bad_page,
-                                             bool& bad_idx) {
-    attn_piece_f32<D, MAXH, SEL>(a.pv, a.Q, a.K, a.V, sr, b, w0, steps, a.Hq, a.scale_log2, smem, sc, arrive, bad_page,
-                                 bad_idx);
+                                             unsigned char* smem, AttnScratch& sc, bool arrive, const Put& put,
+                                             bool& bad_page, bool& bad_idx) {
+    attn_piece_f32<D, MAXH, SEL>(a.pv, a.Q, a.K, a.V, sr, b, w0, steps, a.Hq, a.scale_log2, smem, sc, arrive, put,
+                                 bad_page, bad_idx);
   }
 };
 
@@ -919,7 +923,7 @@ __device__ __forceinline__ void store_out4(float* o, float4 x, float inv) {
 __device__ __forceinline__ float inv_sum(float l) { return l == 0.f ? 0.f : 1.f / l; }
 __device__ __forceinline__ float lse_of(float m, float l) { return l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2; }
 
-// Where element group i of [Hq][D/4] lies in a piece's result.
+// Where element group i of [Hq][D/4] lies in the join buffer.
 template <typename P, int D>
 __device__ __forceinline__ int result_at(int i) {
   return i / (D / 4) * (P::PITCH / 4) + i % (D / 4);
@@ -950,28 +954,33 @@ __global__ void __launch_bounds__(kAttnThreads, (Piece<T, D, MAXH, true>::CTAS))
   const SlotRow sr = slot_row(a, b, bad_page);
   const int n_steps = (a.k + 4) >> 2;   // whatever the length: the idx loads need not wait for it
   const int w0 = (int)((int64_t)n_steps * rank / splits), w1 = (int)((int64_t)n_steps * (rank + 1) / splits);
-  P::run(a, sr, b, w0, w1, dec_smem, sc, splits > 1, bad_page, bad_idx);
-  const float4* o4 = reinterpret_cast<const float4*>(dec_smem);
+  P::run(
+      a, sr, b, w0, w1, dec_smem, sc, splits > 1,
+      [&](int i, int h, float4 x, float4* at) {
+        if (splits == 1)
+          store_out4(a.O + b * a.Hq * D + 4 * i, x, inv_sum(sc.ml[h].y));
+        else
+          *at = x;   // storing to the other CTAs from here took 0.2 us longer
+      },
+      bad_page, bad_idx);
   const int n4 = a.Hq * (D / 4);
   T* out = a.O + b * a.Hq * D;
   float* lse = a.LSE + b * a.Hq;
   if (splits == 1) {
-    for (int i = threadIdx.x; i < n4; i += kAttnThreads) {
-      const float2 ml = sc.ml[i / (D / 4)];
-      store_out4(out + 4 * i, o4[result_at<P, D>(i)], inv_sum(ml.y));
-    }
     if (threadIdx.x < a.Hq) lse[threadIdx.x] = lse_of(sc.ml[threadIdx.x].x, sc.ml[threadIdx.x].y);
   } else {
     // Each CTA writes a share of the row's outputs.  Its inbox, in the tiles
-    // behind its join buffer, takes that share of every CTA's part, and all
-    // bases and sums: the CTAs store there directly, so that nobody waits for
-    // a remote load and nobody has to stay for another's.
+    // behind its join buffer, takes that share of every CTA's part, and all bases
+    // and sums: the CTAs store there directly, so that nobody waits for a remote
+    // load and nobody has to stay for another's.
     constexpr int MAX4 = MAXH * (D / 4);
     static_assert(P::INBOX + 16 * (MAX4 + 16 * 16) + 8 * 16 * MAXH <= P::TILES, "the inbox fits behind the join buffer");
     float4* in4 = reinterpret_cast<float4*>(dec_smem + P::INBOX);                       // [splits][per]
     float2* in_ml = reinterpret_cast<float2*>(in4 + MAX4 + 16 * 16);                    // [splits][Hq]
     const int per = ((n4 + splits - 1) / splits + 15) & ~15;
+    __syncthreads();
     cluster_wait();   // everyone's inbox is free
+    const float4* o4 = reinterpret_cast<const float4*>(dec_smem);
     for (int i = threadIdx.x; i < n4; i += kAttnThreads) {
       const int to = i / per;
       cluster_st4(cluster_map(smem_u32(in4 + rank * per + i - to * per), to), o4[result_at<P, D>(i)]);
@@ -1023,7 +1032,6 @@ __global__ void __launch_bounds__(kAttnThreads, (Piece<T, D, MAXH, false>::CTAS)
   const Cut cut = make_cut(a.pv, a.batch, P::MIN_STEPS, sc);
   const bool by_row = a.batch <= gridDim.x;
   bool bad_page = false, bad_idx = false, item = by_row;
-  const float4* o4 = reinterpret_cast<const float4*>(dec_smem);
   const int n4 = a.Hq * (D / 4);
   int64_t rest = cut.rest, off = cut.off, row_pos = cut.begin - cut.off;
   int pieces = 0;
@@ -1035,7 +1043,24 @@ __global__ void __launch_bounds__(kAttnThreads, (Piece<T, D, MAXH, false>::CTAS)
     const int w0 = (int)max(off - kRowPad, (int64_t)0), w1 = (int)max(end - kRowPad, (int64_t)0);
     if (w1 > w0) {
       if (pieces) __syncthreads();   // the previous results become tiles again
-      P::run(a, sr, b, w0, w1, dec_smem, sc, false, bad_page, bad_idx);
+      const bool whole = w0 == 0 && w1 == n_steps;
+      const int64_t piece = 2 * (int64_t)blockIdx.x + (pieces > 0);
+      P::run(
+          a, sr, b, w0, w1, dec_smem, sc, false,
+          [&](int i, int h, float4 x, float4*) {
+            if (whole)
+              store_out4(a.O + b * a.Hq * D + 4 * i, x, inv_sum(sc.ml[h].y));
+            else
+              reinterpret_cast<float4*>(a.ps.o)[piece * n4 + i] = x;
+          },
+          bad_page, bad_idx);
+      if (threadIdx.x < a.Hq) {
+        const float2 ml = sc.ml[threadIdx.x];
+        if (whole)
+          a.LSE[b * a.Hq + threadIdx.x] = lse_of(ml.x, ml.y);
+        else
+          reinterpret_cast<float2*>(a.ps.ml)[piece * a.Hq + threadIdx.x] = ml;
+      }
       if (w0 == 0) {
         const int64_t last = (row_pos + n_steps - 1) / cut.per;
         const bool joined = last > blockIdx.x;
@@ -1043,19 +1068,6 @@ __global__ void __launch_bounds__(kAttnThreads, (Piece<T, D, MAXH, false>::CTAS)
           put_join_item(a.ps, by_row ? b : blockIdx.x, joined ? (int)b : -1, last, pieces > 0);
           item = true;
         }
-      }
-      if (w0 == 0 && w1 == n_steps) {
-        for (int i = threadIdx.x; i < n4; i += kAttnThreads) {
-          const float2 ml = sc.ml[i / (D / 4)];
-          store_out4(a.O + b * a.Hq * D + 4 * i, o4[result_at<P, D>(i)], inv_sum(ml.y));
-        }
-        if (threadIdx.x < a.Hq)
-          a.LSE[b * a.Hq + threadIdx.x] = lse_of(sc.ml[threadIdx.x].x, sc.ml[threadIdx.x].y);
-      } else {
-        const int64_t piece = 2 * (int64_t)blockIdx.x + (pieces > 0);
-        for (int i = threadIdx.x; i < n4; i += kAttnThreads)
-          reinterpret_cast<float4*>(a.ps.o)[piece * n4 + i] = o4[result_at<P, D>(i)];
-        if (threadIdx.x < a.Hq) reinterpret_cast<float2*>(a.ps.ml)[piece * a.Hq + threadIdx.x] = sc.ml[threadIdx.x];
       }
       ++pieces;
     }
