@@ -35,8 +35,8 @@
  *     dsa_check_device_error).  A row of bad length is treated as idle.  What
  *     is skipped is missing from that row's result; other rows are unaffected.
  *   - Outputs must not overlap inputs or each other, except where said.
- *   - The results of every call are bitwise reproducible run to run on one
- *     GPU model for the same dims and batch.
+ *   - The results of every call are bitwise reproducible run to run on one GPU
+ *     for the same dims and batch.
  *   - Rows are independent: several new tokens of one sequence (a draft to be
  *     verified, say) are rows with the same block-table row and growing lens.
  */
