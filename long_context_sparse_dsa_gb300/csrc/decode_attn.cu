@@ -291,7 +291,8 @@ struct DecCfg {
   static constexpr int NST = D == 128 ? (CTAS == 2 ? 3 : 2) : 4;
   static constexpr int RING = NST * GatherCfg<D>::STAGE_BYTES;
   static constexpr int TILES = WARPS * RING;
-  static constexpr int SMEM = TILES + (int)sizeof(AttnScratch);
+  static constexpr int Q_AT = TILES + (((int)sizeof(AttnScratch) + 127) & ~127);   // Q [NG * 16][D]
+  static constexpr int SMEM = Q_AT + NG * 16 * D * 2;
   static constexpr int PITCH = D + 8;   // floats per head in the join buffer: fragment stores without bank conflicts
   static constexpr int JOIN = WARPS * NG * 16 * PITCH * 4;
   static_assert(TILES >= JOIN, "the rings double as the join buffer");
@@ -350,9 +351,8 @@ __device__ __forceinline__ void attn_piece_bf16(const PagedView& pv, const __nv_
   };
 
   // Start-up, ordered by its chains of dependent loads: the ring's idx entries;
-  // Q, by 16-byte copies into the last stage of the first warp's ring (free
-  // until that warp's first step; fragment-shaped loads of Q from global memory
-  // took the load units 1 us); the pages; the rows; then Q's fragments.
+  // Q, by 16-byte copies (fragment-shaped loads of Q from global memory took the
+  // load units 1 us); the pages; the rows.
   int st = w0 + warp;
   int raws[NST], raw_next;
 #pragma unroll
@@ -362,8 +362,7 @@ __device__ __forceinline__ void attn_piece_bf16(const PagedView& pv, const __nv_
   }
   load_raw(st + NST * WARPS);
   raw_next = raw;
-  const uint32_t q_s = smem_u32(tiles) + (NST - 1) * C::STAGE_BYTES;   // [NG * 16][D], swizzled as the tiles
-  static_assert(NG * 16 * C::ROW_BYTES <= C::STAGE_BYTES, "Q fits a stage");
+  const uint32_t q_s = smem_u32(tiles) + G::Q_AT;   // swizzled as the tiles
 #pragma unroll
   for (int i = threadIdx.x; i < NG * 16 * C::CHUNKS; i += kAttnThreads) {
     const int h = i / C::CHUNKS, ch = i % C::CHUNKS;
@@ -393,17 +392,8 @@ __device__ __forceinline__ void attn_piece_bf16(const PagedView& pv, const __nv_
     }
     raw = raw_next;
   }
-  uint32_t qa[NG][D / 16][4];
   cp_async_wait<NST - 1>();   // all but the rows: Q
   __syncthreads();
-#pragma unroll
-  for (int n = 0; n < NG; ++n)
-#pragma unroll
-    for (int ks = 0; ks < D / 16; ++ks) {
-      const int h = n * 16 + (lane & 15), ch = 2 * ks + (lane >> 4);
-      ldsm_x4(q_s + h * C::ROW_BYTES + ((ch ^ (h & 7)) << 4), qa[n][ks][0], qa[n][ks][1], qa[n][ks][2], qa[n][ks][3]);
-    }
-  __syncthreads();   // the stage is the first warp's again
   float o[NG][D / 8][4];
   float m[NG][2], l[NG][2], top[NG][2];   // heads g and g + 8 of each group
 #pragma unroll
@@ -423,7 +413,10 @@ __device__ __forceinline__ void attn_piece_bf16(const PagedView& pv, const __nv_
     __syncwarp();
     const uint32_t ks_base = ring + stage * C::STAGE_BYTES;
     const uint32_t vs_base = ks_base + C::TILE_BYTES;
-    // S = Q K^T as four independent accumulation chains
+    // S = Q K^T as four independent accumulation chains.  Q's fragments are read
+    // at every step: in registers, 32 heads at d = 128 left no room beside their
+    // sums (64 selected rows 22.4 us against 20.9, a whole cache of 40 rows 74.9
+    // against 72.0, 48 bytes spilled); for 16 heads either is as fast.
     constexpr int CHAINS = NG == 1 ? 2 : 1;
     float s[NG][CHAINS][2][4];
 #pragma unroll
@@ -443,8 +436,11 @@ __device__ __forceinline__ void attn_piece_bf16(const PagedView& pv, const __nv_
 #pragma unroll
         for (int n = 0; n < NG; ++n) {
           float(&sc2)[2][4] = s[n][ks % CHAINS];
-          mma_bf16_16816(sc2[0], qa[n][ks][0], qa[n][ks][1], qa[n][ks][2], qa[n][ks][3], b0, b1);
-          mma_bf16_16816(sc2[1], qa[n][ks][0], qa[n][ks][1], qa[n][ks][2], qa[n][ks][3], b2, b3);
+          uint32_t a[4];
+          const int h = n * 16 + (lane & 15), qch = 2 * ks + (lane >> 4);
+          ldsm_x4(q_s + h * C::ROW_BYTES + ((qch ^ (h & 7)) << 4), a[0], a[1], a[2], a[3]);
+          mma_bf16_16816(sc2[0], a[0], a[1], a[2], a[3], b0, b1);
+          mma_bf16_16816(sc2[1], a[0], a[1], a[2], a[3], b2, b3);
         }
       }
     }
