@@ -34,7 +34,7 @@ namespace dsa {
 constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kCap = 4096;                           // scores selected from exactly
-constexpr int kPerLane = 16;                         // scores a thread holds per chunk
+constexpr int kPerLane = 8;                          // scores a thread holds per chunk
 constexpr int kChunk = kSelThreads * kPerLane;       // scores of a CTA's pass
 constexpr uint32_t kFullMask = 0xffffffffu;
 
@@ -301,32 +301,39 @@ __device__ __forceinline__ void write_selected(F key, G pool, int n, uint32_t T,
   }
 }
 
-// One pass over scores [begin, end) of a row, kChunk at a time, in order:
-// put(pool, score, gt, gt_before, eq_before) for every score > tau or == tau,
-// with the numbers of both before it in the slice.
+// This thread's kPerLane consecutive scores of the chunk of [c0, end) at c0, a
+// multiple of 4.
+__device__ __forceinline__ void load_chunk(const float* __restrict__ row, int64_t c0, int64_t end,
+                                           float (&x)[kPerLane]) {
+  const int64_t e0 = c0 + (int64_t)threadIdx.x * kPerLane;
+#pragma unroll
+  for (int u = 0; u < kPerLane; u += 4) {
+    float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (e0 + u + 3 < end) {
+      f = *reinterpret_cast<const float4*>(row + e0 + u);
+    } else {
+      if (e0 + u < end) f.x = row[e0 + u];
+      if (e0 + u + 1 < end) f.y = row[e0 + u + 1];
+      if (e0 + u + 2 < end) f.z = row[e0 + u + 2];
+    }
+    x[u] = f.x;
+    x[u + 1] = f.y;
+    x[u + 2] = f.z;
+    x[u + 3] = f.w;
+  }
+}
+
+// One pass over scores [begin, end) of a row, kChunk at a time, in order, the
+// first chunk in x: put(pool, score, gt, gt_before, eq_before) for every score
+// > tau or == tau, with the numbers of both before it in the slice.
 template <typename F>
 __device__ __forceinline__ void scan_slice(const float* __restrict__ row, int64_t begin, int64_t end, float tau,
-                                           SelShared& sh, int& n_gt, int& n_eq, F put) {
+                                           float (&x)[kPerLane], SelShared& sh, int& n_gt, int& n_eq, F put) {
   n_gt = n_eq = 0;
   for (int64_t c0 = begin; c0 < end; c0 += kChunk) {
-    // a lane's kPerLane consecutive scores
     const int64_t e0 = c0 + (int64_t)threadIdx.x * kPerLane;
-    float x[kPerLane];
-#pragma unroll
-    for (int u = 0; u < kPerLane; u += 4) {
-      float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (e0 + u + 3 < end) {
-        f = *reinterpret_cast<const float4*>(row + e0 + u);   // begin is a multiple of 4
-      } else {
-        if (e0 + u < end) f.x = row[e0 + u];
-        if (e0 + u + 1 < end) f.y = row[e0 + u + 1];
-        if (e0 + u + 2 < end) f.z = row[e0 + u + 2];
-      }
-      x[u] = f.x;
-      x[u + 1] = f.y;
-      x[u + 2] = f.z;
-      x[u + 3] = f.w;
-    }
+    float next[kPerLane];
+    if (c0 + kChunk < end) load_chunk(row, c0 + kChunk, end, next);   // the coming chunk, on its way
     const int left = (int)max((int64_t)0, min((int64_t)kPerLane, end - e0));
     const uint32_t valid = (1u << left) - 1u;
     uint32_t gt = 0, eq = 0;
@@ -352,6 +359,8 @@ __device__ __forceinline__ void scan_slice(const float* __restrict__ row, int64_
     }
     n_gt += total & 0xffff;
     n_eq += total >> 16;
+#pragma unroll
+    for (int i = 0; i < kPerLane; ++i) x[i] = next[i];
     __syncthreads();   // wsum is free again
   }
 }
@@ -381,6 +390,10 @@ __global__ void __launch_bounds__(kSelThreads, 2)
     return;
   }
   if (ctas > 1) cluster_arrive();
+  const int64_t slice = ((((int64_t)n + ctas - 1) / ctas) + 3) & ~(int64_t)3;
+  const int64_t begin = min((int64_t)n, rank * slice), end = min((int64_t)n, begin + slice);
+  float x[kPerLane];
+  load_chunk(row, begin, end, x);   // on its way while tau is found
   float tau;
   {
     int g = 1;
@@ -388,13 +401,13 @@ __global__ void __launch_bounds__(kSelThreads, 2)
     const uint64_t step = ((uint64_t)n << 20) / (uint32_t)(kSelThreads * g);   // between samples, in 2^-20 scores
     float best = -INFINITY;
     for (int j0 = 0; j0 < g; j0 += 8) {
-      float x[8];
+      float y[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        if (j0 + j < g) x[j] = __ldcg(row + (int)(((uint64_t)(tid + (j0 + j) * kSelThreads) * step) >> 20));
+        if (j0 + j < g) y[j] = __ldcg(row + (int)(((uint64_t)(tid + (j0 + j) * kSelThreads) * step) >> 20));
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        if (j0 + j < g) best = fmaxf(best, x[j]);
+        if (j0 + j < g) best = fmaxf(best, y[j]);
     }
     const float mu = (float)k * (float)(kSelThreads * g) / (float)n;
     int r = (int)(mu + 4.f * sqrtf(mu)) + 2;
@@ -404,12 +417,10 @@ __global__ void __launch_bounds__(kSelThreads, 2)
     tau = key_value(kth_largest_own(own, r, sh, &unused));
     __syncthreads();   // sh.list and wsum are free again
   }
-  const int64_t slice = ((((int64_t)n + ctas - 1) / ctas) + 3) & ~(int64_t)3;
-  const int64_t begin = min((int64_t)n, rank * slice), end = min((int64_t)n, begin + slice);
   int n_gt, n_eq;
-  scan_slice(row, begin, end, tau, sh, n_gt, n_eq, [&](int64_t pool, float x, bool gt, int at, int) {
+  scan_slice(row, begin, end, tau, x, sh, n_gt, n_eq, [&](int64_t pool, float score, bool gt, int at, int) {
     if (gt && at < kCap) {
-      sh.key[at] = own_key(x);
+      sh.key[at] = own_key(score);
       sh.pool[at] = (int32_t)pool;
     }
   });
@@ -447,7 +458,8 @@ __global__ void __launch_bounds__(kSelThreads, 2)
   }
   if (m < k && (int64_t)m + ties >= k) {
     const int need_eq = k - m;
-    scan_slice(row, begin, end, tau, sh, n_gt, n_eq, [&](int64_t pool, float, bool gt, int g, int e) {
+    load_chunk(row, begin, end, x);
+    scan_slice(row, begin, end, tau, x, sh, n_gt, n_eq, [&](int64_t pool, float, bool gt, int g, int e) {
       const int eq = eq_before + e;
       if (gt || eq < need_eq) out[gt_before + g + min(eq, need_eq)] = (int32_t)pool;
     });
