@@ -237,11 +237,10 @@ __device__ __forceinline__ uint32_t kth_largest_own(const uint32_t (&x)[J], int 
   }
 }
 
-// The k largest of m <= kCap keys (own_key's, key(i) by index, m >= k), in
-// order: pool(i) of each goes to `out`.  A thread holds consecutive keys.
-template <typename F, typename G>
-__device__ __forceinline__ void finish_row(F key, G pool, int m, int k, SelShared& sh, int32_t* __restrict__ out) {
-  constexpr int J = kCap / kSelThreads;
+// The k largest of m <= J * kSelThreads keys (own_key's, key(i) by index, m >=
+// k), in order: pool(i) of each goes to `out`.  A thread holds consecutive keys.
+template <int J, typename F, typename G>
+__device__ __forceinline__ void finish_row_of(F key, G pool, int m, int k, SelShared& sh, int32_t* __restrict__ out) {
   const int per = (m + kSelThreads - 1) / kSelThreads, i0 = threadIdx.x * per;
   uint32_t own[J];
 #pragma unroll
@@ -264,6 +263,19 @@ __device__ __forceinline__ void finish_row(F key, G pool, int m, int k, SelShare
     g += is_gt;
     e += is_eq;
   }
+}
+// m <= kCap, with 2 or 4 keys a thread where they suffice (always 8: 64 rows of
+// 1000 pools, scores included, took 8.4 us against 7.1, 16 rows of 8191 pools
+// 13.2 against 12.3).
+template <typename F, typename G>
+__device__ __forceinline__ void finish_row(F key, G pool, int m, int k, SelShared& sh, int32_t* __restrict__ out) {
+  static_assert(kCap == 8 * kSelThreads, "8 keys a thread at most");
+  if (m <= 2 * kSelThreads)
+    finish_row_of<2>(key, pool, m, k, sh, out);
+  else if (m <= 4 * kSelThreads)
+    finish_row_of<4>(key, pool, m, k, sh, out);
+  else
+    finish_row_of<8>(key, pool, m, k, sh, out);
 }
 
 // Writes, in order, the keys > T and the first `ties` keys == T of n keys.  A
