@@ -44,10 +44,8 @@ __device__ __forceinline__ uint32_t own_key(float x) { return max(order_key(x), 
 
 struct SelShared {
   alignas(16) int hist[2048];
-  alignas(16) uint32_t key[kCap];    // this CTA's candidates
+  uint32_t key[kCap];                // this CTA's candidates; behind the first CTA's, finally, all others'
   int32_t pool[kCap];
-  alignas(16) uint32_t gkey[kCap];   // the first CTA: all CTAs' candidates
-  int32_t gpool[kCap];
   alignas(16) int wsum[2][kSelWarps];
   uint32_t lo, hi;
   int sel[3];
@@ -457,19 +455,18 @@ __global__ void __launch_bounds__(kSelThreads, 2)
   const int eq_before = __reduce_add_sync(kFullMask, lane < rank ? eq_c : 0);
   if (m >= k && m <= kCap) {
     if (ctas > 1) {
-      // the candidates go to the first CTA
-      const uint32_t ks = cluster_map(smem_u32(sh.gkey + gt_before), 0);
-      const uint32_t ps = cluster_map(smem_u32(sh.gpool + gt_before), 0);
-      for (int i = tid; i < n_gt; i += kSelThreads) {
-        cluster_st_u32(ks + 4 * i, sh.key[i]);
-        cluster_st_u32(ps + 4 * i, (uint32_t)sh.pool[i]);
-      }
+      // the candidates go to the first CTA, which has its own in place
+      const uint32_t ks = cluster_map(smem_u32(sh.key + gt_before), 0);
+      const uint32_t ps = cluster_map(smem_u32(sh.pool + gt_before), 0);
+      if (rank != 0)
+        for (int i = tid; i < n_gt; i += kSelThreads) {
+          cluster_st_u32(ks + 4 * i, sh.key[i]);
+          cluster_st_u32(ps + 4 * i, (uint32_t)sh.pool[i]);
+        }
       cluster_sync();
     }
-    if (rank != 0) return;
-    const uint32_t* gk = ctas > 1 ? sh.gkey : sh.key;
-    const int32_t* gp = ctas > 1 ? sh.gpool : sh.pool;
-    finish_row([&](int i) { return gk[i]; }, [&](int i) { return gp[i]; }, m, k, sh, out);
+    if (rank == 0)
+      finish_row([&](int i) { return sh.key[i]; }, [&](int i) { return sh.pool[i]; }, m, k, sh, out);
     return;
   }
   if (m < k && (int64_t)m + ties >= k) {
