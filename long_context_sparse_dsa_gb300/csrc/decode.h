@@ -47,24 +47,36 @@ inline PagedView make_paged_view(const int32_t* lens, const int32_t* table, int6
 struct KernelState {
   static constexpr int DEVICES = 64;                 // beyond: found at every launch
   std::atomic<uint64_t> done{0};                     // one bit per device
-  std::atomic<int> fit[DEVICES][17] = {};            // [n]: clusters of n CTAs resident at once, n = 1 .. 8, 16
+  // [n]: clusters of n CTAs, n = 1 .. 8 or 16, that are resident at once, and
+  // that are with no more than one CTA an SM
+  std::atomic<int> fit[DEVICES][17] = {}, alone[DEVICES][17] = {};
 };
 
-// Sets the dynamic shared memory limit and, where `threads` is given, allows
-// clusters of 16 and asks how many clusters of each size are resident at once.
-// That is fewer than the CTAs would fill: a cluster lies within one group of
-// SMs, and what is left over in a group stays empty.  With 3 CTAs an SM there
-// is room for 456 CTAs, but for 59 clusters of 7 (413) and 21 of 16 (336).
+// Shared memory of an SM, in percent of the most, that the indexer's scores and
+// top-k kernels ask for (100 KB; the rest is L1 cache).  Two kernels in a row that
+// want it split differently do not overlap: with each left to the driver's
+// choice 64 rows of 1000 pools took 7.0 us against 6.2, 16 rows of 8191 12.0
+// against 10.9.
+constexpr int kIndexerCarveout = 43;
+
+// The kernel's attributes for `smem` bytes of dynamic shared memory and, where
+// `threads` is given, for clusters of up to 16 CTAs: how many of each size are
+// resident at once is asked too.  That is fewer than the CTAs would fill: a
+// cluster lies within one group of SMs, and what is left over in a group stays
+// empty.  With 3 CTAs an SM there is room for 456 CTAs, but for 59 clusters of 7
+// (413) and 21 of 16 (336).
 template <typename... P>
-inline cudaError_t prepare_kernel(void (*kern)(P...), int smem, unsigned threads, KernelState& st, int& dev) {
+inline cudaError_t prepare_kernel(void (*kern)(P...), int smem, unsigned threads, KernelState& st, int& dev,
+                                  int carveout = cudaSharedmemCarveoutDefault) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const uint64_t bit = dev < KernelState::DEVICES ? (uint64_t)1 << dev : 0;
   dev %= KernelState::DEVICES;
   if (st.done.load(std::memory_order_acquire) & bit) return cudaSuccess;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  if (threads) {
+  constexpr int kAlone = 120 * 1024;   // no SM holds two CTAs with so much
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, threads && smem < kAlone ? kAlone : smem);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, carveout);
+  if (e == cudaSuccess && threads) {
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     for (unsigned n = 1; e == cudaSuccess && n <= 16; n = n == 8 ? 16 : n + 1) {
       cudaLaunchConfig_t cfg = {};
@@ -77,14 +89,16 @@ inline cudaError_t prepare_kernel(void (*kern)(P...), int smem, unsigned threads
       at.val.clusterDim.y = at.val.clusterDim.z = 1;
       cfg.attrs = &at;
       cfg.numAttrs = 1;
-      int clusters = 0;
+      int clusters = 0, alone = 0;
       e = cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg);
+      cfg.dynamicSmemBytes = smem < kAlone ? kAlone : smem;
+      if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&alone, kern, &cfg);
       st.fit[dev][n].store(clusters, std::memory_order_relaxed);
+      st.alone[dev][n].store(alone, std::memory_order_relaxed);
     }
-    if (e != cudaSuccess) return e;
   }
-  st.done.fetch_or(bit, std::memory_order_release);
-  return cudaSuccess;
+  if (e == cudaSuccess) st.done.fetch_or(bit, std::memory_order_release);
+  return e;
 }
 
 // CTAs per row where a row is one cluster: the most, 1 .. 8 or 16 and no more

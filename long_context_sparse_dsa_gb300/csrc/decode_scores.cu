@@ -208,11 +208,16 @@ static cudaError_t launch_scores(bool bf16, const PagedView& pv, int64_t batch, 
                                  const float* w, const void* kpool, float* scores, int64_t pitch, cudaStream_t s) {
   const int64_t P = pv.capacity / 4, per = kScoreWarps * PPW;
   const dim3 grid((unsigned)((P + per - 1) / per), (unsigned)batch), threads(kScoreWarps * 32);
-  if (bf16)
-    return launch_chained(decode_scores_bf16_kernel<DI, PPW>, grid, threads, 0, s, pv, Hi, k,
-                          static_cast<const uint4*>(q_idx), w, static_cast<const uint4*>(kpool), scores, pitch);
-  return launch_chained(Hi > 4 ? decode_scores_f32_kernel<DI, PPW, 8> : decode_scores_f32_kernel<DI, PPW, 4>, grid, threads, 0, s, pv, Hi, k,
-                        static_cast<const float4*>(q_idx), w, static_cast<const float4*>(kpool), scores, pitch);
+  auto launch = [&](auto* kern, auto* q, KernelState& st) {
+    int dev;
+    cudaError_t e = prepare_kernel(kern, 0, 0, st, dev, kIndexerCarveout);
+    if (e != cudaSuccess) return e;
+    return launch_chained(kern, grid, threads, 0, s, pv, Hi, k, q, w, reinterpret_cast<decltype(q)>(kpool), scores, pitch);
+  };
+  static KernelState st16, st4, st8;
+  if (bf16) return launch(decode_scores_bf16_kernel<DI, PPW>, static_cast<const uint4*>(q_idx), st16);
+  if (Hi <= 4) return launch(decode_scores_f32_kernel<DI, PPW, 4>, static_cast<const float4*>(q_idx), st4);
+  return launch(decode_scores_f32_kernel<DI, PPW, 8>, static_cast<const float4*>(q_idx), st8);
 }
 
 cudaError_t launch_decode_scores(bool bf16, const PagedView& pv, int64_t batch, int Hi, int di, int k,
