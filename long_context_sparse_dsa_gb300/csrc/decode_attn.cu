@@ -24,10 +24,11 @@
 //
 // bf16: steps go round-robin to a CTA's warps, each with a ring of its own
 // filled by cp.async, heads (one or two groups of 16) on the M side of
-// m16n8k16 MMAs as in attn_fwd.cu: tcgen05 tiles would be an eighth full.  P
-// enters P V as two bf16 terms (hi + lo, about 2^-17 relative); one term alone
-// ran no faster (83 us against 80 for 40 ragged rows of 32 heads), the MMAs
-// not being what bounds the kernel.
+// m16n8k16 MMAs as in attn_fwd.cu; all arithmetic taken out, the loops ran 1.0
+// to 4.4 us a pass faster (64 selected rows of 32 heads 18.0 us against 20.8, a
+// whole cache of 1M tokens 81.3 against 85.2).  P enters P V as two bf16 terms
+// (hi + lo, about 2^-17 relative); one term alone would save 1.3 us of those
+// 20.8, and nothing for 40 whole rows of 32 heads (72.4 against 71.1).
 // fp32: the same with plain FFMA.
 #include "decode.cuh"
 #include "gather.cuh"
