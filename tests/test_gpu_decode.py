@@ -344,6 +344,29 @@ def test_indexer_topk_many_wide_rows(dtype):
     dsa.check_device_error()
 
 
+@pytest.mark.parametrize("Hi,di", [(1, 64), (3, 128), (4, 64), (4, 128), (5, 64)])
+def test_indexer_topk_many_rows_of_few_heads(Hi, di):
+    """fp32 with at most and just above 4 heads, at a size that gives every warp a full block of pools."""
+    pg = Paged([9000 + 37 * b for b in range(38)], 20, di=di, dtype="fp32", seed=di + Hi).fill()
+    q, w, idx = _topk(pg, Hi, di, 70)
+    assert torch.equal(idx.cpu(), _ref_topk(pg, q, w, 70))
+    dsa.check_device_error()
+
+
+@pytest.mark.parametrize("batch", [2, 15, 18, 19, 37, 77, 153])
+def test_indexer_topk_cluster_sizes(batch):
+    """Rows beyond the exact limit, in batches around those at which the clusters change: alone on the SMs, side by side,
+    smaller, one CTA a row.  The candidates crowd into one CTA's slice in every third row."""
+    g = torch.Generator().manual_seed(batch)
+    values = []
+    for b in range(batch):
+        v = torch.rand(8300 + 61 * (b % 9), generator=g)
+        if b % 3 == 0:
+            v[4100:4900] += 2.0
+        values.append(v)
+    _given_scores(values, 300)
+
+
 def _given_scores(values, k, sign=1.0):
     """Rows of an fp32 layer whose scores are exactly sign * values [B][n] (each >= 0): one indexer head that reads one
     channel."""
