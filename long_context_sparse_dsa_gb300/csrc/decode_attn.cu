@@ -11,8 +11,11 @@
 // page, rows) and the joins.
 //
 // Selected pools: every row has the same number of steps (of 4 slots, 16
-// keys), cut evenly over the CTAs of a cluster, which join through distributed
-// shared memory: one launch, no workspace traffic.
+// keys), dealt out to the warps of a cluster's CTAs, which join through
+// distributed shared memory: one launch, no workspace traffic.  (Dealt out, not
+// cut, and skipped where empty, because a row with fewer pools than k has its
+// empty steps at the end: 112 rows of up to 352 pools, k = 512, 32 heads, took
+// 30.4 us against 23.7.)
 // Whole cache: rows differ, so the rows' steps form one list, cut into equal
 // contiguous ranges, one per CTA: a CTA takes the end of one row, whole rows,
 // the start of another.  Every CTA derives the cut from the lengths itself.
@@ -299,8 +302,8 @@ struct DecCfg {
   static_assert(TILES >= JOIN, "the rings double as the join buffer");
 };
 
-// Steps [w0, steps) of row b; the result goes on through put and sc.ml, as in
-// join_warps.
+// Steps w0 + warp, w0 + warp + stride, .. below `steps` of row b; the result goes
+// on through put and sc.ml, as in join_warps.
 // arrive: arrives at the cluster's barrier as soon as the tiles behind the
 // join buffer are no longer used.
 // SEL: the slots are selected pools; else all pools.
@@ -308,13 +311,12 @@ template <int D, int NG, bool SEL, typename Put>
 __device__ __forceinline__ void attn_piece_bf16(const PagedView& pv, const __nv_bfloat16* __restrict__ Q,
                                                 const __nv_bfloat16* __restrict__ K,
                                                 const __nv_bfloat16* __restrict__ V, const SlotRow& sr, int64_t b,
-                                                int w0, int steps, int Hq, float scale_log2, unsigned char* tiles,
-                                                AttnScratch& sc, bool arrive, const Put& put, bool& bad_page,
+                                                int w0, int steps, int stride, int Hq, float scale_log2,
+                                                unsigned char* tiles, AttnScratch& sc, bool arrive, const Put& put, bool& bad_page,
                                                 bool& bad_idx) {
   using C = GatherCfg<D>;
   using G = DecCfg<D, NG, SEL>;
   constexpr int NST = G::NST;
-  constexpr int WARPS = G::WARPS;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, qi = lane & 3;
   const uint32_t ring = smem_u32(tiles) + warp * G::RING;
@@ -345,7 +347,7 @@ __device__ __forceinline__ void attn_piece_bf16(const PagedView& pv, const __nv_
       }
       if (v == 0x4444u)
         gather_full16<D>(ring + stage * C::STAGE_BYTES, K, V, slots, gl);
-      else
+      else if (!SEL || v != 0u)   // an empty step of selected pools is not computed
         gather_step16<D>(ring + stage * C::STAGE_BYTES, K, V, slots, gl);
     }
     cp_async_commit();
@@ -358,10 +360,10 @@ __device__ __forceinline__ void attn_piece_bf16(const PagedView& pv, const __nv_
   int raws[NST], raw_next;
 #pragma unroll
   for (int i = 0; i < NST; ++i) {
-    load_raw(st + i * WARPS);
+    load_raw(st + i * stride);
     raws[i] = raw;
   }
-  load_raw(st + NST * WARPS);
+  load_raw(st + NST * stride);
   raw_next = raw;
   const uint32_t q_s = smem_u32(tiles) + G::Q_AT;   // swizzled as the tiles
 #pragma unroll
@@ -377,7 +379,7 @@ __device__ __forceinline__ void attn_piece_bf16(const PagedView& pv, const __nv_
 #pragma unroll
     for (int i = 0; i < NST; ++i) {
       raw = raws[i];
-      load_page(st + i * WARPS);
+      load_page(st + i * stride);
       pools[i] = pool;
       rws[i] = rows;
       cols[i] = col;
@@ -389,7 +391,7 @@ __device__ __forceinline__ void attn_piece_bf16(const PagedView& pv, const __nv_
       rows = rws[i];
       col = cols[i];
       page = pgs[i];
-      if (i < NST - 1) fetch(st + i * WARPS, i, vis[i]);
+      if (i < NST - 1) fetch(st + i * stride, i, vis[i]);
     }
     raw = raw_next;
   }
@@ -406,11 +408,20 @@ __device__ __forceinline__ void attn_piece_bf16(const PagedView& pv, const __nv_
   }
 
   int stage = 0;
-  for (; st < steps; st += WARPS) {
-    fetch(st + (NST - 1) * WARPS, stage == 0 ? NST - 1 : stage - 1, vis[NST - 1]);   // the stage consumed last
-    load_page(st + NST * WARPS);
-    load_raw(st + (NST + 1) * WARPS);
+  auto advance = [&] {
+#pragma unroll
+    for (int i = 0; i + 1 < NST; ++i) vis[i] = vis[i + 1];
+    stage = stage == NST - 1 ? 0 : stage + 1;
+  };
+  for (; st < steps; st += stride) {
+    fetch(st + (NST - 1) * stride, stage == 0 ? NST - 1 : stage - 1, vis[NST - 1]);   // the stage consumed last
+    load_page(st + NST * stride);
+    load_raw(st + (NST + 1) * stride);
     cp_async_wait<NST - 1>();
+    if (SEL && vis[0] == 0u) {   // a row with fewer pools than k
+      advance();
+      continue;
+    }
     __syncwarp();
     const uint32_t ks_base = ring + stage * C::STAGE_BYTES;
     const uint32_t vs_base = ks_base + C::TILE_BYTES;
@@ -547,9 +558,7 @@ __device__ __forceinline__ void attn_piece_bf16(const PagedView& pv, const __nv_
       }
     }
     __syncwarp();
-#pragma unroll
-    for (int i = 0; i + 1 < NST; ++i) vis[i] = vis[i + 1];
-    stage = stage == NST - 1 ? 0 : stage + 1;
+    advance();
   }
   cp_async_wait<0>();
 
@@ -617,8 +626,8 @@ struct F32Cfg {
 template <int D, int MAXH, bool SEL, typename Put>
 __device__ __forceinline__ void attn_piece_f32(const PagedView& pv, const float* __restrict__ Q,
                                                const float* __restrict__ K, const float* __restrict__ V,
-                                               const SlotRow& sr, int64_t b, int w0, int steps, int Hq,
-                                               float scale_log2, unsigned char* tiles, AttnScratch& sc, bool arrive,
+                                               const SlotRow& sr, int64_t b, int w0, int steps, int stride,
+                                               int Hq, float scale_log2, unsigned char* tiles, AttnScratch& sc, bool arrive,
                                                const Put& put, bool& bad_page, bool& bad_idx) {
   using F = F32Cfg<D, MAXH>;
   constexpr int NST = F::NST, WARPS = F::WARPS;
@@ -638,7 +647,7 @@ __device__ __forceinline__ void attn_piece_f32(const PagedView& pv, const float*
   // Slot pipeline: half step i of this warp is slots 4 * step + 2 * (i & 1) and
   // the next; lane (lane & 1) decides one of them.
   int raw = -1, pool = 0, rows = 0, col = 0, page = 0;
-  auto step_of = [&](int i) { return w0 + warp + (i >> 1) * WARPS; };
+  auto step_of = [&](int i) { return w0 + warp + (i >> 1) * stride; };
   auto slot_of = [&](int i) { return 4 * step_of(i) + 2 * (i & 1) + (lane & 1); };
   auto load_raw = [&](int i) { raw = step_of(i) < steps ? slot_idx<SEL>(sr, slot_of(i)) : -1; };
   auto load_page = [&](int i) {
@@ -725,11 +734,20 @@ __device__ __forceinline__ void attn_piece_f32(const PagedView& pv, const float*
     l[i] = 0.f;
   }
   int stage = 0;
+  auto advance = [&] {
+#pragma unroll
+    for (int i = 0; i + 1 < NST; ++i) vis[i] = vis[i + 1];
+    stage = stage == NST - 1 ? 0 : stage + 1;
+  };
   for (int it = 0; step_of(it) < steps; ++it) {
     fetch(it + NST - 1, stage == 0 ? NST - 1 : stage - 1, vis[NST - 1]);   // the stage consumed last
     load_page(it + NST);
     load_raw(it + NST + 1);
     cp_async_wait<NST - 1>();
+    if (SEL && vis[0] == 0u) {
+      advance();
+      continue;
+    }
     __syncwarp();
     const float* ks = ring + stage * F::STAGE;
     const float* vs = ks + F::KEYS * F::PITCH;
@@ -830,9 +848,7 @@ __device__ __forceinline__ void attn_piece_f32(const PagedView& pv, const float*
       }
     }
     __syncwarp();   // the stage and p are free again
-#pragma unroll
-    for (int i = 0; i + 1 < NST; ++i) vis[i] = vis[i + 1];
-    stage = stage == NST - 1 ? 0 : stage + 1;
+    advance();
   }
   cp_async_wait<0>();
 #pragma unroll
@@ -885,10 +901,10 @@ struct Piece<__nv_bfloat16, D, MAXH, SEL> {
   static constexpr int SMEM = G::SMEM;
   template <typename Put>
   static __device__ __forceinline__ void run(const AttnArgs<__nv_bfloat16>& a, const SlotRow& sr, int64_t b, int w0,
-                                             int steps, unsigned char* smem, AttnScratch& sc, bool arrive,
+                                             int steps, int stride, unsigned char* smem, AttnScratch& sc, bool arrive,
                                              const Put& put, bool& bad_page, bool& bad_idx) {
-    attn_piece_bf16<D, MAXH / 16, SEL>(a.pv, a.Q, a.K, a.V, sr, b, w0, steps, a.Hq, a.scale_log2, smem, sc, arrive,
-                                       put, bad_page, bad_idx);
+    attn_piece_bf16<D, MAXH / 16, SEL>(a.pv, a.Q, a.K, a.V, sr, b, w0, steps, stride, a.Hq, a.scale_log2, smem, sc,
+                                       arrive, put, bad_page, bad_idx);
   }
 };
 template <int D, int MAXH, bool SEL>
@@ -902,9 +918,9 @@ struct Piece<float, D, MAXH, SEL> {
   static constexpr int SMEM = F::SMEM;
   template <typename Put>
   static __device__ __forceinline__ void run(const AttnArgs<float>& a, const SlotRow& sr, int64_t b, int w0, int steps,
-                                             unsigned char* smem, AttnScratch& sc, bool arrive, const Put& put,
+                                             int stride, unsigned char* smem, AttnScratch& sc, bool arrive, const Put& put,
                                              bool& bad_page, bool& bad_idx) {
-    attn_piece_f32<D, MAXH, SEL>(a.pv, a.Q, a.K, a.V, sr, b, w0, steps, a.Hq, a.scale_log2, smem, sc, arrive, put,
+    attn_piece_f32<D, MAXH, SEL>(a.pv, a.Q, a.K, a.V, sr, b, w0, steps, stride, a.Hq, a.scale_log2, smem, sc, arrive, put,
                                  bad_page, bad_idx);
   }
 };
@@ -950,9 +966,8 @@ __global__ void __launch_bounds__(kAttnThreads, (Piece<T, D, MAXH, true>::CTAS))
   bool bad_page = false, bad_idx = false;
   const SlotRow sr = slot_row(a, b, bad_page);
   const int n_steps = (a.k + 4) >> 2;   // whatever the length: the idx loads need not wait for it
-  const int w0 = (int)((int64_t)n_steps * rank / splits), w1 = (int)((int64_t)n_steps * (rank + 1) / splits);
   P::run(
-      a, sr, b, w0, w1, dec_smem, sc, splits > 1,
+      a, sr, b, rank * P::MIN_STEPS, n_steps, splits * P::MIN_STEPS, dec_smem, sc, splits > 1,
       [&](int i, int h, float4 x, float4* at) {
         if (splits == 1)
           store_out4(a.O + b * a.Hq * D + 4 * i, x, inv_sum(sc.ml[h].y));
@@ -1043,7 +1058,7 @@ __global__ void __launch_bounds__(kAttnThreads, (Piece<T, D, MAXH, false>::CTAS)
       const bool whole = w0 == 0 && w1 == n_steps;
       const int64_t piece = 2 * (int64_t)blockIdx.x + (pieces > 0);
       P::run(
-          a, sr, b, w0, w1, dec_smem, sc, false,
+          a, sr, b, w0, w1, P::MIN_STEPS, dec_smem, sc, false,
           [&](int i, int h, float4 x, float4*) {
             if (whole)
               store_out4(a.O + b * a.Hq * D + 4 * i, x, inv_sum(sc.ml[h].y));
