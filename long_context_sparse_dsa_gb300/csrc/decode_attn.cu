@@ -16,7 +16,8 @@
 // cut, and skipped where empty, because a row with fewer pools than k has its
 // empty steps at the end: 112 rows of up to 352 pools, k = 512, 32 heads, took
 // 30.4 us against 23.7.)
-// Whole cache: rows differ, so the rows' steps form one list, cut into equal
+// Whole cache: where rows are short, likewise (by_rows below).  Else, since rows
+// differ, the rows' steps form one list, cut into equal
 // contiguous ranges, one per CTA: a CTA takes the end of one row, whole rows,
 // the start of another.  Every CTA derives the cut from the lengths itself.
 // A row that lies in one CTA is written out; the pieces of a row that
@@ -952,11 +953,11 @@ __device__ __forceinline__ SlotRow slot_row(const AttnArgs<T>& a, int64_t b, boo
   return sr;
 }
 
-// Selected pools: grid (splits, batch), the splits of a row are one cluster.
-template <typename T, int D, int MAXH>
-__global__ void __launch_bounds__(kAttnThreads, (Piece<T, D, MAXH, true>::CTAS))
-    decode_attn_selected_kernel(const __grid_constant__ AttnArgs<T> a) {
-  using P = Piece<T, D, MAXH, true>;
+// A row per cluster: grid (splits, batch).
+template <typename T, int D, int MAXH, bool SEL>
+__global__ void __launch_bounds__(kAttnThreads, (Piece<T, D, MAXH, SEL>::CTAS))
+    decode_attn_rows_kernel(const __grid_constant__ AttnArgs<T> a) {
+  using P = Piece<T, D, MAXH, SEL>;
   extern __shared__ __align__(128) unsigned char dec_smem[];
   AttnScratch& sc = *reinterpret_cast<AttnScratch*>(dec_smem + P::TILES);
   chain_wait();
@@ -965,7 +966,8 @@ __global__ void __launch_bounds__(kAttnThreads, (Piece<T, D, MAXH, true>::CTAS))
   const int splits = gridDim.x, rank = blockIdx.x;
   bool bad_page = false, bad_idx = false;
   const SlotRow sr = slot_row(a, b, bad_page);
-  const int n_steps = (a.k + 4) >> 2;   // whatever the length: the idx loads need not wait for it
+  // of selected pools whatever the length: the idx loads need not wait for it
+  const int n_steps = SEL ? (a.k + 4) >> 2 : row_steps(sr.len);
   P::run(
       a, sr, b, rank * P::MIN_STEPS, n_steps, splits * P::MIN_STEPS, dec_smem, sc, splits > 1,
       [&](int i, int h, float4 x, float4* at) {
@@ -1182,28 +1184,50 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(Pieces ps, T*
   if (threadIdx.x == 0 && blockIdx.z == 0) LSE[(int64_t)it.row * Hq + h] = lse_of(mm, l);
 }
 
+// Whether a whole cache whose rows have up to `steps` steps is attended to with a
+// cluster of `splits` CTAs per row.  That saves the cut and the join kernel (3
+// us), but takes as long as the longest row, on no more than 16 CTAs a row; the
+// list shares the lengths out evenly, 0.6 of it for ragged rows, and begins
+// every row for the price of kRowPad steps.  Compared are the rounds a warp
+// makes; one is dearer in fp32.  Measured, list and clusters, bf16, 16 heads of
+// 128: 150 rows of up to 1000 tokens 17.1 and 11.7 us, 40 of 500 8.2 and 6.3, 40
+// of up to 4000 11.5 and 12.7, one of 4000 6.2 and 7.1.
+static bool by_rows(int64_t batch, int64_t steps, unsigned splits, int resident, int warps, bool bf16) {
+  const double list = (double)batch * (double)(steps + kRowPad) / ((double)resident * warps);
+  const double waves = (double)batch * splits / resident;
+  const double rows = (waves > 1. ? waves : 1.) * (double)steps / ((double)splits * warps);
+  return rows - 0.6 * list <= (bf16 ? 2.5 : 1.25);
+}
+
+template <typename T, int D, int MAXH, bool SEL>
+static cudaError_t launch_rows(const AttnArgs<T>& a, int64_t steps, cudaStream_t s, bool& launched) {
+  using P = Piece<T, D, MAXH, SEL>;
+  auto kern = decode_attn_rows_kernel<T, D, MAXH, SEL>;
+  static KernelState st;
+  int dev;
+  cudaError_t e = prepare_kernel(kern, P::SMEM, kAttnThreads, st, dev);
+  if (e != cudaSuccess) return e;
+  // a step for every warp
+  const unsigned splits = cluster_per_row(st, dev, a.batch, (steps + P::MIN_STEPS - 1) / P::MIN_STEPS);
+  launched = SEL || by_rows(a.batch, steps, splits, kSms * P::CTAS, P::MIN_STEPS, sizeof(T) == 2);
+  if (!launched) return cudaSuccess;
+  return launch_chained_cluster(splits, kern, dim3(splits, (unsigned)a.batch), dim3(kAttnThreads), P::SMEM, s, a);
+}
+
 template <typename T, int D, int MAXH>
 static cudaError_t launch_shape(const AttnArgs<T>& a, cudaStream_t s) {
-  if (a.idx) {
-    using P = Piece<T, D, MAXH, true>;
-    auto kern = decode_attn_selected_kernel<T, D, MAXH>;
-    static KernelState st;
-    int dev;
-    cudaError_t e = prepare_kernel(kern, P::SMEM, kAttnThreads, st, dev);
-    if (e != cudaSuccess) return e;
-    const int64_t row_steps = (a.k + 4) >> 2;   // a step for every warp
-    const unsigned splits = cluster_per_row(st, dev, a.batch, (row_steps + P::MIN_STEPS - 1) / P::MIN_STEPS);
-    return launch_chained_cluster(splits, kern, dim3(splits, (unsigned)a.batch), dim3(kAttnThreads), P::SMEM,
-                                  s, a);
-  }
+  bool done = false;
+  if (a.idx) return launch_rows<T, D, MAXH, true>(a, (a.k + 4) >> 2, s, done);
+  const int64_t row_max = ((int64_t)a.pv.capacity + 15) >> 4;
+  cudaError_t e = launch_rows<T, D, MAXH, false>(a, row_max, s, done);
+  if (e != cudaSuccess || done) return e;
   using P = Piece<T, D, MAXH, false>;
   auto kern = decode_attn_all_kernel<T, D, MAXH>;
   static KernelState st;
   int dev;
-  cudaError_t e = prepare_kernel(kern, P::SMEM, 0, st, dev);
+  e = prepare_kernel(kern, P::SMEM, 0, st, dev);
   if (e != cudaSuccess) return e;
   // as many CTAs as can have work
-  const int64_t row_max = ((int64_t)a.pv.capacity + 15) >> 4;
   const int64_t want = a.batch * ((row_max + kRowPad + P::MIN_STEPS - 1) / P::MIN_STEPS);
   const unsigned ctas = (unsigned)(want < kSms * P::CTAS ? want : kSms * P::CTAS);
   e = launch_chained(kern, dim3(ctas), dim3(kAttnThreads), P::SMEM, s, a);
