@@ -155,6 +155,55 @@ def test_dense_attention_batches(dtype, lens):
     dsa.check_device_error()
 
 
+@pytest.mark.parametrize("dtype,Hq", [("bf16", 16), ("bf16", 32), ("fp32", 8), ("fp32", 20)])
+@pytest.mark.parametrize("batch", [1, 17, 28, 45, 95, 150, 400, 700])
+def test_dense_attention_short_rows(dtype, Hq, batch):
+    """Whole caches of short rows in every number of CTAs per row, and more rows than fit at once."""
+    lens = [(b * 7919 + 61) % 260 if b % 9 else 0 for b in range(batch)]
+    lens[0] = 301
+    pg = Paged(lens, 16, d=64, dtype=dtype, seed=batch + Hq).fill()
+    q, o, lse = _attn(pg, Hq, 64)
+    _check_attn(pg, q, o, lse, 64 ** -0.5)
+    dsa.check_device_error()
+
+
+@pytest.mark.parametrize("cap", [304, 60000])
+def test_dense_attention_skips_and_reports_bad_rows(cap):
+    """A bad page's tokens are missing, a row of bad length is idle, others are as without: for short rows and long ones."""
+    pg = Paged([300, 170, 0, 65], 16, seed=4, cap=cap).fill()
+    dims = dsa.make_dims(cap, 16, 128, 8, 64, 8)
+    q = torch.randn(4, 16, 128, generator=pg.g).to(torch.bfloat16).to(DEV)
+    lens, table = pg.args()
+
+    def call(l, t):
+        o, lse = torch.full_like(q, 7.0), torch.full((4, 16), 7.0, device=DEV)
+        dsa.decode_attn(dims, pg.cache(), l, t, q, o, lse, _junk_ws(dims, 4))
+        return o, lse
+
+    o, lse = call(lens, table)
+    _check_attn(pg, q.cpu(), o, lse, 128 ** -0.5)
+    dsa.check_device_error()
+    t = table.clone()
+    t[0, 3], t[3, :] = pg.pages, -1
+    o1, lse1 = call(lens, t)
+    with pytest.raises(dsa.DSAError) as e:
+        dsa.check_device_error()
+    assert e.value.status == dsa.DSA_ERR_BAD_PAGE
+    assert torch.equal(o1[1], o[1]) and torch.all(o1[3] == 0) and torch.all(lse1[3] == -math.inf)
+    assert not torch.equal(o1[0], o[0])
+    pg.K[0], pg.V[0] = [torch.cat([x[:48], x[64:]]) for x in (pg.K[0], pg.V[0])]
+    pg.lens_list = [284, 170, 0, 0]
+    _check_attn(pg, q.cpu(), o1, lse1, 128 ** -0.5)
+    l = lens.clone()
+    l[0], l[1] = cap + 1, -2
+    o2, lse2 = call(l, table)
+    with pytest.raises(dsa.DSAError) as e:
+        dsa.check_device_error()
+    assert e.value.status == dsa.DSA_ERR_BAD_PAGE
+    assert torch.all(o2[:2] == 0) and torch.all(lse2[:2] == -math.inf) and torch.equal(o2[3], o[3])
+    dsa.check_device_error()
+
+
 def test_capacity_far_above_the_lengths():
     pg = Paged([5, 1000, 64], 16, cap=1 << 20).fill()
     q, o, lse = _attn(pg, 16, 128)
