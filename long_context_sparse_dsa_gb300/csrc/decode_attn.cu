@@ -16,15 +16,14 @@
 // cut, and skipped where empty, because a row with fewer pools than k has its
 // empty steps at the end: 112 rows of up to 352 pools, k = 512, 32 heads, took
 // 30.4 us against 23.7.)
-// Whole cache: where rows are short, likewise (by_rows below).  Else, since rows
-// differ, the rows' steps form one list, cut into equal
-// contiguous ranges, one per CTA: a CTA takes the end of one row, whole rows,
-// the start of another.  Every CTA derives the cut from the lengths itself.
-// A row that lies in one CTA is written out; the pieces of a row that
-// straddles CTAs (at most two per CTA) go to the workspace as (o, base, sum)
-// and a second kernel joins them.  (Cutting selected rows that way cost a
-// second piece, with its whole load chain, in a fifth of the CTAs: 42 us
-// against 24 for 96 rows of 2051 keys.)
+// Whole cache: where rows are short, likewise (by_rows below).  Else, since
+// rows differ, the rows' steps form one list, cut into equal contiguous ranges,
+// one per CTA: a CTA takes the end of one row, whole rows, the start of another.
+// Every CTA derives the cut from the lengths itself.  A row that lies in one CTA
+// is written out; the pieces of a row that straddles CTAs (at most two per CTA)
+// go to the workspace as (o, base, sum) and a second kernel joins them.
+// (Cutting selected rows that way cost a second piece, with its whole load
+// chain, in a fifth of the CTAs: 42 us against 24 for 96 rows of 2051 keys.)
 //
 // bf16: steps go round-robin to a CTA's warps, each with a ring of its own
 // filled by cp.async, heads (one or two groups of 16) on the M side of
