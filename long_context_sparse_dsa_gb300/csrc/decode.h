@@ -54,8 +54,8 @@ struct KernelState {
 
 // Shared memory of an SM, in percent of the most, that the indexer's scores and
 // top-k kernels ask for (100 KB; the rest is L1 cache).  Two kernels in a row that
-// want it split differently do not overlap: with each left to the driver's
-// choice 64 rows of 1000 pools took 7.0 us against 6.2, 16 rows of 8191 12.0
+// want it split differently do not overlap: with each left at the default,
+// 64 rows of 1000 pools took 7.0 us against 6.2, 16 rows of 8191 12.0
 // against 10.9.
 constexpr int kIndexerCarveout = 43;
 
