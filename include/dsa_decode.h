@@ -110,6 +110,8 @@ size_t dsa_decode_workspace_bytes(const dsa_dims *dims, int64_t batch);
  *   k_out      [n_tokens, d] layer dtype or NULL: the rotated keys as they
  *              enter the cache (dsa_layer_fwd of a prompt wants them
  *              contiguous; k_out may be k itself); only with a rotation
+ * A token whose page is bad does not enter the cache; its q_out and k_out are
+ * written like any other's (its row's attention goes on without its key).
  * Writes k, v, the kpool rows of pools the new tokens complete (bitwise
  * dsa_pool_keys') and ktail.  Rotation: sine and cosine and products in fp32,
  * one rounding.  Two rows must not append to the same page. */

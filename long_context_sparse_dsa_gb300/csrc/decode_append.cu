@@ -58,19 +58,18 @@ struct Place {
   int64_t row;     // its row in the cache (page * page_size + position in the page); -1: nowhere
   int64_t start;   // first new position of its sequence in this call
   int64_t pos;     // its own position
-  int64_t b;       // its sequence
+  int64_t b;       // its sequence; -1: none.  A token of a sequence is without a row where its page is bad
   int len;         // the sequence's length after the call
   int page;
 };
 
 __device__ __forceinline__ Place place_of(const AppendArgs& a, int64_t t, bool& bad) {
   Place p;
-  p.row = -1;
-  p.b = t;
+  p.row = p.b = -1;
   p.start = p.pos = 0;
   p.len = p.page = 0;
   if (t >= a.n_tokens) return p;
-  int64_t begin = t, n_new = 1;
+  int64_t b = t, begin = t, n_new = 1;
   if (a.offsets) {
     if (t >= (int64_t)__ldg(a.offsets + a.batch)) return p;   // behind the last row
     int64_t lo = 0, hi = a.batch;   // offsets[lo] <= t < offsets[hi]
@@ -81,11 +80,11 @@ __device__ __forceinline__ Place place_of(const AppendArgs& a, int64_t t, bool& 
       else
         hi = mid;
     }
-    p.b = lo;
+    b = lo;
     begin = __ldg(a.offsets + lo);
     n_new = (int64_t)__ldg(a.offsets + lo + 1) - begin;
   }
-  p.len = row_length(a.pv, p.b, bad);
+  p.len = row_length(a.pv, b, bad);
   if (!a.offsets && p.len == 0) return p;   // an idle row of a decode step
   const int64_t j = t - begin;
   p.start = (int64_t)p.len - n_new;
@@ -94,9 +93,10 @@ __device__ __forceinline__ Place place_of(const AppendArgs& a, int64_t t, bool& 
     bad = true;
     return p;
   }
+  p.b = b;
   const int pool = (int)(p.pos >> 2);
   const int col = page_of_pool(a.pv, pool);
-  p.page = __ldg(a.pv.table + p.b * a.pv.cols + col);
+  p.page = __ldg(a.pv.table + b * a.pv.cols + col);
   const int pp = phys_pool(a.pv, pool, col, p.page, bad);
   if (pp >= 0) p.row = (int64_t)pp * 4 + (p.pos & 3);
   return p;
@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32) cache_append_rotated_kernel
   bool bad = false;
   const Place p = place_of(a, t, bad);
   if (bad && lane == 0) record_error(DSA_DEV_ERR_BAD_PAGE);
-  if (p.row < 0) return;
+  if (p.b < 0) return;   // without a row: q_out and k_out are written, the cache is not
 
   float cs[N], sn[N];
   {
@@ -268,16 +268,18 @@ __global__ void __launch_bounds__(kAppendWarps * 32) cache_append_rotated_kernel
   }
   if (lane < UN) {
     if (rotated) rotate_unit<T>(kx, ky, cs, sn, inter);
-    uint4* ck = static_cast<uint4*>(a.ck) + p.row * CH;
-    ck[c0] = kx;
-    ck[c1] = ky;
+    if (p.row >= 0) {
+      uint4* ck = static_cast<uint4*>(a.ck) + p.row * CH;
+      ck[c0] = kx;
+      ck[c1] = ky;
+    }
     if (a.k_out) {
       uint4* ko = static_cast<uint4*>(a.k_out) + t * CH;
       ko[c0] = kx;
       ko[c1] = ky;
     }
   }
-  if (lane < CH) (static_cast<uint4*>(a.cv) + p.row * CH)[lane] = vx;
+  if (lane < CH && p.row >= 0) (static_cast<uint4*>(a.cv) + p.row * CH)[lane] = vx;
   if (a.q) {
     for (int h0 = 0; h0 < a.Hq; h0 += AHEAD * HPP) {
       if (h0) load_q(h0);
@@ -292,7 +294,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32) cache_append_rotated_kernel
       }
     }
   }
-  put_index_key<T>(a, t, p, lane, 32);
+  if (p.row >= 0) put_index_key<T>(a, t, p, lane, 32);
 }
 
 template <typename T, int D>

@@ -1,0 +1,73 @@
+"""What the header of the paged decode operators promises beside the ordinary calls.  Caches, references and tolerances are
+those of test_gpu_decode.
+"""
+import pytest
+import torch
+
+import long_context_sparse_dsa_gb300 as dsa
+from test_gpu_decode import (DEV, Paged, _built, _check_attn, _close_rotated, _freq, _junk_ws, _ref_topk,  # noqa: F401
+                             _rotate)
+
+pytestmark = pytest.mark.gpu
+
+
+def _reports(status):
+    with pytest.raises(dsa.DSAError) as e:
+        dsa.check_device_error()
+    assert e.value.status == status
+
+
+# ---------------------------------------------------------------- the newest token's page is bad
+@pytest.mark.parametrize("dtype,Hq,inter", [("bf16", 16, False), ("bf16", 32, True), ("fp32", 8, False)])
+def test_step_of_a_row_whose_newest_page_is_bad(dtype, Hq, inter):
+    """Rows 0 and 2 begin a page that is not there: only the new token is missing from their results, which are those of
+    their own, rotated query whatever the workspace held."""
+    k, page, d = 6, 16, 128
+    pg = Paged([161, 90, 49, 33], page, dtype=dtype, seed=110 + Hq).fill([160, 89, 48, 32])
+    dims = dsa.make_dims(pg.cap, Hq, d, 8, 64, k, dtype=dtype)
+    lens, table = pg.args()
+    bad = table.clone()
+    bad[0, 10], bad[2, 3] = pg.pages, -1
+    rot = dsa.make_rotation(_freq(64), interleaved=inter)
+    g = pg.g
+    q = torch.randn(4, Hq, d, generator=g).to(pg.dt)
+    qi = torch.randint(-3, 4, (4, 8, 64), generator=g).to(pg.dt)
+    w = torch.randint(1, 5, (4, 8), generator=g).float()
+    last = lambda xs: torch.stack([x[-1] for x in xs]).to(DEV)
+    o, lse = torch.full((4, Hq, d), 7.0, dtype=pg.dt, device=DEV), torch.full((4, Hq), 7.0, device=DEV)
+    idx = torch.full((4, k), -9, dtype=torch.int32, device=DEV)
+    cache = pg.cache()
+    dsa.decode_step(dims, cache, lens, bad, q.to(DEV), last(pg.K), last(pg.V), qi.to(DEV), last(pg.KI), w.to(DEV), o, lse, idx,
+                    _junk_ws(dims, 4), rotation=rot)
+    _reports(dsa.DSA_ERR_BAD_PAGE)
+    assert torch.equal(idx.cpu(), _ref_topk(pg, qi, w, k))
+    # the queries as an append with a sound table rotates them; where the new key went in, it is the rotated one
+    q_rot = torch.full((4, Hq, d), 7.0, dtype=pg.dt, device=DEV)
+    dsa.cache_append(dims, pg.cache(), lens, table, last(pg.K), last(pg.V), last(pg.KI), rotation=rot, q=q.to(DEV), q_out=q_rot)
+    dsa.check_device_error()
+    for b in (1, 3):
+        at, r = pg.where(b, lens[b].item() - 1)
+        pg.K[b][-1] = cache.k[at, r].cpu()
+    pg.lens_list = [160, 90, 48, 33]         # what rows 0 and 2 have left
+    _check_attn(pg, q_rot.cpu(), o, lse, d ** -0.5, idx.cpu())
+
+
+@pytest.mark.parametrize("with_offsets", [False, True])
+def test_append_to_a_bad_page_still_rotates(with_offsets):
+    """q_out and k_out of a token whose page is bad are its rotated rows; nothing of it enters the cache."""
+    pg = Paged([17, 40], 16, seed=112)
+    dims = dsa.make_dims(pg.cap, 5, 128, 8, 64, 8)
+    lens, table = pg.args()
+    table[0, 1] = pg.pages
+    q = torch.randn(2, 5, 128, generator=pg.g).to(torch.bfloat16)
+    k = torch.stack([x[-1] for x in pg.K])
+    q_out, k_out = torch.full_like(q, 7.0).to(DEV), torch.full_like(k, 7.0).to(DEV)
+    off = torch.tensor([0, 1, 2], dtype=torch.int32, device=DEV) if with_offsets else None
+    cache = pg.cache()
+    dsa.cache_append(dims, cache, lens, table, k.to(DEV), k.to(DEV), torch.ones(2, 64, dtype=torch.bfloat16, device=DEV),
+                     offsets=off, rotation=dsa.make_rotation(_freq(128)), q=q.to(DEV), q_out=q_out, k_out=k_out)
+    _reports(dsa.DSA_ERR_BAD_PAGE)
+    pos = torch.tensor([16, 39])
+    _close_rotated(q_out, _rotate(q.double(), pos, _freq(128), False), "bf16")
+    _close_rotated(k_out, _rotate(k.double(), pos, _freq(128), False), "bf16")
+    assert int((~torch.isnan(cache.k.float()).any(-1)).sum()) == 1
