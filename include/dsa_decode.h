@@ -101,8 +101,11 @@ size_t dsa_decode_workspace_bytes(const dsa_dims *dims, int64_t batch);
  *   n_tokens   rows of the new-token tensors
  *   offsets    [batch+1] int32: row b's new tokens are rows offsets[b] ..
  *              offsets[b+1]-1, the last one at position lens[b]-1.  offsets
- *              ascend; rows behind offsets[batch] are left alone.  NULL: one
- *              token per row (n_tokens == batch); idle rows append nothing
+ *              ascend within 0 .. n_tokens; rows before offsets[0] and behind
+ *              offsets[batch] are left alone (part of a batch: lens,
+ *              block_table and offsets from that row on, the tokens as they
+ *              are).  NULL: one token per row (n_tokens == batch); idle rows
+ *              append nothing
  *   k, v       [n_tokens, d] layer dtype; k_idx [n_tokens, di] layer dtype
  *   rotation   NULL (no rotation), or applied to k, and to q if given
  *   q, q_out   [n_tokens, Hq, d] layer dtype: q rotated into q_out (q_out may

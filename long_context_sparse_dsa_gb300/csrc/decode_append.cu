@@ -71,7 +71,9 @@ __device__ __forceinline__ Place place_of(const AppendArgs& a, int64_t t, bool& 
   if (t >= a.n_tokens) return p;
   int64_t b = t, begin = t, n_new = 1;
   if (a.offsets) {
-    if (t >= (int64_t)__ldg(a.offsets + a.batch)) return p;   // behind the last row
+    // before the first row, or behind the last
+    const int64_t from = __ldg(a.offsets), to = __ldg(a.offsets + a.batch);
+    if (t >= to || (t < from && from <= a.n_tokens)) return p;
     int64_t lo = 0, hi = a.batch;   // offsets[lo] <= t < offsets[hi]
     while (hi - lo > 1) {
       const int64_t mid = (lo + hi) >> 1;

@@ -71,3 +71,33 @@ def test_append_to_a_bad_page_still_rotates(with_offsets):
     _close_rotated(q_out, _rotate(q.double(), pos, _freq(128), False), "bf16")
     _close_rotated(k_out, _rotate(k.double(), pos, _freq(128), False), "bf16")
     assert int((~torch.isnan(cache.k.float()).any(-1)).sum()) == 1
+
+
+# ---------------------------------------------------------------- part of a batch
+@pytest.mark.parametrize("rot", [0, 64])
+@pytest.mark.parametrize("n", [9, 4000])
+def test_append_of_part_of_a_batch(n, rot):
+    """offsets[0] > 0: the second half of a batch's rows, out of the tokens of the whole batch.  Rows before offsets[0] are
+    left alone like those behind the last, and are no error."""
+    total = [n, 1, 2 * n, 3, n + 5, 0, 3 * n, 2]
+    pg = Paged(total, 16, seed=120 + n)
+    dims = dsa.make_dims(pg.cap, 2, 128, 8, 64, 8)
+    lens, table = pg.args()
+    off = torch.tensor([0] + total, dtype=torch.int32).cumsum(0).to(torch.int32).to(DEV)
+    cat = lambda xs: torch.cat(xs).to(DEV)
+    kw = {}
+    if rot:
+        kw = dict(rotation=dsa.make_rotation(_freq(rot)), k_out=torch.full((sum(total), 128), 7.0, dtype=torch.bfloat16, device=DEV))
+    half, whole = pg.cache(), pg.cache()
+    dsa.cache_append(dims, half, lens[4:], table[4:], cat(pg.K), cat(pg.V), cat(pg.KI), offsets=off[4:], **kw)
+    dsa.check_device_error()
+    if rot:
+        assert torch.all(kw["k_out"][:off[4]] == 7) and not torch.any((kw["k_out"][off[4]:] == 7).all(-1))
+    there = ~torch.isnan(half.k.float()).any(-1)
+    assert int(there.sum()) == sum(total[4:])
+    dsa.cache_append(dims, half, lens[:4], table[:4], cat(pg.K), cat(pg.V), cat(pg.KI), offsets=off[:5], **kw)
+    dsa.cache_append(dims, whole, lens, table, cat(pg.K), cat(pg.V), cat(pg.KI), offsets=off, **kw)
+    dsa.check_device_error()
+    for x in ("k", "v", "kpool", "ktail"):
+        a, b = getattr(half, x), getattr(whole, x)
+        assert torch.equal(a.view(torch.int16), b.view(torch.int16)), x
