@@ -71,9 +71,10 @@ __device__ __forceinline__ Place place_of(const AppendArgs& a, int64_t t, bool& 
   if (t >= a.n_tokens) return p;
   int64_t b = t, begin = t, n_new = 1;
   if (a.offsets) {
-    // before the first row, or behind the last
     const int64_t from = __ldg(a.offsets), to = __ldg(a.offsets + a.batch);
-    if (t >= to || (t < from && from <= a.n_tokens)) return p;
+    // rows that have no token at all among the call's would not show below
+    if (t == 0 && (from < 0 || from > to || to > a.n_tokens)) record_error(DSA_DEV_ERR_BAD_PAGE);
+    if (t < from || t >= to) return p;   // before the first row, or behind the last
     int64_t lo = 0, hi = a.batch;   // offsets[lo] <= t < offsets[hi]
     while (hi - lo > 1) {
       const int64_t mid = (lo + hi) >> 1;

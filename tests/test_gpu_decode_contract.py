@@ -101,3 +101,29 @@ def test_append_of_part_of_a_batch(n, rot):
     for x in ("k", "v", "kpool", "ktail"):
         a, b = getattr(half, x), getattr(whole, x)
         assert torch.equal(a.view(torch.int16), b.view(torch.int16)), x
+
+
+@pytest.mark.parametrize("off,appended", [([0, 2, 5, 9], [0, 1]), ([0, 2, 5, 5], [0, 1]), ([9, 9, 9, 9], []), ([0, 0, 0, -1], []),
+                                          ([3, 3, 3, 2], []), ([1, 3, 3, 5], [0, 2])])
+def test_offsets_outside_the_tokens_are_reported(off, appended):
+    """Rows that the offsets put behind the call's 5 tokens, or that descend, are skipped and reported, other rows appended;
+    offsets within 0 .. 5 that leave tokens out are no error."""
+    pg = Paged([8, 11, 6], 16, seed=130)
+    dims = dsa.make_dims(pg.cap, 4, 128, 8, 64, 8)
+    lens, table = pg.args()
+    cache = pg.cache()
+    k = torch.randn(5, 128, generator=pg.g).to(torch.bfloat16).to(DEV)
+    dsa.cache_append(dims, cache, lens, table, k, k, torch.ones(5, 64, dtype=torch.bfloat16, device=DEV),
+                     offsets=torch.tensor(off, dtype=torch.int32, device=DEV))
+    if 0 <= off[0] <= off[-1] <= 5:
+        dsa.check_device_error()
+    else:
+        _reports(dsa.DSA_ERR_BAD_PAGE)
+    want = torch.full_like(cache.k, float("nan"))
+    for b in appended:
+        n = off[b + 1] - off[b]
+        pos = torch.arange(pg.lens_list[b] - n, pg.lens_list[b])
+        at, r = pg.where(b, pos)
+        want[at, r] = k[off[b]:off[b + 1]]
+    for got in (cache.k, cache.v):
+        assert torch.equal(got.nan_to_num(9.0), want.nan_to_num(9.0))
