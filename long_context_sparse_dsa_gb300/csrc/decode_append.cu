@@ -105,8 +105,8 @@ __device__ __forceinline__ Place place_of(const AppendArgs& a, int64_t t, bool& 
   return p;
 }
 
-// The part of token t that concerns pool keys and the tail; `c0` is this
-// lane's first chunk of the indexer key, `step` the distance to its next.
+// The part of token t, of a sequence, that concerns pool keys and the tail; `c0`
+// is this lane's first chunk of the indexer key, `step` the distance to its next.
 template <typename T>
 __device__ __forceinline__ void put_index_key(const AppendArgs& a, int64_t t, const Place& p, int c0, int step) {
   constexpr int N = Vec16<T>::N;
@@ -116,12 +116,13 @@ __device__ __forceinline__ void put_index_key(const AppendArgs& a, int64_t t, co
   const int64_t open = (int64_t)(p.len >> 2) << 2;      // first position of the incomplete pool
   // The row's first pool may mix kept and new keys; the lanes that complete it
   // read the page's ktail rows and only then write the keys of the row's last
-  // pool (possibly into the same rows), for the tokens that would otherwise.
+  // pool (possibly into the same rows), for the tokens that would otherwise: also
+  // when their own page is bad, since the last pool's may be good.
   const bool mixed = (p.start & 3) != 0 && (p.start >> 2) < (p.len >> 2);
   if (r == 3) {
     const bool first = mixed && (p.pos >> 2) == (p.start >> 2);
     const uint4* kept = static_cast<const uint4*>(a.cktail) + (int64_t)p.page * 3 * CI;
-    for (int c = c0; c < CI; c += step) {
+    for (int c = c0; c < CI && p.row >= 0; c += step) {
       uint4 raw[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -149,7 +150,7 @@ __device__ __forceinline__ void put_index_key(const AppendArgs& a, int64_t t, co
       for (int i = 0; i < (int)(p.len - open); ++i)
         for (int c = c0; c < CI; c += step) tail[i * CI + c] = __ldg(ki + (open + i - p.pos) * CI + c);
     }
-  } else if (p.pos >= open && !mixed) {
+  } else if (p.pos >= open && !mixed && p.row >= 0) {
     uint4* tail = static_cast<uint4*>(a.cktail) + ((int64_t)p.page * 3 + r) * CI;
     for (int c = c0; c < CI; c += step) tail[c] = __ldg(ki + c);
   }
@@ -202,7 +203,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32) cache_append_kernel(const _
     q.b = __shfl_sync(0xffffffffu, p.b, j);
     q.len = __shfl_sync(0xffffffffu, p.len, j);
     q.page = __shfl_sync(0xffffffffu, p.page, j);
-    if (q.row >= 0) put_index_key<T>(a, t0 + j, q, lane % LPT, LPT);
+    if (q.b >= 0) put_index_key<T>(a, t0 + j, q, lane % LPT, LPT);
   }
 }
 
@@ -297,7 +298,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32) cache_append_rotated_kernel
       }
     }
   }
-  if (p.row >= 0) put_index_key<T>(a, t, p, lane, 32);
+  put_index_key<T>(a, t, p, lane, 32);
 }
 
 template <typename T, int D>

@@ -127,3 +127,30 @@ def test_offsets_outside_the_tokens_are_reported(off, appended):
         want[at, r] = k[off[b]:off[b + 1]]
     for got in (cache.k, cache.v):
         assert torch.equal(got.nan_to_num(9.0), want.nan_to_num(9.0))
+
+
+# ---------------------------------------------------------------- an append across a bad page
+@pytest.mark.parametrize("rot", [0, 64])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_append_across_a_bad_page_keeps_the_open_pool(dtype, rot):
+    """A prompt piece begins inside a pool on a bad page and ends inside a pool on a good one: the good page's tokens are
+    all kept, so that the pool they begin is completed by a later append as if nothing had happened."""
+    pg = Paged([8, 30], 4, dtype=dtype, seed=115)
+    dims = dsa.make_dims(pg.cap, 4, 128, 8, 64, 8, dtype=dtype)
+    table = pg.table.clone()
+    table[0, 0] = -1
+    cache = pg.cache()
+    rotation = dsa.make_rotation(_freq(rot)) if rot else None
+
+    def put(a, z):
+        cat = lambda xs: torch.cat([x[i:j] for x, i, j in zip(xs, a, z)]).to(DEV)
+        off = torch.tensor([0, z[0] - a[0], z[0] - a[0] + z[1] - a[1]], dtype=torch.int32, device=DEV)
+        dsa.cache_append(dims, cache, torch.tensor(z, dtype=torch.int32, device=DEV), table.to(DEV), cat(pg.K), cat(pg.V),
+                         cat(pg.KI), offsets=off, rotation=rotation)
+    put([2, 0], [6, 22])                     # row 0: tokens 2, 3 on the bad page, 4, 5 on the next
+    _reports(dsa.DSA_ERR_BAD_PAGE)
+    put([6, 22], [8, 30])
+    dsa.check_device_error()
+    kp = cache.kpool.cpu()
+    assert torch.equal(kp[pg.table[0, 1].long(), 0], pg.pool_keys(0)[1])
+    assert torch.equal(kp[pg.table[1, :7].long(), 0], pg.pool_keys(1)[:7])
