@@ -126,7 +126,10 @@ dsa_status dsa_cache_append(const dsa_dims *dims, const dsa_paged_cache *cache, 
 /* Indexer scores and top-k selection of one query per row over the paged pool
  * keys: s[b,p] = sum_h w[b,h] * max(0, q_idx[b,h] . kpool[p]) for p <
  * elig(b); the min(k, elig(b)) best by (score desc, pool asc), ascending,
- * padded with -1.  Exact selection on the fp32 scores as in dsa_topk.
+ * padded with -1.  Exact selection on the fp32 scores as in dsa_topk.  A pool
+ * on a bad page ranks behind all others: it is named only where fewer than k
+ * others are there (a row of at most k pools names all of them and its pages
+ * are not looked at), and dsa_decode_attn skips it.
  *   q_idx  [batch, Hi, di] layer dtype    w [batch, Hi] fp32
  *   idx    [batch, k] int32, output       ws >= dsa_decode_workspace_bytes */
 dsa_status dsa_decode_indexer_topk(const dsa_dims *dims, const dsa_paged_cache *cache, int64_t batch,

@@ -41,6 +41,18 @@ struct PoolBlock {
   __device__ __forceinline__ int get(int i, int j) const {   // pool p0 + 32 i + j
     return __shfl_sync(0xffffffffu, pp[i], j);
   }
+  // Behind the warp's scores, by all of its lanes: reports pools on bad pages,
+  // which rank behind all others.  (Chosen where the scores are stored, it cost
+  // registers: one fp32 row of 262144 pools with 8 heads 40.0 us against 27.7.)
+  __device__ __forceinline__ void finish(float* srow, int p0, int n, bool bad) const {
+    if (!__any_sync(0xffffffffu, bad)) return;
+    __syncwarp();   // after the other lanes' stores
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (pp[i] < 0 && 32 * i + lane < PPW && p0 + 32 * i + lane < n) srow[p0 + 32 * i + lane] = -INFINITY;
+    if (bad) record_error(DSA_DEV_ERR_BAD_PAGE);
+  }
 };
 
 template <int DI, int PPW>
@@ -101,7 +113,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32)
       if (p + 8 < n) srow[p + 8] = s1;
     }
   }
-  if (bad) record_error(DSA_DEV_ERR_BAD_PAGE);
+  pools.finish(srow, p0, n, bad);
 }
 
 template <int DI, int PPW, int NH>
@@ -175,8 +187,8 @@ __global__ void __launch_bounds__(kScoreWarps * 32)
     if (li == 0 && p < n) scores[b * pitch + p] = s;
   };
   if (NH == 4) {
-    // the loads of 4 passes run ahead; where the heads take 128 registers the
-    // compiler's own order is faster (1M tokens, di 64: 28.6 us against 34.3)
+    // the loads of 4 passes run ahead; where the heads' channels take 64 registers
+    // requesting 4 passes together is faster (1M tokens, di 64: 27.0 us against 34.3)
     constexpr int AHEAD = 4;
     static_assert(PPW / RPW % AHEAD == 0, "whole rounds");
     float4 kf[AHEAD][2];
@@ -193,14 +205,17 @@ __global__ void __launch_bounds__(kScoreWarps * 32)
       }
     }
   } else {
-#pragma unroll 4
-    for (int i = 0; i < PPW; i += RPW) {
-      float4 kf[2];
-      load(i, kf);
-      score(i, kf[0], kf[1]);
+    constexpr int BATCH = 4;   // passes requested together
+#pragma unroll 1
+    for (int i0 = 0; i0 < PPW; i0 += BATCH * RPW) {
+      float4 kf[BATCH][2];
+#pragma unroll
+      for (int u = 0; u < BATCH; ++u) load(i0 + u * RPW, kf[u]);
+#pragma unroll
+      for (int u = 0; u < BATCH; ++u) score(i0 + u * RPW, kf[u][0], kf[u][1]);
     }
   }
-  if (bad) record_error(DSA_DEV_ERR_BAD_PAGE);
+  pools.finish(scores + b * pitch, p0, n, bad);
 }
 
 template <int DI, int PPW>

@@ -1,6 +1,8 @@
 """What the header of the paged decode operators promises beside the ordinary calls.  Caches, references and tolerances are
 those of test_gpu_decode.
 """
+import math
+
 import pytest
 import torch
 
@@ -154,3 +156,31 @@ def test_append_across_a_bad_page_keeps_the_open_pool(dtype, rot):
     kp = cache.kpool.cpu()
     assert torch.equal(kp[pg.table[0, 1].long(), 0], pg.pool_keys(0)[1])
     assert torch.equal(kp[pg.table[1, :7].long(), 0], pg.pool_keys(1)[:7])
+
+
+# ---------------------------------------------------------------- pools on bad pages
+@pytest.mark.parametrize("dtype,Hi,di", [("bf16", 8, 64), ("bf16", 3, 128), ("fp32", 4, 64), ("fp32", 8, 128)])
+@pytest.mark.parametrize("n,k", [(400, 20), (4096, 60), (40000, 700)])
+def test_pools_on_bad_pages_rank_last(dtype, Hi, di, n, k):
+    """Weights of both signs, so that many scores lie below 0: no pool of a bad page is selected while k others are there;
+    where they are not, the others are all selected.  Rows of a few, thousands and tens of thousands of tokens."""
+    pg = Paged([n, n - 3, n], 16, di=di, dtype=dtype, seed=n + k + di).fill()
+    dims = dsa.make_dims(pg.cap, 16, 128, Hi, di, k, dtype=dtype)
+    lens, table = pg.args()
+    cols = table.shape[1]
+    gone = [torch.arange(cols) % 3 == 1, torch.zeros(cols, dtype=torch.bool), torch.arange(cols) >= 2]
+    for b, m in enumerate(gone):
+        table[b, m.to(DEV)] = pg.pages if b else -1
+    q = torch.randint(-3, 4, (3, Hi, di), generator=pg.g).to(pg.dt)
+    w = -torch.randint(1, 5, (3, Hi), generator=pg.g).float()
+    w[:, 0] = 1.0
+    idx = torch.full((3, k), -9, dtype=torch.int32, device=DEV)
+    dsa.decode_indexer_topk(dims, pg.cache(), lens, table, q.to(DEV), w.to(DEV), idx, _junk_ws(dims, 3))
+    _reports(dsa.DSA_ERR_BAD_PAGE)
+    for b in range(3):
+        P = pg.lens_list[b] // 4
+        ok = ~gone[b][torch.arange(P) * 4 // 16]
+        s = ((q[b].double() @ pg.pool_keys(b)[:P].double().T).clamp(min=0) * w[b].double()[:, None]).sum(0)
+        s[~ok] = -math.inf
+        best = torch.sort(s, descending=True, stable=True).indices[:k].sort().values
+        assert torch.equal(idx[b].cpu().long(), best), b
