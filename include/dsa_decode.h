@@ -22,7 +22,7 @@
  *   - lens [batch] int32: tokens of each row, the current one included, 0 ..
  *     L.  A row of length 0 is idle: its idx row is -1, its o row 0 and its
  *     lse row -infinity.  The append, the indexer and the attention of one
- *     step take the same lens.
+ *     step take the same lens (but for drafts, below).
  *   - block_table [batch, ceil(L/page_size)] int32: page of the row's tokens
  *     c*page_size .. ; entries behind a row's last page are not read.  Rows
  *     may share pages they only read.
@@ -37,8 +37,14 @@
  *   - Outputs must not overlap inputs or each other, except where said.
  *   - The results of every call are bitwise reproducible run to run on one GPU
  *     for the same dims and batch.
- *   - Rows are independent: several new tokens of one sequence (a draft to be
- *     verified, say) are rows with the same block-table row and growing lens.
+ *   - Rows are independent in the calls that only read the cache
+ *     (dsa_decode_indexer_topk, dsa_decode_attn): they may share pages, and
+ *     several tokens of one sequence are rows with the same block-table row
+ *     and growing lens.  The calls that append (dsa_cache_append,
+ *     dsa_decode_step) take a sequence once: two of their rows must not append
+ *     to the same page, which is not checked.  So tokens of a draft to be
+ *     verified are appended by one dsa_cache_append, a row per sequence with
+ *     its tokens by offsets, and then scored and attended to as a row each.
  */
 #ifndef DSA_GB300_DECODE_H
 #define DSA_GB300_DECODE_H
@@ -151,7 +157,8 @@ dsa_status dsa_decode_attn(const dsa_dims *dims, const dsa_paged_cache *cache, i
                            void *ws, size_t ws_bytes, dsa_stream_t stream);
 
 /* One decode step of the layer: dsa_cache_append of one token per row, then
- * dsa_decode_indexer_topk, then dsa_decode_attn over the selection.
+ * dsa_decode_indexer_topk, then dsa_decode_attn over the selection.  Every
+ * row is a sequence of its own (two rows must not append to the same page).
  *   q, k, v, q_idx, k_idx, w, lens: row b's new token (lens count it)
  *   rotation  NULL, or applied to k and q (q itself is not changed)
  *   outputs   o [batch,Hq,d], lse [batch,Hq], idx [batch,k] */

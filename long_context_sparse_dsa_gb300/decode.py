@@ -7,6 +7,8 @@ block tables) are easily of another type.
 A decoder keeps a ``PagedCache``, a workspace (``alloc_decode_workspace``) and, if its model rotates keys and
 queries, a ``Rotation``; per step it advances ``lens`` and calls ``decode_step``, or the three calls it is made
 of: ``cache_append``, ``decode_indexer_topk``, ``decode_attn``.  All of them can be captured into a CUDA graph.
+``cache_append`` and ``decode_step`` take a sequence once per call; the draft tokens of a sequence are appended together
+(offsets) and then are a row each, with the same block-table row and growing lens, for the other two.
 """
 from __future__ import annotations
 
@@ -172,7 +174,7 @@ def cache_append(dims, cache, lens, block_table, k, v, k_idx, offsets=None, rota
                  k_out=None, stream=None):
     """New tokens into the cache; lens [batch] int32 count them.  Without offsets one token per row, with offsets
     [batch + 1] int32 rows offsets[b] .. offsets[b+1]-1 of k, v, k_idx (q) are row b's.  With a rotation, k enters the
-    cache rotated to its position (and goes to k_out), and q goes to q_out rotated."""
+    cache rotated to its position (and goes to k_out), and q goes to q_out rotated.  No two rows append to the same page."""
     dt, i32, dev = _DTYPES[dims.dtype], torch.int32, cache._device
     batch, n, d = lens.numel(), k.shape[0], dims.d
     cols = -(-dims.L // cache.page_size)
@@ -268,7 +270,8 @@ def decode_attn(dims, cache, lens, block_table, q, o, lse, ws, idx=None, stream=
 
 
 def decode_step(dims, cache, lens, block_table, q, k, v, q_idx, k_idx, w, o, lse, idx, ws, rotation=None, stream=None):
-    """One decode step: append one token per row, select its pools (idx), attend to them (o, lse)."""
+    """One decode step: append one token per row, select its pools (idx), attend to them (o, lse).  No two rows append to
+    the same page."""
     dt, i32, f32, dev, batch = _DTYPES[dims.dtype], torch.int32, torch.float32, cache._device, lens.numel()
     specs = (("lens", lens, i32, (batch,)), ("block_table", block_table, i32, (batch, -(-dims.L // cache.page_size))),
              ("q", q, dt, (batch, dims.Hq, dims.d)), ("k", k, dt, (batch, dims.d)), ("v", v, dt, (batch, dims.d)),

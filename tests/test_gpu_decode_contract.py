@@ -184,3 +184,48 @@ def test_pools_on_bad_pages_rank_last(dtype, Hi, di, n, k):
         s[~ok] = -math.inf
         best = torch.sort(s, descending=True, stable=True).indices[:k].sort().values
         assert torch.equal(idx[b].cpu().long(), best), b
+
+
+# ---------------------------------------------------------------- drafts
+@pytest.mark.parametrize("dtype,rot", [("bf16", 0), ("bf16", 64), ("fp32", 64)])
+def test_draft_tokens_are_appended_together_and_verified_as_rows(dtype, rot):
+    """Three sequences, drafts of 6, 1 and 5 tokens across pools and pages: one append with a row per sequence, then a row
+    per draft token for the indexer and the attention, each of which sees its sequence up to itself.  Then a draft is cut
+    back to a multiple of 4 and other tokens follow: the pool keys are those of the sequence as it went on."""
+    Hq, k, page = 8, 9, 16
+    base, draft = [61, 40, 127], [6, 1, 5]
+    n = [a + m for a, m in zip(base, draft)]
+    pg = Paged(n, page, dtype=dtype, seed=140 + rot, cap=144).fill(base)
+    dims = dsa.make_dims(pg.cap, Hq, 128, 8, 64, k, dtype=dtype)
+    table = pg.table.to(DEV)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=DEV)
+    T = sum(draft)
+    q = torch.randn(T, Hq, 128, generator=pg.g).to(pg.dt)
+    qi = torch.randint(-3, 4, (T, 8, 64), generator=pg.g).to(pg.dt)
+    w = torch.randint(1, 5, (T, 8), generator=pg.g).float()
+    cat = lambda xs, a=base, z=n: torch.cat([x[i:j] for x, i, j in zip(xs, a, z)]).to(DEV)
+    qd, cache = q.to(DEV), pg.cache()
+    kw = dict(rotation=dsa.make_rotation(_freq(rot)), q=qd, q_out=qd) if rot else {}
+    dsa.cache_append(dims, cache, i32(n), table, cat(pg.K), cat(pg.V), cat(pg.KI), offsets=i32([0, 6, 7, 12]), **kw)
+    seq = [b for b, m in enumerate(draft) for _ in range(m)]
+    rows = i32([base[b] + j + 1 for b, m in enumerate(draft) for j in range(m)])
+    each = table[torch.tensor(seq, device=DEV)].contiguous()
+    ws, idx = _junk_ws(dims, T), torch.full((T, k), -9, dtype=torch.int32, device=DEV)
+    o, lse = torch.empty_like(qd), torch.empty(T, Hq, device=DEV)
+    dsa.decode_indexer_topk(dims, cache, rows, each, qi.to(DEV), w.to(DEV), idx, ws)
+    dsa.decode_attn(dims, cache, rows, each, qd, o, lse, ws, idx=idx)
+    dsa.check_device_error()
+    if rot:     # the keys as they went into the cache
+        for b in range(3):
+            at, r = pg.where(b, torch.arange(n[b]))
+            pg.K[b] = cache.k.cpu()[at, r]
+    pg.lens_list, pg.K, pg.V, pg.KI = rows.tolist(), *([x[b] for b in seq] for x in (pg.K, pg.V, pg.KI))
+    assert torch.equal(idx.cpu(), _ref_topk(pg, qi, w, k))
+    _check_attn(pg, qd.cpu(), o, lse, 128 ** -0.5, idx.cpu())
+    # sequence 0 keeps 64 of its tokens and goes on otherwise
+    more = torch.randint(-3, 4, (5, 64), generator=pg.g).to(pg.dt)
+    kv = torch.zeros(5, 128, dtype=pg.dt, device=DEV)
+    dsa.cache_append(dims, cache, i32([69]), table[:1], kv, kv, more.to(DEV), offsets=i32([0, 5]))
+    dsa.check_device_error()
+    got = cache.kpool.cpu()[pg.table[0, 64 // page].long(), 0]
+    assert torch.equal(got, more[:4].double().sum(0).to(pg.dt))
