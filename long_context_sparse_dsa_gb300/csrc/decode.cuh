@@ -15,13 +15,22 @@
 
 namespace dsa {
 
+// Load of what the kernel before this one on the stream may have written while
+// this one was resident (chain_wait below): a plain one.  The non-coherent path
+// (__ldg, or a const __restrict__ pointer) is for data that nobody writes in a
+// kernel's life.
+template <typename T>
+__device__ __forceinline__ T ld_live(const T* p) {
+  return *p;
+}
+
 __device__ __forceinline__ int page_of_pool(const PagedView& pv, int p) {
   return (int)(((uint64_t)(uint32_t)p * pv.div_mul) >> pv.div_shift);
 }
 
 // Length of row b, 0 (idle) when it lies outside 0..capacity.
 __device__ __forceinline__ int row_length(const PagedView& pv, int64_t b, bool& bad) {
-  const int n = __ldg(pv.lens + b);
+  const int n = ld_live(pv.lens + b);
   if (n < 0 || n > pv.capacity) {
     bad = true;
     return 0;

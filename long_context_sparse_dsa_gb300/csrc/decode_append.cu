@@ -71,21 +71,21 @@ __device__ __forceinline__ Place place_of(const AppendArgs& a, int64_t t, bool& 
   if (t >= a.n_tokens) return p;
   int64_t b = t, begin = t, n_new = 1;
   if (a.offsets) {
-    const int64_t from = __ldg(a.offsets), to = __ldg(a.offsets + a.batch);
+    const int64_t from = ld_live(a.offsets), to = ld_live(a.offsets + a.batch);
     // rows that have no token at all among the call's would not show below
     if (t == 0 && (from < 0 || from > to || to > a.n_tokens)) record_error(DSA_DEV_ERR_BAD_PAGE);
     if (t < from || t >= to) return p;   // before the first row, or behind the last
     int64_t lo = 0, hi = a.batch;   // offsets[lo] <= t < offsets[hi]
     while (hi - lo > 1) {
       const int64_t mid = (lo + hi) >> 1;
-      if ((int64_t)__ldg(a.offsets + mid) <= t)
+      if ((int64_t)ld_live(a.offsets + mid) <= t)
         lo = mid;
       else
         hi = mid;
     }
     b = lo;
-    begin = __ldg(a.offsets + lo);
-    n_new = (int64_t)__ldg(a.offsets + lo + 1) - begin;
+    begin = ld_live(a.offsets + lo);
+    n_new = (int64_t)ld_live(a.offsets + lo + 1) - begin;
   }
   p.len = row_length(a.pv, b, bad);
   if (!a.offsets && p.len == 0) return p;   // an idle row of a decode step
@@ -99,7 +99,7 @@ __device__ __forceinline__ Place place_of(const AppendArgs& a, int64_t t, bool& 
   p.b = b;
   const int pool = (int)(p.pos >> 2);
   const int col = page_of_pool(a.pv, pool);
-  p.page = __ldg(a.pv.table + b * a.pv.cols + col);
+  p.page = ld_live(a.pv.table + b * a.pv.cols + col);
   const int pp = phys_pool(a.pv, pool, col, p.page, bad);
   if (pp >= 0) p.row = (int64_t)pp * 4 + (p.pos & 3);
   return p;
@@ -127,7 +127,7 @@ __device__ __forceinline__ void put_index_key(const AppendArgs& a, int64_t t, co
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const bool old = first && p.pos - (3 - i) < p.start;   // kept by an earlier append (i < 3)
-        raw[i] = old ? kept[i * CI + c] : __ldg(ki - (int64_t)(3 - i) * CI + c);
+        raw[i] = old ? kept[i * CI + c] : ld_live(ki - (int64_t)(3 - i) * CI + c);
       }
       float acc[N], x[N];
       unpack16<T>(raw[0], acc);
@@ -141,18 +141,18 @@ __device__ __forceinline__ void put_index_key(const AppendArgs& a, int64_t t, co
     }
     if (first && open < p.len) {
       const int ocol = page_of_pool(a.pv, (int)(open >> 2));
-      const int opage = __ldg(a.pv.table + p.b * a.pv.cols + ocol);
+      const int opage = ld_live(a.pv.table + p.b * a.pv.cols + ocol);
       if ((uint32_t)opage >= (uint32_t)a.pv.num_pages) {
         record_error(DSA_DEV_ERR_BAD_PAGE);
         return;
       }
       uint4* tail = static_cast<uint4*>(a.cktail) + (int64_t)opage * 3 * CI;
       for (int i = 0; i < (int)(p.len - open); ++i)
-        for (int c = c0; c < CI; c += step) tail[i * CI + c] = __ldg(ki + (open + i - p.pos) * CI + c);
+        for (int c = c0; c < CI; c += step) tail[i * CI + c] = ld_live(ki + (open + i - p.pos) * CI + c);
     }
   } else if (p.pos >= open && !mixed && p.row >= 0) {
     uint4* tail = static_cast<uint4*>(a.cktail) + ((int64_t)p.page * 3 + r) * CI;
-    for (int c = c0; c < CI; c += step) tail[c] = __ldg(ki + c);
+    for (int c = c0; c < CI; c += step) tail[c] = ld_live(ki + c);
   }
 }
 
@@ -175,8 +175,8 @@ __global__ void __launch_bounds__(kAppendWarps * 32) cache_append_kernel(const _
   for (int i = 0; i < PER; ++i) {
     const int c = i * 32 + lane;
     if (c < TPW * CH && c < most) {
-      kx[i] = __ldg(k + c);
-      vx[i] = __ldg(v + c);
+      kx[i] = ld_live(k + c);
+      vx[i] = ld_live(v + c);
     }
   }
   bool bad = false;
@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32) cache_append_rotated_kernel
     kx = (static_cast<const uint4*>(a.k) + t * CH)[c0];
     ky = (static_cast<const uint4*>(a.k) + t * CH)[c1];
   }
-  if (lane < CH) vx = __ldg(static_cast<const uint4*>(a.v) + t * CH + lane);
+  if (lane < CH) vx = ld_live(static_cast<const uint4*>(a.v) + t * CH + lane);
   if (a.q) load_q(0);
   bool bad = false;
   const Place p = place_of(a, t, bad);
@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32) cache_append_rotated_kernel
     for (int i = 0; i < 2; ++i) {
       const int f = 2 * lane + i;
       if (f < a.rot.dim / 2) {
-        const uint64_t w = (uint64_t)p.pos * __ldg(a.rot.turns + f);
+        const uint64_t w = (uint64_t)p.pos * ld_live(a.rot.turns + f);
         sincospif((float)(int32_t)(w >> 32) * 4.656612873077393e-10f, &s2[i], &c2[i]);   // 2^-31 half turns
       }
     }

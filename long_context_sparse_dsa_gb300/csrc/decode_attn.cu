@@ -90,7 +90,7 @@ __device__ __forceinline__ int row_steps(int len) { return len == 0 ? 1 : (int)(
 // ahead: the idx entry, the pool and its visible rows, the physical pool.
 template <bool SEL>
 __device__ __forceinline__ int slot_idx(const SlotRow& r, int i) {
-  return (SEL && i < r.k) ? __ldg(r.idx + i) : -1;
+  return (SEL && i < r.k) ? ld_live(r.idx + i) : -1;
 }
 template <bool SEL>
 __device__ __forceinline__ void slot_pool_rows(const SlotRow& r, int i, int raw, int& pool, int& rows, bool& bad) {
@@ -261,8 +261,8 @@ __device__ __forceinline__ void join_warps(unsigned char* tiles, AttnScratch& sc
 // ------------------------------------------------------------------- bf16
 // gather_step16 (gather.cuh) for a step whose 16 keys are all visible.
 template <int D>
-__device__ __forceinline__ void gather_full16(uint32_t stage, const __nv_bfloat16* __restrict__ K,
-                                              const __nv_bfloat16* __restrict__ V, const uint32_t (&slots)[4],
+__device__ __forceinline__ void gather_full16(uint32_t stage, const __nv_bfloat16* K,
+                                              const __nv_bfloat16* V, const uint32_t (&slots)[4],
                                               const GatherLane<D>& gl) {
   using C = GatherCfg<D>;
   constexpr int NRB = GatherLane<D>::NRB;
@@ -308,9 +308,9 @@ struct DecCfg {
 // join buffer are no longer used.
 // SEL: the slots are selected pools; else all pools.
 template <int D, int NG, bool SEL, typename Put>
-__device__ __forceinline__ void attn_piece_bf16(const PagedView& pv, const __nv_bfloat16* __restrict__ Q,
-                                                const __nv_bfloat16* __restrict__ K,
-                                                const __nv_bfloat16* __restrict__ V, const SlotRow& sr, int64_t b,
+__device__ __forceinline__ void attn_piece_bf16(const PagedView& pv, const __nv_bfloat16* Q,
+                                                const __nv_bfloat16* K,
+                                                const __nv_bfloat16* V, const SlotRow& sr, int64_t b,
                                                 int w0, int steps, int stride, int Hq, float scale_log2,
                                                 unsigned char* tiles, AttnScratch& sc, bool arrive, const Put& put, bool& bad_page,
                                                 bool& bad_idx) {
@@ -329,7 +329,7 @@ __device__ __forceinline__ void attn_piece_bf16(const PagedView& pv, const __nv_
     slot_pool_rows<SEL>(sr, st * 4 + (lane & 3), raw, pool, rows, bad_idx);
     if (st >= steps) rows = 0;
     col = page_of_pool(pv, pool);
-    page = rows ? __ldg(sr.trow + col) : 0;
+    page = rows ? ld_live(sr.trow + col) : 0;
   };
   uint32_t vis[NST];   // visible rows of the ring's steps: 4 bits per slot
   auto fetch = [&](int st, int stage, uint32_t& v) {
@@ -624,8 +624,8 @@ struct F32Cfg {
 
 // As attn_piece_bf16; heads from Hq to MAXH are computed as zeros.
 template <int D, int MAXH, bool SEL, typename Put>
-__device__ __forceinline__ void attn_piece_f32(const PagedView& pv, const float* __restrict__ Q,
-                                               const float* __restrict__ K, const float* __restrict__ V,
+__device__ __forceinline__ void attn_piece_f32(const PagedView& pv, const float* Q,
+                                               const float* K, const float* V,
                                                const SlotRow& sr, int64_t b, int w0, int steps, int stride,
                                                int Hq, float scale_log2, unsigned char* tiles, AttnScratch& sc, bool arrive,
                                                const Put& put, bool& bad_page, bool& bad_idx) {
@@ -654,7 +654,7 @@ __device__ __forceinline__ void attn_piece_f32(const PagedView& pv, const float*
     slot_pool_rows<SEL>(sr, slot_of(i), raw, pool, rows, bad_idx);
     if (step_of(i) >= steps) rows = 0;
     col = page_of_pool(pv, pool);
-    page = rows ? __ldg(sr.trow + col) : 0;
+    page = rows ? ld_live(sr.trow + col) : 0;
   };
   uint32_t vis[NST];   // visible rows of the ring's half steps: 4 bits per slot
   auto fetch = [&](int i, int stage, uint32_t& v) {
@@ -1098,8 +1098,8 @@ __global__ void __launch_bounds__(kAttnThreads, (Piece<T, D, MAXH, false>::CTAS)
 // lane reads 16 bytes of a piece, CW/4 lanes a piece; the first pieces' loads
 // are issued before their weights are known.  Sums are added in a fixed order.
 template <typename T, int D, int CW>
-__global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(Pieces ps, T* __restrict__ O,
-                                                                   float* __restrict__ LSE, int Hq) {
+__global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(Pieces ps, T* O,
+                                                                   float* LSE, int Hq) {
   constexpr int LPP = CW / 4;                    // lanes per piece
   constexpr int PAR = kJoinThreads / LPP;        // pieces read at once
   constexpr int AHEAD = 4;                       // loads a thread has in flight

@@ -34,7 +34,7 @@ struct PoolBlock {
       pp[i] = -1;
       if (p < n && 32 * i + lane < PPW) {
         const int col = page_of_pool(pv, p);
-        pp[i] = phys_pool(pv, p, col, __ldg(trow + col), bad);
+        pp[i] = phys_pool(pv, p, col, ld_live(trow + col), bad);
       }
     }
   }
@@ -57,8 +57,8 @@ struct PoolBlock {
 
 template <int DI, int PPW>
 __global__ void __launch_bounds__(kScoreWarps * 32)
-    decode_scores_bf16_kernel(PagedView pv, int Hi, int k, const uint4* __restrict__ q_idx, const float* __restrict__ w,
-                              const uint4* __restrict__ kpool, float* __restrict__ scores, int64_t pitch) {
+    decode_scores_bf16_kernel(PagedView pv, int Hi, int k, const uint4* q_idx, const float* w,
+                              const uint4* kpool, float* scores, int64_t pitch) {
   constexpr int CH = DI / 8;     // 16-byte chunks per row
   constexpr int CL = CH / 4;     // chunks per lane and row
   chain_wait();
@@ -80,10 +80,10 @@ __global__ void __launch_bounds__(kScoreWarps * 32)
   if (g < Hi) {
     const uint4* q = q_idx + (b * Hi + g) * CH;
 #pragma unroll
-    for (int c = 0; c < CL; ++c) qf[c] = __ldg(q + qi + 4 * c);
+    for (int c = 0; c < CL; ++c) qf[c] = ld_live(q + qi + 4 * c);
   }
-  if (2 * qi < Hi) w0 = __ldg(w + b * Hi + 2 * qi);
-  if (2 * qi + 1 < Hi) w1 = __ldg(w + b * Hi + 2 * qi + 1);
+  if (2 * qi < Hi) w0 = ld_live(w + b * Hi + 2 * qi);
+  if (2 * qi + 1 < Hi) w1 = ld_live(w + b * Hi + 2 * qi + 1);
   float* srow = scores + b * pitch;
 #pragma unroll
   for (int i = 0; i < PPW / 16; ++i) {
@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32)
       const int pp = pools.get(i / 2, (i & 1) * 16 + r * 8 + g);
 #pragma unroll
       for (int c = 0; c < CL; ++c)
-        kf[r][c] = pp >= 0 ? __ldg(kpool + (int64_t)pp * CH + qi + 4 * c) : make_uint4(0u, 0u, 0u, 0u);
+        kf[r][c] = pp >= 0 ? ld_live(kpool + (int64_t)pp * CH + qi + 4 * c) : make_uint4(0u, 0u, 0u, 0u);
     }
     float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -118,8 +118,8 @@ __global__ void __launch_bounds__(kScoreWarps * 32)
 
 template <int DI, int PPW, int NH>
 __global__ void __launch_bounds__(kScoreWarps * 32)
-    decode_scores_f32_kernel(PagedView pv, int Hi, int k, const float4* __restrict__ q_idx, const float* __restrict__ w,
-                             const float4* __restrict__ kpool, float* __restrict__ scores, int64_t pitch) {
+    decode_scores_f32_kernel(PagedView pv, int Hi, int k, const float4* q_idx, const float* w,
+                             const float4* kpool, float* scores, int64_t pitch) {
   constexpr int LPR = DI / 8;          // lanes per pool row, 8 channels each
   constexpr int RPW = 32 / LPR;        // pool rows per warp and pass
   chain_wait();
@@ -139,18 +139,18 @@ __global__ void __launch_bounds__(kScoreWarps * 32)
   for (int h = 0; h < NH; ++h) {
     qf[h][0] = qf[h][1] = make_float4(0.f, 0.f, 0.f, 0.f);
     if (h < Hi) {
-      qf[h][0] = __ldg(q_idx + (b * Hi + h) * (DI / 4) + li);
-      qf[h][1] = __ldg(q_idx + (b * Hi + h) * (DI / 4) + LPR + li);
+      qf[h][0] = ld_live(q_idx + (b * Hi + h) * (DI / 4) + li);
+      qf[h][1] = ld_live(q_idx + (b * Hi + h) * (DI / 4) + LPR + li);
     }
   }
   // after the reduction below lane li holds head li & (NH - 1)
-  const float wh = (li & (NH - 1)) < Hi ? __ldg(w + b * Hi + (li & (NH - 1))) : 0.f;
+  const float wh = (li & (NH - 1)) < Hi ? ld_live(w + b * Hi + (li & (NH - 1))) : 0.f;
   auto load = [&](int i, float4(&x)[2]) {   // this lane's part of pool p0 + i + sub
     const int pp = pools.get(PPW > 32 && i >= 32 ? 1 : 0, (i & 31) + sub);
     x[0] = x[1] = make_float4(0.f, 0.f, 0.f, 0.f);
     if (pp >= 0) {
-      x[0] = __ldg(kpool + (int64_t)pp * (DI / 4) + li);
-      x[1] = __ldg(kpool + (int64_t)pp * (DI / 4) + LPR + li);
+      x[0] = ld_live(kpool + (int64_t)pp * (DI / 4) + li);
+      x[1] = ld_live(kpool + (int64_t)pp * (DI / 4) + LPR + li);
     }
   };
   auto score = [&](int i, float4 k0, float4 k1) {
@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32)
   };
   if (NH == 4) {
     // the loads of 4 passes run ahead; where the heads' channels take 64 registers
-    // requesting 4 passes together is faster (1M tokens, di 64: 27.0 us against 34.3)
+    // requesting whole batches is faster (1M tokens, di 64: 27.0 us against 34.3)
     constexpr int AHEAD = 4;
     static_assert(PPW / RPW % AHEAD == 0, "whole rounds");
     float4 kf[AHEAD][2];
@@ -205,7 +205,9 @@ __global__ void __launch_bounds__(kScoreWarps * 32)
       }
     }
   } else {
-    constexpr int BATCH = 4;   // passes requested together
+    // 16 pools requested together (half of that: 31.9 us for 1M tokens, di 64; and 32
+    // rows of 16383 pools, di 128, take 79.6 us against 68.9)
+    constexpr int BATCH = 16 / RPW;
 #pragma unroll 1
     for (int i0 = 0; i0 < PPW; i0 += BATCH * RPW) {
       float4 kf[BATCH][2];

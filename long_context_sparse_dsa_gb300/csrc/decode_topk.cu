@@ -242,7 +242,7 @@ __device__ __forceinline__ uint32_t kth_largest_own(const uint32_t (&x)[J], int 
 // The k largest of m <= J * kSelThreads keys (own_key's, key(i) by index, m >=
 // k), in order: pool(i) of each goes to `out`.  A thread holds consecutive keys.
 template <int J, typename F, typename G>
-__device__ __forceinline__ void finish_row_of(F key, G pool, int m, int k, SelShared& sh, int32_t* __restrict__ out) {
+__device__ __forceinline__ void finish_row_of(F key, G pool, int m, int k, SelShared& sh, int32_t* out) {
   const int per = (m + kSelThreads - 1) / kSelThreads, i0 = threadIdx.x * per;
   uint32_t own[J];
 #pragma unroll
@@ -270,7 +270,7 @@ __device__ __forceinline__ void finish_row_of(F key, G pool, int m, int k, SelSh
 // 1000 pools, scores included, took 8.4 us against 7.1, 16 rows of 8191 pools
 // 13.2 against 12.3).
 template <typename F, typename G>
-__device__ __forceinline__ void finish_row(F key, G pool, int m, int k, SelShared& sh, int32_t* __restrict__ out) {
+__device__ __forceinline__ void finish_row(F key, G pool, int m, int k, SelShared& sh, int32_t* out) {
   static_assert(kCap == 8 * kSelThreads, "8 keys a thread at most");
   if (m <= 2 * kSelThreads)
     finish_row_of<2>(key, pool, m, k, sh, out);
@@ -284,7 +284,7 @@ __device__ __forceinline__ void finish_row(F key, G pool, int m, int k, SelShare
 // thread takes up to 8 consecutive keys at a time.
 template <typename F, typename G>
 __device__ __forceinline__ void write_selected(F key, G pool, int n, uint32_t T, int ties, SelShared& sh,
-                                               int32_t* __restrict__ out) {
+                                               int32_t* out) {
   constexpr int J = 8;
   int gt_base = 0, eq_base = 0;
   const int per = n < J * kSelThreads ? (n + kSelThreads - 1) / kSelThreads : J;
@@ -317,7 +317,7 @@ __device__ __forceinline__ void write_selected(F key, G pool, int n, uint32_t T,
 
 // This thread's kPerLane consecutive scores of the chunk of [c0, end) at c0, a
 // multiple of 4.
-__device__ __forceinline__ void load_chunk(const float* __restrict__ row, int64_t c0, int64_t end,
+__device__ __forceinline__ void load_chunk(const float* row, int64_t c0, int64_t end,
                                            float (&x)[kPerLane]) {
   const int64_t e0 = c0 + (int64_t)threadIdx.x * kPerLane;
 #pragma unroll
@@ -341,7 +341,7 @@ __device__ __forceinline__ void load_chunk(const float* __restrict__ row, int64_
 // first chunk in x: put(pool, score, gt, gt_before, eq_before) for every score
 // > tau or == tau, with the numbers of both before it in the slice.
 template <typename F>
-__device__ __forceinline__ void scan_slice(const float* __restrict__ row, int64_t begin, int64_t end, float tau,
+__device__ __forceinline__ void scan_slice(const float* row, int64_t begin, int64_t end, float tau,
                                            float (&x)[kPerLane], SelShared& sh, int& n_gt, int& n_eq, F put) {
   n_gt = n_eq = 0;
   for (int64_t c0 = begin; c0 < end; c0 += kChunk) {
@@ -380,8 +380,8 @@ __device__ __forceinline__ void scan_slice(const float* __restrict__ row, int64_
 }
 
 __global__ void __launch_bounds__(kSelThreads, 2)
-    decode_topk_kernel(PagedView pv, const float* __restrict__ scores, int64_t pitch, int k,
-                       int32_t* __restrict__ idx) {
+    decode_topk_kernel(PagedView pv, const float* scores, int64_t pitch, int k,
+                       int32_t* idx) {
   extern __shared__ __align__(16) unsigned char sel_smem[];
   SelShared& sh = *reinterpret_cast<SelShared*>(sel_smem);
   chain_wait();
