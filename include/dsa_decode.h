@@ -109,8 +109,8 @@ size_t dsa_decode_workspace_bytes(const dsa_dims *dims, int64_t batch);
  *              offsets[b+1]-1, the last one at position lens[b]-1.  offsets
  *              ascend within 0 .. n_tokens; rows before offsets[0] and behind
  *              offsets[batch] are left alone (part of a batch: lens,
- *              block_table and offsets from that row on, the tokens as they
- *              are).  NULL: one token per row (n_tokens == batch); idle rows
+ *              block_table and offsets from that row on, a multiple of 4 for
+ *              their alignment, the tokens as they are).  NULL: one token per row (n_tokens == batch); idle rows
  *              append nothing
  *   k, v       [n_tokens, d] layer dtype; k_idx [n_tokens, di] layer dtype
  *   rotation   NULL (no rotation), or applied to k, and to q if given

@@ -98,9 +98,14 @@ def alloc_paged_cache(dims, pages: int, page_size: int = 64, device="cuda") -> P
 
 
 class Rotation:
-    """Position rotation of the first 2 * len(freq) channels: see ``make_rotation``."""
+    """Position rotation of the first 2 * len(freq) channels: see ``make_rotation``.  turns: the frequencies as turns per
+    position in units of 2^-64, an int64 tensor."""
 
     def __init__(self, turns, interleaved: bool):
+        _need_torch()
+        if not (isinstance(turns, torch.Tensor) and turns.dtype is torch.int64 and turns.dim() == 1 and
+                turns.is_contiguous() and turns.numel() and turns.numel() % 8 == 0):
+            raise ValueError("a rotation's turns are a contiguous int64 tensor of a multiple of 8 frequencies")
         self.turns = turns
         self.dim = 2 * turns.numel()
         self._c = _CRotation(turns.data_ptr(), self.dim, int(bool(interleaved)))
