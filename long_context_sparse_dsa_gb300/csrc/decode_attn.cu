@@ -590,9 +590,12 @@ __device__ __forceinline__ void attn_piece_bf16(const PagedView& pv, const __nv_
 
 // ------------------------------------------------------------------- fp32 (FFMA)
 // As in bf16, a warp takes every 4th step with a ring of its own, here in halves
-// of 8 keys (2 slots).  Bound by FFMAs where there are more than about 20 heads
-// (4*Hq*d flops for 8*d bytes a key), so the tiles are chosen to keep the loads
-// from shared memory below them:
+// of 8 keys (2 slots).  FFMAs outweigh the bytes where there are more than about
+// 20 heads (4*Hq*d flops for 8*d bytes a key), so the tiles are chosen to keep
+// the loads from shared memory below them.  Neither pipe is full, though: with 32
+// heads of 128 a thread holds 255 registers, an SM 8 warps, and these issue on 63%
+// of the cycles (FMA pipe 52%, shared-memory wavefronts 53%, most stalls on loads
+// from shared memory): latency that too few warps cover.
 //   S: a quarter of the lanes takes every 4th 16-byte chunk of d, a lane of it
 //      4 keys and MAXH/4 heads; the quarters' sums are then scattered, one key
 //      to a lane.  (With 2 keys and MAXH/8 heads over all of d, twice the
@@ -1188,9 +1191,17 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(Pieces ps, T*
 // us), but takes as long as the longest row, on no more than 16 CTAs a row; the
 // list shares the lengths out evenly, 0.6 of it for ragged rows, and begins
 // every row for the price of kRowPad steps.  Compared are the rounds a warp
-// makes; one is dearer in fp32.  Measured, list and clusters, bf16, 16 heads of
-// 128: 150 rows of up to 1000 tokens 17.1 and 11.7 us, 40 of 500 8.2 and 6.3, 40
-// of up to 4000 11.5 and 12.7, one of 4000 6.2 and 7.1.
+// makes; one is dearer in fp32.  Measured, list and clusters, us, with the one that
+// the rule takes marked (~: ragged rows of up to so many tokens):
+//                 bf16 16x128   bf16 32x128   bf16 32x64    fp32 8x128    fp32 32x128
+//   1 of 4000      6.2*  6.9     8.3*  9.0     6.3*  6.9     7.3* 12.7    15.4* 25.4
+//   40 of 500      9.0   6.6*   12.5   9.3*   11.1   6.9*   12.9   9.8*   26.6  22.9*
+//   40 of ~4000   14.5* 14.4    19.3* 19.3    13.3* 12.2    23.9* 34.3    50.7* 80.2
+//   150 of ~1000  19.8  13.2*   29.0  17.9*   22.4* 12.9    31.0* 34.4    73.0* 66.7
+//   150 of 1000   26.0  17.3*   36.5  20.4*   29.3* 15.9    43.2* 39.6   105.4* 70.2
+//   150 of ~2000  25.3* 20.1    35.2* 27.1    28.3* 20.5
+// It errs towards the list, for batches of some hundred rows of thousands of
+// tokens, and most for even ones, whose list costs all of its steps and not 0.6.
 static bool by_rows(int64_t batch, int64_t steps, unsigned splits, int resident, int warps, bool bf16) {
   const double list = (double)batch * (double)(steps + kRowPad) / ((double)resident * warps);
   const double waves = (double)batch * splits / resident;
@@ -1255,14 +1266,10 @@ static cudaError_t launch_typed(const DecodeAttnArgs& g, cudaStream_t s) {
   a.Hq = g.Hq;
   a.k = g.k;
   a.scale_log2 = g.scale * 1.4426950408889634f;
-  if (g.d == 128) {
-    if (g.Hq > 16) return launch_shape<T, 128, 32>(a, s);
-    if (sizeof(T) == 2 || g.Hq > 8) return launch_shape<T, 128, 16>(a, s);
-    return launch_shape<T, 128, sizeof(T) == 2 ? 16 : 8>(a, s);
-  }
-  if (g.Hq > 16) return launch_shape<T, 64, 32>(a, s);
-  if (sizeof(T) == 2 || g.Hq > 8) return launch_shape<T, 64, 16>(a, s);
-  return launch_shape<T, 64, sizeof(T) == 2 ? 16 : 8>(a, s);
+  if constexpr (sizeof(T) == 4)   // bf16 heads come in groups of 16
+    if (g.Hq <= 8) return g.d == 128 ? launch_shape<T, 128, 8>(a, s) : launch_shape<T, 64, 8>(a, s);
+  if (g.Hq <= 16) return g.d == 128 ? launch_shape<T, 128, 16>(a, s) : launch_shape<T, 64, 16>(a, s);
+  return g.d == 128 ? launch_shape<T, 128, 32>(a, s) : launch_shape<T, 64, 32>(a, s);
 }
 
 cudaError_t launch_decode_attn(bool bf16, const DecodeAttnArgs& a, cudaStream_t s) {
