@@ -11,7 +11,9 @@
 // The angle of position p and frequency f is p * turns[f] modulo 2^64, in
 // units of 2^-64 turns: an exact reduction in integers, whatever the
 // position, of which the top 32 bits go to sincospi as a signed fraction of
-// half a turn (error 2^-33 turns).  A lane forms the angles of two
+// half a turn.  The fraction is a float: off by at most 2^-26 turns (9.4e-8
+// rad, near half a turn) and the 2^-32 that were cut off, about what fp32
+// leaves of a sine anyway.  A lane forms the angles of two
 // frequencies and the warp shares them by shuffles: a lane handles two 16-byte
 // chunks of a head (the two halves of its pairs, or two neighbouring chunks),
 // the same ones for every head, so each lane needs the same 8 (fp32: 4) pairs
