@@ -14,7 +14,12 @@ validate_dims, layer_fwd_noalloc; the measurement probe probe_traffic
 (``include/dsa_probe.h``); and decoding from a paged cache (``decode.py``,
 ``include/dsa_decode.h``): cache_append, decode_indexer_topk, decode_attn,
 decode_step, with PagedCache, alloc_paged_cache, make_rotation,
-decode_workspace_bytes, alloc_decode_workspace, validate_decode_dims.
+decode_workspace_bytes, alloc_decode_workspace, validate_decode_dims; norm and
+rotation of heads (``heads.py``, ``include/dsa_heads.h``): qk_norm_rotate,
+qk_norm_rotate_bwd; trees of drafted tokens and the cache's pages (``tree.py``,
+``include/dsa_tree.h``, ``include/dsa_pages.h``): decode_tree_attn,
+cache_commit, cache_reserve, cache_fork, cache_release, cache_compact,
+cache_copy_pages.
 """
 from __future__ import annotations
 
@@ -89,6 +94,8 @@ def _load():
             "dsa_selftest_bounded_wait": ([u32, P], ctypes.c_int),
             "dsa_probe_traffic": ([D, P, P, P, P, P, P], ctypes.c_int),
             **_decode_signatures(D),
+            **_heads_signatures(D),
+            **_tree_signatures(D),
         }
         for name, (args, res) in sig.items():
             f = getattr(lib, name)
@@ -316,3 +323,9 @@ from .decode import (PagedCache, Rotation, alloc_decode_workspace, alloc_paged_c
                      cache_append, decode_attn, decode_indexer_topk, decode_step, decode_workspace_bytes,
                      make_rotation, validate_decode_dims)
 from .decode import _signatures as _decode_signatures  # noqa: E402
+from .heads import qk_norm_bwd_workspace_bytes, qk_norm_rotate, qk_norm_rotate_bwd  # noqa: E402
+from .heads import _signatures as _heads_signatures  # noqa: E402
+from .tree import (MAX_TREE_NODES, alloc_page_workspace, alloc_tree_workspace, cache_commit,  # noqa: E402
+                   cache_compact, cache_copy_pages, cache_fork, cache_release, cache_reserve, decode_tree_attn,
+                   page_workspace_bytes, tree_workspace_bytes)
+from .tree import _signatures as _tree_signatures  # noqa: E402

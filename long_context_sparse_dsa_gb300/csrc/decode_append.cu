@@ -22,38 +22,11 @@
 // Bound: HBM (every byte is moved once); a call of a few tokens is bound by
 // the launch and two dependent loads.
 #include "decode.cuh"
-#include "vec16.cuh"
+#include "rotate.cuh"
 
 namespace dsa {
 
 constexpr int kAppendWarps = 4;
-
-template <typename T>
-__device__ __forceinline__ void rotate_unit(uint4& u0, uint4& u1, const float* cs, const float* sn, bool interleaved) {
-  constexpr int N = Vec16<T>::N;
-  float a[N], b[N];
-  unpack16<T>(u0, a);
-  unpack16<T>(u1, b);
-  if (!interleaved) {
-#pragma unroll
-    for (int e = 0; e < N; ++e) {
-      const float x = a[e], y = b[e];
-      a[e] = x * cs[e] - y * sn[e];
-      b[e] = x * sn[e] + y * cs[e];
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < N / 2; ++e) {
-      const float x = a[2 * e], y = a[2 * e + 1], z = b[2 * e], w = b[2 * e + 1];
-      a[2 * e] = x * cs[e] - y * sn[e];
-      a[2 * e + 1] = x * sn[e] + y * cs[e];
-      b[2 * e] = z * cs[N / 2 + e] - w * sn[N / 2 + e];
-      b[2 * e + 1] = z * sn[N / 2 + e] + w * cs[N / 2 + e];
-    }
-  }
-  u0 = pack16<T>(a);
-  u1 = pack16<T>(b);
-}
 
 // Where new token t goes.
 struct Place {
@@ -260,10 +233,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32) cache_append_rotated_kernel
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int f = 2 * lane + i;
-      if (f < a.rot.dim / 2) {
-        const uint64_t w = (uint64_t)p.pos * ld_live(a.rot.turns + f);
-        sincospif((float)(int32_t)(w >> 32) * 4.656612873077393e-10f, &s2[i], &c2[i]);   // 2^-31 half turns
-      }
+      if (f < a.rot.dim / 2) rotation_at(p.pos, ld_live(a.rot.turns + f), c2[i], s2[i]);
     }
 #pragma unroll
     for (int e = 0; e < N; ++e) {

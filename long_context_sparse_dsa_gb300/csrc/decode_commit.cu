@@ -1,0 +1,119 @@
+// decode_commit.cu -- the accepted path of each draft tree into the paged cache.
+//
+// A CTA takes a row.  The row's parents go to shared memory, one thread walks
+// from the accepted node to the root, then all threads copy: k and v of the
+// path's tokens, the keys of the pools that they complete (fp32 sums in token
+// order, rounded once: what dsa_pool_keys gives), the keys of the incomplete
+// pool behind them.
+//
+// Bound: the chain of dependent loads (offsets, parents, the walk, pages, rows),
+// about 4 us; a few KB a row.
+#include "decode.cuh"
+#include "decode_tree.h"
+#include "vec16.cuh"
+
+namespace dsa {
+
+constexpr int kCommitThreads = 256;
+
+template <typename T>
+__global__ void __launch_bounds__(kCommitThreads) cache_commit_kernel(const __grid_constant__ CommitArgs a) {
+  constexpr int N = Vec16<T>::N;
+  __shared__ int up[kMaxTreeNodes], path[kMaxTreeNodes];   // path: from the accepted node to the root
+  __shared__ int s_depth;
+  chain_wait();
+  chain_release();
+  const int64_t b = blockIdx.x;
+  const int CH = a.d / N, CI = a.di / N;
+  const int raw_len = ld_live(a.pv.lens + b);
+  const int64_t from = ld_live(a.tree.offsets + b), to = ld_live(a.tree.offsets + b + 1);
+  int last = ld_live(a.accepted + b);
+  bool bad = false, bad_idx = false;
+  const int len = row_length(a.pv, b, bad);
+  if (from < 0 || to < from || to > a.tree.n_nodes || to - from > kMaxTreeNodes) bad = true;
+  const int n = bad ? 0 : (int)(to - from);
+  if (last < -1 || (last >= n && !bad)) {
+    bad_idx = true;
+    last = -1;
+  }
+  if (bad) last = -1;
+  if (last >= 0 && a.tree.parents && (int)threadIdx.x <= last) up[threadIdx.x] = ld_live(a.tree.parents + from + threadIdx.x);
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    int depth = 0;
+    for (int j = last; j >= 0;) {
+      path[depth++] = j;
+      int p = a.tree.parents ? up[j] : j - 1;
+      if (p < -1 || p >= j) {
+        bad_idx = true;
+        p = -1;
+      }
+      j = p;
+    }
+    if ((int64_t)len + depth > a.pv.capacity) {
+      bad = true;
+      depth = 0;
+    }
+    s_depth = depth;
+    a.lens_out[b] = raw_len + depth;   // a row of bad length has no path
+    if (bad_idx) record_error(DSA_DEV_ERR_BAD_INDEX);
+    if (bad) record_error(DSA_DEV_ERR_BAD_PAGE);
+  }
+  __syncthreads();
+  const int depth = s_depth;
+  if (depth == 0) return;
+  bad = false;
+  const int32_t* trow = a.pv.table + b * a.pv.cols;
+  // first row of the pool at position pos; -1: its page is bad
+  auto pool_at = [&](int pos, int& page) -> int64_t {
+    const int pool = pos >> 2, col = page_of_pool(a.pv, pool);
+    page = ld_live(trow + col);
+    return phys_pool(a.pv, pool, col, page, bad);
+  };
+  auto node_of = [&](int i) { return from + path[depth - 1 - i]; };   // of the path's token i
+  int page;
+  for (int i = threadIdx.x; i < depth * CH; i += kCommitThreads) {
+    const int j = i / CH, c = i % CH, pos = len + j;
+    const int64_t pool = pool_at(pos, page);
+    if (pool < 0) continue;
+    const int64_t at = (pool * 4 + (pos & 3)) * CH + c, src = node_of(j) * CH + c;
+    const uint4 x = ld_live(static_cast<const uint4*>(a.k) + src), y = ld_live(static_cast<const uint4*>(a.v) + src);
+    static_cast<uint4*>(a.ck)[at] = x;
+    static_cast<uint4*>(a.cv)[at] = y;
+  }
+  const uint4* ki = static_cast<const uint4*>(a.k_idx);
+  const int first = len & ~3, open = (len + depth) & ~3;
+  for (int i = threadIdx.x; i < (open - first) / 4 * CI; i += kCommitThreads) {
+    const int c = i % CI, p0 = first + i / CI * 4;
+    const int64_t pool = pool_at(p0, page);
+    if (pool < 0) continue;
+    float acc[N], x[N];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      // tokens before len: kept by an earlier append (j < 3)
+      const uint4 raw = p0 + j < len ? ld_live(static_cast<const uint4*>(a.cktail) + ((int64_t)page * 3 + j) * CI + c)
+                                     : ld_live(ki + node_of(p0 + j - len) * CI + c);
+      unpack16<T>(raw, j ? x : acc);
+      if (j)
+#pragma unroll
+        for (int e = 0; e < N; ++e) acc[e] = __fadd_rn(acc[e], x[e]);
+    }
+    static_cast<uint4*>(a.ckpool)[pool * CI + c] = pack16<T>(acc);
+  }
+  __syncthreads();   // the kept keys have been read; the new ones may take their place
+  const int keep = max(open, len);
+  for (int i = threadIdx.x; i < (len + depth - keep) * CI; i += kCommitThreads) {
+    const int c = i % CI, pos = keep + i / CI;
+    if (pool_at(pos, page) < 0) continue;
+    static_cast<uint4*>(a.cktail)[((int64_t)page * 3 + (pos & 3)) * CI + c] = ld_live(ki + node_of(pos - len) * CI + c);
+  }
+  if (bad) record_error(DSA_DEV_ERR_BAD_PAGE);
+}
+
+cudaError_t launch_cache_commit(bool bf16, const CommitArgs& a, cudaStream_t s) {
+  const dim3 grid((unsigned)a.tree.batch), block(kCommitThreads);
+  if (bf16) return launch_chained(cache_commit_kernel<__nv_bfloat16>, grid, block, 0, s, a);
+  return launch_chained(cache_commit_kernel<float>, grid, block, 0, s, a);
+}
+
+}  // namespace dsa

@@ -1,0 +1,461 @@
+// decode_pages.cu -- pages of the paged cache: given to rows, taken back,
+// shared, moved (include/dsa_pages.h).
+//
+// Which page goes where is decided by ranks, so that it does not depend on the
+// order in which the GPU runs things: the i-th request takes the i-th free page,
+// the i-th used page behind the front moves to the i-th hole in it.  Ranks come
+// in two launches: segments of the pages (and of the rows) are counted, then
+// every CTA adds up the segments before its own and numbers its own.  Counts are
+// integers and added with atomics.
+//
+// Bound: the launches, 2 to 4 in a row, each about 2 us; where pages are copied
+// HBM, every byte once in and once out.
+#include "decode.cuh"
+#include "decode_pages.h"
+
+namespace dsa {
+
+constexpr int kPageThreads = 256;
+constexpr int kPageSms = 152;
+constexpr int kSegments = 128;                 // most segments that pages are counted in
+constexpr int kSegmentMin = 4 * kPageThreads;  // pages of a segment, at the least
+
+// The workspace: totals, the segments' counts, then lists.
+struct PagesWs {
+  int64_t* free_in;     // [kSegments] free (reserve) or used (compact) pages of a segment
+  int64_t* want_in;     // [kSegments] requests of a segment of the rows
+  int32_t* go;          // reserve: whether there are pages enough.  compact: pages that move
+  int32_t* want;        // [batch] requests of a row; the top bit: the first is a copy
+  int32_t* old;         // [batch] the page that is copied
+  int64_t* at;          // [batch] rank of a row's first request
+  int32_t *list, *holes;   // [num_pages] each
+};
+static size_t up(size_t n) { return (n + 255) & ~(size_t)255; }
+static size_t carve(PagesWs& w, void* ws, int64_t num_pages, int64_t batch) {
+  char* p = static_cast<char*>(ws);
+  size_t n = 0;
+  auto take = [&](size_t bytes) {
+    char* q = p + n;
+    n += up(bytes);
+    return q;
+  };
+  w.free_in = reinterpret_cast<int64_t*>(take(8 * kSegments));
+  w.want_in = reinterpret_cast<int64_t*>(take(8 * kSegments));
+  w.go = reinterpret_cast<int32_t*>(take(4));
+  w.want = reinterpret_cast<int32_t*>(take(4 * (size_t)batch));
+  w.old = reinterpret_cast<int32_t*>(take(4 * (size_t)batch));
+  w.at = reinterpret_cast<int64_t*>(take(8 * (size_t)batch));
+  w.list = reinterpret_cast<int32_t*>(take(4 * (size_t)num_pages));
+  w.holes = reinterpret_cast<int32_t*>(take(4 * (size_t)num_pages));
+  return n;
+}
+size_t pages_ws_bytes(int64_t num_pages, int64_t batch) {
+  PagesWs w;
+  return carve(w, nullptr, num_pages, batch);
+}
+
+__device__ __forceinline__ int pages_of(int tokens, int page_size) {
+  return (int)(((int64_t)tokens + page_size - 1) / page_size);
+}
+__device__ __forceinline__ bool page_ok(const PagesArgs& a, int page) {
+  return (uint32_t)page < (uint32_t)a.cache.num_pages;
+}
+
+// Exclusive sum over the CTA's threads, and the total; scratch: a warp's each.
+__device__ __forceinline__ int64_t cta_scan(int64_t x, int64_t& total, int64_t* scratch) {
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  int64_t incl = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  __syncthreads();   // the scratch of the call before
+  if (lane == 31) scratch[wid] = incl;
+  __syncthreads();
+  int64_t before = 0;
+  total = 0;
+#pragma unroll
+  for (int w = 0; w < kPageThreads / 32; ++w) {
+    if (w < wid) before += scratch[w];
+    total += scratch[w];
+  }
+  return before + incl - x;
+}
+// Sum of in[0 .. n), and of in[0 .. m): every thread gets both.
+__device__ __forceinline__ void cta_sums(const int64_t* in, int n, int m, int64_t& all, int64_t& first, int64_t* scratch) {
+  const int64_t x = (int)threadIdx.x < n ? ld_live(in + threadIdx.x) : 0;   // n <= kSegments <= kPageThreads
+  cta_scan(x, all, scratch);
+  cta_scan((int)threadIdx.x < m ? x : 0, first, scratch);
+}
+
+__device__ __forceinline__ int page_count(const PagesArgs& a, int64_t p) { return ld_live(a.refs + p); }
+
+// ------------------------------------------------------------------- copies
+// Chunks part, part + parts, .. of a page's arrays (counted through k, v, kpool,
+// ktail): of k and v the first kv, of kpool the first kp, of ktail the first kt.
+__device__ __forceinline__ void copy_page(const PageArrays& from, const PageArrays& to, int64_t src, int64_t dst, int kv,
+                                          int kp, int kt, int part, int parts) {
+  constexpr int AHEAD = 8;
+  const int k_n = from.k ? kv : 0, v_n = from.v ? kv : 0, p_n = from.kpool ? kp : 0, t_n = from.ktail ? kt : 0;
+  const int n = k_n + v_n + p_n + t_n;
+  auto where = [&](const PageArrays& c, int64_t page, int i) -> uint4* {
+    if (i < k_n) return c.k + page * c.kv + i;
+    if ((i -= k_n) < v_n) return c.v + page * c.kv + i;
+    if ((i -= v_n) < p_n) return c.kpool + page * c.kp + i;
+    return c.ktail + page * c.kt + (i - p_n);
+  };
+  const int step = parts * kPageThreads;
+  for (int i0 = part * kPageThreads + (int)threadIdx.x; i0 < n; i0 += AHEAD * step) {
+    uint4 x[AHEAD];
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j)
+      if (i0 + j * step < n) x[j] = ld_live(where(from, src, i0 + j * step));
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j)
+      if (i0 + j * step < n) *where(to, dst, i0 + j * step) = x[j];
+  }
+}
+
+__global__ void __launch_bounds__(kPageThreads)
+    copy_pages_kernel(const __grid_constant__ PageArrays from, const __grid_constant__ PageArrays to, int64_t n,
+                      const int32_t* src, const int32_t* dst, int parts) {
+  chain_wait();
+  chain_release();
+  bool bad = false;
+  for (int64_t u = blockIdx.x; u < n * parts; u += gridDim.x) {
+    const int s = ld_live(src + u / parts), d = ld_live(dst + u / parts);
+    if (s < 0 || d < 0) continue;
+    if (s >= from.num_pages || d >= to.num_pages) {
+      bad = true;
+      continue;
+    }
+    copy_page(from, to, s, d, from.kv, from.kp, from.kt, (int)(u % parts), parts);
+  }
+  if (bad && threadIdx.x == 0) record_error(DSA_DEV_ERR_BAD_PAGE);
+}
+
+// ------------------------------------------------------------------- release, fork
+__global__ void __launch_bounds__(kPageThreads)
+    cache_release_kernel(const __grid_constant__ PagesArgs a, const int32_t* keep) {
+  chain_wait();
+  chain_release();
+  const int64_t b = blockIdx.y;
+  bool bad = false;
+  const int len = row_length(a.pv, b, bad);
+  const int left = keep ? ld_live(keep + b) : 0;
+  if (left < 0) bad = true;
+  const int end = bad ? 0 : pages_of(len, a.page_size);
+  int32_t* row = a.table + b * a.pv.cols;
+  for (int c = (bad ? 0 : pages_of(left, a.page_size)) + blockIdx.x * kPageThreads + threadIdx.x; c < end;
+       c += gridDim.x * kPageThreads) {
+    const int page = ld_live(row + c);
+    if (page_ok(a, page)) {
+      if (atomicSub(a.refs + page, 1) <= 0) {   // had none left
+        atomicAdd(a.refs + page, 1);
+        bad = true;
+      }
+    } else {
+      bad = true;
+    }
+    row[c] = -1;
+  }
+  if (bad) record_error(DSA_DEV_ERR_BAD_PAGE);
+}
+
+__global__ void __launch_bounds__(kPageThreads)
+    cache_fork_kernel(const __grid_constant__ PagesArgs a, const int32_t* parents, int32_t* lens_out, int32_t* table_out) {
+  chain_wait();
+  chain_release();
+  const int64_t i = blockIdx.y;
+  bool bad = false;
+  int64_t p = ld_live(parents + i);
+  if (p < -1 || p >= a.batch) {
+    if (threadIdx.x == 0 && blockIdx.x == 0) record_error(DSA_DEV_ERR_BAD_INDEX);
+    p = -1;
+  }
+  const int len = p < 0 ? 0 : row_length(a.pv, p, bad);
+  if (threadIdx.x == 0 && blockIdx.x == 0) lens_out[i] = len;
+  const int held = pages_of(len, a.page_size);
+  for (int c = blockIdx.x * kPageThreads + threadIdx.x; c < a.pv.cols; c += gridDim.x * kPageThreads) {
+    int page = -1;
+    if (c < held) {
+      page = ld_live(a.pv.table + p * a.pv.cols + c);
+      if (page_ok(a, page)) {
+        atomicAdd(a.refs + page, 1);
+      } else {
+        page = -1;
+        bad = true;
+      }
+    }
+    table_out[i * a.pv.cols + c] = page;
+  }
+  if (bad) record_error(DSA_DEV_ERR_BAD_PAGE);
+}
+
+// ------------------------------------------------------------------- reserve
+constexpr uint32_t kCopyBit = 0x80000000u;
+
+// Free pages and requests of every segment; every row's requests.
+__global__ void __launch_bounds__(kPageThreads)
+    reserve_count_kernel(const __grid_constant__ PagesArgs a, const __grid_constant__ PagesWs w, const int32_t* new_lens,
+                         int64_t pages_per, int64_t rows_per) {
+  __shared__ int64_t scratch[kPageThreads / 32];
+  chain_wait();
+  chain_release();
+  const int64_t p1 = min((blockIdx.x + 1) * pages_per, a.cache.num_pages);
+  int64_t free_ = 0, want = 0, total;
+  for (int64_t p = blockIdx.x * pages_per + threadIdx.x; p < p1; p += kPageThreads) free_ += page_count(a, p) == 0;
+  const int64_t b1 = min((blockIdx.x + 1) * rows_per, a.batch);
+  for (int64_t b = blockIdx.x * rows_per + threadIdx.x; b < b1; b += kPageThreads) {
+    bool bad = false;
+    const int len = row_length(a.pv, b, bad), to = ld_live(new_lens + b);
+    if (to < 0 || to > a.pv.capacity) bad = true;
+    uint32_t n = 0;
+    int page = -1;
+    if (!bad && to > len) {
+      n = (uint32_t)(pages_of(to, a.page_size) - pages_of(len, a.page_size));
+      if (len % a.page_size) {
+        page = ld_live(a.pv.table + b * a.pv.cols + len / a.page_size);
+        if (!page_ok(a, page)) {
+          bad = true;
+          n = 0;
+        } else if (page_count(a, page) > 1) {
+          n = (n + 1) | kCopyBit;
+        }
+      }
+    }
+    w.want[b] = (int)n;
+    w.old[b] = page;
+    want += n & ~kCopyBit;
+    if (bad) record_error(DSA_DEV_ERR_BAD_PAGE);
+  }
+  cta_scan(free_, total, scratch);
+  if (threadIdx.x == 0) w.free_in[blockIdx.x] = total;
+  cta_scan(want, total, scratch);
+  if (threadIdx.x == 0) w.want_in[blockIdx.x] = total;
+}
+
+// The free pages as a list, as far as they are wanted, and where in it a row's begin.
+__global__ void __launch_bounds__(kPageThreads)
+    reserve_place_kernel(const __grid_constant__ PagesArgs a, const __grid_constant__ PagesWs w, int32_t* missing,
+                         int64_t pages_per, int64_t rows_per) {
+  __shared__ int64_t scratch[kPageThreads / 32];
+  chain_wait();
+  chain_release();
+  int64_t have, rank, wanted, at, total;
+  cta_sums(w.free_in, gridDim.x, blockIdx.x, have, rank, scratch);
+  cta_sums(w.want_in, gridDim.x, blockIdx.x, wanted, at, scratch);
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    *w.go = wanted <= have;
+    *missing = wanted <= have ? 0 : (int)min(wanted - have, (int64_t)INT32_MAX);
+  }
+  if (wanted > have) return;
+  const int64_t p1 = min((blockIdx.x + 1) * pages_per, a.cache.num_pages);
+  for (int64_t p0 = blockIdx.x * pages_per; p0 < p1 && rank < wanted; p0 += kPageThreads) {
+    const int64_t p = p0 + threadIdx.x;
+    const bool is_free = p < p1 && page_count(a, p) == 0;
+    const int64_t r = rank + cta_scan(is_free, total, scratch);
+    if (is_free && r < wanted) w.list[r] = (int)p;
+    rank += total;
+  }
+  const int64_t b1 = min((blockIdx.x + 1) * rows_per, a.batch);
+  for (int64_t b0 = blockIdx.x * rows_per; b0 < b1; b0 += kPageThreads) {
+    const int64_t b = b0 + threadIdx.x;
+    const int64_t n = b < b1 ? (int64_t)((uint32_t)ld_live(w.want + b) & ~kCopyBit) : 0;
+    const int64_t r = at + cta_scan(n, total, scratch);
+    if (b < b1) w.at[b] = r;
+    at += total;
+  }
+}
+
+// The pages to the rows: grid (parts, batch); a row's CTAs share its copy.
+__global__ void __launch_bounds__(kPageThreads)
+    reserve_give_kernel(const __grid_constant__ PagesArgs a, const __grid_constant__ PagesWs w) {
+  chain_wait();
+  chain_release();
+  const int64_t b = blockIdx.y;
+  if (!ld_live(w.go)) return;
+  const uint32_t want = (uint32_t)ld_live(w.want + b);
+  if (want == 0) return;
+  const int copy = (want & kCopyBit) != 0, n = (int)(want & ~kCopyBit);
+  const int len = ld_live(a.pv.lens + b);   // good: the row asked
+  const int32_t* list = w.list + ld_live(w.at + b);
+  int32_t* row = a.table + b * a.pv.cols;
+  if (copy) {
+    const int src = ld_live(w.old + b), dst = ld_live(list), part = len % a.page_size;
+    copy_page(a.cache, a.cache, src, dst, part * a.cache.kv_row, part / 4 * a.cache.kp_row, a.cache.kt, blockIdx.x,
+              gridDim.x);
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+      row[len / a.page_size] = dst;
+      a.refs[dst] = 1;
+      atomicSub(a.refs + src, 1);
+    }
+  }
+  const int c0 = pages_of(len, a.page_size);
+  for (int i = blockIdx.x * kPageThreads + threadIdx.x; i < n - copy; i += gridDim.x * kPageThreads) {
+    const int page = ld_live(list + copy + i);
+    row[c0 + i] = page;
+    a.refs[page] = 1;
+  }
+}
+
+// ------------------------------------------------------------------- compact
+__global__ void __launch_bounds__(kPageThreads)
+    compact_count_kernel(const __grid_constant__ PagesArgs a, const __grid_constant__ PagesWs w, int64_t pages_per) {
+  __shared__ int64_t scratch[kPageThreads / 32];
+  chain_wait();
+  chain_release();
+  const int64_t p1 = min((blockIdx.x + 1) * pages_per, a.cache.num_pages);
+  int64_t n = 0, total;
+  for (int64_t p = blockIdx.x * pages_per + threadIdx.x; p < p1; p += kPageThreads) n += page_count(a, p) > 0;
+  cta_scan(n, total, scratch);
+  if (threadIdx.x == 0) w.free_in[blockIdx.x] = total;
+}
+
+__global__ void __launch_bounds__(kPageThreads)
+    compact_place_kernel(const __grid_constant__ PagesArgs a, const __grid_constant__ PagesWs w, int32_t* remap,
+                         int32_t* used, int64_t pages_per) {
+  __shared__ int64_t scratch[kPageThreads / 32];
+  chain_wait();
+  chain_release();
+  int64_t U, before, total, below;
+  cta_sums(w.free_in, gridDim.x, blockIdx.x, U, before, scratch);
+  // used pages below U: whole segments, and the part of U's own that lies below it
+  {
+    const int64_t seg = U / pages_per;
+    int64_t n = 0, first;
+    for (int64_t p = seg * pages_per + threadIdx.x; p < U; p += kPageThreads) n += page_count(a, p) > 0;
+    cta_scan(n, below, scratch);
+    cta_sums(w.free_in, gridDim.x, (int)seg, total, first, scratch);   // seg <= gridDim.x: U <= num_pages
+    below += first;
+  }
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    *used = (int)U;
+    *w.go = (int)(U - below);
+  }
+  const int64_t p1 = min((blockIdx.x + 1) * pages_per, a.cache.num_pages);
+  for (int64_t p0 = blockIdx.x * pages_per; p0 < p1; p0 += kPageThreads) {
+    const int64_t p = p0 + threadIdx.x;
+    const bool is_used = p < p1 && page_count(a, p) > 0;
+    const int64_t r = before + cta_scan(is_used, total, scratch);   // used pages below p
+    if (p < p1) {
+      if (!is_used) {
+        remap[p] = -1;
+        if (p < U) w.holes[p - r] = (int)p;
+      } else if (p < U) {
+        remap[p] = (int)p;
+      } else {
+        w.list[r - below] = (int)p;   // its new number: compact_move_kernel
+      }
+    }
+    before += total;
+  }
+}
+
+__global__ void __launch_bounds__(kPageThreads)
+    compact_move_kernel(const __grid_constant__ PagesArgs a, const __grid_constant__ PagesWs w, int32_t* remap,
+                        int parts) {
+  chain_wait();
+  chain_release();
+  const int64_t n = (int64_t)ld_live(w.go) * parts;
+  for (int64_t u = blockIdx.x; u < n; u += gridDim.x) {
+    const int src = ld_live(w.list + u / parts), dst = ld_live(w.holes + u / parts), part = (int)(u % parts);
+    copy_page(a.cache, a.cache, src, dst, a.cache.kv, a.cache.kp, a.cache.kt, part, parts);
+    if (part == 0 && threadIdx.x == 0) {
+      remap[src] = dst;
+      a.refs[dst] = ld_live(a.refs + src);
+      a.refs[src] = 0;
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kPageThreads)
+    compact_table_kernel(const __grid_constant__ PagesArgs a, const int32_t* remap) {
+  chain_wait();
+  chain_release();
+  const int64_t b = blockIdx.y;
+  bool bad = false;
+  const int held = pages_of(row_length(a.pv, b, bad), a.page_size);
+  int32_t* row = a.table + b * a.pv.cols;
+  for (int c = blockIdx.x * kPageThreads + threadIdx.x; c < held; c += gridDim.x * kPageThreads) {
+    const int page = ld_live(row + c);
+    const int to = page_ok(a, page) ? ld_live(remap + page) : -1;
+    if (to < 0) bad = true;
+    if (to != page) row[c] = to;
+  }
+  if (bad) record_error(DSA_DEV_ERR_BAD_PAGE);
+}
+
+// ------------------------------------------------------------------- launches
+// CTAs along a row's columns: the rows' capacity, not their lengths, is known
+// here, so few, each with a loop.
+static dim3 row_grid(const PagesArgs& a, int64_t rows) {
+  const int x = (a.pv.cols + kPageThreads - 1) / kPageThreads;
+  return dim3((unsigned)(x < 4 ? x : 4), (unsigned)rows);
+}
+static unsigned segments_of(const PagesArgs& a, int64_t& pages_per) {
+  pages_per = (a.cache.num_pages + kSegments - 1) / kSegments;
+  if (pages_per < kSegmentMin) pages_per = kSegmentMin;
+  return (unsigned)((a.cache.num_pages + pages_per - 1) / pages_per);
+}
+// CTAs that share the copy of a page where `pages` are copied: up to 4 while the SMs
+// have room for them, of no less than 4 KB each.
+static int copy_parts(const PageArrays& c, int64_t pages) {
+  const int chunks = 2 * c.kv + c.kp + c.kt;
+  int parts = 1;
+  while (parts < 4 && chunks / (2 * parts) >= 256 && pages * parts * 2 <= 4 * kPageSms) parts *= 2;
+  return parts;
+}
+
+cudaError_t launch_copy_pages(const PageArrays& from, const PageArrays& to, int64_t n, const int32_t* src,
+                              const int32_t* dst, cudaStream_t s) {
+  if (n == 0) return cudaSuccess;
+  const int parts = copy_parts(from, n);
+  const int64_t most = 8 * kPageSms, units = n * parts;
+  return launch_chained(copy_pages_kernel, dim3((unsigned)(units < most ? units : most)), dim3(kPageThreads), 0, s, from,
+                        to, n, src, dst, parts);
+}
+
+cudaError_t launch_cache_release(const PagesArgs& a, const int32_t* keep, cudaStream_t s) {
+  return launch_chained(cache_release_kernel, row_grid(a, a.batch), dim3(kPageThreads), 0, s, a, keep);
+}
+
+cudaError_t launch_cache_fork(const PagesArgs& a, int64_t n_out, const int32_t* parents, int32_t* lens_out,
+                              int32_t* table_out, cudaStream_t s) {
+  return launch_chained(cache_fork_kernel, row_grid(a, n_out), dim3(kPageThreads), 0, s, a, parents, lens_out, table_out);
+}
+
+cudaError_t launch_cache_reserve(const PagesArgs& a, const int32_t* new_lens, int32_t* missing, cudaStream_t s) {
+  PagesWs w;
+  carve(w, a.ws, a.cache.num_pages, a.batch);
+  int64_t pages_per;
+  const unsigned g = segments_of(a, pages_per);
+  const int64_t rows_per = (a.batch + g - 1) / g;
+  cudaError_t e = launch_chained(reserve_count_kernel, dim3(g), dim3(kPageThreads), 0, s, a, w, new_lens, pages_per, rows_per);
+  if (e != cudaSuccess) return e;
+  e = launch_chained(reserve_place_kernel, dim3(g), dim3(kPageThreads), 0, s, a, w, missing, pages_per, rows_per);
+  if (e != cudaSuccess) return e;
+  return launch_chained(reserve_give_kernel, dim3((unsigned)copy_parts(a.cache, a.batch), (unsigned)a.batch),
+                        dim3(kPageThreads), 0, s, a, w);
+}
+
+cudaError_t launch_cache_compact(const PagesArgs& a, int32_t* remap, int32_t* used, cudaStream_t s) {
+  PagesWs w;
+  carve(w, a.ws, a.cache.num_pages, a.batch);
+  int64_t pages_per;
+  const unsigned g = segments_of(a, pages_per);
+  cudaError_t e = launch_chained(compact_count_kernel, dim3(g), dim3(kPageThreads), 0, s, a, w, pages_per);
+  if (e != cudaSuccess) return e;
+  e = launch_chained(compact_place_kernel, dim3(g), dim3(kPageThreads), 0, s, a, w, remap, used, pages_per);
+  if (e != cudaSuccess) return e;
+  // at most half of the pages move
+  const int parts = copy_parts(a.cache, a.cache.num_pages / 2);
+  const int64_t units = (a.cache.num_pages / 2 + 1) * parts, most = 8 * kPageSms;
+  e = launch_chained(compact_move_kernel, dim3((unsigned)(units < most ? units : most)), dim3(kPageThreads), 0, s, a, w,
+                     remap, parts);
+  if (e != cudaSuccess) return e;
+  return launch_chained(compact_table_kernel, row_grid(a, a.batch), dim3(kPageThreads), 0, s, a, (const int32_t*)remap);
+}
+
+}  // namespace dsa
