@@ -58,7 +58,8 @@ size_t dsa_qk_norm_bwd_workspace_bytes(const dsa_dims *dims, int64_t n_tokens);
  *              dq_out itself, dk dk_out
  *   dq_weight, dk_weight [d] fp32, outputs, written (not added to); NULL where
  *              not wanted
- * With q NULL, dq_out, dq and dq_weight are NULL too; the same for k. */
+ * With q NULL, dq_out, dq and dq_weight are NULL too; the same for k.  Without
+ * tokens the tensors may all be NULL, and the weights' gradients are 0. */
 dsa_status dsa_qk_norm_rotate_bwd(const dsa_dims *dims, int64_t n_tokens, const void *q, int64_t q_stride,
                                   const void *k, int64_t k_stride, const float *q_weight, const float *k_weight,
                                   float eps, const dsa_rotation *rotation, const int32_t *positions,

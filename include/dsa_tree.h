@@ -59,7 +59,9 @@ size_t dsa_tree_workspace_bytes(const dsa_dims *dims, int64_t batch, int64_t n_n
  *   o          [n_nodes, Hq, d] layer dtype, output
  *   lse        [n_nodes, Hq] fp32, output (natural log)
  * Nothing of a node that is not an ancestor enters: it may hold infinities or
- * NaN.  With idx, pools that drafted tokens complete are not selected from:
+ * NaN.  (An infinite value that does enter makes that channel of o infinite or
+ * NaN: bf16 weights are carried as two terms, which may have either sign.)
+ * With idx, pools that drafted tokens complete are not selected from:
  * all of a branch is attended to.
  * A branch of one node per row, without a second token of its pool's, gives
  * what dsa_cache_append and dsa_decode_attn give (not bit for bit). */

@@ -442,7 +442,14 @@ __device__ __forceinline__ void attn_piece_bf16(const PagedView& pv, const __nv_
 #pragma unroll
         for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
-          for (int e = 2 * r; e < 2 * r + 2; ++e) z[nt][e] = ex2_approx(fmaf(z[nt][e], scale_log2, -base));
+          for (int e = 2 * r; e < 2 * r + 2; ++e) {
+            // A drafted token's largest score minus the base is 0 at any magnitude: the
+            // fused form leaves the product's rounding, which passes 2^7 for scores above 2^31.
+            if constexpr (TREE)
+              z[nt][e] = ex2_approx(__fsub_rn(__fmul_rn(z[nt][e], scale_log2), base));
+            else
+              z[nt][e] = ex2_approx(fmaf(z[nt][e], scale_log2, -base));
+          }
         l[n][r] += (z[0][2 * r] + z[0][2 * r + 1]) + (z[1][2 * r] + z[1][2 * r + 1]);
       }
 #pragma unroll

@@ -90,7 +90,7 @@ dsa_status dsa_qk_norm_rotate_bwd(const dsa_dims* dims, int64_t n_tokens, const 
   if (st) return st;
   if ((dq == nullptr) != (q == nullptr) || (dk == nullptr) != (k == nullptr))
     return fail(DSA_ERR_INVALID_ARG, "an input without its gradient, or the reverse");
-  if ((q == nullptr && dq_weight != nullptr) || (k == nullptr && dk_weight != nullptr))
+  if (n_tokens > 0 && ((q == nullptr && dq_weight != nullptr) || (k == nullptr && dk_weight != nullptr)))
     return fail(DSA_ERR_INVALID_ARG, "a weight's gradient without its heads");
   if (!aligned16(dq) || !aligned16(dk) || !aligned16(dq_weight) || !aligned16(dk_weight))
     return fail(DSA_ERR_INVALID_ARG, "a gradient is not 16-byte aligned");
