@@ -9,6 +9,7 @@
 // attend to whole caches share them by rows: decode_tree_tc.cu.
 #include "decode_attn.cuh"
 #include "decode_tree.cuh"
+#include "decode_tree_tc.h"
 
 namespace dsa {
 
@@ -114,7 +115,7 @@ static cudaError_t launch_typed(const TreeAttnArgs& g, const TreeNode* nodes, cu
 static size_t node_bytes(int64_t n) { return ((size_t)n * sizeof(TreeNode) + 255) & ~(size_t)255; }
 
 size_t tree_attn_ws_bytes(bool bf16, int Hq, int d, int64_t batch, int64_t n_nodes) {
-  return node_bytes(n_nodes) + 256;
+  return node_bytes(n_nodes) + (bf16 ? tree_tc_ws_bytes(d) : 256);
 }
 
 cudaError_t launch_tree_attn(bool bf16, const TreeAttnArgs& a, cudaStream_t s) {
@@ -122,6 +123,7 @@ cudaError_t launch_tree_attn(bool bf16, const TreeAttnArgs& a, cudaStream_t s) {
   TreeNode* nodes = static_cast<TreeNode*>(a.ws);
   const cudaError_t e = launch_tree_nodes(a.pv, a.tree, nodes, s);
   if (e != cudaSuccess) return e;
+  if (bf16 && a.idx == nullptr) return launch_tree_tc(a, nodes, static_cast<char*>(a.ws) + node_bytes(a.tree.n_nodes), s);
   return bf16 ? launch_typed<__nv_bfloat16>(a, nodes, s) : launch_typed<float>(a, nodes, s);
 }
 
