@@ -1,11 +1,11 @@
 // decode_heads.cu -- norm and rotation of every head of q and k, and their gradient.
 //
-// A group of d/16 (bf16) or d/8 (fp32) lanes takes a token and walks through
-// its heads, the key's last.  A lane holds two 16-byte chunks of a head, chosen
-// so that they hold whole pairs (rotate.cuh), and the same ones for every head:
-// the sine and cosine of its pairs are formed once per token, the weights once.
-// The sum of squares is a shuffle over the group.  With few tokens the heads of
-// a token are dealt out to several groups (grid y).
+// A group of d/16 (bf16) or d/8 (fp32) lanes takes some heads of a token.  A lane
+// holds two 16-byte chunks of a head, chosen so that they hold whole pairs
+// (rotate.cuh), the same ones for every head.  A CTA's groups are `tokens` tokens
+// by `slices` shares of their heads (the key is the last head); the sine and
+// cosine of a token's pairs are formed once, by all threads, and shared through
+// shared memory.  The sum of squares is a shuffle over the group.
 //
 // Gradient: y = R(w * xn), xn = x r, so with g = R^T dy
 //   dx = r (w g - xn mean(w g xn)),  dw = sum g xn.
@@ -22,19 +22,25 @@ namespace dsa {
 
 constexpr int kHeadThreads = 256;
 constexpr int kHeadSms = 152;
-constexpr int kGradCtas = 3 * kHeadSms;   // most CTAs of the gradient kernel
+constexpr int kGradCtas = 2 * kHeadSms;   // CTAs of the gradient kernel: as many as are resident
 
-// What a lane holds: its chunks, its group's token.
+// How a CTA's groups share a block of tokens.
+struct HeadSplit {
+  int tokens, slices;   // tokens * slices groups; slice s takes heads s, s + slices, ..
+};
+
 template <typename T, int D>
 struct HeadLane {
   static constexpr int N = Vec16<T>::N;
   static constexpr int UN = D / N / 2;                  // lanes per head
   static constexpr int GROUPS = kHeadThreads / UN;      // groups per CTA
+  static constexpr int PAIRS = D / 2;                   // at most
+  // of the CTA's tokens, [tokens][PAIRS] each
+  static constexpr int TURNS = GROUPS * PAIRS;
   int c0, c1;                                           // chunks
   bool rotated, inter;
-  float cs[N], sn[N];
 
-  __device__ __forceinline__ HeadLane(const HeadsArgs& a) {
+  __device__ __forceinline__ explicit HeadLane(const HeadsArgs& a) {
     const int u = threadIdx.x % UN, ru = a.rot.dim / (2 * N);
     inter = a.rot.interleaved != 0;
     rotated = u < ru;
@@ -42,15 +48,14 @@ struct HeadLane {
     c0 = halves ? u : 2 * u;
     c1 = halves ? u + ru : 2 * u + 1;
   }
-  // `back`: the turn's transpose
-  __device__ __forceinline__ void turn_to(const HeadsArgs& a, int64_t t, bool back) {
-    if (!rotated) return;
-    const int64_t pos = a.positions ? ld_live(a.positions + t) : t;
-    const uint64_t* f = a.rot.turns + threadIdx.x % UN * N;
+  // this lane's pairs of token `tok` of the block
+  __device__ __forceinline__ void turn(const float* turns, int tok, float (&cs)[N], float (&sn)[N]) const {
+    const uint32_t c = smem_u32(turns + tok * PAIRS + threadIdx.x % UN * N);
 #pragma unroll
-    for (int e = 0; e < N; ++e) {
-      rotation_at(pos, ld_live(f + e), cs[e], sn[e]);
-      if (back) sn[e] = -sn[e];
+    for (int e = 0; e < N; e += 4) {
+      const float4 x = ld_shared_v4(c + 4 * e), y = ld_shared_v4(c + 4 * (TURNS + e));
+      cs[e] = x.x, cs[e + 1] = x.y, cs[e + 2] = x.z, cs[e + 3] = x.w;
+      sn[e] = y.x, sn[e + 1] = y.y, sn[e + 2] = y.z, sn[e + 3] = y.w;
     }
   }
   __device__ __forceinline__ void weights(const float* w, float (&w0)[N], float (&w1)[N]) const {
@@ -67,6 +72,21 @@ struct HeadLane {
   }
 };
 
+// Cosines, then sines, of all pairs of the block's tokens t0 ..; `back`: the turn's transpose.
+template <int PAIRS, int TURNS>
+__device__ __forceinline__ void form_turns(const HeadsArgs& a, int64_t t0, int tokens, bool back, float* turns) {
+  const int n = a.rot.dim / 2;
+  for (int i = threadIdx.x; i < tokens * PAIRS; i += kHeadThreads) {
+    const int tok = i / PAIRS, f = i % PAIRS;
+    if (f >= n || t0 + tok >= a.n_tokens) continue;
+    const int64_t pos = a.positions ? ld_live(a.positions + t0 + tok) : t0 + tok;
+    float c, s;
+    rotation_at(pos, ld_live(a.rot.turns + f), c, s);
+    turns[i] = c;
+    turns[TURNS + i] = back ? -s : s;
+  }
+}
+
 template <int UN>
 __device__ __forceinline__ float group_sum(float x) {
 #pragma unroll
@@ -74,53 +94,54 @@ __device__ __forceinline__ float group_sum(float x) {
   return x;
 }
 
-// The heads [h0, h1) of a token that the groups of grid row y take: head Hq is the key.
-__device__ __forceinline__ void head_range(const HeadsArgs& a, int& h0, int& h1) {
-  const int heads = a.Hq + (a.k != nullptr), per = (heads + gridDim.y - 1) / gridDim.y;
-  h0 = blockIdx.y * per;
-  h1 = min(h0 + per, heads);
-}
-
 template <typename T, int D>
-__global__ void __launch_bounds__(kHeadThreads) qk_norm_rotate_kernel(const __grid_constant__ HeadsArgs a) {
+__global__ void __launch_bounds__(kHeadThreads, 2)
+    qk_norm_rotate_kernel(const __grid_constant__ HeadsArgs a, HeadSplit hs) {
   using L = HeadLane<T, D>;
   constexpr int N = L::N, CH = D / N;
   constexpr int AHEAD = 4;   // heads requested at once
+  extern __shared__ __align__(16) float turns[];   // [2][TURNS], as far as tokens fill it
   chain_wait();
   chain_release();
-  const int64_t t = (int64_t)blockIdx.x * L::GROUPS + threadIdx.x / L::UN;
+  const int64_t t0 = (int64_t)blockIdx.x * hs.tokens;
+  const int group = threadIdx.x / L::UN, tok = group / hs.slices, slice = group % hs.slices;
+  const int64_t t = t0 + tok;
   const bool live = t < a.n_tokens;   // all lanes stay for the shuffles
-  const int64_t tt = live ? t : 0;
-  L l(a);
-  int h0, h1;
-  head_range(a, h0, h1);
+  const int64_t tt = live ? t : t0;
+  const L l(a);
+  const int heads = a.Hq + (a.k != nullptr);
   const uint4* q = static_cast<const uint4*>(a.q) + tt * (a.q_stride / N);
   const uint4* k = static_cast<const uint4*>(a.k) + tt * (a.k_stride / N);
   uint4* qo = static_cast<uint4*>(a.q_out) + tt * a.Hq * CH;
   uint4* ko = static_cast<uint4*>(a.k_out) + tt * CH;
   uint4 x[AHEAD], y[AHEAD];
-  auto load = [&](int h) {
-#pragma unroll
-    for (int i = 0; i < AHEAD; ++i)
-      if (h + i < h1) {   // q_out may be q: a lane reads its own chunks before it writes them
-        const uint4* p = h + i < a.Hq ? q + (h + i) * CH : k;
-        x[i] = ld_live(p + l.c0);
-        y[i] = ld_live(p + l.c1);
-      }
+  auto load = [&](int i, int h) {
+    if (h < heads) {   // q_out may be q: a lane reads its own chunks before it writes them
+      const uint4* p = h < a.Hq ? q + h * CH : k;
+      x[i] = ld_live(p + l.c0);
+      y[i] = ld_live(p + l.c1);
+    }
   };
-  load(h0);
-  float w0[N], w1[N];
-  l.weights(h0 < a.Hq ? a.q_weight : a.k_weight, w0, w1);
-  l.turn_to(a, tt, false);
-  for (int h = h0; h < h1; h += AHEAD) {
-    if (h != h0) load(h);
+#pragma unroll
+  for (int i = 0; i < AHEAD; ++i) load(i, slice + i * hs.slices);
+  float cs[N], sn[N], w0[N], w1[N];
+  if (a.rot.dim) {
+    form_turns<L::PAIRS, L::TURNS>(a, t0, hs.tokens, false, turns);
+    __syncthreads();
+    if (l.rotated) l.turn(turns, tok, cs, sn);
+  }
+  l.weights(slice < a.Hq ? a.q_weight : a.k_weight, w0, w1);
+  // all groups make the same rounds, for the shuffles
+  for (int h0 = 0; h0 < heads; h0 += AHEAD * hs.slices) {
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i) {
-      if (h + i >= h1) break;
-      if (h + i == a.Hq && h + i != h0) l.weights(a.k_weight, w0, w1);
+      const int h = h0 + i * hs.slices + slice;
+      if (h0 + i * hs.slices >= heads) break;
+      if (h == a.Hq && h != slice) l.weights(a.k_weight, w0, w1);
       float u[N], v[N], ss = 0.f;
       unpack16<T>(x[i], u);
       unpack16<T>(y[i], v);
+      load(i, h + AHEAD * hs.slices);
 #pragma unroll
       for (int e = 0; e < N; ++e) ss = fmaf(u[e], u[e], fmaf(v[e], v[e], ss));
       const float r = rsqrtf(group_sum<L::UN>(ss) * (1.f / D) + a.eps);
@@ -129,9 +150,9 @@ __global__ void __launch_bounds__(kHeadThreads) qk_norm_rotate_kernel(const __gr
         u[e] = u[e] * r * w0[e];
         v[e] = v[e] * r * w1[e];
       }
-      if (l.rotated) rotate_values<N>(u, v, l.cs, l.sn, l.inter);
-      if (live) {
-        uint4* p = h + i < a.Hq ? qo + (h + i) * CH : ko;
+      if (l.rotated) rotate_values<N>(u, v, cs, sn, l.inter);
+      if (live && h < heads) {
+        uint4* p = h < a.Hq ? qo + h * CH : ko;
         p[l.c0] = pack16<T>(u);
         p[l.c1] = pack16<T>(v);
       }
@@ -155,55 +176,91 @@ __device__ __forceinline__ void store_row(float* p, const float (&x)[N]) {
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kHeadThreads) qk_norm_rotate_bwd_kernel(const __grid_constant__ HeadsArgs a) {
+__global__ void __launch_bounds__(kHeadThreads, 2)
+    qk_norm_rotate_bwd_kernel(const __grid_constant__ HeadsArgs a, HeadSplit hs) {
   using L = HeadLane<T, D>;
   constexpr int N = L::N, CH = D / N;
-  __shared__ float sums[L::GROUPS][D];
+  extern __shared__ __align__(16) float turns[];   // [2][TURNS]; then the groups' sums [GROUPS][D] in its place
   chain_wait();
   chain_release();
-  L l(a);
-  int h0, h1;
-  head_range(a, h0, h1);
-  float w0[N], w1[N], dq0[N], dq1[N], dk0[N], dk1[N];   // the weights' gradients of this lane's channels
+  const L l(a);
+  const int group = threadIdx.x / L::UN, tok = group / hs.slices, slice = group % hs.slices;
+  const int heads = a.Hq + (a.k != nullptr);
+  float w0[N], w1[N], dq0[N], dq1[N], dk0[N], dk1[N];   // d..: this lane's channels of the weights' gradients
 #pragma unroll
   for (int e = 0; e < N; ++e) dq0[e] = dq1[e] = dk0[e] = dk1[e] = 0.f;
-  // all groups of a warp make the same rounds, for the shuffles
-  for (int64_t base = (int64_t)blockIdx.x * L::GROUPS; base < a.n_tokens; base += (int64_t)gridDim.x * L::GROUPS) {
-    const int64_t t = base + threadIdx.x / L::UN;
-    const bool live = t < a.n_tokens;
-    const int64_t tt = live ? t : 0;
-    l.turn_to(a, tt, true);
-    const uint4* q = static_cast<const uint4*>(a.q) + tt * (a.q_stride / N);
-    const uint4* k = static_cast<const uint4*>(a.k) + tt * (a.k_stride / N);
-    for (int h = h0; h < h1; ++h) {
-      const bool is_q = h < a.Hq;
-      if (h == h0 || h == a.Hq) l.weights(is_q ? a.q_weight : a.k_weight, w0, w1);
-      const uint4* p = is_q ? q + h * CH : k;
-      const int64_t at = is_q ? (tt * a.Hq + h) * D : tt * D;
-      const float* gy = (is_q ? a.dq_out : a.dk_out) + at;
-      float* gx = (is_q ? a.dq : a.dk) + at;
+  struct Row {
+    uint4 x, y;
+    float g0[N], g1[N];
+  };
+  Row next;
+  // head h of token t; nothing for h >= heads
+  auto load = [&](Row& r, int64_t t, int h) {
+    if (h >= heads) return;
+    const bool is_q = h < a.Hq;
+    const uint4* p = is_q ? static_cast<const uint4*>(a.q) + t * (a.q_stride / N) + h * CH
+                          : static_cast<const uint4*>(a.k) + t * (a.k_stride / N);
+    const float* gy = is_q ? a.dq_out + (t * a.Hq + h) * D : a.dk_out + t * D;
+    r.x = ld_live(p + l.c0);
+    r.y = ld_live(p + l.c1);
+    load_row<N>(gy + l.c0 * N, r.g0);   // dq may be dq_out: a lane reads its own channels before it writes them
+    load_row<N>(gy + l.c1 * N, r.g1);
+  };
+  const int64_t stride = (int64_t)gridDim.x * hs.tokens;
+  auto own = [&](int64_t base) { return base + tok < a.n_tokens ? base + tok : base; };
+  bool is_key = false;
+  l.weights(slice < a.Hq ? a.q_weight : a.k_weight, w0, w1);
+  if (slice >= a.Hq) is_key = true;
+  // all groups make the same rounds, for the shuffles
+  int64_t base = (int64_t)blockIdx.x * hs.tokens;
+  if (base < a.n_tokens) load(next, own(base), slice);
+  for (; base < a.n_tokens; base += stride) {
+    const bool live = base + tok < a.n_tokens;
+    const int64_t t = own(base);
+    if (a.rot.dim) {
+      __syncthreads();   // the turns of the block before
+      form_turns<L::PAIRS, L::TURNS>(a, base, hs.tokens, true, turns);
+      __syncthreads();
+    }
+    for (int h0 = 0; h0 < heads; h0 += hs.slices) {
+      const int h = h0 + slice;
+      const bool is_q = h < a.Hq, there = live && h < heads;
+      if (is_key == is_q && h < heads) {   // the last head's weights, or back to the others'
+        is_key = !is_q;
+        l.weights(is_q ? a.q_weight : a.k_weight, w0, w1);
+      }
       float u[N], v[N], g0[N], g1[N];
-      unpack16<T>(ld_live(p + l.c0), u);
-      unpack16<T>(ld_live(p + l.c1), v);
-      load_row<N>(gy + l.c0 * N, g0);   // dq may be dq_out: a lane reads its own channels before it writes them
-      load_row<N>(gy + l.c1 * N, g1);
+      unpack16<T>(next.x, u);
+      unpack16<T>(next.y, v);
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        g0[e] = next.g0[e];
+        g1[e] = next.g1[e];
+      }
+      if (h0 + hs.slices < heads)
+        load(next, t, h + hs.slices);
+      else if (base + stride < a.n_tokens)
+        load(next, own(base + stride), slice);
       float ss = 0.f;
 #pragma unroll
       for (int e = 0; e < N; ++e) ss = fmaf(u[e], u[e], fmaf(v[e], v[e], ss));
       const float r = rsqrtf(group_sum<L::UN>(ss) * (1.f / D) + a.eps);
-      if (l.rotated) rotate_values<N>(g0, g1, l.cs, l.sn, l.inter);
+      if (l.rotated) {   // read again for every head: held, they would not leave registers for the next head's rows
+        float cs[N], sn[N];
+        l.turn(turns, tok, cs, sn);
+        rotate_values<N>(g0, g1, cs, sn, l.inter);
+      }
       float dot = 0.f;
 #pragma unroll
       for (int e = 0; e < N; ++e) {
         u[e] *= r;
         v[e] *= r;
-        const float p0 = live ? g0[e] * u[e] : 0.f, p1 = live ? g1[e] * v[e] : 0.f;
-        if (is_q) {
-          dq0[e] += p0;
-          dq1[e] += p1;
-        } else {
-          dk0[e] += p0;
-          dk1[e] += p1;
+        if (there && is_q) {
+          dq0[e] = fmaf(g0[e], u[e], dq0[e]);
+          dq1[e] = fmaf(g1[e], v[e], dq1[e]);
+        } else if (there) {
+          dk0[e] = fmaf(g0[e], u[e], dk0[e]);
+          dk1[e] = fmaf(g1[e], v[e], dk1[e]);
         }
         g0[e] *= w0[e];
         g1[e] *= w1[e];
@@ -215,83 +272,95 @@ __global__ void __launch_bounds__(kHeadThreads) qk_norm_rotate_bwd_kernel(const 
         g0[e] = r * (g0[e] - u[e] * m);
         g1[e] = r * (g1[e] - v[e] * m);
       }
-      if (live) {
+      if (there) {
+        float* gx = is_q ? a.dq + (t * a.Hq + h) * D : a.dk + t * D;
         store_row<N>(gx + l.c0 * N, g0);
         store_row<N>(gx + l.c1 * N, g1);
       }
     }
   }
-  const int64_t cta = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+  static_assert(2 * L::TURNS >= L::GROUPS * D, "the sums fit in the turns' place");
 #pragma unroll
   for (int which = 0; which < 2; ++which) {
     if ((which ? a.dk_weight : a.dq_weight) == nullptr) continue;
     __syncthreads();
-    float* mine = sums[threadIdx.x / L::UN];
+    float* mine = turns + group * D;
     store_row<N>(mine + l.c0 * N, which ? dk0 : dq0);
     store_row<N>(mine + l.c1 * N, which ? dk1 : dq1);
     __syncthreads();
     for (int c = threadIdx.x; c < D; c += kHeadThreads) {
       float s = 0.f;
 #pragma unroll 8
-      for (int g = 0; g < L::GROUPS; ++g) s += sums[g][c];
-      a.ws[(cta * 2 + which) * D + c] = s;
+      for (int g = 0; g < L::GROUPS; ++g) s += turns[g * D + c];
+      a.ws[((int64_t)blockIdx.x * 2 + which) * D + c] = s;
     }
   }
 }
 
-// Adds up the CTAs' sums: a block per 32 channels of one weight.
-__global__ void __launch_bounds__(kHeadThreads) weight_grad_kernel(const float* parts, int ctas, int d, float* dq_weight,
-                                                                   float* dk_weight) {
-  constexpr int ROWS = kHeadThreads / 32;
+// Adds up the CTAs' sums: a block per 32 channels of one weight, all of a
+// thread's loads at once (one after the other they took 30 us).
+constexpr int kWeightThreads = 1024;
+__global__ void __launch_bounds__(kWeightThreads) weight_grad_kernel(const float* parts, int ctas, int d, float* dq_weight,
+                                                                     float* dk_weight) {
+  constexpr int ROWS = kWeightThreads / 32;
+  constexpr int MOST = (kGradCtas + ROWS - 1) / ROWS;
   __shared__ double part[ROWS][32];
   chain_wait();
   chain_release();
   float* out = blockIdx.y ? dk_weight : dq_weight;
   if (out == nullptr) return;
   const int c = blockIdx.x * 32 + (threadIdx.x & 31), r = threadIdx.x >> 5;
+  float x[MOST];
+#pragma unroll
+  for (int i = 0; i < MOST; ++i)
+    x[i] = r + i * ROWS < ctas ? ld_live(parts + ((int64_t)(r + i * ROWS) * 2 + blockIdx.y) * d + c) : 0.f;
   double s = 0.;
-  for (int i = r; i < ctas; i += ROWS) s += ld_live(parts + ((int64_t)i * 2 + blockIdx.y) * d + c);
+#pragma unroll
+  for (int i = 0; i < MOST; ++i) s += x[i];
   part[r][threadIdx.x & 31] = s;
   __syncthreads();
   if (r == 0) {
-#pragma unroll
+#pragma unroll 8
     for (int i = 1; i < ROWS; ++i) s += part[i][threadIdx.x];
     out[c] = (float)s;
   }
 }
 
-// Groups that share a token's heads: as many as it takes to give every SM about
-// 32 warps, up to a group for each head.
-static unsigned head_slices(const HeadsArgs& a, int lanes) {
+// Slices: a power of two, so that a group has no more than `most` heads, and more
+// while there are not CTAs enough for the SMs.
+template <typename L>
+static HeadSplit head_split(const HeadsArgs& a, int most) {
   const int heads = a.Hq + (a.k != nullptr);
-  const int64_t warps = (a.n_tokens * lanes + 31) / 32;
-  int64_t n = (kHeadSms * 32 + warps - 1) / warps;
-  if (n > heads) n = heads;
-  const int per = (heads + (int)n - 1) / (int)n;
-  return (unsigned)((heads + per - 1) / per);
+  int slices = 1;
+  while (slices < L::GROUPS &&
+         (slices * most < heads || (slices < heads && a.n_tokens * slices < (int64_t)2 * kHeadSms * L::GROUPS)))
+    slices *= 2;
+  return {L::GROUPS / slices, slices};
 }
 
 template <typename T, int D>
 static cudaError_t launch_fwd(const HeadsArgs& a, cudaStream_t s) {
   using L = HeadLane<T, D>;
-  const dim3 grid((unsigned)((a.n_tokens + L::GROUPS - 1) / L::GROUPS), head_slices(a, L::UN));
-  return launch_chained(qk_norm_rotate_kernel<T, D>, grid, dim3(kHeadThreads), 0, s, a);
+  const HeadSplit hs = head_split<L>(a, 6);
+  return launch_chained(qk_norm_rotate_kernel<T, D>, dim3((unsigned)((a.n_tokens + hs.tokens - 1) / hs.tokens)),
+                        dim3(kHeadThreads), a.rot.dim ? 2 * L::TURNS * sizeof(float) : 0, s, a, hs);
 }
 
 template <typename T, int D>
 static cudaError_t launch_bwd(const HeadsArgs& a, cudaStream_t s) {
   using L = HeadLane<T, D>;
-  dim3 grid(0, 1);
+  unsigned ctas = 0;
   if (a.n_tokens > 0) {
-    grid.y = head_slices(a, L::UN);
-    const int64_t x = (a.n_tokens + L::GROUPS - 1) / L::GROUPS, most = kGradCtas / grid.y;
-    grid.x = (unsigned)(x < most ? x : most);
-    const cudaError_t e = launch_chained(qk_norm_rotate_bwd_kernel<T, D>, grid, dim3(kHeadThreads), 0, s, a);
+    const HeadSplit hs = head_split<L>(a, 6);
+    const int64_t x = (a.n_tokens + hs.tokens - 1) / hs.tokens;
+    ctas = (unsigned)(x < kGradCtas ? x : kGradCtas);
+    const cudaError_t e = launch_chained(qk_norm_rotate_bwd_kernel<T, D>, dim3(ctas), dim3(kHeadThreads),
+                                         2 * L::TURNS * sizeof(float), s, a, hs);
     if (e != cudaSuccess) return e;
   }
   if (a.dq_weight == nullptr && a.dk_weight == nullptr) return cudaSuccess;
-  return launch_chained(weight_grad_kernel, dim3(D / 32, 2), dim3(kHeadThreads), 0, s, (const float*)a.ws,
-                        (int)(grid.x * grid.y), D, a.dq_weight, a.dk_weight);
+  return launch_chained(weight_grad_kernel, dim3(D / 32, 2), dim3(kWeightThreads), 0, s, (const float*)a.ws, (int)ctas, D,
+                        a.dq_weight, a.dk_weight);
 }
 
 cudaError_t launch_qk_norm_rotate(bool bf16, const HeadsArgs& a, cudaStream_t s) {

@@ -92,32 +92,40 @@ __device__ __forceinline__ void cta_sums(const int64_t* in, int n, int m, int64_
 __device__ __forceinline__ int page_count(const PagesArgs& a, int64_t p) { return ld_live(a.refs + p); }
 
 // ------------------------------------------------------------------- copies
-// Chunks part, part + parts, .. of a page's arrays (counted through k, v, kpool,
-// ktail): of k and v the first kv, of kpool the first kp, of ktail the first kt.
+// A part of a page, every `parts`th piece of CTA size, of each array: of k and v
+// the first kv chunks, of kpool the first kp, of ktail the first kt.  k and v go
+// together, 4 chunks of each on their way per thread.
 __device__ __forceinline__ void copy_page(const PageArrays& from, const PageArrays& to, int64_t src, int64_t dst, int kv,
                                           int kp, int kt, int part, int parts) {
-  constexpr int AHEAD = 8;
-  const int k_n = from.k ? kv : 0, v_n = from.v ? kv : 0, p_n = from.kpool ? kp : 0, t_n = from.ktail ? kt : 0;
-  const int n = k_n + v_n + p_n + t_n;
-  auto where = [&](const PageArrays& c, int64_t page, int i) -> uint4* {
-    if (i < k_n) return c.k + page * c.kv + i;
-    if ((i -= k_n) < v_n) return c.v + page * c.kv + i;
-    if ((i -= v_n) < p_n) return c.kpool + page * c.kp + i;
-    return c.ktail + page * c.kt + (i - p_n);
-  };
-  const int step = parts * kPageThreads;
-  for (int i0 = part * kPageThreads + (int)threadIdx.x; i0 < n; i0 += AHEAD * step) {
-    uint4 x[AHEAD];
+  constexpr int AHEAD = 4;
+  const int step = parts * kPageThreads, i0 = part * kPageThreads + (int)threadIdx.x;
+  if (from.k) {
+    const uint4 *ks = from.k + src * from.kv, *vs = from.v + src * from.kv;
+    uint4 *kd = to.k + dst * to.kv, *vd = to.v + dst * to.kv;
+    for (int i = i0; i < kv; i += AHEAD * step) {
+      uint4 x[AHEAD], y[AHEAD];
 #pragma unroll
-    for (int j = 0; j < AHEAD; ++j)
-      if (i0 + j * step < n) x[j] = ld_live(where(from, src, i0 + j * step));
+      for (int j = 0; j < AHEAD; ++j)
+        if (i + j * step < kv) {
+          x[j] = ld_live(ks + i + j * step);
+          y[j] = ld_live(vs + i + j * step);
+        }
 #pragma unroll
-    for (int j = 0; j < AHEAD; ++j)
-      if (i0 + j * step < n) *where(to, dst, i0 + j * step) = x[j];
+      for (int j = 0; j < AHEAD; ++j)
+        if (i + j * step < kv) {
+          kd[i + j * step] = x[j];
+          vd[i + j * step] = y[j];
+        }
+    }
+  }
+  if (from.kpool) {
+    for (int i = i0; i < kp; i += step) to.kpool[dst * to.kp + i] = ld_live(from.kpool + src * from.kp + i);
+    if (from.ktail)
+      for (int i = i0; i < kt; i += step) to.ktail[dst * to.kt + i] = ld_live(from.ktail + src * from.kt + i);
   }
 }
 
-__global__ void __launch_bounds__(kPageThreads)
+__global__ void __launch_bounds__(kPageThreads, 4)
     copy_pages_kernel(const __grid_constant__ PageArrays from, const __grid_constant__ PageArrays to, int64_t n,
                       const int32_t* src, const int32_t* dst, int parts) {
   chain_wait();
@@ -353,7 +361,7 @@ __global__ void __launch_bounds__(kPageThreads)
   }
 }
 
-__global__ void __launch_bounds__(kPageThreads)
+__global__ void __launch_bounds__(kPageThreads, 4)
     compact_move_kernel(const __grid_constant__ PagesArgs a, const __grid_constant__ PagesWs w, int32_t* remap,
                         int parts) {
   chain_wait();

@@ -947,8 +947,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 // ------------------------------------------------------------------- the join
 // o = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s over a group's pieces s, for
 // every query row.  A lane is a row; a CTA has 32 of them.  With few pieces its
-// warps share the columns, with many the pieces of two columns' quarters each,
-// which they add up in shared memory, in a fixed order.
+// warps share the columns, with many the pieces, of eight columns at a time, which
+// they add up in shared memory, in a fixed order.
 template <int D>
 __global__ void __launch_bounds__(kTcJoinThreads) tree_join_kernel(const __grid_constant__ TcArgs a, int ctas) {
   constexpr int WARPS = kTcJoinThreads / 32;
