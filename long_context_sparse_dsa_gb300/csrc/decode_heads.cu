@@ -3,9 +3,11 @@
 // A group of d/16 (bf16) or d/8 (fp32) lanes takes some heads of a token.  A lane
 // holds two 16-byte chunks of a head, chosen so that they hold whole pairs
 // (rotate.cuh), the same ones for every head.  A CTA's groups are `tokens` tokens
-// by `slices` shares of their heads (the key is the last head); the sine and
-// cosine of a token's pairs are formed once, by all threads, and shared through
-// shared memory.  The sum of squares is a shuffle over the group.
+// by `slices` shares of their query heads; the first `tokens` groups take the keys
+// too, one token's each.  The sine and cosine of a token's pairs are formed once,
+// by all threads, and shared through shared memory.  The sum of squares is a
+// shuffle over the group.  A CTA goes from block to block of tokens, the next
+// rows on their way while it works on one.
 //
 // Gradient: y = R(w * xn), xn = x r, so with g = R^T dy
 //   dx = r (w g - xn mean(w g xn)),  dw = sum g xn.
@@ -22,6 +24,7 @@ namespace dsa {
 
 constexpr int kHeadThreads = 256;
 constexpr int kHeadSms = 152;
+constexpr int kFwdCtas = 3;               // CTAs an SM
 constexpr int kGradCtas = 2 * kHeadSms;   // CTAs of the gradient kernel: as many as are resident
 
 // How a CTA's groups share a block of tokens.
@@ -32,6 +35,7 @@ struct HeadSplit {
 template <typename T, int D>
 struct HeadLane {
   static constexpr int N = Vec16<T>::N;
+  static constexpr int H = N / 2;                       // pairs of neighbouring channels in a chunk
   static constexpr int UN = D / N / 2;                  // lanes per head
   static constexpr int GROUPS = kHeadThreads / UN;      // groups per CTA
   static constexpr int PAIRS = D / 2;                   // at most
@@ -49,25 +53,43 @@ struct HeadLane {
     c1 = halves ? u + ru : 2 * u + 1;
   }
   // this lane's pairs of token `tok` of the block
-  __device__ __forceinline__ void turn(const float* turns, int tok, float (&cs)[N], float (&sn)[N]) const {
+  __device__ __forceinline__ void turn(const float* turns, int tok, uint64_t (&cs)[H], uint64_t (&sn)[H]) const {
     const uint32_t c = smem_u32(turns + tok * PAIRS + threadIdx.x % UN * N);
 #pragma unroll
-    for (int e = 0; e < N; e += 4) {
-      const float4 x = ld_shared_v4(c + 4 * e), y = ld_shared_v4(c + 4 * (TURNS + e));
-      cs[e] = x.x, cs[e + 1] = x.y, cs[e + 2] = x.z, cs[e + 3] = x.w;
-      sn[e] = y.x, sn[e + 1] = y.y, sn[e + 2] = y.z, sn[e + 3] = y.w;
+    for (int e = 0; e < H; e += 2) {
+      const float4 x = ld_shared_v4(c + 8 * e), y = ld_shared_v4(c + 4 * TURNS + 8 * e);
+      cs[e] = pair_of(x.x, x.y), cs[e + 1] = pair_of(x.z, x.w);
+      sn[e] = pair_of(y.x, y.y), sn[e + 1] = pair_of(y.z, y.w);
+    }
+  }
+  __device__ __forceinline__ void turn(const float* turns, int tok, float (&cs)[N], float (&sn)[N]) const {
+    uint64_t c[H], s[H];
+    turn(turns, tok, c, s);
+#pragma unroll
+    for (int e = 0; e < H; ++e) {
+      pair_split(c[e], cs[2 * e], cs[2 * e + 1]);
+      pair_split(s[e], sn[2 * e], sn[2 * e + 1]);
     }
   }
   __device__ __forceinline__ void weights(const float* w, float (&w0)[N], float (&w1)[N]) const {
+    uint64_t a[H], b[H];
+    weights(w, a, b);
 #pragma unroll
-    for (int e = 0; e < N; e += 4) {
+    for (int e = 0; e < H; ++e) {
+      pair_split(a[e], w0[2 * e], w0[2 * e + 1]);
+      pair_split(b[e], w1[2 * e], w1[2 * e + 1]);
+    }
+  }
+  __device__ __forceinline__ void weights(const float* w, uint64_t (&w0)[H], uint64_t (&w1)[H]) const {
+#pragma unroll
+    for (int e = 0; e < H; e += 2) {
       float4 x = make_float4(1.f, 1.f, 1.f, 1.f), y = x;
       if (w) {
-        x = ld_live(reinterpret_cast<const float4*>(w + c0 * N + e));
-        y = ld_live(reinterpret_cast<const float4*>(w + c1 * N + e));
+        x = ld_live(reinterpret_cast<const float4*>(w + c0 * N + 2 * e));
+        y = ld_live(reinterpret_cast<const float4*>(w + c1 * N + 2 * e));
       }
-      w0[e] = x.x, w0[e + 1] = x.y, w0[e + 2] = x.z, w0[e + 3] = x.w;
-      w1[e] = y.x, w1[e + 1] = y.y, w1[e + 2] = y.z, w1[e + 3] = y.w;
+      w0[e] = pair_of(x.x, x.y), w0[e + 1] = pair_of(x.z, x.w);
+      w1[e] = pair_of(y.x, y.y), w1[e + 1] = pair_of(y.z, y.w);
     }
   }
 };
@@ -95,67 +117,93 @@ __device__ __forceinline__ float group_sum(float x) {
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kHeadThreads, 2)
+__global__ void __launch_bounds__(kHeadThreads, kFwdCtas)
     qk_norm_rotate_kernel(const __grid_constant__ HeadsArgs a, HeadSplit hs) {
   using L = HeadLane<T, D>;
-  constexpr int N = L::N, CH = D / N;
-  constexpr int AHEAD = 4;   // heads requested at once
+  constexpr int N = L::N, H = L::H, CH = D / N;
+  constexpr int AHEAD = 2;   // heads on their way (4 and two CTAs an SM: 211 us against 208 for 131072 tokens)
   extern __shared__ __align__(16) float turns[];   // [2][TURNS], as far as tokens fill it
   chain_wait();
   chain_release();
-  const int64_t t0 = (int64_t)blockIdx.x * hs.tokens;
-  const int group = threadIdx.x / L::UN, tok = group / hs.slices, slice = group % hs.slices;
-  const int64_t t = t0 + tok;
-  const bool live = t < a.n_tokens;   // all lanes stay for the shuffles
-  const int64_t tt = live ? t : t0;
   const L l(a);
-  const int heads = a.Hq + (a.k != nullptr);
-  const uint4* q = static_cast<const uint4*>(a.q) + tt * (a.q_stride / N);
-  const uint4* k = static_cast<const uint4*>(a.k) + tt * (a.k_stride / N);
-  uint4* qo = static_cast<uint4*>(a.q_out) + tt * a.Hq * CH;
-  uint4* ko = static_cast<uint4*>(a.k_out) + tt * CH;
-  uint4 x[AHEAD], y[AHEAD];
-  auto load = [&](int i, int h) {
-    if (h < heads) {   // q_out may be q: a lane reads its own chunks before it writes them
-      const uint4* p = h < a.Hq ? q + h * CH : k;
+  const int group = threadIdx.x / L::UN, tok = group / hs.slices, slice = group % hs.slices;
+  const bool keys = a.k != nullptr && group < hs.tokens;   // this group takes the key of the block's token `group`
+  const int64_t stride = (int64_t)gridDim.x * hs.tokens;
+  uint4 x[AHEAD], y[AHEAD], kx, ky;
+  // head h of this group's token of the block at `base`
+  auto load = [&](int i, int64_t base, int h) {
+    const int64_t t = base + tok;
+    if (t < a.n_tokens && h < a.Hq) {   // q_out may be q: a lane reads its own chunks before it writes them
+      const uint4* p = static_cast<const uint4*>(a.q) + t * (a.q_stride / N) + h * CH;
       x[i] = ld_live(p + l.c0);
       y[i] = ld_live(p + l.c1);
     }
   };
+  auto load_key = [&](int64_t base) {
+    if (keys && base + group < a.n_tokens) {
+      const uint4* p = static_cast<const uint4*>(a.k) + (base + group) * (a.k_stride / N);
+      kx = ld_live(p + l.c0);
+      ky = ld_live(p + l.c1);
+    }
+  };
+  // a head's chunks, with weights w0, w1 and the turns of the block's token i, to dst
+  auto finish = [&](uint64_t (&u)[H], uint64_t (&v)[H], const uint64_t (&w0)[H], const uint64_t (&w1)[H], int i, uint4* dst,
+                    bool there) {
+    uint64_t ss = pair_of(0.f, 0.f);
 #pragma unroll
-  for (int i = 0; i < AHEAD; ++i) load(i, slice + i * hs.slices);
-  float cs[N], sn[N], w0[N], w1[N];
-  if (a.rot.dim) {
-    form_turns<L::PAIRS, L::TURNS>(a, t0, hs.tokens, false, turns);
-    __syncthreads();
-    if (l.rotated) l.turn(turns, tok, cs, sn);
-  }
-  l.weights(slice < a.Hq ? a.q_weight : a.k_weight, w0, w1);
-  // all groups make the same rounds, for the shuffles
-  for (int h0 = 0; h0 < heads; h0 += AHEAD * hs.slices) {
+    for (int e = 0; e < H; ++e) ss = fma2(u[e], u[e], fma2(v[e], v[e], ss));
+    const float r1 = rsqrtf(group_sum<L::UN>(pair_sum(ss)) * (1.f / D) + a.eps);
+    const uint64_t r = pair_of(r1, r1);
 #pragma unroll
-    for (int i = 0; i < AHEAD; ++i) {
-      const int h = h0 + i * hs.slices + slice;
-      if (h0 + i * hs.slices >= heads) break;
-      if (h == a.Hq && h != slice) l.weights(a.k_weight, w0, w1);
-      float u[N], v[N], ss = 0.f;
-      unpack16<T>(x[i], u);
-      unpack16<T>(y[i], v);
-      load(i, h + AHEAD * hs.slices);
+    for (int e = 0; e < H; ++e) {
+      u[e] = mul2(mul2(u[e], r), w0[e]);
+      v[e] = mul2(mul2(v[e], r), w1[e]);
+    }
+    if (l.rotated) {   // read again for every head: that leaves registers for the rows on their way
+      uint64_t cs[H], sn[H];
+      l.turn(turns, i, cs, sn);
+      rotate_pairs<N>(u, v, cs, sn, l.inter);
+    }
+    if (there) {
+      dst[l.c0] = pack_pairs<T>(u);
+      dst[l.c1] = pack_pairs<T>(v);
+    }
+  };
+  int64_t base = (int64_t)blockIdx.x * hs.tokens;
 #pragma unroll
-      for (int e = 0; e < N; ++e) ss = fmaf(u[e], u[e], fmaf(v[e], v[e], ss));
-      const float r = rsqrtf(group_sum<L::UN>(ss) * (1.f / D) + a.eps);
+  for (int i = 0; i < AHEAD; ++i) load(i, base, slice + i * hs.slices);
+  load_key(base);
+  uint64_t w0[H], w1[H];
+  l.weights(a.Hq ? a.q_weight : a.k_weight, w0, w1);
+  for (; base < a.n_tokens; base += stride) {
+    const int64_t t = base + tok;
+    if (a.rot.dim) {
+      __syncthreads();   // the turns of the block before
+      form_turns<L::PAIRS, L::TURNS>(a, base, hs.tokens, false, turns);
+      __syncthreads();
+    }
+    // all groups make the same rounds, for the shuffles
+    for (int h0 = 0; h0 < a.Hq; h0 += AHEAD * hs.slices) {
+      const bool last = h0 + AHEAD * hs.slices >= a.Hq;
 #pragma unroll
-      for (int e = 0; e < N; ++e) {
-        u[e] = u[e] * r * w0[e];
-        v[e] = v[e] * r * w1[e];
+      for (int i = 0; i < AHEAD; ++i) {
+        const int h = h0 + i * hs.slices + slice;
+        uint64_t u[H], v[H];
+        unpack_pairs<T>(x[i], u);
+        unpack_pairs<T>(y[i], v);
+        load(i, last ? base + stride : base, last ? slice + i * hs.slices : h + AHEAD * hs.slices);
+        if (h0 + i * hs.slices < a.Hq)
+          finish(u, v, w0, w1, tok, static_cast<uint4*>(a.q_out) + (t * a.Hq + h) * CH, t < a.n_tokens && h < a.Hq);
       }
-      if (l.rotated) rotate_values<N>(u, v, cs, sn, l.inter);
-      if (live && h < heads) {
-        uint4* p = h < a.Hq ? qo + h * CH : ko;
-        p[l.c0] = pack16<T>(u);
-        p[l.c1] = pack16<T>(v);
-      }
+    }
+    if (a.k != nullptr && __any_sync(0xffffffffu, keys)) {
+      uint64_t u[H], v[H], k0[H], k1[H];
+      unpack_pairs<T>(kx, u);
+      unpack_pairs<T>(ky, v);
+      load_key(base + stride);
+      l.weights(a.k_weight, k0, k1);
+      const int64_t tk = base + group;
+      finish(u, v, k0, k1, keys ? group : 0, static_cast<uint4*>(a.k_out) + tk * CH, keys && tk < a.n_tokens);
     }
   }
 }
@@ -185,7 +233,7 @@ __global__ void __launch_bounds__(kHeadThreads, 2)
   chain_release();
   const L l(a);
   const int group = threadIdx.x / L::UN, tok = group / hs.slices, slice = group % hs.slices;
-  const int heads = a.Hq + (a.k != nullptr);
+  const bool keys = a.k != nullptr && group < hs.tokens;   // this group takes the key of the block's token `group`
   float w0[N], w1[N], dq0[N], dq1[N], dk0[N], dk1[N];   // d..: this lane's channels of the weights' gradients
 #pragma unroll
   for (int e = 0; e < N; ++e) dq0[e] = dq1[e] = dk0[e] = dk1[e] = 0.f;
@@ -194,89 +242,101 @@ __global__ void __launch_bounds__(kHeadThreads, 2)
     float g0[N], g1[N];
   };
   Row next;
-  // head h of token t; nothing for h >= heads
-  auto load = [&](Row& r, int64_t t, int h) {
-    if (h >= heads) return;
-    const bool is_q = h < a.Hq;
-    const uint4* p = is_q ? static_cast<const uint4*>(a.q) + t * (a.q_stride / N) + h * CH
-                          : static_cast<const uint4*>(a.k) + t * (a.k_stride / N);
-    const float* gy = is_q ? a.dq_out + (t * a.Hq + h) * D : a.dk_out + t * D;
-    r.x = ld_live(p + l.c0);
-    r.y = ld_live(p + l.c1);
-    load_row<N>(gy + l.c0 * N, r.g0);   // dq may be dq_out: a lane reads its own channels before it writes them
-    load_row<N>(gy + l.c1 * N, r.g1);
+  auto load_from = [&](const uint4* p, const float* gy) {
+    next.x = ld_live(p + l.c0);
+    next.y = ld_live(p + l.c1);
+    load_row<N>(gy + l.c0 * N, next.g0);   // dq may be dq_out: a lane reads its own channels before it writes them
+    load_row<N>(gy + l.c1 * N, next.g1);
+  };
+  // head h of this group's token of the block at `base`; the key of its token `group`
+  auto load = [&](int64_t base, int h) {
+    const int64_t t = base + tok;
+    if (t < a.n_tokens && h < a.Hq)
+      load_from(static_cast<const uint4*>(a.q) + t * (a.q_stride / N) + h * CH, a.dq_out + (t * a.Hq + h) * D);
+  };
+  auto load_key = [&](int64_t base) {
+    if (keys && base + group < a.n_tokens)
+      load_from(static_cast<const uint4*>(a.k) + (base + group) * (a.k_stride / N), a.dk_out + (base + group) * D);
+  };
+  // row `now`, of the block's token i: its gradient to gx, its part of the weight's to d0, d1
+  auto finish = [&](const Row& now, int i, float* gx, bool there, float (&d0)[N], float (&d1)[N]) {
+    float u[N], v[N], g0[N], g1[N];
+    unpack16<T>(now.x, u);
+    unpack16<T>(now.y, v);
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      g0[e] = now.g0[e];
+      g1[e] = now.g1[e];
+    }
+    float ss = 0.f;
+#pragma unroll
+    for (int e = 0; e < N; ++e) ss = fmaf(u[e], u[e], fmaf(v[e], v[e], ss));
+    const float r = rsqrtf(group_sum<L::UN>(ss) * (1.f / D) + a.eps);
+    if (l.rotated) {   // read again for every head: held, they would not leave registers for the next head's rows
+      float cs[N], sn[N];
+      l.turn(turns, i, cs, sn);
+      rotate_values<N>(g0, g1, cs, sn, l.inter);
+    }
+    float dot = 0.f;
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      u[e] *= r;
+      v[e] *= r;
+      if (there) {
+        d0[e] = fmaf(g0[e], u[e], d0[e]);
+        d1[e] = fmaf(g1[e], v[e], d1[e]);
+      }
+      g0[e] *= w0[e];
+      g1[e] *= w1[e];
+      dot = fmaf(g0[e], u[e], fmaf(g1[e], v[e], dot));
+    }
+    const float m = group_sum<L::UN>(dot) * (1.f / D);
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      g0[e] = r * (g0[e] - u[e] * m);
+      g1[e] = r * (g1[e] - v[e] * m);
+    }
+    if (there) {
+      store_row<N>(gx + l.c0 * N, g0);
+      store_row<N>(gx + l.c1 * N, g1);
+    }
   };
   const int64_t stride = (int64_t)gridDim.x * hs.tokens;
-  auto own = [&](int64_t base) { return base + tok < a.n_tokens ? base + tok : base; };
-  bool is_key = false;
-  l.weights(slice < a.Hq ? a.q_weight : a.k_weight, w0, w1);
-  if (slice >= a.Hq) is_key = true;
-  // all groups make the same rounds, for the shuffles
   int64_t base = (int64_t)blockIdx.x * hs.tokens;
-  if (base < a.n_tokens) load(next, own(base), slice);
+  const bool warp_keys = a.k != nullptr && __any_sync(0xffffffffu, keys);
+  l.weights(a.q_weight, w0, w1);
+  if (a.Hq)
+    load(base, slice);
+  else
+    load_key(base);
   for (; base < a.n_tokens; base += stride) {
-    const bool live = base + tok < a.n_tokens;
-    const int64_t t = own(base);
+    const int64_t t = base + tok, tk = base + group;
     if (a.rot.dim) {
       __syncthreads();   // the turns of the block before
       form_turns<L::PAIRS, L::TURNS>(a, base, hs.tokens, true, turns);
       __syncthreads();
     }
-    for (int h0 = 0; h0 < heads; h0 += hs.slices) {
+    // all groups of a warp make the same rounds, for the shuffles
+    for (int h0 = 0; h0 < a.Hq; h0 += hs.slices) {
       const int h = h0 + slice;
-      const bool is_q = h < a.Hq, there = live && h < heads;
-      if (is_key == is_q && h < heads) {   // the last head's weights, or back to the others'
-        is_key = !is_q;
-        l.weights(is_q ? a.q_weight : a.k_weight, w0, w1);
-      }
-      float u[N], v[N], g0[N], g1[N];
-      unpack16<T>(next.x, u);
-      unpack16<T>(next.y, v);
-#pragma unroll
-      for (int e = 0; e < N; ++e) {
-        g0[e] = next.g0[e];
-        g1[e] = next.g1[e];
-      }
-      if (h0 + hs.slices < heads)
-        load(next, t, h + hs.slices);
-      else if (base + stride < a.n_tokens)
-        load(next, own(base + stride), slice);
-      float ss = 0.f;
-#pragma unroll
-      for (int e = 0; e < N; ++e) ss = fmaf(u[e], u[e], fmaf(v[e], v[e], ss));
-      const float r = rsqrtf(group_sum<L::UN>(ss) * (1.f / D) + a.eps);
-      if (l.rotated) {   // read again for every head: held, they would not leave registers for the next head's rows
-        float cs[N], sn[N];
-        l.turn(turns, tok, cs, sn);
-        rotate_values<N>(g0, g1, cs, sn, l.inter);
-      }
-      float dot = 0.f;
-#pragma unroll
-      for (int e = 0; e < N; ++e) {
-        u[e] *= r;
-        v[e] *= r;
-        if (there && is_q) {
-          dq0[e] = fmaf(g0[e], u[e], dq0[e]);
-          dq1[e] = fmaf(g1[e], v[e], dq1[e]);
-        } else if (there) {
-          dk0[e] = fmaf(g0[e], u[e], dk0[e]);
-          dk1[e] = fmaf(g1[e], v[e], dk1[e]);
-        }
-        g0[e] *= w0[e];
-        g1[e] *= w1[e];
-        dot = fmaf(g0[e], u[e], fmaf(g1[e], v[e], dot));
-      }
-      const float m = group_sum<L::UN>(dot) * (1.f / D);
-#pragma unroll
-      for (int e = 0; e < N; ++e) {
-        g0[e] = r * (g0[e] - u[e] * m);
-        g1[e] = r * (g1[e] - v[e] * m);
-      }
-      if (there) {
-        float* gx = is_q ? a.dq + (t * a.Hq + h) * D : a.dk + t * D;
-        store_row<N>(gx + l.c0 * N, g0);
-        store_row<N>(gx + l.c1 * N, g1);
-      }
+      const Row now = next;
+      if (h0 + hs.slices < a.Hq)
+        load(base, h + hs.slices);
+      else if (warp_keys)
+        load_key(base);
+      else
+        load(base + stride, slice);
+      finish(now, tok, a.dq + (t * a.Hq + h) * D, t < a.n_tokens && h < a.Hq, dq0, dq1);
+    }
+    if (warp_keys) {
+      const Row now = next;
+      if (a.Hq)
+        load(base + stride, slice);
+      else
+        load_key(base + stride);
+      l.weights(a.k_weight, w0, w1);
+      finish(now, keys ? group : 0, a.dk + tk * D, keys && tk < a.n_tokens, dk0, dk1);
+      if (a.Hq) l.weights(a.q_weight, w0, w1);
     }
   }
   static_assert(2 * L::TURNS >= L::GROUPS * D, "the sums fit in the turns' place");
@@ -326,14 +386,13 @@ __global__ void __launch_bounds__(kWeightThreads) weight_grad_kernel(const float
   }
 }
 
-// Slices: a power of two, so that a group has no more than `most` heads, and more
-// while there are not CTAs enough for the SMs.
+// Slices of the query heads: a power of two, so that a group has no more than 4,
+// and more while there are not CTAs enough for the SMs.
 template <typename L>
-static HeadSplit head_split(const HeadsArgs& a, int most) {
-  const int heads = a.Hq + (a.k != nullptr);
+static HeadSplit head_split(const HeadsArgs& a) {
   int slices = 1;
-  while (slices < L::GROUPS &&
-         (slices * most < heads || (slices < heads && a.n_tokens * slices < (int64_t)2 * kHeadSms * L::GROUPS)))
+  while (slices < L::GROUPS && slices < a.Hq &&
+         (slices * 4 < a.Hq || a.n_tokens * slices < (int64_t)2 * kHeadSms * L::GROUPS))
     slices *= 2;
   return {L::GROUPS / slices, slices};
 }
@@ -341,9 +400,9 @@ static HeadSplit head_split(const HeadsArgs& a, int most) {
 template <typename T, int D>
 static cudaError_t launch_fwd(const HeadsArgs& a, cudaStream_t s) {
   using L = HeadLane<T, D>;
-  const HeadSplit hs = head_split<L>(a, 6);
-  return launch_chained(qk_norm_rotate_kernel<T, D>, dim3((unsigned)((a.n_tokens + hs.tokens - 1) / hs.tokens)),
-                        dim3(kHeadThreads), a.rot.dim ? 2 * L::TURNS * sizeof(float) : 0, s, a, hs);
+  const HeadSplit hs = head_split<L>(a);
+  const int64_t x = (a.n_tokens + hs.tokens - 1) / hs.tokens, most = kFwdCtas * kHeadSms;
+  return launch_chained(qk_norm_rotate_kernel<T, D>, dim3((unsigned)(x < most ? x : most)), dim3(kHeadThreads), a.rot.dim ? 2 * L::TURNS * sizeof(float) : 0, s, a, hs);
 }
 
 template <typename T, int D>
@@ -351,7 +410,7 @@ static cudaError_t launch_bwd(const HeadsArgs& a, cudaStream_t s) {
   using L = HeadLane<T, D>;
   unsigned ctas = 0;
   if (a.n_tokens > 0) {
-    const HeadSplit hs = head_split<L>(a, 6);
+    const HeadSplit hs = head_split<L>(a);
     const int64_t x = (a.n_tokens + hs.tokens - 1) / hs.tokens;
     ctas = (unsigned)(x < kGradCtas ? x : kGradCtas);
     const cudaError_t e = launch_chained(qk_norm_rotate_bwd_kernel<T, D>, dim3(ctas), dim3(kHeadThreads),

@@ -45,6 +45,7 @@
 
 #include "decode_tree.cuh"
 #include "decode_tree_tc.h"
+#include "packed.cuh"
 
 namespace dsa {
 
@@ -330,43 +331,23 @@ struct TcWalk {
 };
 
 // ------------------------------------------------------------------- a unit's softmax
-// Two fp32 values in one operand of the packed instructions.
-__device__ __forceinline__ uint64_t tc_pair(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ void tc_unpair(uint64_t r, float& a, float& b) {
-  asm("mov.b64 {%0, %1}, %2;\n" : "=f"(a), "=f"(b) : "l"(r));
-}
-__device__ __forceinline__ uint64_t tc_fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t tc_add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-
 // 32 scores x of a row to p = 2^(x c - base), as 16 words of bf16 hi terms and 16
 // of lo; adds p to the sums.  The product is fused with the base: where that is
 // large, tc_unit_any rounds the product first.
 constexpr float kTcSmallBase = 65536.f;   // below, the fused product's own rounding moves a weight by 2^-8 at most
 __device__ __forceinline__ void tc_weights(const float (&x)[32], uint64_t sl2, uint64_t base, uint64_t& sum, uint32_t (&y)[32]) {
-  const uint64_t minus1 = tc_pair(-1.f, -1.f);
+  const uint64_t minus1 = pair_of(-1.f, -1.f);
 #pragma unroll
   for (int e = 0; e < 32; e += 2) {
     float p0, p1;
-    tc_unpair(tc_fma2(tc_pair(x[e], x[e + 1]), sl2, base), p0, p1);
+    pair_split(fma2(pair_of(x[e], x[e + 1]), sl2, base), p0, p1);
     p0 = ex2_approx(p0);
     p1 = ex2_approx(p1);
-    const uint64_t p = tc_pair(p0, p1);
-    sum = tc_add2(sum, p);
+    const uint64_t p = pair_of(p0, p1);
+    sum = add2(sum, p);
     const uint32_t hi = pack_bf16(p0, p1);
     float l0, l1;
-    tc_unpair(tc_fma2(tc_pair(__uint_as_float(hi << 16), __uint_as_float(hi & 0xFFFF0000u)), minus1, p), l0, l1);
+    pair_split(fma2(pair_of(__uint_as_float(hi << 16), __uint_as_float(hi & 0xFFFF0000u)), minus1, p), l0, l1);
     y[e / 2] = hi;
     y[16 + e / 2] = pack_bf16(l0, l1);
   }
@@ -418,8 +399,8 @@ __device__ __forceinline__ bool tc_unit(uint32_t tS, uint32_t tO, float sl2, boo
   const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
   if (__any_sync(0xffffffffu, !(fabsf(fmaxf(mx * sl2, m)) < kTcSmallBase))) return false;   // tc_unit_any
   tc_move_base<D>(mx, tO, sl2, begun, m, top, l);
-  const uint64_t sl22 = tc_pair(sl2, sl2), base = tc_pair(-m, -m);
-  uint64_t sum = tc_pair(0.f, 0.f);
+  const uint64_t sl22 = pair_of(sl2, sl2), base = pair_of(-m, -m);
+  uint64_t sum = pair_of(0.f, 0.f);
   float x[32], z[32];
   tc_ld32(tS, x);
 #pragma unroll 1
@@ -436,7 +417,7 @@ __device__ __forceinline__ bool tc_unit(uint32_t tS, uint32_t tO, float sl2, boo
     half_done(c >> 6);
   }
   float s0, s1;
-  tc_unpair(sum, s0, s1);
+  pair_split(sum, s0, s1);
   l += s0 + s1;
   return true;
 }

@@ -4,7 +4,7 @@
 // interleaved, two neighbouring chunks, whose pairs are its N in order.
 #pragma once
 
-#include "vec16.cuh"
+#include "packed.cuh"
 
 namespace dsa {
 
@@ -34,6 +34,32 @@ __device__ __forceinline__ void rotate_values(float* a, float* b, const float* c
       a[2 * e + 1] = x * sn[e] + y * cs[e];
       b[2 * e] = z * cs[N / 2 + e] - w * sn[N / 2 + e];
       b[2 * e + 1] = z * sn[N / 2 + e] + w * cs[N / 2 + e];
+    }
+  }
+}
+// The same of pairs of neighbouring values.
+template <int N>
+__device__ __forceinline__ void rotate_pairs(uint64_t* a, uint64_t* b, const uint64_t* cs, const uint64_t* sn, bool interleaved) {
+  if (!interleaved) {
+    const uint64_t minus1 = pair_of(-1.f, -1.f);
+#pragma unroll
+    for (int e = 0; e < N / 2; ++e) {
+      const uint64_t x = a[e], y = b[e];
+      a[e] = fma2(x, cs[e], mul2(mul2(y, minus1), sn[e]));
+      b[e] = fma2(y, cs[e], mul2(x, sn[e]));
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < N / 2; ++e) {
+      float c[2], s[2], x, y;
+      pair_split(cs[e], c[0], c[1]);   // of values 2 e and 2 e + 1 of the lane's N pairs
+      pair_split(sn[e], s[0], s[1]);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint64_t& p = 2 * e + h < N / 2 ? a[2 * e + h] : b[2 * e + h - N / 2];
+        pair_split(p, x, y);
+        p = pair_of(x * c[h] - y * s[h], x * s[h] + y * c[h]);
+      }
     }
   }
 }
