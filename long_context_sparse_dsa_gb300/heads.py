@@ -11,44 +11,48 @@ import long_context_sparse_dsa_gb300 as _dsa
 from long_context_sparse_dsa_gb300 import decode as _dec
 
 
-def _fail(func, name, t, want):
-    got = type(t).__name__ if not hasattr(t, "stride") else f"{t.dtype}, {tuple(t.shape)}, strides {t.stride()}, {t.device}"
-    raise ValueError(f"{func}: {name} must be {want} (got {got})")
+def _refuse(func, dims, *specs):
+    """Raise for the first of `specs` (name, tensor, dtype, shape, rows) that is not what the call takes; rows: any distance
+    between tokens will do."""
+    dev = _dec.torch.cuda.current_device()
+    for name, t, dtype, shape, rows in specs:
+        if t is None:
+            continue
+        if not hasattr(t, "get_device") or t.get_device() != dev:
+            raise ValueError(f"{func}: {name} must be a tensor on the current device, cuda:{dev} (got {getattr(t, 'device', type(t))})")
+        if t.dtype is not dtype or t.shape != shape or not (t.is_contiguous() or rows and len(t) and t[0].is_contiguous()):
+            raise ValueError(f"{func}: {name} must be a {dtype} of shape {shape}, {'its tokens' if rows else 'all'} contiguous "
+                             f"(got {t.dtype}, {tuple(t.shape)}, strides {t.stride()})")
+    raise ValueError(f"{func}: unusable arguments")
 
 
-def _need(func, dev, *specs):
-    """Raise for the first of `specs` (name, tensor or None, dtype, shape) that is not contiguous, of that type, shape, device."""
-    for name, t, dtype, shape in specs:
-        if t is not None and not (t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous()):
-            _fail(func, name, t, f"a contiguous {dtype} of shape {shape} on cuda:{dev}")
-
-
-def _device(func, t):
-    dev = t.get_device()
-    if dev < 0 or dev != _dec.torch.cuda.current_device():
-        raise ValueError(f"{func}: the tensors must be on the current CUDA device (got {t.device})")
-    return dev
+def _rows(t, n, dt, shape, row, dev):
+    """(fits, distance between tokens) of q or k: the heads of a token are contiguous, tokens any distance apart."""
+    if t.dtype is not dt or t.shape != shape or t.get_device() != dev:
+        return False, 0
+    if t.is_contiguous():
+        return True, row
+    st = t.stride()
+    return st[-1] == 1 and (len(st) == 2 or st[1] == shape[2] or shape[1] == 1), st[0]
 
 
 def _heads(func, dims, q, k):
-    """(device, tokens, q's stride, k's): the heads of a token are contiguous, tokens any distance apart."""
+    """(device, tokens, layer dtype, fits, q's distance, k's)"""
     first = q if q is not None else k
     if first is None:
         raise ValueError(f"{func}: neither q nor k is given")
     _dec._need_torch()
-    dev, n, dt = _device(func, first), first.shape[0], _dec._DTYPES[dims.dtype]
-    strides = []
-    for name, t, shape in (("q", q, (n, dims.Hq, dims.d)), ("k", k, (n, dims.d))):
-        if t is None:
-            strides.append(0)
-            continue
-        inner = (dims.d, 1) if t.dim() == 3 else (1,)
-        if not (t.dtype is dt and t.shape == shape and t.get_device() == dev and
-                (t.stride()[1:] == inner or n == 0 or name == "q" and dims.Hq == 1 and t.stride()[2] == 1)):
-            _fail(func, name, t, f"a {dt} of shape {shape} on cuda:{dev} whose rows are contiguous")
-        row = dims.Hq * dims.d if name == "q" else dims.d
-        strides.append(t.stride(0) if n > 1 else row)
-    return dev, n, strides[0], strides[1]
+    dev, n, dt, d = first.get_device(), first.shape[0], _dec._DTYPES[dims.dtype], dims.d
+    ok, qs, ks = dev == _dec.torch.cuda.current_device(), 0, 0
+    if q is not None and ok:
+        ok, qs = _rows(q, n, dt, (n, dims.Hq, d), dims.Hq * d, dev)
+    if k is not None and ok:
+        ok, ks = _rows(k, n, dt, (n, d), d, dev)
+    return dev, n, dt, ok, qs, ks
+
+
+def _is(t, dtype, shape, dev):
+    return t is None or t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous()
 
 
 def _p(t):
@@ -67,11 +71,13 @@ def qk_norm_rotate(dims, q, k, q_out, k_out, eps, q_weight=None, k_weight=None, 
     """q_out [T, Hq, d] and k_out [T, d] = the heads of q and k divided by their root mean square, times the weights [d]
     (fp32; None: 1), rotated to positions [T] int32 (None: token t is at t).  q and k may be slices of a wider tensor (any
     distance between tokens); either pair may be None.  The outputs may be q and k themselves where these are contiguous."""
-    dev, n, qs, ks = _heads("qk_norm_rotate", dims, q, k)
-    dt, f32 = _dec._DTYPES[dims.dtype], _dec.torch.float32
-    _need("qk_norm_rotate", dev, ("q_out", q_out, dt, (n, dims.Hq, dims.d)), ("k_out", k_out, dt, (n, dims.d)),
-          ("q_weight", q_weight, f32, (dims.d,)), ("k_weight", k_weight, f32, (dims.d,)),
-          ("positions", positions, _dec.torch.int32, (n,)))
+    dev, n, dt, ok, qs, ks = _heads("qk_norm_rotate", dims, q, k)
+    f32, i32, heads, row, w = _dec.torch.float32, _dec.torch.int32, (n, dims.Hq, dims.d), (n, dims.d), (dims.d,)
+    if not (ok and _is(q_out, dt, heads, dev) and _is(k_out, dt, row, dev) and _is(q_weight, f32, w, dev) and
+            _is(k_weight, f32, w, dev) and _is(positions, i32, (n,), dev)):
+        _refuse("qk_norm_rotate", dims, ("q", q, dt, heads, True), ("k", k, dt, row, True), ("q_out", q_out, dt, heads, False),
+                ("k_out", k_out, dt, row, False), ("q_weight", q_weight, f32, w, False), ("k_weight", k_weight, f32, w, False),
+                ("positions", positions, i32, (n,), False))
     if (q is None) != (q_out is None) or (k is None) != (k_out is None):
         raise ValueError("qk_norm_rotate: an input without its output, or the reverse")
     st = _dsa._load().dsa_qk_norm_rotate(
@@ -89,13 +95,18 @@ def qk_norm_rotate_bwd(dims, q, k, dq_out, dk_out, dq, dk, eps, ws, q_weight=Non
                        dk_weight=None, rotation=None, positions=None, stream=None):
     """Gradients of ``qk_norm_rotate``: dq, dk (fp32; may be dq_out, dk_out themselves) of its inputs q, k, and, where
     given, dq_weight, dk_weight [d] fp32 (written, not added to).  dq_out, dk_out: fp32, as ``layer_bwd`` leaves them."""
-    dev, n, qs, ks = _heads("qk_norm_rotate_bwd", dims, q, k)
-    f32 = _dec.torch.float32
-    heads, row = (n, dims.Hq, dims.d), (n, dims.d)
-    _need("qk_norm_rotate_bwd", dev, ("dq_out", dq_out, f32, heads), ("dk_out", dk_out, f32, row), ("dq", dq, f32, heads),
-          ("dk", dk, f32, row), ("q_weight", q_weight, f32, (dims.d,)), ("k_weight", k_weight, f32, (dims.d,)),
-          ("dq_weight", dq_weight, f32, (dims.d,)), ("dk_weight", dk_weight, f32, (dims.d,)),
-          ("positions", positions, _dec.torch.int32, (n,)), ("ws", ws, _dec.torch.uint8, ws.shape if ws is not None else None))
+    dev, n, dt, ok, qs, ks = _heads("qk_norm_rotate_bwd", dims, q, k)
+    f32, i32, heads, row, w = _dec.torch.float32, _dec.torch.int32, (n, dims.Hq, dims.d), (n, dims.d), (dims.d,)
+    if not (ok and _is(dq_out, f32, heads, dev) and _is(dk_out, f32, row, dev) and _is(dq, f32, heads, dev) and
+            _is(dk, f32, row, dev) and _is(q_weight, f32, w, dev) and _is(k_weight, f32, w, dev) and
+            _is(dq_weight, f32, w, dev) and _is(dk_weight, f32, w, dev) and _is(positions, i32, (n,), dev) and
+            (ws is None or ws.get_device() == dev and ws.is_contiguous())):
+        _refuse("qk_norm_rotate_bwd", dims, ("q", q, dt, heads, True), ("k", k, dt, row, True),
+                ("dq_out", dq_out, f32, heads, False), ("dk_out", dk_out, f32, row, False), ("dq", dq, f32, heads, False),
+                ("dk", dk, f32, row, False), ("q_weight", q_weight, f32, w, False), ("k_weight", k_weight, f32, w, False),
+                ("dq_weight", dq_weight, f32, w, False), ("dk_weight", dk_weight, f32, w, False),
+                ("positions", positions, i32, (n,), False), ("ws", ws, ws.dtype if ws is not None else None,
+                                                             ws.shape if ws is not None else None, False))
     if any((x is None) != (y is None) for x, y in ((q, dq_out), (q, dq), (k, dk_out), (k, dk))):
         raise ValueError("qk_norm_rotate_bwd: an input without its gradients, or the reverse")
     st = _dsa._load().dsa_qk_norm_rotate_bwd(

@@ -16,8 +16,8 @@ from long_context_sparse_dsa_gb300 import decode as _dec
 MAX_TREE_NODES = 128
 
 
-def _ok(t, dtype, shape, dev):
-    return t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous()
+# As in decode.py, the calls that a decoder makes for every step check their tensors in one plain condition and look for
+# what is wrong only when it fails.
 
 
 def _check_all(func, dims, cache, specs, ws=None):
@@ -25,7 +25,7 @@ def _check_all(func, dims, cache, specs, ws=None):
     dev = cache._device
     ok = _dec._cache_ok(dims, cache, _dec._DTYPES[dims.dtype])
     for _, t, dtype, shape in specs:
-        ok = ok and (t is None or _ok(t, dtype, shape, dev))
+        ok = ok and (t is None or t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous())
     if not ok or ws is not None and not (ws.get_device() == dev and ws.is_contiguous()):
         _dec._refuse(func, dims, cache, *specs, ("ws", ws, None, None))
 
@@ -62,13 +62,28 @@ def decode_tree_attn(dims, cache, lens, block_table, offsets, parents, q, k, v, 
     parents [T] int32: a node's parent within its row, -1 for the cached tokens' end (None: chains).  Node t attends to
     the row's tokens (or, with idx [T, k], to the pools named and the row's partial pool), its ancestors and itself.
     q [T, Hq, d], k, v [T, d] -> o [T, Hq, d], lse [T, Hq] fp32."""
-    i32, f32, batch, n = _dec.torch.int32, _dec.torch.float32, lens.numel(), q.shape[0]
-    dt, heads = _dec._DTYPES[dims.dtype], (n, dims.Hq, dims.d)
-    _check_all("decode_tree_attn", dims, cache, (
-        ("lens", lens, i32, (batch,)), ("block_table", block_table, i32, (batch, _cols(dims, cache))),
-        ("offsets", offsets, i32, (batch + 1,)), ("parents", parents, i32, (n,)), ("idx", idx, i32, (n, dims.k)),
-        ("q", q, dt, heads), ("k", k, dt, (n, dims.d)), ("v", v, dt, (n, dims.d)), ("o", o, dt, heads),
-        ("lse", lse, f32, heads[:2])), ws)
+    torch, dev, batch, n, d = _dec.torch, cache._device, lens.numel(), q.shape[0], dims.d
+    i32, dt, heads, cols = torch.int32, _dec._DTYPES[dims.dtype], (n, dims.Hq, d), -(-dims.L // cache.page_size)
+    if not (_dec._cache_ok(dims, cache, dt) and
+            lens.dtype is i32 and lens.shape == (batch,) and lens.get_device() == dev and lens.is_contiguous() and
+            block_table.dtype is i32 and block_table.shape == (batch, cols) and block_table.get_device() == dev and
+            block_table.is_contiguous() and
+            offsets.dtype is i32 and offsets.shape == (batch + 1,) and offsets.get_device() == dev and
+            offsets.is_contiguous() and
+            (parents is None or parents.dtype is i32 and parents.shape == (n,) and parents.get_device() == dev and
+             parents.is_contiguous()) and
+            (idx is None or idx.dtype is i32 and idx.shape == (n, dims.k) and idx.get_device() == dev and
+             idx.is_contiguous()) and
+            q.dtype is dt and q.shape == heads and q.get_device() == dev and q.is_contiguous() and
+            k.dtype is dt and k.shape == (n, d) and k.get_device() == dev and k.is_contiguous() and
+            v.dtype is dt and v.shape == (n, d) and v.get_device() == dev and v.is_contiguous() and
+            o.dtype is dt and o.shape == heads and o.get_device() == dev and o.is_contiguous() and
+            lse.dtype is torch.float32 and lse.shape == heads[:2] and lse.get_device() == dev and lse.is_contiguous() and
+            (ws is None or ws.get_device() == dev and ws.is_contiguous())):
+        _dec._refuse("decode_tree_attn", dims, cache, ("lens", lens, i32, (batch,)), ("block_table", block_table, i32, (batch, cols)),
+                     ("offsets", offsets, i32, (batch + 1,)), ("parents", parents, i32, (n,)), ("idx", idx, i32, (n, dims.k)),
+                     ("q", q, dt, heads), ("k", k, dt, (n, d)), ("v", v, dt, (n, d)), ("o", o, dt, heads),
+                     ("lse", lse, torch.float32, heads[:2]), ("ws", ws, None, None))
     pw, nw = _ws(ws)
     st = _dsa._load().dsa_decode_tree_attn(
         ctypes.byref(dims), cache._ref, batch, lens.data_ptr(), block_table.data_ptr(), n, offsets.data_ptr(), _p(parents),
@@ -82,13 +97,27 @@ def cache_commit(dims, cache, lens, block_table, offsets, parents, accepted, k, 
     """The path from the root to node accepted[b] ([batch] int32; -1: nothing) of each row's draft tree becomes the row's
     next tokens, from position lens[b] on: k, v [T, d] and k_idx [T, di] of its nodes enter the cache.  lens_out [batch]
     int32 (may be lens): the new lengths.  offsets, parents: as in ``decode_tree_attn``."""
-    i32, batch, n = _dec.torch.int32, lens.numel(), k.shape[0]
-    dt = _dec._DTYPES[dims.dtype]
-    _check_all("cache_commit", dims, cache, (
-        ("lens", lens, i32, (batch,)), ("block_table", block_table, i32, (batch, _cols(dims, cache))),
-        ("offsets", offsets, i32, (batch + 1,)), ("parents", parents, i32, (n,)), ("accepted", accepted, i32, (batch,)),
-        ("k", k, dt, (n, dims.d)), ("v", v, dt, (n, dims.d)), ("k_idx", k_idx, dt, (n, dims.di)),
-        ("lens_out", lens_out, i32, (batch,))))
+    i32, dev, batch, n, d = _dec.torch.int32, cache._device, lens.numel(), k.shape[0], dims.d
+    dt, cols = _dec._DTYPES[dims.dtype], -(-dims.L // cache.page_size)
+    if not (_dec._cache_ok(dims, cache, dt) and
+            lens.dtype is i32 and lens.shape == (batch,) and lens.get_device() == dev and lens.is_contiguous() and
+            block_table.dtype is i32 and block_table.shape == (batch, cols) and block_table.get_device() == dev and
+            block_table.is_contiguous() and
+            offsets.dtype is i32 and offsets.shape == (batch + 1,) and offsets.get_device() == dev and
+            offsets.is_contiguous() and
+            (parents is None or parents.dtype is i32 and parents.shape == (n,) and parents.get_device() == dev and
+             parents.is_contiguous()) and
+            accepted.dtype is i32 and accepted.shape == (batch,) and accepted.get_device() == dev and
+            accepted.is_contiguous() and
+            k.dtype is dt and k.shape == (n, d) and k.get_device() == dev and k.is_contiguous() and
+            v.dtype is dt and v.shape == (n, d) and v.get_device() == dev and v.is_contiguous() and
+            k_idx.dtype is dt and k_idx.shape == (n, dims.di) and k_idx.get_device() == dev and k_idx.is_contiguous() and
+            lens_out.dtype is i32 and lens_out.shape == (batch,) and lens_out.get_device() == dev and
+            lens_out.is_contiguous()):
+        _dec._refuse("cache_commit", dims, cache, ("lens", lens, i32, (batch,)), ("block_table", block_table, i32, (batch, cols)),
+                     ("offsets", offsets, i32, (batch + 1,)), ("parents", parents, i32, (n,)),
+                     ("accepted", accepted, i32, (batch,)), ("k", k, dt, (n, d)), ("v", v, dt, (n, d)),
+                     ("k_idx", k_idx, dt, (n, dims.di)), ("lens_out", lens_out, i32, (batch,)))
     st = _dsa._load().dsa_cache_commit(
         ctypes.byref(dims), cache._ref, batch, lens.data_ptr(), block_table.data_ptr(), n, offsets.data_ptr(), _p(parents),
         accepted.data_ptr(), k.data_ptr(), v.data_ptr(), k_idx.data_ptr(), lens_out.data_ptr(),
@@ -114,10 +143,19 @@ def cache_reserve(dims, cache, refs, lens, new_lens, block_table, missing, ws, s
     """Pages for rows to grow from lens [batch] to new_lens [batch] int32: free ones, ascending, into block_table, and a
     page of its own, with a copy, for a row whose next token would go to a page that others hold too.  Nothing is changed
     where missing [1] int32 comes back above 0: so many pages are wanting."""
-    i32, batch = _dec.torch.int32, lens.numel()
-    _check_all("cache_reserve", dims, cache, (
-        ("refs", refs, i32, (cache.pages,)), ("lens", lens, i32, (batch,)), ("new_lens", new_lens, i32, (batch,)),
-        ("block_table", block_table, i32, (batch, _cols(dims, cache))), ("missing", missing, i32, (1,))), ws)
+    i32, dev, batch, cols = _dec.torch.int32, cache._device, lens.numel(), -(-dims.L // cache.page_size)
+    if not (_dec._cache_ok(dims, cache, _dec._DTYPES[dims.dtype]) and
+            refs.dtype is i32 and refs.shape == (cache.pages,) and refs.get_device() == dev and refs.is_contiguous() and
+            lens.dtype is i32 and lens.shape == (batch,) and lens.get_device() == dev and lens.is_contiguous() and
+            new_lens.dtype is i32 and new_lens.shape == (batch,) and new_lens.get_device() == dev and
+            new_lens.is_contiguous() and
+            block_table.dtype is i32 and block_table.shape == (batch, cols) and block_table.get_device() == dev and
+            block_table.is_contiguous() and
+            missing.dtype is i32 and missing.shape == (1,) and missing.get_device() == dev and
+            (ws is None or ws.get_device() == dev and ws.is_contiguous())):
+        _dec._refuse("cache_reserve", dims, cache, ("refs", refs, i32, (cache.pages,)), ("lens", lens, i32, (batch,)),
+                     ("new_lens", new_lens, i32, (batch,)), ("block_table", block_table, i32, (batch, cols)),
+                     ("missing", missing, i32, (1,)), ("ws", ws, None, None))
     pw, nw = _ws(ws)
     st = _dsa._load().dsa_cache_reserve(
         ctypes.byref(dims), cache._ref, refs.data_ptr(), batch, lens.data_ptr(), new_lens.data_ptr(), block_table.data_ptr(),
@@ -128,11 +166,20 @@ def cache_reserve(dims, cache, refs, lens, new_lens, block_table, missing, ws, s
 
 def cache_fork(dims, cache, refs, lens, block_table, parents, lens_out, table_out, stream=None):
     """Row i of table_out, lens_out shares the pages of row parents[i] ([n_out] int32; -1: an empty row) of block_table, lens."""
-    i32, batch, n = _dec.torch.int32, lens.numel(), parents.numel()
-    cols = _cols(dims, cache)
-    _check_all("cache_fork", dims, cache, (
-        ("refs", refs, i32, (cache.pages,)), ("lens", lens, i32, (batch,)), ("block_table", block_table, i32, (batch, cols)),
-        ("parents", parents, i32, (n,)), ("lens_out", lens_out, i32, (n,)), ("table_out", table_out, i32, (n, cols))))
+    i32, dev, batch, n = _dec.torch.int32, cache._device, lens.numel(), parents.numel()
+    cols = -(-dims.L // cache.page_size)
+    if not (_dec._cache_ok(dims, cache, _dec._DTYPES[dims.dtype]) and
+            refs.dtype is i32 and refs.shape == (cache.pages,) and refs.get_device() == dev and refs.is_contiguous() and
+            lens.dtype is i32 and lens.shape == (batch,) and lens.get_device() == dev and lens.is_contiguous() and
+            block_table.dtype is i32 and block_table.shape == (batch, cols) and block_table.get_device() == dev and
+            block_table.is_contiguous() and
+            parents.dtype is i32 and parents.shape == (n,) and parents.get_device() == dev and parents.is_contiguous() and
+            lens_out.dtype is i32 and lens_out.shape == (n,) and lens_out.get_device() == dev and lens_out.is_contiguous() and
+            table_out.dtype is i32 and table_out.shape == (n, cols) and table_out.get_device() == dev and
+            table_out.is_contiguous()):
+        _dec._refuse("cache_fork", dims, cache, ("refs", refs, i32, (cache.pages,)), ("lens", lens, i32, (batch,)),
+                     ("block_table", block_table, i32, (batch, cols)), ("parents", parents, i32, (n,)),
+                     ("lens_out", lens_out, i32, (n,)), ("table_out", table_out, i32, (n, cols)))
     st = _dsa._load().dsa_cache_fork(
         ctypes.byref(dims), cache._ref, refs.data_ptr(), batch, lens.data_ptr(), block_table.data_ptr(), n,
         parents.data_ptr(), lens_out.data_ptr(), table_out.data_ptr(), _dec._raw_stream(stream, cache._device))
@@ -142,10 +189,16 @@ def cache_fork(dims, cache, refs, lens, block_table, parents, lens_out, table_ou
 
 def cache_release(dims, cache, refs, lens, block_table, keep=None, stream=None):
     """Rows give back the pages behind their first keep [batch] int32 tokens (None: all of them)."""
-    i32, batch = _dec.torch.int32, lens.numel()
-    _check_all("cache_release", dims, cache, (
-        ("refs", refs, i32, (cache.pages,)), ("lens", lens, i32, (batch,)), ("keep", keep, i32, (batch,)),
-        ("block_table", block_table, i32, (batch, _cols(dims, cache)))))
+    i32, dev, batch, cols = _dec.torch.int32, cache._device, lens.numel(), -(-dims.L // cache.page_size)
+    if not (_dec._cache_ok(dims, cache, _dec._DTYPES[dims.dtype]) and
+            refs.dtype is i32 and refs.shape == (cache.pages,) and refs.get_device() == dev and refs.is_contiguous() and
+            lens.dtype is i32 and lens.shape == (batch,) and lens.get_device() == dev and lens.is_contiguous() and
+            (keep is None or keep.dtype is i32 and keep.shape == (batch,) and keep.get_device() == dev and
+             keep.is_contiguous()) and
+            block_table.dtype is i32 and block_table.shape == (batch, cols) and block_table.get_device() == dev and
+            block_table.is_contiguous()):
+        _dec._refuse("cache_release", dims, cache, ("refs", refs, i32, (cache.pages,)), ("lens", lens, i32, (batch,)),
+                     ("keep", keep, i32, (batch,)), ("block_table", block_table, i32, (batch, cols)))
     st = _dsa._load().dsa_cache_release(
         ctypes.byref(dims), cache._ref, refs.data_ptr(), batch, lens.data_ptr(), _p(keep), block_table.data_ptr(),
         _dec._raw_stream(stream, cache._device))
