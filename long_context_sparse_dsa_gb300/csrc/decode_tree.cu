@@ -1,12 +1,12 @@
 // decode_tree.cu -- attention of drafted tokens over the paged cache and their
 // own branches (include/dsa_tree.h).
 //
-// A first kernel (decode_tree_nodes.cu) finds every node's row and ancestors.
-// Then, in this file, a node is a row of its own to the loops of decode_attn.cuh: a cluster of CTAs per node walks through the
-// selected pools (or all tokens) of its row and, as last steps, through its
-// branch, one ancestor per slot.  That is how selections are attended to, each
-// node having its own, and what fp32 layers use.  Nodes of a bf16 layer that
-// attend to whole caches share them by rows: decode_tree_tc.cu.
+// In this file a node is a row of its own to the loops of decode_attn.cuh: a
+// cluster of CTAs per node walks through the selected pools (or all tokens) of its
+// row and, as last steps, through its branch, one ancestor per slot.  That is how
+// selections are attended to, each node having its own, what fp32 layers use, and
+// short caches.  Nodes of a bf16 layer that attend to long caches share them by
+// rows: decode_tree_tc.cu.
 #include "decode_attn.cuh"
 #include "decode_tree.cuh"
 #include "decode_tree_tc.h"
@@ -18,47 +18,83 @@ template <typename T>
 struct TreeRowsArgs {
   AttnArgs<T> at;          // batch: nodes
   TreeView tv;
-  const TreeNode* nodes;
   const T *k, *v;          // [n_nodes][D]
   int64_t t0;              // the launch's first node
 };
 
+// Shared scratch, behind the loops' own.
+struct TreeScratch {
+  int row;                     // the node's, -1: none
+  int count;                   // ancestors, the node itself included
+  uint8_t up[kMaxTreeNodes];   // parents + 1
+  uint8_t list[kMaxTreeNodes]; // the ancestors, from the node to the root
+};
+
+// Node t's row, by all threads; -1 where it has none.
+__device__ __forceinline__ int find_row(const TreeView& tv, int64_t t, TreeScratch& ts) {
+  if (threadIdx.x == 0) ts.row = -1;
+  __syncthreads();
+  auto holds = [&](int64_t b) {
+    int64_t from;
+    int n;
+    return tree_row(tv, b, from, n) && from <= t && t < from + n;
+  };
+  if (tv.batch <= 4 * kAttnThreads) {   // a few loads at once; the offsets of a good batch name one row only
+    for (int64_t b = threadIdx.x; b < tv.batch; b += kAttnThreads)
+      if (holds(b)) atomicMax(&ts.row, (int)b);
+  } else if (threadIdx.x == 0) {
+    int64_t lo = 0, hi = tv.batch;   // offsets[lo] <= t < offsets[hi], if they ascend
+    while (hi - lo > 1) {
+      const int64_t mid = (lo + hi) >> 1;
+      if ((int64_t)ld_live(tv.offsets + mid) <= t)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    if (holds(lo)) ts.row = (int)lo;
+  }
+  __syncthreads();
+  return ts.row;
+}
+
 template <typename T, int D, int MAXH, bool SEL>
 __global__ void __launch_bounds__(kAttnThreads, (Piece<T, D, MAXH, SEL>::CTAS))
     decode_tree_rows_kernel(const __grid_constant__ TreeRowsArgs<T> a) {
+  static_assert(kAttnThreads == kMaxTreeNodes, "a thread per node");
   extern __shared__ __align__(128) unsigned char dec_smem[];
-  uint8_t* list = dec_smem + Piece<T, D, MAXH, SEL>::SMEM;
+  TreeScratch& ts = *reinterpret_cast<TreeScratch*>(dec_smem + Piece<T, D, MAXH, SEL>::SMEM);
   chain_wait();
   chain_release();
   const int64_t t = a.t0 + blockIdx.y;
-  TreeNode nd;
-  int64_t from;
-  if (!tree_node(a.tv, a.nodes, t, nd, from)) return;   // the whole cluster
+  if (t == 0 && blockIdx.x == 0) tree_check_rows(a.at.pv, a.tv);
+  const int b = find_row(a.tv, t, ts);
+  if (b < 0) return;   // the whole cluster
   bool bad_page = false, bad_idx = false;
   TreeRow<T> sr;
+  int64_t from;
+  int n;
+  tree_row(a.tv, b, from, n);
+  if ((int)threadIdx.x < n) ts.up[threadIdx.x] = (uint8_t)(tree_parent(a.tv, from, threadIdx.x, bad_idx) + 1);
   sr.idx = SEL ? a.at.idx + t * a.at.k : nullptr;
-  sr.trow = a.at.pv.table + (int64_t)nd.row * a.at.pv.cols;
+  sr.trow = a.at.pv.table + (int64_t)b * a.at.pv.cols;
   sr.k = a.at.k;
   {
-    bool bad_len = false;   // recorded by tree_nodes_kernel
-    sr.len = row_length(a.at.pv, nd.row, bad_len);
-  }
-  sr.first = SEL ? (a.at.k + 4) >> 2 : (int)(((int64_t)sr.len + 15) >> 4);
-  sr.count = nd.count;
-  sr.list = list;
-  sr.k_rows = a.k + from * D;
-  sr.v_rows = a.v + from * D;
-  {
-    const uint32_t m[4] = {nd.mask.x, nd.mask.y, nd.mask.z, nd.mask.w};
-    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    int at = __popc(m[w] & ((1u << lane) - 1u));
-#pragma unroll
-    for (int j = 0; j < 3; ++j)
-      if (j < w) at += __popc(m[j]);
-    if (m[w] >> lane & 1u) list[at] = (uint8_t)threadIdx.x;
+    bool bad_len = false;   // reported by tree_check_rows
+    sr.len = row_length(a.at.pv, b, bad_len);
   }
   __syncthreads();
-  attn_by_cluster<T, D, MAXH, SEL>(a.at, sr, t, sr.first + ((nd.count + 3) >> 2), dec_smem, bad_page, bad_idx);
+  if (threadIdx.x == 0) {
+    int count = 0;
+    for (int j = (int)(t - from); j >= 0; j = ts.up[j] - 1) ts.list[count++] = (uint8_t)j;   // parents come before
+    ts.count = count;
+  }
+  __syncthreads();
+  sr.first = SEL ? (a.at.k + 4) >> 2 : (int)(((int64_t)sr.len + 15) >> 4);
+  sr.count = ts.count;
+  sr.list = ts.list;
+  sr.k_rows = a.k + from * D;
+  sr.v_rows = a.v + from * D;
+  attn_by_cluster<T, D, MAXH, SEL>(a.at, sr, t, sr.first + ((sr.count + 3) >> 2), dec_smem, bad_page, bad_idx);
   if (bad_idx) record_error(DSA_DEV_ERR_BAD_INDEX);
   if (bad_page) record_error(DSA_DEV_ERR_BAD_PAGE);
 }
@@ -67,7 +103,7 @@ template <typename T, int D, int MAXH, bool SEL>
 static cudaError_t launch_rows(TreeRowsArgs<T>& a, cudaStream_t s) {
   using P = Piece<T, D, MAXH, SEL>;
   auto kern = decode_tree_rows_kernel<T, D, MAXH, SEL>;
-  constexpr int SMEM = P::SMEM + kMaxTreeNodes;
+  constexpr int SMEM = P::SMEM + (int)sizeof(TreeScratch);
   static KernelState st;
   int dev;
   cudaError_t e = prepare_kernel(kern, SMEM, kAttnThreads, st, dev);
@@ -88,7 +124,7 @@ static cudaError_t launch_shape(TreeRowsArgs<T>& a, cudaStream_t s) {
 }
 
 template <typename T>
-static cudaError_t launch_typed(const TreeAttnArgs& g, const TreeNode* nodes, cudaStream_t s) {
+static cudaError_t launch_typed(const TreeAttnArgs& g, cudaStream_t s) {
   TreeRowsArgs<T> a = {};
   a.at.pv = g.pv;
   a.at.batch = g.tree.n_nodes;
@@ -102,7 +138,6 @@ static cudaError_t launch_typed(const TreeAttnArgs& g, const TreeNode* nodes, cu
   a.at.k = g.k;
   a.at.scale_log2 = g.scale * 1.4426950408889634f;
   a.tv = g.tree;
-  a.nodes = nodes;
   a.k = static_cast<const T*>(g.nk);
   a.v = static_cast<const T*>(g.nv);
   if constexpr (sizeof(T) == 4)   // bf16 heads come in groups of 16
@@ -112,19 +147,35 @@ static cudaError_t launch_typed(const TreeAttnArgs& g, const TreeNode* nodes, cu
 }
 
 // ------------------------------------------------------------------- launches
-static size_t node_bytes(int64_t n) { return ((size_t)n * sizeof(TreeNode) + 255) & ~(size_t)255; }
-
 size_t tree_attn_ws_bytes(bool bf16, int Hq, int d, int64_t batch, int64_t n_nodes) {
-  return node_bytes(n_nodes) + (bf16 ? tree_tc_ws_bytes(d) : 256);
+  return bf16 ? tree_tc_ws_bytes(d) : 256;
+}
+
+// Whether whole bf16 caches are attended to by rows on the tensor cores or by
+// nodes.  Estimates in us from what the host knows, the rows' capacity in place of
+// their lengths, and the nodes spread evenly:
+//   nodes: 6 for the launch and the chains of loads, then a warp's step of 16 keys
+//          takes about 1 (16 heads) or 1.6 (32), with 8 warps an SM and no more
+//          than 64 a node
+//   rows:  13 for two launches, a first and a last tile, then a tile of 128 keys and
+//          up to 256 query rows takes about 2
+static bool by_tensor_rows(const TreeAttnArgs& a) {
+  constexpr double kStart = 13., kSms = 152.;
+  const double batch = (double)a.tree.batch, nodes = (double)a.tree.n_nodes, cap = (double)a.pv.capacity;
+  const double steps = nodes * (cap / 16. + 1.);
+  const double warps = 64. * nodes < 8. * kSms ? 64. * nodes : 8. * kSms;
+  const double by_nodes = 6. + steps * (a.Hq > 16 ? 1.6 : 1.) / warps;
+  double groups = batch;   // of 256 query rows
+  if (nodes * a.Hq > 256. * batch) groups = nodes * a.Hq / 256.;
+  if (nodes < batch) groups = nodes;
+  const double by_rows = kStart + groups * (cap / 128. + 1.) * 2. / kSms;
+  return by_rows < by_nodes;
 }
 
 cudaError_t launch_tree_attn(bool bf16, const TreeAttnArgs& a, cudaStream_t s) {
   if (a.tree.n_nodes == 0) return cudaSuccess;
-  TreeNode* nodes = static_cast<TreeNode*>(a.ws);
-  const cudaError_t e = launch_tree_nodes(a.pv, a.tree, nodes, s);
-  if (e != cudaSuccess) return e;
-  if (bf16 && a.idx == nullptr) return launch_tree_tc(a, nodes, static_cast<char*>(a.ws) + node_bytes(a.tree.n_nodes), s);
-  return bf16 ? launch_typed<__nv_bfloat16>(a, nodes, s) : launch_typed<float>(a, nodes, s);
+  if (bf16 && a.idx == nullptr && by_tensor_rows(a)) return launch_tree_tc(a, a.ws, s);
+  return bf16 ? launch_typed<__nv_bfloat16>(a, s) : launch_typed<float>(a, s);
 }
 
 }  // namespace dsa

@@ -1,4 +1,5 @@
-// decode_tree.cuh -- what the draft tree kernels know of a node.
+// decode_tree.cuh -- what the draft tree kernels share: rows of nodes and their
+// ancestors.
 #pragma once
 
 #include "decode.cuh"
@@ -6,24 +7,35 @@
 
 namespace dsa {
 
-struct alignas(16) TreeNode {
-  uint4 mask;     // its ancestors' numbers in the row, its own among them
-  int row;        // -1: of no row, or of a bad one
-  int count;      // bits of the mask
-  int pad[2];
-};
+// A row's nodes: [from, from + n); false where its offsets are bad.
+__device__ __forceinline__ bool tree_row(const TreeView& tv, int64_t b, int64_t& from, int& n) {
+  from = ld_live(tv.offsets + b);
+  const int64_t to = ld_live(tv.offsets + b + 1);
+  const bool good = from >= 0 && to >= from && to <= tv.n_nodes && to - from <= kMaxTreeNodes;
+  n = good ? (int)(to - from) : 0;
+  return good;
+}
 
-cudaError_t launch_tree_nodes(const PagedView& pv, const TreeView& tv, TreeNode* nodes, cudaStream_t s);
+// Node i's parent as the walks take it: -1 for a bad one.
+__device__ __forceinline__ int tree_parent(const TreeView& tv, int64_t from, int i, bool& bad) {
+  int p = tv.parents ? ld_live(tv.parents + from + i) : i - 1;
+  if (p < -1 || p >= i) {
+    bad = true;
+    p = -1;
+  }
+  return p;
+}
 
-// Node t and its row's first node; false where it has no row.  An entry is only
-// believed where the offsets say that its row's CTA has written it.
-__device__ __forceinline__ bool tree_node(const TreeView& tv, const TreeNode* nodes, int64_t t, TreeNode& nd,
-                                          int64_t& from) {
-  nd = ld_live(nodes + t);
-  if ((uint32_t)nd.row >= (uint32_t)tv.batch) return false;
-  from = ld_live(tv.offsets + nd.row);
-  return from >= 0 && from <= t && t < ld_live(tv.offsets + nd.row + 1) && t - from < kMaxTreeNodes &&
-         (uint32_t)(nd.count - 1) < (uint32_t)kMaxTreeNodes;
+// Reports rows with bad offsets or lengths; called by one CTA of a launch.
+__device__ __forceinline__ void tree_check_rows(const PagedView& pv, const TreeView& tv) {
+  bool bad = false;
+  for (int64_t b = threadIdx.x; b < tv.batch; b += blockDim.x) {
+    int64_t from;
+    int n;
+    if (!tree_row(tv, b, from, n)) bad = true;
+    row_length(pv, b, bad);
+  }
+  if (bad) record_error(DSA_DEV_ERR_BAD_PAGE);
 }
 
 }  // namespace dsa

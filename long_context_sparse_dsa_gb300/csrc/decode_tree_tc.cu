@@ -68,7 +68,6 @@ struct TcItem {
 struct TcArgs {
   PagedView pv;
   TreeView tv;
-  const TreeNode* nodes;
   const __nv_bfloat16 *Q, *K, *V, *nK, *nV;
   __nv_bfloat16* O;
   float* LSE;
@@ -90,7 +89,7 @@ struct TcCfg {
   static constexpr int OFF_BAR = OFF_KV + NS * TILE;
   static constexpr int NBAR = 2 * NS + 2 + 8 + 1;   // full, free; Q full, free; S, P's halves, PV of each accumulator; drain
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
-  static constexpr int MISC = 1536;
+  static constexpr int MISC = 1664;
   static constexpr int SMEM = OFF_MISC + MISC + 1024;   // + alignment slack
   static_assert(SMEM <= 227 * 1024, "shared memory per CTA");
   static constexpr uint32_t TMEM_COLS = 512;
@@ -106,6 +105,7 @@ struct TcMisc {
   int64_t scan[16];
   int64_t row, off, per, rest, begin;
   float2 xml[128];          // base and sum of the second accumulator's rows
+  uint8_t up[kMaxTreeNodes];   // parents + 1 of the segment's row
 };
 static_assert(sizeof(TcMisc) <= TcCfg<128>::MISC, "");
 
@@ -229,12 +229,9 @@ struct TcRow {
 };
 __device__ __forceinline__ TcRow tc_row(const TcArgs& a, int64_t b) {
   TcRow r;
-  r.from = ld_live(a.tv.offsets + b);
-  const int64_t to = ld_live(a.tv.offsets + b + 1);
-  bool bad = false;   // recorded by tree_nodes_kernel
+  tree_row(a.tv, b, r.from, r.n);
+  bool bad = false;   // reported by tree_check_rows
   r.len = row_length(a.pv, b, bad);
-  const bool good = r.from >= 0 && to >= r.from && to <= a.tv.n_nodes && to - r.from <= kMaxTreeNodes;
-  r.n = good ? (int)(to - r.from) : 0;
   r.groups = (r.n * a.Hq + kGroupRows - 1) / kGroupRows;
   r.tiles = (int)(((int64_t)r.len + kTileKeys - 1) / kTileKeys) + 1;
   return r;
@@ -525,6 +522,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   chain_wait();
   chain_release();
   tc_cut(a, ms);
+  if (blockIdx.x == gridDim.x - 1) tree_check_rows(a.pv, a.tv);
   __syncthreads();
 
   if (warp >= 9) {
@@ -757,8 +755,27 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const int row = both ? g * 128 + r : r;                    // of the group
       const bool live = row < s.rows;
       const int64_t out = s.r.from * a.Hq + s.g * kGroupRows + row;   // of q, o and lse
-      uint4 mask = make_uint4(0u, 0u, 0u, 0u);
-      if (live && s.t1 == s.r.tiles) mask = ld_live(&a.nodes[out / a.Hq].mask);
+      uint4 mask = make_uint4(0u, 0u, 0u, 0u);   // the node's ancestors, itself among them
+      if (s.t1 == s.r.tiles) {
+        bool bad = false;
+        tc_bar(1, 256);   // nobody walks through the segment before's any more
+        if (g == 0 && r < s.r.n) ms.up[r] = (uint8_t)(tree_parent(a.tv, s.r.from, r, bad) + 1);
+        if (bad) record_error(DSA_DEV_ERR_BAD_INDEX);
+        tc_bar(1, 256);
+        if (live)
+          for (int j = (int)(out / a.Hq - s.r.from); j >= 0; j = ms.up[j] - 1) {   // parents come before
+            const uint32_t x = 1u << (j & 31);
+            if (j < 32)
+              mask.x |= x;
+            else if (j < 64)
+              mask.y |= x;
+            else if (j < 96)
+              mask.z |= x;
+            else
+              mask.w |= x;
+          }
+        __syncwarp();
+      }
       float m = -INFINITY, top = -INFINITY, l = 0.f;   // base (log2 units); its limit in raw scores; sum
       bool mine = false, tree_mine = false;            // this accumulator has units; among them the drafted tokens
       for (int u = g; u < units; u += 2) {
@@ -1112,11 +1129,10 @@ static cudaError_t launch_tc(TcArgs& a, cudaStream_t s) {
   return launch_chained(tree_join_kernel<D>, dim3(4 * kTcSms), dim3(kTcJoinThreads), 0, s, a, kTcSms);
 }
 
-cudaError_t launch_tree_tc(const TreeAttnArgs& g, const TreeNode* nodes, void* ws, cudaStream_t s) {
+cudaError_t launch_tree_tc(const TreeAttnArgs& g, void* ws, cudaStream_t s) {
   TcArgs a;
   a.pv = g.pv;
   a.tv = g.tree;
-  a.nodes = nodes;
   a.Q = static_cast<const __nv_bfloat16*>(g.q);
   a.K = static_cast<const __nv_bfloat16*>(g.ck);
   a.V = static_cast<const __nv_bfloat16*>(g.cv);

@@ -5,9 +5,7 @@
 
 namespace dsa {
 
-struct TreeNode;
-
 size_t tree_tc_ws_bytes(int d);
-cudaError_t launch_tree_tc(const TreeAttnArgs& a, const TreeNode* nodes, void* ws, cudaStream_t s);
+cudaError_t launch_tree_tc(const TreeAttnArgs& a, void* ws, cudaStream_t s);
 
 }  // namespace dsa

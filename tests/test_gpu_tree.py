@@ -97,6 +97,13 @@ def _selection(pg, tr, k, seed=3):
     return idx
 
 
+@pytest.fixture(params=[None, 60000], ids=["near", "far"])
+def cap(request):
+    """The rows' capacity: by it a call goes through whole caches node by node or, where it is far above these lengths, by rows
+    on the tensor cores."""
+    return request.param
+
+
 LENS = [0, 1, 3, 4, 17, 64, 127, 128, 129, 300, 515, 1003]
 NODES = [3, 0, 1, 2, 8, 9, 16, 17, 33, 128, 5, 64]
 SHAPES = [("bf16", 16, 128, 64), ("bf16", 32, 128, 16), ("bf16", 16, 64, 4), ("bf16", 1, 128, 12), ("bf16", 5, 64, 100),
@@ -106,8 +113,8 @@ SHAPES = [("bf16", 16, 128, 64), ("bf16", 32, 128, 16), ("bf16", 16, 64, 4), ("b
 # ---------------------------------------------------------------- attention
 @pytest.mark.parametrize("dtype,Hq,d,page", SHAPES)
 @pytest.mark.parametrize("form", ["all", "chains", "selected"])
-def test_tree_attention(dtype, Hq, d, page, form):
-    pg = Paged(LENS, page, d=d, dtype=dtype, seed=Hq + d + page).fill()
+def test_tree_attention(dtype, Hq, d, page, form, cap):
+    pg = Paged(LENS, page, d=d, dtype=dtype, seed=Hq + d + page, cap=cap).fill()
     tr = Trees(pg, NODES, Hq, chain=form == "chains", seed=page)
     dims = _dims(pg, Hq, k=9)
     idx = _selection(pg, tr, 9) if form == "selected" else None
@@ -119,8 +126,8 @@ def test_tree_attention(dtype, Hq, d, page, form):
 @pytest.mark.parametrize("dtype,Hq", [("bf16", 16), ("bf16", 32), ("bf16", 24), ("fp32", 8)])
 @pytest.mark.parametrize("lens,nodes", [([20011], [16]), ([9001, 3, 0, 12289], [7, 1, 0, 12]), ([700] * 40, [3] * 40),
                                         ([130] * 300, [1] * 300), ([2500, 40], [100, 128]), ([0] * 5, [2] * 5), ([6000], [1])])
-def test_tree_attention_batches(dtype, Hq, lens, nodes):
-    pg = Paged(lens, 16, dtype=dtype, seed=len(lens) + Hq).fill()
+def test_tree_attention_batches(dtype, Hq, lens, nodes, cap):
+    pg = Paged(lens, 16, dtype=dtype, seed=len(lens) + Hq, cap=cap).fill()
     tr = Trees(pg, nodes, Hq, seed=5)
     dims = _dims(pg, Hq)
     o, lse = _run(pg, tr, dims)
@@ -141,9 +148,9 @@ def test_tree_attention_of_selected_pools_in_batches(batch):
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("how", ["large", "rising", "lowest"])
-def test_tree_attention_of_awkward_scores(dtype, how):
+def test_tree_attention_of_awkward_scores(dtype, how, cap):
     """Scores far apart, rising along the keys (the running maximum moves all the time), and at the type's lowest values."""
-    pg = Paged([900, 77], 16, dtype=dtype, seed=31)
+    pg = Paged([900, 77], 16, dtype=dtype, seed=31, cap=cap)
     tr = Trees(pg, [20, 3], 16, seed=32)
     if how == "large":
         tr.q = (tr.q.float() * 40).to(pg.dt)
@@ -168,9 +175,9 @@ def test_tree_attention_of_awkward_scores(dtype, how):
 
 @pytest.mark.parametrize("dtype,Hq", [("bf16", 16), ("bf16", 32), ("fp32", 8)])
 @pytest.mark.parametrize("selected", [False, True])
-def test_other_branches_may_hold_anything(dtype, Hq, selected):
+def test_other_branches_may_hold_anything(dtype, Hq, selected, cap):
     """NaN and infinities in the keys and values of nodes that are no ancestors change nothing; descendants get them."""
-    pg = Paged([300, 9], 16, dtype=dtype, seed=41).fill()
+    pg = Paged([300, 9], 16, dtype=dtype, seed=41, cap=cap).fill()
     tr = Trees(pg, [40, 40], Hq, seed=42)
     tr.up = [[-1] + [i - 2 if i > 1 else -1 for i in range(1, 40)] for _ in range(2)]   # two branches: even and odd nodes
     sound = Trees(pg, [40, 40], Hq, seed=42)
@@ -195,10 +202,10 @@ def test_other_branches_may_hold_anything(dtype, Hq, selected):
 
 
 @pytest.mark.parametrize("dtype,Hq", [("bf16", 16), ("fp32", 8)])
-def test_values_behind_a_row_are_not_read(dtype, Hq):
+def test_values_behind_a_row_are_not_read(dtype, Hq, cap):
     """Keys behind a row's length are NaN in the cache, also on its last page: test_tree_attention has that everywhere; here
     infinities of the row itself reach its nodes only (as infinities or NaN, the header says)."""
-    pg = Paged([40, 200, 40], 16, dtype=dtype, seed=43)
+    pg = Paged([40, 200, 40], 16, dtype=dtype, seed=43, cap=cap)
     pg.V[1][100] = math.inf
     pg.fill()
     tr = Trees(pg, [4, 4, 4], Hq, seed=44)
@@ -211,10 +218,10 @@ def test_values_behind_a_row_are_not_read(dtype, Hq):
 
 @pytest.mark.parametrize("dtype,Hq", [("bf16", 16), ("bf16", 32), ("fp32", 8)])
 @pytest.mark.parametrize("selected", [False, True])
-def test_bad_rows_are_skipped_and_reported(dtype, Hq, selected):
+def test_bad_rows_are_skipped_and_reported(dtype, Hq, selected, cap):
     lens = [100, 50, 70, 33, 20, 64]
     nodes = [4, 129, 3, 5, 6, 2]
-    pg = Paged(lens, 16, dtype=dtype, seed=51).fill()
+    pg = Paged(lens, 16, dtype=dtype, seed=51, cap=cap).fill()
     tr = Trees(pg, nodes, Hq, seed=52)
     dims = _dims(pg, Hq, k=5)
     idx = _selection(pg, tr, 5) if selected else None
@@ -272,8 +279,8 @@ def test_bad_rows_are_skipped_and_reported(dtype, Hq, selected):
         _check(pg, tr, o, lse, dims.scale, rows=[0])
 
 
-def test_no_nodes_and_no_rows():
-    pg = Paged([20, 5], 16, seed=53).fill()
+def test_no_nodes_and_no_rows(cap):
+    pg = Paged([20, 5], 16, seed=53, cap=cap).fill()
     dims = _dims(pg, 16)
     tr = Trees(pg, [0, 0], 16)
     o, lse = _run(pg, tr, dims)
@@ -287,8 +294,8 @@ def test_no_nodes_and_no_rows():
     assert torch.all(o == 7) and torch.all(lse == 7)
 
 
-def test_graph_replay_other_streams_and_reproducibility():
-    pg = Paged([2000, 150, 0, 31], 16, seed=61).fill()
+def test_graph_replay_other_streams_and_reproducibility(cap):
+    pg = Paged([2000, 150, 0, 31], 16, seed=61, cap=cap).fill()
     Hq = 16
     dims = _dims(pg, Hq)
     trees = [Trees(pg, n, Hq, seed=62 + i) for i, n in enumerate(([9, 30, 2, 7], [20, 0, 25, 3], [1, 1, 1, 45]))]
@@ -332,11 +339,11 @@ def test_graph_replay_other_streams_and_reproducibility():
 
 
 @pytest.mark.parametrize("Hq,chain", [(16, False), (16, True)])
-def test_cache_beyond_32_bit_offsets(Hq, chain):
+def test_cache_beyond_32_bit_offsets(Hq, chain, cap):
     """The same row at the far end of a cache of 4.6 GB a tensor gives the same bits."""
     page, d = 128, 128
     pages = (1 << 31) // (page * d) + 8
-    pg = Paged([1000], page, seed=71).fill()
+    pg = Paged([1000], page, seed=71, cap=cap).fill()
     tr = Trees(pg, [20], Hq, chain=chain, seed=72)
     dims = _dims(pg, Hq)
     near = _run(pg, tr, dims)
@@ -352,9 +359,9 @@ def test_cache_beyond_32_bit_offsets(Hq, chain):
     assert torch.equal(near[0], far[0]) and torch.equal(near[1], far[1])
 
 
-def test_rows_may_share_pages():
+def test_rows_may_share_pages(cap):
     """Two rows with one table row: each as if it were alone."""
-    pg = Paged([517, 517], 64, seed=73).fill()
+    pg = Paged([517, 517], 64, seed=73, cap=cap).fill()
     pg.table[1], pg.K[1], pg.V[1] = pg.table[0], pg.K[0], pg.V[0]
     tr = Trees(pg, [7, 11], 16, seed=74)
     dims = _dims(pg, 16)
