@@ -112,7 +112,7 @@ static_assert(sizeof(TcMisc) <= TcCfg<128>::MISC, "");
 __device__ __forceinline__ void tc_mbar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(bar) : "memory");
 }
-// Waits for a phase, all lanes together.  The first polls are plain ones: through
+// Waits for a phase, or one a lane, all lanes together.  The first polls are plain ones: through
 // mbar_wait a phase that had long completed cost 300 cycles, three times a unit.
 __device__ __forceinline__ bool tc_poll(uint32_t bar, uint32_t parity) {
   uint32_t ok;
@@ -677,10 +677,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     for (; ok && walk.next(a, s); ++nseg) {
       const bool both = __shfl_sync(0xffffffffu, (int)s.both(), 0) != 0;
       const int n = __shfl_sync(0xffffffffu, s.t1 - s.t0, 0), units = both ? 2 * n : n;
-      auto form_s = [&](int u) -> bool {
-        const uint32_t it = it0 + 2 * (both ? u >> 1 : u);
+      auto item = [&](int u) { return it0 + 2 * (both ? u >> 1 : u); };   // the unit's K in the ring; V is the next
+      // S of unit u, whose K is there
+      auto form_s = [&](int u) {
+        const uint32_t it = item(u);
         const int g = u & 1;
-        if (!wait(full(it), (it / C::NS) & 1)) return false;
         fence_proxy_async_shared();   // copies that did not come by TMA, seen through the barrier
         tc_fence_after();
         const uint32_t kt = sKV + (it % C::NS) * C::TILE, qt = sQ + (both ? g * C::TILE : 0);
@@ -693,33 +694,48 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         tc_one_arrive(sfull(g));   // hands on what the fetching warps wrote of the tile
         if (!both || g) tc_mma_arrive(empty(it));
         if (u == units - 1) tc_mma_arrive(qfree);
-        return true;
+      };
+      auto k_full = [&](int u, uint32_t& bar, uint32_t& parity) {
+        const uint32_t it = item(u);
+        bar = full(it);
+        parity = (it / C::NS) & 1;
       };
       if (!(ok = wait(qfull, nseg & 1))) break;
-      for (int u = 0; ok && u < 2 && u < units; ++u) ok = form_s(u);
+      for (int u = 0; ok && u < 2 && u < units; ++u) {
+        uint32_t bar, parity;
+        k_full(u, bar, parity);
+        if ((ok = wait(bar, parity))) form_s(u);
+      }
       for (int u = 0; ok && u < units; ++u) {
         const int g = u & 1;
-        const uint32_t it = it0 + 2 * (both ? u >> 1 : u) + 1;
+        const uint32_t it = item(u) + 1, par = (g ? np1 : np0) & 1;
         const uint32_t tS = tmem + C::S_AT + 128 * g, tO = tmem + C::O_AT + D * g;
-        if (!(ok = wait(full(it), (it / C::NS) & 1))) break;
         const uint32_t vt = sKV + (it % C::NS) * C::TILE;
+        auto weigh = [&](int half) {
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          if (!(ok = wait(phalf(g) + 8 * half, (g ? np1 : np0) & 1))) break;
-          if (half == 0) fence_proxy_async_shared();
-          tc_fence_after();
-#pragma unroll
-          for (int kk = 4 * half; kk < 4 * half + 4; ++kk) {
-            const uint64_t bd = tc_desc_mn(vt + kk * 16 * 128, C::CB);
-            const uint32_t pa = tS + 32 * (kk >> 1) + 8 * (kk & 1);
-            tc_mma_ts(tO, pa, bd, idesc_pv, !(u < 2 && kk == 0));
+          for (int kk = 0; kk < 4; ++kk) {
+            const uint64_t bd = tc_desc_mn(vt + (4 * half + kk) * 16 * 128, C::CB);
+            const uint32_t pa = tS + 64 * half + 32 * (kk >> 1) + 8 * (kk & 1);
+            tc_mma_ts(tO, pa, bd, idesc_pv, !(u < 2 && half == 0 && kk == 0));
             tc_mma_ts(tO, pa + 16, bd, idesc_pv, 1u);
           }
-        }
-        if (!ok) break;
+        };
+        // A look at a barrier takes the issuer some 200 cycles, ready or not, so its lanes
+        // look at two at once: V and P's first half, then P's second and the next K.
+        const bool odd = lane & 1, more = u + 2 < units;
+        uint32_t bar, parity;
+        if (!(ok = wait(odd ? phalf(g) : full(it), odd ? par : (it / C::NS) & 1))) break;
+        fence_proxy_async_shared();
+        tc_fence_after();
+        weigh(0);
+        k_full(more ? u + 2 : u, bar, parity);
+        const bool next = odd && more;
+        if (!(ok = wait(next ? bar : phalf(g) + 8, next ? parity : par))) break;
+        tc_fence_after();
+        weigh(1);
         g ? ++np1 : ++np0;
-        if (u + 2 < units) {
-          ok = form_s(u + 2);
+        if (more) {
+          form_s(u + 2);
         } else {   // the accumulator's last of the segment
           tc_mma_arrive(pvdone(g));
           tc_one_arrive(pvdone(g));
