@@ -37,13 +37,18 @@ __global__ void __launch_bounds__(kCommitThreads) cache_commit_kernel(const __gr
     last = -1;
   }
   if (bad) last = -1;
-  if (last >= 0 && a.tree.parents && (int)threadIdx.x <= last) up[threadIdx.x] = ld_live(a.tree.parents + from + threadIdx.x);
+  if ((int)threadIdx.x <= last) {
+    if (a.tree.parents)
+      up[threadIdx.x] = ld_live(a.tree.parents + from + threadIdx.x);
+    else
+      path[threadIdx.x] = last - threadIdx.x;
+  }
   __syncthreads();
   if (threadIdx.x == 0) {
-    int depth = 0;
-    for (int j = last; j >= 0;) {
+    int depth = a.tree.parents ? 0 : last + 1;
+    for (int j = a.tree.parents ? last : -1; j >= 0;) {
       path[depth++] = j;
-      int p = a.tree.parents ? up[j] : j - 1;
+      int p = up[j];
       if (p < -1 || p >= j) {
         bad_idx = true;
         p = -1;
@@ -72,19 +77,35 @@ __global__ void __launch_bounds__(kCommitThreads) cache_commit_kernel(const __gr
   };
   auto node_of = [&](int i) { return from + path[depth - 1 - i]; };   // of the path's token i
   int page;
-  for (int i = threadIdx.x; i < depth * CH; i += kCommitThreads) {
-    const int j = i / CH, c = i % CH, pos = len + j;
-    const int64_t pool = pool_at(pos, page);
-    if (pool < 0) continue;
-    const int64_t at = (pool * 4 + (pos & 3)) * CH + c, src = node_of(j) * CH + c;
-    const uint4 x = ld_live(static_cast<const uint4*>(a.k) + src), y = ld_live(static_cast<const uint4*>(a.v) + src);
-    static_cast<uint4*>(a.ck)[at] = x;
-    static_cast<uint4*>(a.cv)[at] = y;
+  // CH and CI are powers of two, up to 32
+  const int sh = __ffs(CH) - 1, shi = __ffs(CI) - 1;
+  constexpr int AHEAD = 4;   // tokens a thread has on their way
+  const int step = kCommitThreads >> sh, c0 = threadIdx.x & (CH - 1);
+  for (int j0 = threadIdx.x >> sh; j0 < depth; j0 += AHEAD * step) {
+    uint4 x[AHEAD], y[AHEAD];
+    int64_t at[AHEAD];
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      const int j = j0 + i * step;
+      at[i] = -1;
+      if (j >= depth) continue;
+      const int64_t src = node_of(j) * CH + c0;
+      x[i] = ld_live(static_cast<const uint4*>(a.k) + src);
+      y[i] = ld_live(static_cast<const uint4*>(a.v) + src);
+      const int64_t pool = pool_at(len + j, page);
+      if (pool >= 0) at[i] = (pool * 4 + ((len + j) & 3)) * CH + c0;
+    }
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i)
+      if (at[i] >= 0) {
+        static_cast<uint4*>(a.ck)[at[i]] = x[i];
+        static_cast<uint4*>(a.cv)[at[i]] = y[i];
+      }
   }
   const uint4* ki = static_cast<const uint4*>(a.k_idx);
   const int first = len & ~3, open = (len + depth) & ~3;
   for (int i = threadIdx.x; i < (open - first) / 4 * CI; i += kCommitThreads) {
-    const int c = i % CI, p0 = first + i / CI * 4;
+    const int c = i & (CI - 1), p0 = first + (i >> shi) * 4;
     const int64_t pool = pool_at(p0, page);
     if (pool < 0) continue;
     float acc[N], x[N];
@@ -103,7 +124,7 @@ __global__ void __launch_bounds__(kCommitThreads) cache_commit_kernel(const __gr
   __syncthreads();   // the kept keys have been read; the new ones may take their place
   const int keep = max(open, len);
   for (int i = threadIdx.x; i < (len + depth - keep) * CI; i += kCommitThreads) {
-    const int c = i % CI, pos = keep + i / CI;
+    const int c = i & (CI - 1), pos = keep + (i >> shi);
     if (pool_at(pos, page) < 0) continue;
     static_cast<uint4*>(a.cktail)[((int64_t)page * 3 + (pos & 3)) * CI + c] = ld_live(ki + node_of(pos - len) * CI + c);
   }

@@ -18,7 +18,7 @@ namespace dsa {
 constexpr int kPageThreads = 256;
 constexpr int kPageSms = 152;
 constexpr int kSegments = 128;                 // most segments that pages are counted in
-constexpr int kSegmentMin = 4 * kPageThreads;  // pages of a segment, at the least
+constexpr int kSegmentMin = kPageThreads;      // pages of a segment, at the least
 
 // The workspace: totals, the segments' counts, then lists.
 struct PagesWs {
@@ -82,11 +82,26 @@ __device__ __forceinline__ int64_t cta_scan(int64_t x, int64_t& total, int64_t* 
   }
   return before + incl - x;
 }
-// Sum of in[0 .. n), and of in[0 .. m): every thread gets both.
-__device__ __forceinline__ void cta_sums(const int64_t* in, int n, int m, int64_t& all, int64_t& first, int64_t* scratch) {
-  const int64_t x = (int)threadIdx.x < n ? ld_live(in + threadIdx.x) : 0;   // n <= kSegments <= kPageThreads
-  cta_scan(x, all, scratch);
-  cta_scan((int)threadIdx.x < m ? x : 0, first, scratch);
+// Sum of in[0 .. n), and of in[0 .. m): every thread gets both, each warp by itself.
+__device__ __forceinline__ void warp_sums(const int64_t* in, int n, int m, int64_t& all, int64_t& first) {
+  static_assert(kSegments == 128, "four to a lane");
+  all = first = 0;
+  int64_t x[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int i = 32 * j + (threadIdx.x & 31);
+    x[j] = i < n ? ld_live(in + i) : 0;
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    all += x[j];
+    if (32 * j + (int)(threadIdx.x & 31) < m) first += x[j];
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    all += __shfl_xor_sync(0xffffffffu, all, o);
+    first += __shfl_xor_sync(0xffffffffu, first, o);
+  }
 }
 
 __device__ __forceinline__ int page_count(const PagesArgs& a, int64_t p) { return ld_live(a.refs + p); }
@@ -252,8 +267,8 @@ __global__ void __launch_bounds__(kPageThreads)
   chain_wait();
   chain_release();
   int64_t have, rank, wanted, at, total;
-  cta_sums(w.free_in, gridDim.x, blockIdx.x, have, rank, scratch);
-  cta_sums(w.want_in, gridDim.x, blockIdx.x, wanted, at, scratch);
+  warp_sums(w.free_in, gridDim.x, blockIdx.x, have, rank);
+  warp_sums(w.want_in, gridDim.x, blockIdx.x, wanted, at);
   if (blockIdx.x == 0 && threadIdx.x == 0) {
     *w.go = wanted <= have;
     *missing = wanted <= have ? 0 : (int)min(wanted - have, (int64_t)INT32_MAX);
@@ -328,14 +343,14 @@ __global__ void __launch_bounds__(kPageThreads)
   chain_wait();
   chain_release();
   int64_t U, before, total, below;
-  cta_sums(w.free_in, gridDim.x, blockIdx.x, U, before, scratch);
+  warp_sums(w.free_in, gridDim.x, blockIdx.x, U, before);
   // used pages below U: whole segments, and the part of U's own that lies below it
   {
     const int64_t seg = U / pages_per;
     int64_t n = 0, first;
     for (int64_t p = seg * pages_per + threadIdx.x; p < U; p += kPageThreads) n += page_count(a, p) > 0;
     cta_scan(n, below, scratch);
-    cta_sums(w.free_in, gridDim.x, (int)seg, total, first, scratch);   // seg <= gridDim.x: U <= num_pages
+    warp_sums(w.free_in, gridDim.x, (int)seg, total, first);   // seg <= gridDim.x: U <= num_pages
     below += first;
   }
   if (blockIdx.x == 0 && threadIdx.x == 0) {
