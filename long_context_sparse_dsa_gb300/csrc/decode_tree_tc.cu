@@ -510,6 +510,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     mbar_init(drain, 1);
     ms.abort = 0;
     fence_mbar_init();
+    prefetch_tmap(&map_q);
+    prefetch_tmap(&map_k);
+    prefetch_tmap(&map_v);
   }
   if (warp == 8) {
     tmem_alloc(smem_u32(&ms.tmem), C::TMEM_COLS);
@@ -624,27 +627,37 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           ++it;
           if (!wait(empty(it), ((it / C::NS) & 1) ^ 1)) break;
           st = sKV + (it % C::NS) * C::TILE;
-          for (int r = rlo; r < kTileKeys / kTcFetch; r += RPC) {
-            const int j = pw * (kTileKeys / kTcFetch) + r;
-            uint4 x = make_uint4(0u, 0u, 0u, 0u);
-            if (j < s.r.n) x = ld_live(reinterpret_cast<const uint4*>(a.nV + (s.r.from + j) * D) + ch);
-            uint32_t* w = &x.x;
-            bool odd = false;
+          constexpr int BATCH = 8;   // rows on their way at once: their latency is met once, not per row
+#pragma unroll 1
+          for (int r0 = rlo; r0 < kTileKeys / kTcFetch; r0 += BATCH * RPC) {
+            uint4 x[BATCH];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {   // exponent all ones: infinity or NaN
-              if ((w[e] & 0x7F80u) == 0x7F80u) {
-                w[e] &= 0xFFFF0000u;
-                odd = true;
-              }
-              if ((w[e] & 0x7F800000u) == 0x7F800000u) {
-                w[e] &= 0xFFFFu;
-                odd = true;
-              }
+            for (int i = 0; i < BATCH; ++i) {
+              const int j = pw * (kTileKeys / kTcFetch) + r0 + i * RPC;
+              x[i] = make_uint4(0u, 0u, 0u, 0u);
+              if (j < s.r.n) x[i] = ld_live(reinterpret_cast<const uint4*>(a.nV + (s.r.from + j) * D) + ch);
             }
-            if (odd) atomicOr(&ms.bad_v[j >> 5], 1u << (j & 31));
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(st + at_of(j)), "r"(x.x), "r"(x.y), "r"(x.z),
-                         "r"(x.w)
-                         : "memory");
+#pragma unroll
+            for (int i = 0; i < BATCH; ++i) {
+              const int j = pw * (kTileKeys / kTcFetch) + r0 + i * RPC;
+              uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+              bool odd = false;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {   // exponent all ones: infinity or NaN
+                if ((w[e] & 0x7F80u) == 0x7F80u) {
+                  w[e] &= 0xFFFF0000u;
+                  odd = true;
+                }
+                if ((w[e] & 0x7F800000u) == 0x7F800000u) {
+                  w[e] &= 0xFFFFu;
+                  odd = true;
+                }
+              }
+              if (odd) atomicOr(&ms.bad_v[j >> 5], 1u << (j & 31));
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(st + at_of(j)), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                           "r"(w[3])
+                           : "memory");
+            }
           }
           fence_proxy_async_shared();
           word(full(it));
@@ -967,7 +980,7 @@ template <int D>
 __global__ void __launch_bounds__(kTcJoinThreads) tree_join_kernel(const __grid_constant__ TcArgs a, int ctas) {
   constexpr int WARPS = kTcJoinThreads / 32;
   constexpr int Q4 = D / 4;             // float4s of a row
-  constexpr int FEW = 6;                // pieces
+  constexpr int FEW = 16;               // pieces
   constexpr int CM = 2;                 // float4s of a unit with many pieces
   constexpr int CF = Q4 / WARPS;        // float4s of a warp with few
   __shared__ int begin[kTcSms + 1];
@@ -1037,15 +1050,25 @@ __global__ void __launch_bounds__(kTcJoinThreads) tree_join_kernel(const __grid_
 #pragma unroll
       for (int c = 0; c < CF; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (live) {
-        for (int s = 0; s < n; ++s) {
-          const int64_t p = piece(s);
-          float4 x[CF];
+        constexpr int AHEAD = 4;
+        for (int s0 = 0; s0 < n; s0 += AHEAD) {
+          float2 ml[AHEAD];
+          float4 x[AHEAD][CF];
 #pragma unroll
-          for (int c = 0; c < CF; ++c) x[c] = ld_live(po + (p * Q4 + q0 + c) * kGroupRows + row);
-          const float2 ml = ld_live(a.pml + p * kGroupRows + row);
-          meet(ml.x, ml.y, mm, l, fo, fn);
+          for (int i = 0; i < AHEAD; ++i) {
+            if (s0 + i >= n) break;
+            const int64_t p = piece(s0 + i);
+            ml[i] = ld_live(a.pml + p * kGroupRows + row);
 #pragma unroll
-          for (int c = 0; c < CF; ++c) acc[c] = add4(scale4(acc[c], fo), fn, x[c]);
+            for (int c = 0; c < CF; ++c) x[i][c] = ld_live(po + (p * Q4 + q0 + c) * kGroupRows + row);
+          }
+#pragma unroll
+          for (int i = 0; i < AHEAD; ++i) {
+            if (s0 + i >= n) break;
+            meet(ml[i].x, ml[i].y, mm, l, fo, fn);
+#pragma unroll
+            for (int c = 0; c < CF; ++c) acc[c] = add4(scale4(acc[c], fo), fn, x[i][c]);
+          }
         }
 #pragma unroll
         for (int c = 0; c < CF; ++c) out(q0 + c, acc[c]);
