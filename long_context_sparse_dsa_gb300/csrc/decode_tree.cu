@@ -153,22 +153,30 @@ size_t tree_attn_ws_bytes(bool bf16, int Hq, int d, int64_t batch, int64_t n_nod
 
 // Whether whole bf16 caches are attended to by rows on the tensor cores or by
 // nodes.  Estimates in us from what the host knows, the rows' capacity in place of
-// their lengths, and the nodes spread evenly:
-//   nodes: 6 for the launch and the chains of loads, then a warp's step of 16 keys
-//          takes about 1 (16 heads) or 1.6 (32), with 8 warps an SM and no more
-//          than 64 a node
-//   rows:  13 for two launches, a first and a last tile, then a tile of 128 keys and
-//          up to 256 query rows takes about 2
+// their lengths, and the nodes spread evenly; the constants are those that chose
+// best between the measured times of 30 shapes:
+//   nodes: 7.5 for the launch and the chains of loads, then a warp's step of 16 keys
+//          takes 0.75 (16 heads) or 1.2 (32), with 8 warps an SM and no more than 64
+//          a node
+//   rows:  19 for two launches, a first and a last tile; then a group of 256 query
+//          rows takes an SM 10 for what it begins and ends, and a tile of 128 keys
+//          1.5, or 3 where more than 128 of the rows are used
+// In us, rows and nodes: 1 row of 1 node over 4000 tokens 15.4 and 8.8, over 40000
+// 17.5 and 30.4; 1 of 64 over 4000 28.2 and 20.0; 16 of 4 over 3000 25.5 and 17.0; 64
+// of 16 over 1000 41 and 68.  The farthest misses are 1 row of 16 over 12000, 20 and
+// 25, and 64 of 16 over 300, 30 and 32, which go by nodes.
 static bool by_tensor_rows(const TreeAttnArgs& a) {
-  constexpr double kStart = 13., kSms = 152.;
+  constexpr double kSms = 152.;
   const double batch = (double)a.tree.batch, nodes = (double)a.tree.n_nodes, cap = (double)a.pv.capacity;
   const double steps = nodes * (cap / 16. + 1.);
   const double warps = 64. * nodes < 8. * kSms ? 64. * nodes : 8. * kSms;
-  const double by_nodes = 6. + steps * (a.Hq > 16 ? 1.6 : 1.) / warps;
+  const double by_nodes = 7.5 + steps * (a.Hq > 16 ? 1.2 : 0.75) / warps;
+  const double rows = nodes * a.Hq;
   double groups = batch;   // of 256 query rows
-  if (nodes * a.Hq > 256. * batch) groups = nodes * a.Hq / 256.;
+  if (rows > 256. * batch) groups = rows / 256.;
   if (nodes < batch) groups = nodes;
-  const double by_rows = kStart + groups * (cap / 128. + 1.) * 2. / kSms;
+  const double tile = rows > 128. * batch ? 3. : 1.5;
+  const double by_rows = 19. + groups * (10. + tile * (cap / 128. + 1.)) / kSms;
   return by_rows < by_nodes;
 }
 
