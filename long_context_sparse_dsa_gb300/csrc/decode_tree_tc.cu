@@ -15,10 +15,10 @@
 //
 // Warps: 0-3 and 4-7 own one accumulator each, a query row per thread; 8 issues
 // the MMAs; 9 and 10 fetch.
-//   * K and V tiles come through one ring of stages (K, V, K, V, ..) by 16-byte
-//     cp.async into the 128-byte-swizzled layout: pages may be as small as 4
-//     tokens, and a TMA box of 4 rows costs more than it moves.  The copies
-//     arrive on the stage's barrier by themselves.
+//   * K and V tiles come through one ring of stages (K, V, K, V, ..), in the
+//     128-byte-swizzled layout: by TMA boxes of 64, 32 or 16 rows where the page
+//     size is a multiple of that and a warp's 64 keys are all there, else by 16-byte
+//     cp.async, whose copies arrive on the stage's barrier by themselves.
 //   * S = Q K^T (128 x 128, fp32) goes to tensor memory.  The owning warps read
 //     it twice: for the row's maximum, then to form p = 2^(s c - base), which
 //     takes S's place as bf16 hi + lo terms (p to about 2^-17; one term would
@@ -140,10 +140,10 @@ __device__ __forceinline__ bool tc_wait(uint32_t bar, uint32_t parity, volatile 
 __device__ __forceinline__ void tc_copies_arrive(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.shared::cta.b64 [%0];\n" ::"r"(bar) : "memory");
 }
-// The whole warp calls these, with the same arguments, and one thread issues.
-// (Issued from a branch that only one thread takes, an MMA cost about 190 cycles
-// whatever its size: its operands are uniform registers, which the compiler then
-// has to make out of a thread's.)
+// The whole warp calls these, with the same arguments, and one thread issues: the
+// operands are uniform registers, which the compiler has to make out of a thread's
+// where only one thread takes the branch (80.8 us against 77.5 for 8 rows of 128
+// drafts, 2000 tokens, 32 heads).
 // D[tmem] (+)= A[tmem] * B[smem]
 __device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
                                           uint32_t accumulate) {
@@ -531,7 +531,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   if (warp >= 9) {
     // ------------------------------------------------------------ fetching warps
     // Warp pw takes pools kTcPools pw .. of every tile.
-    const int pw = warp - 9, tid = threadIdx.x - 9 * 32;
+    const int pw = warp - 9;
     const int rlo = lane / CH, ch = lane % CH;
     bool ok = true, bad = false;
     uint32_t it = 0, nseg = 0;
@@ -549,7 +549,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     for (; ok && walk.next(a, s); ++nseg) {
       // Q: 256 (128) rows from the group's first on; what is behind its last is other rows' or none (zeros), and unused
       if (!wait(qfree, (nseg & 1) ^ 1)) break;
-      if (tid < 4) ms.bad_v[tid] = 0u;   // read before qfree by the segment before
+      // the words of this warp's keys, read before qfree by the segment before.  Each warp
+      // clears its own: one that gave up leaves no other at a barrier
+      if (lane < 4 / kTcFetch) ms.bad_v[pw * (4 / kTcFetch) + lane] = 0u;
+      __syncwarp();
       if (pw == 0) {
         const int tiles = s.both() ? 2 : 1;
         if (lane == 0) mbar_arrive_expect_tx(qfull, tiles * C::TILE);
@@ -560,7 +563,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                       (int32_t)(s.r.from * a.Hq + s.g * kGroupRows + 64 * h));
         }
       }
-      tc_bar(2, kTcFetch * 32);   // bad_v is zero
       const int32_t* trow = a.pv.table + s.row * a.pv.cols;
       // this lane's pool of a tile (lanes below kTcPools): its block-table entry is loaded a tile ahead
       auto col_of = [&](int t) { return page_of_pool(a.pv, t * 32 + pw * kTcPools + lane % kTcPools); };
