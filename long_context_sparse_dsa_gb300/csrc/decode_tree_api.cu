@@ -229,7 +229,9 @@ dsa_status dsa_cache_compact(const dsa_dims* dims, const dsa_paged_cache* cache,
 
 dsa_status dsa_cache_copy_pages(const dsa_dims* dims, const dsa_paged_cache* from, const dsa_paged_cache* to,
                                 int64_t n, const int32_t* src, const int32_t* dst, dsa_stream_t stream) {
-  dsa_status st = check_common(dims, from, 1, src, dst);   // src and dst are checked as its device arrays are
+  REQUIRE_PTR(src);
+  REQUIRE_PTR(dst);
+  dsa_status st = check_common(dims, from, 1, src, dst);   // as a row's
   if (st) return st;
   if ((st = check_common(dims, to, 1, src, dst))) return st;
   if ((st = check_arrays(from)) || (st = check_arrays(to))) return st;

@@ -114,6 +114,14 @@ def test_copy_pages_refuses(lib, to, n, src, status):
     assert lib.dsa_cache_copy_pages(ctypes.byref(_dims()), ctypes.byref(_cache()), ctypes.byref(to), n, src, P, None) == status
 
 
+def test_copy_pages_names_what_it_refuses(lib):
+    ref = ctypes.byref(_cache())
+    for src, dst, name in ((None, P, "src is NULL"), (P, ODD, "dst is not 16-byte aligned")):
+        assert lib.dsa_cache_copy_pages(ctypes.byref(_dims()), ref, ref, 1, src, dst, None) == INV
+        with pytest.raises(dsa.DSAError, match=name):
+            dsa._check(INV, "dsa_cache_copy_pages")
+
+
 def _norm(lib, **kw):
     a = {**dict(d=_dims(), n=3, q=P, qs=2048, k=P, ks=128, qw=P, kw=P, eps=1e-6, rot=None, pos=P, qo=P, ko=P), **kw}
     return lib.dsa_qk_norm_rotate(ctypes.byref(a["d"]), a["n"], a["q"], a["qs"], a["k"], a["ks"], a["qw"], a["kw"], a["eps"],
