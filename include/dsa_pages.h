@@ -77,7 +77,10 @@ dsa_status dsa_cache_fork(const dsa_dims *dims, const dsa_paged_cache *cache, in
  *   keep  [batch] int32, or NULL: 0, the rows end.  keep[b] >= lens[b] gives
  *         nothing back
  * A row with a bad length or a negative keep is left alone, an entry outside
- * the cache or with no count left is skipped (DSA_ERR_BAD_PAGE). */
+ * the cache or with no count left is skipped (DSA_ERR_BAD_PAGE).
+ * A row that is cut back and then grows again needs the keys of its open pool
+ * (ktail), and the cache has those of the last one only: keep[b] has to be a
+ * multiple of 4 or within the pool that lens[b] leaves open. */
 dsa_status dsa_cache_release(const dsa_dims *dims, const dsa_paged_cache *cache, int32_t *refs, int64_t batch,
                              const int32_t *lens, const int32_t *keep, int32_t *block_table, dsa_stream_t stream);
 

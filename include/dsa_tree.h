@@ -28,7 +28,8 @@
  *     CUDA graph and replayed with other contents.
  *   - Checked where they are used, and reported by dsa_check_device_error: a
  *     row whose offsets do not ascend or that has too many nodes is skipped,
- *     its outputs left as they were (DSA_ERR_BAD_PAGE); a row of bad length is
+ *     its outputs left as they were (DSA_ERR_BAD_PAGE; of nodes that two other
+ *     rows then claim the outputs are undefined); a row of bad length is
  *     taken as empty (DSA_ERR_BAD_PAGE); a parent outside -1 .. i-1 is taken
  *     as -1 (DSA_ERR_BAD_INDEX).
  */
@@ -63,8 +64,8 @@ size_t dsa_tree_workspace_bytes(const dsa_dims *dims, int64_t batch, int64_t n_n
  * NaN: bf16 weights are carried as two terms, which may have either sign.)
  * With idx, pools that drafted tokens complete are not selected from:
  * all of a branch is attended to.
- * A branch of one node per row, without a second token of its pool's, gives
- * what dsa_cache_append and dsa_decode_attn give (not bit for bit). */
+ * For a row of one node, without idx, that is what dsa_cache_append and
+ * dsa_decode_attn of its token give (not bit for bit). */
 dsa_status dsa_decode_tree_attn(const dsa_dims *dims, const dsa_paged_cache *cache, int64_t batch, const int32_t *lens,
                                 const int32_t *block_table, int64_t n_nodes, const int32_t *offsets,
                                 const int32_t *parents, const int32_t *idx, const void *q, const void *k,

@@ -196,6 +196,28 @@ def test_decoding_with_draft_trees(dtype, Hq, k):
     _check_attn(View, q, o, lse, d.dims.scale)
 
 
+@pytest.mark.parametrize("lens", [[61, 23, 130], [64, 3, 95]])
+def test_rows_cut_back_grow_again(lens):
+    """A row goes back to the end of a pool, to a place within its open pool, or to a page's end: the pages behind are given back,
+    and the pools completed later are those of the tokens that are there."""
+    d = Decoder("bf16", 16, 9, seed=sum(lens))
+    d.prompt(lens)
+    for i in range(3):
+        up, acc = d.draw()
+        d.step()
+        d.check(up, acc)
+        n = [len(x) for x in d.K]
+        keep = [max(0, n[0] // 4 * 4 - 8 * i), n[1] // 4 * 4 + n[1] % 4 // 2, n[2] // 16 * 16]
+        dsa.cache_release(d.dims, d.cache, d.refs, d.lens, d.table, keep=_i32(keep))
+        d.lens.copy_(_i32(keep))
+        d.K, d.V, d.KI = ([x[:m] for x, m in zip(y, keep)] for y in (d.K, d.V, d.KI))
+        d.check_pages()
+    up, acc = d.draw()
+    d.step()
+    d.check(up, acc)
+    d.check_pages()
+
+
 def test_a_captured_step_decodes():
     """One graph of a whole step, replayed with other drafts, lengths and pages; forks and compaction between replays."""
     d = Decoder("bf16", 16, 9, seed=5)
