@@ -9,7 +9,7 @@
 // integers and added with atomics.
 //
 // Bound: the launches, up to 4 in a row, each about 3 us (256 branches released, forked
-// from 64 rows and given pages, with some 36 KB copied for each: 17.8 us, 5 launches); where
+// from 64 rows and given pages, with some 36 KB copied for each: 16.4 us, 4 launches); where
 // pages are copied HBM, every byte once in and once out (a cache of 1M tokens, 60% in use:
 // 37.8 us, of which the move 24.6 at 5.9 TB/s).
 #include "decode.cuh"
@@ -220,6 +220,35 @@ __global__ void __launch_bounds__(kPageThreads)
 
 // ------------------------------------------------------------------- reserve
 constexpr uint32_t kCopyBit = 0x80000000u;
+// Up to so many pages and rows every CTA of reserve_place_kernel counts them itself, one
+// launch less.  That way and with the count before it, with a release behind: 512 pages, 4
+// rows 7.2 us and 8.3; 8192, 256 8.7 and 9.6; 8192, 512 9.6 and 10.1; 8192, 1024 12.6 and
+// 11.6; 16384, 256 9.3 and 9.7; 32768, 256 10.8 and 10.1.
+constexpr int64_t kOnePages = 16384, kOneRows = 512;
+static_assert(kOnePages <= kSegments * kSegmentMin && kSegmentMin % 4 == 0, "its segments begin at multiples of 4 pages");
+
+// What row b asks for (the top bit: the first is a copy, of `page`).
+__device__ __forceinline__ uint32_t row_wants(const PagesArgs& a, const int32_t* new_lens, int64_t b, int& page, bool& bad) {
+  bool off = false;
+  const int len = row_length(a.pv, b, off), to = ld_live(new_lens + b);
+  if (to < 0 || to > a.pv.capacity) off = true;
+  uint32_t n = 0;
+  page = -1;
+  if (!off && to > len) {
+    n = (uint32_t)(pages_of(to, a.page_size) - pages_of(len, a.page_size));
+    if (len % a.page_size) {
+      page = ld_live(a.pv.table + b * a.pv.cols + len / a.page_size);
+      if (!page_ok(a, page)) {
+        off = true;
+        n = 0;
+      } else if (page_count(a, page) > 1) {
+        n = (n + 1) | kCopyBit;
+      }
+    }
+  }
+  bad |= off;
+  return n;
+}
 
 // Free pages and requests of every segment; every row's requests.
 __global__ void __launch_bounds__(kPageThreads)
@@ -234,22 +263,8 @@ __global__ void __launch_bounds__(kPageThreads)
   const int64_t b1 = min((blockIdx.x + 1) * rows_per, a.batch);
   for (int64_t b = blockIdx.x * rows_per + threadIdx.x; b < b1; b += kPageThreads) {
     bool bad = false;
-    const int len = row_length(a.pv, b, bad), to = ld_live(new_lens + b);
-    if (to < 0 || to > a.pv.capacity) bad = true;
-    uint32_t n = 0;
-    int page = -1;
-    if (!bad && to > len) {
-      n = (uint32_t)(pages_of(to, a.page_size) - pages_of(len, a.page_size));
-      if (len % a.page_size) {
-        page = ld_live(a.pv.table + b * a.pv.cols + len / a.page_size);
-        if (!page_ok(a, page)) {
-          bad = true;
-          n = 0;
-        } else if (page_count(a, page) > 1) {
-          n = (n + 1) | kCopyBit;
-        }
-      }
-    }
+    int page;
+    const uint32_t n = row_wants(a, new_lens, b, page, bad);
     w.want[b] = (int)n;
     w.old[b] = page;
     want += n & ~kCopyBit;
@@ -262,15 +277,48 @@ __global__ void __launch_bounds__(kPageThreads)
 }
 
 // The free pages as a list, as far as they are wanted, and where in it a row's begin.
+// ONE: without a count before it.  Every CTA then counts all pages and all rows itself.
+template <bool ONE>
 __global__ void __launch_bounds__(kPageThreads)
-    reserve_place_kernel(const __grid_constant__ PagesArgs a, const __grid_constant__ PagesWs w, int32_t* missing,
-                         int64_t pages_per, int64_t rows_per) {
+    reserve_place_kernel(const __grid_constant__ PagesArgs a, const __grid_constant__ PagesWs w, const int32_t* new_lens,
+                         int32_t* missing, int64_t pages_per, int64_t rows_per) {
   __shared__ int64_t scratch[kPageThreads / 32];
   chain_wait();
   chain_release();
   int64_t have, rank, wanted, at, total;
-  warp_sums(w.free_in, gridDim.x, blockIdx.x, have, rank);
-  warp_sums(w.want_in, gridDim.x, blockIdx.x, wanted, at);
+  if constexpr (ONE) {
+    int64_t n = 0, first = 0;   // all free pages; those of the segments before
+    const int64_t p0 = blockIdx.x * pages_per, b0 = blockIdx.x * rows_per;   // p0: a multiple of 4
+#pragma unroll 4
+    for (int64_t i = threadIdx.x; i < a.cache.num_pages / 4; i += kPageThreads) {
+      const int4 x = ld_live(reinterpret_cast<const int4*>(a.refs) + i);
+      const int64_t k = (x.x == 0) + (x.y == 0) + (x.z == 0) + (x.w == 0);
+      n += k;
+      if (4 * i < p0) first += k;
+    }
+    for (int64_t p = (a.cache.num_pages & ~(int64_t)3) + threadIdx.x; p < a.cache.num_pages; p += kPageThreads)
+      n += page_count(a, p) == 0;   // not before p0
+    int64_t m = 0, m_first = 0;
+    for (int64_t b = threadIdx.x; b < a.batch; b += kPageThreads) {
+      bool bad = false;
+      int page;
+      const uint32_t want = row_wants(a, new_lens, b, page, bad);
+      m += want & ~kCopyBit;
+      if (b < b0) m_first += want & ~kCopyBit;
+      if (b >= b0 && b < b0 + rows_per) {
+        w.want[b] = (int)want;
+        w.old[b] = page;
+        if (bad) record_error(DSA_DEV_ERR_BAD_PAGE);
+      }
+    }
+    cta_scan(n, have, scratch);
+    cta_scan(first, rank, scratch);
+    cta_scan(m, wanted, scratch);
+    cta_scan(m_first, at, scratch);
+  } else {
+    warp_sums(w.free_in, gridDim.x, blockIdx.x, have, rank);
+    warp_sums(w.want_in, gridDim.x, blockIdx.x, wanted, at);
+  }
   if (blockIdx.x == 0 && threadIdx.x == 0) {
     *w.go = wanted <= have;
     *missing = wanted <= have ? 0 : (int)min(wanted - have, (int64_t)INT32_MAX);
@@ -458,9 +506,16 @@ cudaError_t launch_cache_reserve(const PagesArgs& a, const int32_t* new_lens, in
   int64_t pages_per;
   const unsigned g = segments_of(a, pages_per);
   const int64_t rows_per = (a.batch + g - 1) / g;
-  cudaError_t e = launch_chained(reserve_count_kernel, dim3(g), dim3(kPageThreads), 0, s, a, w, new_lens, pages_per, rows_per);
-  if (e != cudaSuccess) return e;
-  e = launch_chained(reserve_place_kernel, dim3(g), dim3(kPageThreads), 0, s, a, w, missing, pages_per, rows_per);
+  cudaError_t e;
+  if (a.cache.num_pages <= kOnePages && a.batch <= kOneRows) {
+    e = launch_chained(reserve_place_kernel<true>, dim3(g), dim3(kPageThreads), 0, s, a, w, new_lens, missing, pages_per,
+                       rows_per);
+  } else {
+    e = launch_chained(reserve_count_kernel, dim3(g), dim3(kPageThreads), 0, s, a, w, new_lens, pages_per, rows_per);
+    if (e != cudaSuccess) return e;
+    e = launch_chained(reserve_place_kernel<false>, dim3(g), dim3(kPageThreads), 0, s, a, w, new_lens, missing, pages_per,
+                       rows_per);
+  }
   if (e != cudaSuccess) return e;
   return launch_chained(reserve_give_kernel, dim3((unsigned)copy_parts(a.cache, a.batch), (unsigned)a.batch),
                         dim3(kPageThreads), 0, s, a, w);

@@ -211,6 +211,31 @@ def test_compact_of_any_cache(pages, fill):
     assert torch.equal(got[stay], old[stay]) and torch.equal(remap[old].long(), got)
 
 
+@pytest.mark.parametrize("pages,rows", [(1, 1), (3, 2), (257, 5), (1030, 40), (16383, 512), (16384, 513), (16385, 30), (40001, 512)])
+@pytest.mark.parametrize("room", [True, False])
+def test_reserve_in_any_cache(pages, rows, room):
+    """Around the sizes at which the calls' kernels change; with too few free pages nothing changes."""
+    w = World(pages, 4, 32, seed=pages + rows)
+    r = random.Random(rows)
+    full = [p for p in range(pages) if r.random() < (0.3 if room else 0.97)] or [0]
+    for p in full:
+        w.m_refs[p] = r.choice([1, 1, 2, 3])
+    w.refs.copy_(_i32(w.m_refs))
+    lens, table = [r.randrange(9) for _ in range(rows)], [[-1] * w.cols for _ in range(rows)]
+    own = r.sample(full, len(full))
+    for b, n in enumerate(lens):
+        for c in range(w.held(n)):
+            if not own:      # the pages are given away: this row has fewer
+                lens[b] = 4 * c
+                break
+            table[b][c] = own.pop()
+    new = [n + r.choice([0, 1, 2, 5, 23]) for n in lens]
+    dev, missing = _i32(table), _i32([-1])
+    dsa.cache_reserve(w.dims, w.cache, w.refs, _i32(lens), _i32(new), dev, missing, w.ws(rows))
+    assert missing.item() == w.m_reserve(lens, new, table)
+    w.same(dev, table)
+
+
 @pytest.mark.parametrize("dtype,page,n", [("bf16", 64, 1), ("fp32", 20, 37), ("bf16", 4, 2000), ("bf16", 128, 300)])
 def test_copy_pages_between_caches(dtype, page, n):
     a, b = World(n + 3, page, 64, dtype=dtype, seed=1), World(2 * n + 5, page, 64, dtype=dtype, seed=2)
