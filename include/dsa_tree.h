@@ -64,7 +64,7 @@ size_t dsa_tree_workspace_bytes(const dsa_dims *dims, int64_t batch, int64_t n_n
  * NaN: bf16 weights are carried as two terms, which may have either sign.)
  * With idx, pools that drafted tokens complete are not selected from:
  * all of a branch is attended to.
- * For a row of one node, without idx, that is what dsa_cache_append and
+ * The only node of a row has, without idx, what dsa_cache_append and
  * dsa_decode_attn of its token give (not bit for bit). */
 dsa_status dsa_decode_tree_attn(const dsa_dims *dims, const dsa_paged_cache *cache, int64_t batch, const int32_t *lens,
                                 const int32_t *block_table, int64_t n_nodes, const int32_t *offsets,
