@@ -3,11 +3,12 @@
 // A group of d/16 (bf16) or d/8 (fp32) lanes takes some heads of a token.  A lane
 // holds two 16-byte chunks of a head, chosen so that they hold whole pairs
 // (rotate.cuh), the same ones for every head.  A CTA's groups are `tokens` tokens
-// by `slices` shares of their query heads; the first `tokens` groups take the keys
-// too, one token's each.  The sine and cosine of a token's pairs are formed once,
-// by all threads, and shared through shared memory.  The sum of squares is a
-// shuffle over the group.  A CTA goes from block to block of tokens, the next
-// rows on their way while it works on one.
+// by `slices` shares of their query heads; the first of a token's groups takes its
+// key too.  A warp forms the sines and cosines of its own tokens, once for all
+// heads, in its own part of shared memory.  (Formed by all threads for all of a CTA's
+// tokens, with barriers, four slices and two heads ahead: 206 us against 178 for 131072
+// tokens, their gradient 485 against 453.)  The sum of squares is a shuffle over the group.  A CTA goes from block to
+// block of tokens, the next rows on their way while it works on one.
 //
 // Gradient: y = R(w * xn), xn = x r, so with g = R^T dy
 //   dx = r (w g - xn mean(w g xn)),  dw = sum g xn.
@@ -16,7 +17,7 @@
 // sums, in fp64.
 //
 // Bound: HBM, every byte moved once: 131072 tokens of 16 heads of 128 out of a wider
-// projection's rows take 207 us (5.5 TB/s), their gradient 487 (5.9 TB/s); a plain
+// projection's rows take 178 us (6.4 TB/s), their gradient 453 (6.3 TB/s); a plain
 // copy moves 6.8.  Few tokens are bound by the launch and a chain of loads, sines
 // and shuffles: 300 tokens 3.3 us.
 #include "decode.cuh"
@@ -27,12 +28,13 @@ namespace dsa {
 
 constexpr int kHeadThreads = 256;
 constexpr int kHeadSms = 152;
-constexpr int kFwdCtas = 3;               // CTAs an SM
+constexpr int kFwdCtas = 2;               // CTAs an SM
 constexpr int kGradCtas = 2 * kHeadSms;   // CTAs of the gradient kernel: as many as are resident
 
 // How a CTA's groups share a block of tokens.
 struct HeadSplit {
   int tokens, slices;   // tokens * slices groups; slice s takes heads s, s + slices, ..
+  int shift;            // slices = 1 << shift
 };
 
 template <typename T, int D>
@@ -42,7 +44,7 @@ struct HeadLane {
   static constexpr int UN = D / N / 2;                  // lanes per head
   static constexpr int GROUPS = kHeadThreads / UN;      // groups per CTA
   static constexpr int PAIRS = D / 2;                   // at most
-  // of the CTA's tokens, [tokens][PAIRS] each
+  // of all groups, [GROUPS][PAIRS] each
   static constexpr int TURNS = GROUPS * PAIRS;
   int c0, c1;                                           // chunks
   bool rotated, inter;
@@ -55,7 +57,7 @@ struct HeadLane {
     c0 = halves ? u : 2 * u;
     c1 = halves ? u + ru : 2 * u + 1;
   }
-  // this lane's pairs of token `tok` of the block
+  // this lane's pairs of the warp's token `tok`
   __device__ __forceinline__ void turn(const float* turns, int tok, uint64_t (&cs)[H], uint64_t (&sn)[H]) const {
     const uint32_t c = smem_u32(turns + tok * PAIRS + threadIdx.x % UN * N);
 #pragma unroll
@@ -97,11 +99,11 @@ struct HeadLane {
   }
 };
 
-// Cosines, then sines, of all pairs of the block's tokens t0 ..; `back`: the turn's transpose.
+// Cosines, then sines, of all pairs of a warp's tokens t0 ..; `back`: the turn's transpose.
 template <int PAIRS, int TURNS>
 __device__ __forceinline__ void form_turns(const HeadsArgs& a, int64_t t0, int tokens, bool back, float* turns) {
   const int n = a.rot.dim / 2;
-  for (int i = threadIdx.x; i < tokens * PAIRS; i += kHeadThreads) {
+  for (int i = threadIdx.x & 31; i < tokens * PAIRS; i += 32) {
     const int tok = i / PAIRS, f = i % PAIRS;
     if (f >= n || t0 + tok >= a.n_tokens) continue;
     const int64_t pos = a.positions ? ld_live(a.positions + t0 + tok) : t0 + tok;
@@ -124,13 +126,17 @@ __global__ void __launch_bounds__(kHeadThreads, kFwdCtas)
     qk_norm_rotate_kernel(const __grid_constant__ HeadsArgs a, HeadSplit hs) {
   using L = HeadLane<T, D>;
   constexpr int N = L::N, H = L::H, CH = D / N;
-  constexpr int AHEAD = 2;   // heads on their way (4 and two CTAs an SM: 211 us against 208 for 131072 tokens)
-  extern __shared__ __align__(16) float turns[];   // [2][TURNS], as far as tokens fill it
+  constexpr int AHEAD = 4;   // heads on their way (131072 tokens 178 us; 2 and three CTAs an SM 186, 3 184, 6 188)
+  extern __shared__ __align__(16) float all_turns[];   // [2][TURNS], a part for each warp
   chain_wait();
   chain_release();
   const L l(a);
-  const int group = threadIdx.x / L::UN, tok = group / hs.slices, slice = group % hs.slices;
-  const bool keys = a.k != nullptr && group < hs.tokens;   // this group takes the key of the block's token `group`
+  const int group = threadIdx.x / L::UN, tok = group >> hs.shift, slice = group & (hs.slices - 1);
+  const bool keys = a.k != nullptr && slice == 0;   // this group takes its token's key too
+  // the warp's tokens of the block, and their turns
+  constexpr int GW = 32 / L::UN;
+  const int warp = threadIdx.x >> 5, tok0 = warp * GW >> hs.shift, toks = max(GW >> hs.shift, 1);
+  float* turns = all_turns + warp * GW * L::PAIRS;
   const int64_t stride = (int64_t)gridDim.x * hs.tokens;
   uint4 x[AHEAD], y[AHEAD], kx, ky;
   // head h of this group's token of the block at `base`
@@ -143,13 +149,13 @@ __global__ void __launch_bounds__(kHeadThreads, kFwdCtas)
     }
   };
   auto load_key = [&](int64_t base) {
-    if (keys && base + group < a.n_tokens) {
-      const uint4* p = static_cast<const uint4*>(a.k) + (base + group) * (a.k_stride / N);
+    if (keys && base + tok < a.n_tokens) {
+      const uint4* p = static_cast<const uint4*>(a.k) + (base + tok) * (a.k_stride / N);
       kx = ld_live(p + l.c0);
       ky = ld_live(p + l.c1);
     }
   };
-  // a head's chunks, with weights w0, w1 and the turns of the block's token i, to dst
+  // a head's chunks, with weights w0, w1 and the turns of the warp's token i, to dst
   auto finish = [&](uint64_t (&u)[H], uint64_t (&v)[H], const uint64_t (&w0)[H], const uint64_t (&w1)[H], int i, uint4* dst,
                     bool there) {
     uint64_t ss = pair_of(0.f, 0.f);
@@ -181,9 +187,9 @@ __global__ void __launch_bounds__(kHeadThreads, kFwdCtas)
   for (; base < a.n_tokens; base += stride) {
     const int64_t t = base + tok;
     if (a.rot.dim) {
-      __syncthreads();   // the turns of the block before
-      form_turns<L::PAIRS, L::TURNS>(a, base, hs.tokens, false, turns);
-      __syncthreads();
+      __syncwarp();   // the turns of the block before
+      form_turns<L::PAIRS, L::TURNS>(a, base + tok0, toks, false, turns);
+      __syncwarp();
     }
     // all groups make the same rounds, for the shuffles
     for (int h0 = 0; h0 < a.Hq; h0 += AHEAD * hs.slices) {
@@ -196,7 +202,7 @@ __global__ void __launch_bounds__(kHeadThreads, kFwdCtas)
         unpack_pairs<T>(y[i], v);
         load(i, last ? base + stride : base, last ? slice + i * hs.slices : h + AHEAD * hs.slices);
         if (h0 + i * hs.slices < a.Hq)
-          finish(u, v, w0, w1, tok, static_cast<uint4*>(a.q_out) + (t * a.Hq + h) * CH, t < a.n_tokens && h < a.Hq);
+          finish(u, v, w0, w1, tok - tok0, static_cast<uint4*>(a.q_out) + (t * a.Hq + h) * CH, t < a.n_tokens && h < a.Hq);
       }
     }
     if (a.k != nullptr && __any_sync(0xffffffffu, keys)) {
@@ -205,8 +211,7 @@ __global__ void __launch_bounds__(kHeadThreads, kFwdCtas)
       unpack_pairs<T>(ky, v);
       load_key(base + stride);
       l.weights(a.k_weight, k0, k1);
-      const int64_t tk = base + group;
-      finish(u, v, k0, k1, keys ? group : 0, static_cast<uint4*>(a.k_out) + tk * CH, keys && tk < a.n_tokens);
+      finish(u, v, k0, k1, tok - tok0, static_cast<uint4*>(a.k_out) + t * CH, keys && t < a.n_tokens);
     }
   }
 }
@@ -231,12 +236,16 @@ __global__ void __launch_bounds__(kHeadThreads, 2)
     qk_norm_rotate_bwd_kernel(const __grid_constant__ HeadsArgs a, HeadSplit hs) {
   using L = HeadLane<T, D>;
   constexpr int N = L::N, CH = D / N;
-  extern __shared__ __align__(16) float turns[];   // [2][TURNS]; then the groups' sums [GROUPS][D] in its place
+  extern __shared__ __align__(16) float all_turns[];   // [2][TURNS]; then the groups' sums [GROUPS][D] in its place
   chain_wait();
   chain_release();
   const L l(a);
-  const int group = threadIdx.x / L::UN, tok = group / hs.slices, slice = group % hs.slices;
-  const bool keys = a.k != nullptr && group < hs.tokens;   // this group takes the key of the block's token `group`
+  const int group = threadIdx.x / L::UN, tok = group >> hs.shift, slice = group & (hs.slices - 1);
+  const bool keys = a.k != nullptr && slice == 0;   // this group takes its token's key too
+  // the warp's tokens of the block, and their turns
+  constexpr int GW = 32 / L::UN;
+  const int warp = threadIdx.x >> 5, tok0 = warp * GW >> hs.shift, toks = max(GW >> hs.shift, 1);
+  float* turns = all_turns + warp * GW * L::PAIRS;
   float w0[N], w1[N], dq0[N], dq1[N], dk0[N], dk1[N];   // d..: this lane's channels of the weights' gradients
 #pragma unroll
   for (int e = 0; e < N; ++e) dq0[e] = dq1[e] = dk0[e] = dk1[e] = 0.f;
@@ -251,17 +260,17 @@ __global__ void __launch_bounds__(kHeadThreads, 2)
     load_row<N>(gy + l.c0 * N, next.g0);   // dq may be dq_out: a lane reads its own channels before it writes them
     load_row<N>(gy + l.c1 * N, next.g1);
   };
-  // head h of this group's token of the block at `base`; the key of its token `group`
+  // head h of this group's token of the block at `base`; its key
   auto load = [&](int64_t base, int h) {
     const int64_t t = base + tok;
     if (t < a.n_tokens && h < a.Hq)
       load_from(static_cast<const uint4*>(a.q) + t * (a.q_stride / N) + h * CH, a.dq_out + (t * a.Hq + h) * D);
   };
   auto load_key = [&](int64_t base) {
-    if (keys && base + group < a.n_tokens)
-      load_from(static_cast<const uint4*>(a.k) + (base + group) * (a.k_stride / N), a.dk_out + (base + group) * D);
+    if (keys && base + tok < a.n_tokens)
+      load_from(static_cast<const uint4*>(a.k) + (base + tok) * (a.k_stride / N), a.dk_out + (base + tok) * D);
   };
-  // row `now`, of the block's token i: its gradient to gx, its part of the weight's to d0, d1
+  // row `now`, of the warp's token i: its gradient to gx, its part of the weight's to d0, d1
   auto finish = [&](const Row& now, int i, float* gx, bool there, float (&d0)[N], float (&d1)[N]) {
     float u[N], v[N], g0[N], g1[N];
     unpack16<T>(now.x, u);
@@ -313,11 +322,11 @@ __global__ void __launch_bounds__(kHeadThreads, 2)
   else
     load_key(base);
   for (; base < a.n_tokens; base += stride) {
-    const int64_t t = base + tok, tk = base + group;
+    const int64_t t = base + tok;
     if (a.rot.dim) {
-      __syncthreads();   // the turns of the block before
-      form_turns<L::PAIRS, L::TURNS>(a, base, hs.tokens, true, turns);
-      __syncthreads();
+      __syncwarp();   // the turns of the block before
+      form_turns<L::PAIRS, L::TURNS>(a, base + tok0, toks, true, turns);
+      __syncwarp();
     }
     // all groups of a warp make the same rounds, for the shuffles
     for (int h0 = 0; h0 < a.Hq; h0 += hs.slices) {
@@ -329,7 +338,7 @@ __global__ void __launch_bounds__(kHeadThreads, 2)
         load_key(base);
       else
         load(base + stride, slice);
-      finish(now, tok, a.dq + (t * a.Hq + h) * D, t < a.n_tokens && h < a.Hq, dq0, dq1);
+      finish(now, tok - tok0, a.dq + (t * a.Hq + h) * D, t < a.n_tokens && h < a.Hq, dq0, dq1);
     }
     if (warp_keys) {
       const Row now = next;
@@ -338,7 +347,7 @@ __global__ void __launch_bounds__(kHeadThreads, 2)
       else
         load_key(base + stride);
       l.weights(a.k_weight, w0, w1);
-      finish(now, keys ? group : 0, a.dk + tk * D, keys && tk < a.n_tokens, dk0, dk1);
+      finish(now, tok - tok0, a.dk + t * D, keys && t < a.n_tokens, dk0, dk1);
       if (a.Hq) l.weights(a.q_weight, w0, w1);
     }
   }
@@ -347,14 +356,14 @@ __global__ void __launch_bounds__(kHeadThreads, 2)
   for (int which = 0; which < 2; ++which) {
     if ((which ? a.dk_weight : a.dq_weight) == nullptr) continue;
     __syncthreads();
-    float* mine = turns + group * D;
+    float* mine = all_turns + group * D;
     store_row<N>(mine + l.c0 * N, which ? dk0 : dq0);
     store_row<N>(mine + l.c1 * N, which ? dk1 : dq1);
     __syncthreads();
     for (int c = threadIdx.x; c < D; c += kHeadThreads) {
       float s = 0.f;
 #pragma unroll 8
-      for (int g = 0; g < L::GROUPS; ++g) s += turns[g * D + c];
+      for (int g = 0; g < L::GROUPS; ++g) s += all_turns[g * D + c];
       a.ws[((int64_t)blockIdx.x * 2 + which) * D + c] = s;
     }
   }
@@ -389,22 +398,34 @@ __global__ void __launch_bounds__(kWeightThreads) weight_grad_kernel(const float
   }
 }
 
-// Slices of the query heads: a power of two, so that a group has no more than 4,
-// and more while there are not CTAs enough for the SMs.
+// The slices, a power of two, that take the fewest turns: the rounds that `ctas` CTAs
+// make through the blocks of tokens, times a group's heads, its key and what beginning
+// a block takes, as long as half a head.  (16 heads of 128, forward, us with 1, 2, 4, 8
+// and 16 slices: 300 tokens 8.4, 5.5, 4.1, 3.4 and 3.3; 1200 8.4, 5.7, 4.3, 4.1 and 5.2;
+// 4000 10.6, 8.8, 9.6, 10.8 and 13.7; 10000 22.9, 19.7, 18.3, 21.1 and 29.1; 40000 61.4,
+// 57.1, 57.4, 70.6 and 105.)
 template <typename L>
-static HeadSplit head_split(const HeadsArgs& a) {
-  int slices = 1;
-  while (slices < L::GROUPS && slices < a.Hq &&
-         (slices * 4 < a.Hq || a.n_tokens * slices < (int64_t)2 * kHeadSms * L::GROUPS))
-    slices *= 2;
-  return {L::GROUPS / slices, slices};
+static HeadSplit head_split(const HeadsArgs& a, int ctas) {
+  HeadSplit best = {};
+  int64_t least = 0;
+  for (int shift = 0; shift == 0 || (1 << shift) <= L::GROUPS && 1 << (shift - 1) < a.Hq; ++shift) {
+    const int slices = 1 << shift, tokens = L::GROUPS / slices;
+    const int64_t blocks = (a.n_tokens + tokens - 1) / tokens;
+    const int64_t turns = (blocks + ctas - 1) / ctas * (2 * ((a.Hq + slices - 1) / slices) + 3);
+    if (shift == 0 || turns < least) {
+      least = turns;
+      best = {tokens, slices, shift};
+    }
+  }
+  return best;
 }
 
 template <typename T, int D>
 static cudaError_t launch_fwd(const HeadsArgs& a, cudaStream_t s) {
   using L = HeadLane<T, D>;
-  const HeadSplit hs = head_split<L>(a);
-  const int64_t x = (a.n_tokens + hs.tokens - 1) / hs.tokens, most = kFwdCtas * kHeadSms;
+  const int64_t most = kFwdCtas * kHeadSms;
+  const HeadSplit hs = head_split<L>(a, (int)most);
+  const int64_t x = (a.n_tokens + hs.tokens - 1) / hs.tokens;
   return launch_chained(qk_norm_rotate_kernel<T, D>, dim3((unsigned)(x < most ? x : most)), dim3(kHeadThreads), a.rot.dim ? 2 * L::TURNS * sizeof(float) : 0, s, a, hs);
 }
 
@@ -413,7 +434,7 @@ static cudaError_t launch_bwd(const HeadsArgs& a, cudaStream_t s) {
   using L = HeadLane<T, D>;
   unsigned ctas = 0;
   if (a.n_tokens > 0) {
-    const HeadSplit hs = head_split<L>(a);
+    const HeadSplit hs = head_split<L>(a, kGradCtas);
     const int64_t x = (a.n_tokens + hs.tokens - 1) / hs.tokens;
     ctas = (unsigned)(x < kGradCtas ? x : kGradCtas);
     const cudaError_t e = launch_chained(qk_norm_rotate_bwd_kernel<T, D>, dim3(ctas), dim3(kHeadThreads),
