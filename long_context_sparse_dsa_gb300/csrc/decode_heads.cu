@@ -7,17 +7,17 @@
 // key too.  A warp forms the sines and cosines of its own tokens, once for all
 // heads, in its own part of shared memory.  (Formed by all threads for all of a CTA's
 // tokens, with barriers, four slices and two heads ahead: 206 us against 178 for 131072
-// tokens, their gradient 485 against 453.)  The sum of squares is a shuffle over the group.  A CTA goes from block to
-// block of tokens, the next rows on their way while it works on one.
+// tokens, their gradient 485 against 453.)  The sum of squares is a shuffle over the
+// group.  A CTA goes from block to block of tokens, the next rows on their way while it
+// works on one.
 //
 // Gradient: y = R(w * xn), xn = x r, so with g = R^T dy
 //   dx = r (w g - xn mean(w g xn)),  dw = sum g xn.
 // A lane adds up its channels' part of dw over all the heads and tokens it sees;
-// a CTA's groups are added in a fixed order, and a second kernel adds the CTAs'
-// sums, in fp64.
+// a CTA's are added in a fixed order, and a second kernel adds the CTAs' sums.
 //
 // Bound: HBM, every byte moved once: 131072 tokens of 16 heads of 128 out of a wider
-// projection's rows take 178 us (6.4 TB/s), their gradient 453 (6.3 TB/s); a plain
+// projection's rows take 177 us (6.4 TB/s), their gradient 448 (6.4 TB/s); a plain
 // copy moves 6.8.  Few tokens are bound by the launch and a chain of loads, sines
 // and shuffles: 300 tokens 3.3 us.
 #include "decode.cuh"
@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(kHeadThreads, 2)
     qk_norm_rotate_bwd_kernel(const __grid_constant__ HeadsArgs a, HeadSplit hs) {
   using L = HeadLane<T, D>;
   constexpr int N = L::N, CH = D / N;
-  extern __shared__ __align__(16) float all_turns[];   // [2][TURNS]; then the groups' sums [GROUPS][D] in its place
+  extern __shared__ __align__(16) float all_turns[];   // [2][TURNS]; then the warps' sums [2][WARPS][D] in its place
   chain_wait();
   chain_release();
   const L l(a);
@@ -351,51 +351,78 @@ __global__ void __launch_bounds__(kHeadThreads, 2)
       if (a.Hq) l.weights(a.q_weight, w0, w1);
     }
   }
-  static_assert(2 * L::TURNS >= L::GROUPS * D, "the sums fit in the turns' place");
+  if (a.dq_weight == nullptr && a.dk_weight == nullptr) return;
+  // over a warp's groups, then over the warps
+  constexpr int WARPS = kHeadThreads / 32;
+  static_assert(2 * L::TURNS >= 2 * WARPS * D, "the sums fit in the turns' place");
 #pragma unroll
-  for (int which = 0; which < 2; ++which) {
-    if ((which ? a.dk_weight : a.dq_weight) == nullptr) continue;
-    __syncthreads();
-    float* mine = all_turns + group * D;
-    store_row<N>(mine + l.c0 * N, which ? dk0 : dq0);
-    store_row<N>(mine + l.c1 * N, which ? dk1 : dq1);
-    __syncthreads();
-    for (int c = threadIdx.x; c < D; c += kHeadThreads) {
-      float s = 0.f;
-#pragma unroll 8
-      for (int g = 0; g < L::GROUPS; ++g) s += all_turns[g * D + c];
-      a.ws[((int64_t)blockIdx.x * 2 + which) * D + c] = s;
+  for (int o = L::UN; o < 32; o <<= 1)
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      dq0[e] += __shfl_xor_sync(0xffffffffu, dq0[e], o);
+      dq1[e] += __shfl_xor_sync(0xffffffffu, dq1[e], o);
+      dk0[e] += __shfl_xor_sync(0xffffffffu, dk0[e], o);
+      dk1[e] += __shfl_xor_sync(0xffffffffu, dk1[e], o);
     }
+  __syncthreads();
+  if ((threadIdx.x & 31) < L::UN) {
+    float *mq = all_turns + warp * D, *mk = mq + WARPS * D;
+    store_row<N>(mq + l.c0 * N, dq0);
+    store_row<N>(mq + l.c1 * N, dq1);
+    store_row<N>(mk + l.c0 * N, dk0);
+    store_row<N>(mk + l.c1 * N, dk1);
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < 2 * D; i += kHeadThreads) {
+    const float* p = all_turns + i / D * WARPS * D + i % D;
+    float s = p[0];
+#pragma unroll
+    for (int w = 1; w < WARPS; ++w) s += p[w * D];
+    a.ws[(int64_t)blockIdx.x * 2 * D + i] = s;
   }
 }
 
+// s + c with x added: s the rounded sum, c what its roundings left out.
+__device__ __forceinline__ void add_exact(float& s, float& c, float x) {
+  const float t = __fadd_rn(s, x), z = __fsub_rn(t, s);
+  c = __fadd_rn(c, __fadd_rn(__fsub_rn(s, __fsub_rn(t, z)), __fsub_rn(x, z)));
+  s = t;
+}
+
 // Adds up the CTAs' sums: a block per 32 channels of one weight, all of a
-// thread's loads at once (one after the other they took 30 us).
+// thread's loads at once (one after the other they took 30 us).  Sums carry their
+// rounding errors along: as good as fp64, of which the GPU has few units (the gradient
+// of one token 11.8 us with it, 5.7 without).
 constexpr int kWeightThreads = 1024;
 __global__ void __launch_bounds__(kWeightThreads) weight_grad_kernel(const float* parts, int ctas, int d, float* dq_weight,
                                                                      float* dk_weight) {
   constexpr int ROWS = kWeightThreads / 32;
   constexpr int MOST = (kGradCtas + ROWS - 1) / ROWS;
-  __shared__ double part[ROWS][32];
+  __shared__ float2 part[ROWS][33];
   chain_wait();
   chain_release();
   float* out = blockIdx.y ? dk_weight : dq_weight;
   if (out == nullptr) return;
-  const int c = blockIdx.x * 32 + (threadIdx.x & 31), r = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, r = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
   float x[MOST];
 #pragma unroll
   for (int i = 0; i < MOST; ++i)
     x[i] = r + i * ROWS < ctas ? ld_live(parts + ((int64_t)(r + i * ROWS) * 2 + blockIdx.y) * d + c) : 0.f;
-  double s = 0.;
+  float s = x[0], left = 0.f;
 #pragma unroll
-  for (int i = 0; i < MOST; ++i) s += x[i];
-  part[r][threadIdx.x & 31] = s;
+  for (int i = 1; i < MOST; ++i) add_exact(s, left, x[i]);
+  part[r][lane] = make_float2(s, left);
   __syncthreads();
-  if (r == 0) {
-#pragma unroll 8
-    for (int i = 1; i < ROWS; ++i) s += part[i][threadIdx.x];
-    out[c] = (float)s;
+  const float2 y = part[lane][r];   // warp r: channel r of the block
+  s = y.x;
+  left = y.y;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    const float so = __shfl_xor_sync(0xffffffffu, s, o);
+    left += __shfl_xor_sync(0xffffffffu, left, o);
+    add_exact(s, left, so);
   }
+  if (lane == 0) out[blockIdx.x * 32 + r] = fabsf(s) < INFINITY ? s + left : s;   // infinity leaves NaN behind
 }
 
 // The slices, a power of two, that take the fewest turns: the rounds that `ctas` CTAs
