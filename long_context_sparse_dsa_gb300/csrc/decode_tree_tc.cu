@@ -63,7 +63,7 @@ constexpr int kTcThreads = (9 + kTcFetch) * 32;
 constexpr int kTcPools = 32 / kTcFetch;   // pools of a tile that one of them takes
 constexpr int kGroupRows = 256;        // query rows of a CTA
 constexpr int kTileKeys = 128;
-constexpr int kTcJoinThreads = 256;
+constexpr int kTcJoinThreads = 512;
 constexpr float kTcLazyLog2 = 8.f;     // the base lags the running max by at most this (log2 units)
 constexpr float kTcLn2 = 0.6931471805599453f;
 
@@ -988,8 +988,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 // they add up in shared memory, in a fixed order.  (FEW 6 instead of 16 and no loads
 // ahead: 45.9 us against 26.3 in all for 1 row of 128 nodes, 32 heads, 1500 tokens, with
 // the drafts' values read one row at a time.  152 pieces of 256 rows take 9 us, bound by
-// the launch and the L2 cache; ten pieces ahead instead of four 193 against 189 us for
-// 24 rows of up to 61 nodes, one column group a unit slower too.)
+// the launch and the L2 cache; with 8 warps a CTA instead of 16 all took 34.9 us against
+// 34.0 for 1 row of 16 nodes over 131069 tokens, with one column group a unit 37.7.)
 template <int D>
 __global__ void __launch_bounds__(kTcJoinThreads) tree_join_kernel(const __grid_constant__ TcArgs a, int ctas) {
   constexpr int WARPS = kTcJoinThreads / 32;
@@ -1179,7 +1179,7 @@ static cudaError_t launch_tc(TcArgs& a, cudaStream_t s) {
     return cudaErrorInvalidValue;
   e = launch_chained(kern, dim3(kTcSms), dim3(kTcThreads), TcCfg<D>::SMEM, s, q, k, v, a);
   if (e != cudaSuccess) return e;
-  return launch_chained(tree_join_kernel<D>, dim3(4 * kTcSms), dim3(kTcJoinThreads), 0, s, a, kTcSms);
+  return launch_chained(tree_join_kernel<D>, dim3(2 * kTcSms), dim3(kTcJoinThreads), 0, s, a, kTcSms);
 }
 
 cudaError_t launch_tree_tc(const TreeAttnArgs& g, void* ws, cudaStream_t s) {
