@@ -39,11 +39,11 @@
 // from 0 times infinity.
 //
 // Bound: the MMAs and what lies between them.  2 rows of 128 nodes of 32 heads over
-// 32000 tokens take 145 us: 925 TFLOP/s, or 1390 with both terms of P counted, the
+// 32000 tokens take 143 us: 940 TFLOP/s, or 1410 with both terms of P counted, the
 // tensor pipe active on 59% of the cycles.  A tile of 128 keys and 256 query rows takes
 // 2.3 us, 2.16 with the softmax taken out, 1.5 with S and P V alone, one behind the
 // other.  (Two threads for each query row: 119 us against 110 for 64 rows of 8 nodes
-// over 16000 tokens.)  Few nodes are bound by the two launches and the first and last
+// over 16000 tokens, which ask for 78 us of HBM.)  Few nodes are bound by the two launches and the first and last
 // tiles, about 15 us, then by HBM at 5.5 TB/s.
 //
 // Every wait is bounded; on expiry the CTA records a timeout, waits for its own
@@ -745,6 +745,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         };
         // A look at a barrier takes the issuer some 200 cycles, ready or not, so its lanes
         // look at two at once: V and P's first half, then P's second and the next K.
+        // Where a tile is one unit, the next K may well be late, and P V does not wait for it
+        // (64 rows of 8 nodes over 16000 tokens 112 us, 119 with the wait; where it is two,
+        // 8 rows of 128 nodes, 32 heads, 2000 tokens, 69 without and 68 with it).
         const bool odd = lane & 1, more = u + 2 < units;
         uint32_t bar, parity;
         if (!(ok = wait(odd ? phalf(g) : full(it), odd ? par : (it / C::NS) & 1))) break;
@@ -752,12 +755,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         tc_fence_after();
         weigh(0);
         k_full(more ? u + 2 : u, bar, parity);
-        const bool next = odd && more;
-        if (!(ok = wait(next ? bar : phalf(g) + 8, next ? parity : par))) break;
+        const bool k = odd && more && both;
+        if (!(ok = wait(k ? bar : phalf(g) + 8, k ? parity : par))) break;
         tc_fence_after();
         weigh(1);
         g ? ++np1 : ++np0;
         if (more) {
+          if (!both && !(ok = wait(bar, parity))) break;
           form_s(u + 2);
         } else {   // the accumulator's last of the segment
           tc_mma_arrive(pvdone(g));
