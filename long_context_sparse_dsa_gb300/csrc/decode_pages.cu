@@ -11,7 +11,7 @@
 // Bound: the launches, up to 4 in a row, each about 3 us (256 branches released, forked
 // from 64 rows and given pages, with some 36 KB copied for each: 16.4 us, 4 launches); where
 // pages are copied HBM, every byte once in and once out (a cache of 1M tokens, 60% in use:
-// 35.6 us, of which the move some 23 at 6.2 TB/s).
+// 36 us, of which the move some 24 at 6 TB/s).
 #include "decode.cuh"
 #include "decode_pages.h"
 
@@ -476,7 +476,7 @@ static unsigned segments_of(const PagesArgs& a, int64_t& pages_per) {
   if (pages_per < kSegmentMin) pages_per = kSegmentMin;
   return (unsigned)((a.cache.num_pages + pages_per - 1) / pages_per);
 }
-// CTAs that copy pages, at most (8 an SM 36.5 us for a cache of 1M tokens compacted, 16 or 64 35.6).
+// CTAs that copy pages, at most (8 an SM 36.5 us for a cache of 1M tokens compacted, 16 or 64 35.6, in one run).
 constexpr int64_t kMostCopies = 16 * kPageSms;
 // CTAs that share the copy of a page where `pages` are copied: up to 4 while the SMs
 // have room for them, of no less than 4 KB each.  Their number's logarithm.
