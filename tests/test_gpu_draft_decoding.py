@@ -3,7 +3,10 @@ node, the trees attended to, an accepted path committed to pages that were reser
 compacted on the way.  The sequences' own contiguous copies in 64 bits say what every node has to see.  The steps of one test
 are calls, those of the other replays of one captured graph.  Tolerances: those of test_gpu_decode."""
 import math
+import os
 import random
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -12,6 +15,7 @@ import long_context_sparse_dsa_gb300 as dsa
 from test_gpu_decode import DEV, HALF, _built, _check_attn, _dt, _freq, _junk_ws  # noqa: F401
 
 pytestmark = pytest.mark.gpu
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 def _i32(x):
@@ -246,3 +250,55 @@ def test_a_captured_step_decodes():
         torch.cuda.synchronize()
         d.check(up, acc)
         d.check_pages()
+
+
+def test_the_first_call_of_a_process_may_be_captured():
+    """Nothing that a call sets up the first time stands in the way of a capture."""
+    code = """
+import torch, long_context_sparse_dsa_gb300 as dsa
+i32 = dict(dtype=torch.int32, device="cuda")
+for dtype, cap in (("bf16", 64), ("bf16", 65536), ("fp32", 64)):
+    dt = dict(dtype=torch.bfloat16 if dtype == "bf16" else torch.float32, device="cuda")
+    dims = dsa.make_dims(cap, 16, 128, 8, 64, 8, dtype=dtype)
+    cache = dsa.alloc_paged_cache(dims, 8, 16)
+    for x in (cache.k, cache.v, cache.kpool, cache.ktail):
+        x.normal_()
+    refs, missing, remap = torch.zeros(8, **i32), torch.zeros(1, **i32), torch.zeros(8, **i32)
+    lens, new, zero = torch.full((2,), 30, **i32), torch.full((2,), 36, **i32), torch.zeros(2, **i32)
+    table = torch.full((2, cap // 16), -1, **i32)
+    offsets, accepted = torch.tensor([0, 6, 12], **i32), torch.tensor([5, 2], **i32)
+    q, k, v, ki = torch.randn(12, 16, 128, **dt), torch.randn(12, 128, **dt), torch.randn(12, 128, **dt), torch.randn(12, 64, **dt)
+    dq, dk, w = torch.randn(12, 16, 128, device="cuda"), torch.randn(12, 128, device="cuda"), torch.zeros(128, device="cuda")
+    qn, kn, o, lse = torch.empty_like(q), torch.empty_like(k), torch.empty_like(q), torch.empty(12, 16, device="cuda")
+    gq, gk, out = torch.empty_like(dq), torch.empty_like(dk), torch.zeros_like(lens)
+    ws, pws = dsa.alloc_tree_workspace(dims, 2, 12), dsa.alloc_page_workspace(dims, cache, 2)
+    nws = torch.empty(dsa.qk_norm_bwd_workspace_bytes(dims, 12), dtype=torch.uint8, device="cuda")
+    kept = [x.clone() for x in (refs, table, cache.k, cache.v, cache.kpool, cache.ktail)]
+
+    def step():
+        dsa.qk_norm_rotate(dims, q, k, qn, kn, 1e-6)
+        dsa.qk_norm_rotate_bwd(dims, q, k, dq, dk, gq, gk, 1e-6, nws, dq_weight=w)
+        dsa.cache_reserve(dims, cache, refs, zero, new, table, missing, pws)
+        dsa.decode_tree_attn(dims, cache, lens, table, offsets, None, qn, kn, v, o, lse, ws)
+        dsa.cache_commit(dims, cache, lens, table, offsets, None, accepted, kn, v, ki, out)
+        dsa.cache_release(dims, cache, refs, new, table, keep=out)
+        dsa.cache_compact(dims, cache, refs, out, table, remap, missing, pws)
+
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    seen = []
+    for go in (graph.replay, step):
+        for x, y in zip((refs, table, cache.k, cache.v, cache.kpool, cache.ktail), kept):
+            x.copy_(y)
+        go()
+        torch.cuda.synchronize()
+        dsa.check_device_error()
+        seen.append([x.clone() for x in (o, lse, gq, gk, w, out, refs, table, cache.k, cache.kpool, missing)])
+    assert all(torch.equal(x, y) for x, y in zip(*seen)), [torch.equal(x, y) for x, y in zip(*seen)]
+    assert out.tolist() == [36, 33] and missing.item() == 6 and bool(torch.isfinite(o).all())
+print("captured")
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stdout + r.stderr

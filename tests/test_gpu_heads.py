@@ -7,7 +7,7 @@ pair's sizes.  So with P the sum of the pair's magnitudes (or the channel's own,
 half a step of the type.  The gradient's g = R^T dy is off by (b + 2^-22) P(dy); dx = r (w g - xn m), with m the mean of d terms
 w g xn, by r (|w| (b + 2^-22) P + a |w g| + |xn| (mean |w xn| ((b + 2^-22) P + a |g|) + d 2^-24 mean |w g xn|) + a |xn m|),
 twice that for the products' own roundings.  dw sums T Hq terms g xn, each off by (b + 2^-22) P |xn| + a |g xn|, in fp32
-runs and a sum in fp64: T Hq 2^-24 of the terms' magnitudes at most.
+with no more than T Hq additions that round: T Hq 2^-24 of the terms' magnitudes at most.
 """
 import math
 

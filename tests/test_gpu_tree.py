@@ -294,6 +294,30 @@ def test_no_nodes_and_no_rows(cap):
     assert torch.all(o == 7) and torch.all(lse == 7)
 
 
+def test_calls_at_the_same_time(cap):
+    """Calls on two streams, each with its own workspace, in flight together, give the bits that one alone gives."""
+    pg = Paged([900, 1500, 4, 260], 16, seed=59, cap=cap).fill()
+    Hq = 16
+    dims = _dims(pg, Hq)
+    trees = [Trees(pg, n, Hq, seed=57 + i) for i, n in enumerate(([40, 7, 1, 90], [3, 120, 0, 12]))]
+    alone = [_run(pg, tr, dims) for tr in trees]
+    cache, (lens, table) = pg.cache(), pg.args()
+    args = [(*tr.args(), tr.q.to(DEV), tr.k.to(DEV), tr.v.to(DEV)) for tr in trees]
+    outs = [[(torch.zeros_like(o), torch.zeros_like(l)) for _ in range(12)] for o, l in alone]
+    ws = [_ws(dims, 4, tr.q.shape[0]) for tr in trees]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for i in range(12):
+        for j in (0, 1):
+            with torch.cuda.stream(streams[j]):
+                dsa.decode_tree_attn(dims, cache, lens, table, *args[j], *outs[j][i], ws[j])
+    torch.cuda.synchronize()
+    dsa.check_device_error()
+    for j in (0, 1):
+        for o, lse in outs[j]:
+            assert torch.equal(o, alone[j][0]) and torch.equal(lse, alone[j][1])
+
+
 def test_graph_replay_other_streams_and_reproducibility(cap):
     pg = Paged([2000, 150, 0, 31], 16, seed=61, cap=cap).fill()
     Hq = 16
