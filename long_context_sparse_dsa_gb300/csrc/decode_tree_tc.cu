@@ -952,7 +952,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
             if (half == 1) m = fmaxf(m, box_ml[r].x);
           }
-          if (half == 0) tc_bar(1, 256);
+          // Read, so free again, behind the second half too: where the next segment is one tile, and not
+          // its group's last, warps 4-7 have no unit in it and would write their sums, none, at once.
+          tc_bar(1, 256);
         }
       }
       if (live && (both || g == 0)) {
