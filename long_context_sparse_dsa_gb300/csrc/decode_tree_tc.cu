@@ -121,7 +121,9 @@ __device__ __forceinline__ void tc_mbar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(bar) : "memory");
 }
 // Waits for a phase, or one a lane, all lanes together.  The first polls are plain ones: through
-// mbar_wait a phase that had long completed cost 300 cycles, three times a unit.
+// mbar_wait a phase that had long completed cost 300 cycles, three times a unit.  A vote orders
+// no memory: where the lanes look at two barriers, __syncwarp() hands what each lane's phase
+// makes visible on to the others, the issuing one among them.
 __device__ __forceinline__ bool tc_poll(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
@@ -139,8 +141,13 @@ __device__ __noinline__ bool tc_wait_long(uint32_t bar, uint32_t parity, volatil
 __device__ __forceinline__ bool tc_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
 #pragma unroll 1
   for (int i = 0; i < 64; ++i)
-    if (__all_sync(0xffffffffu, tc_poll(bar, parity))) return true;
-  return __all_sync(0xffffffffu, tc_wait_long(bar, parity, abort_flag)) != 0;
+    if (__all_sync(0xffffffffu, tc_poll(bar, parity))) {
+      __syncwarp();
+      return true;
+    }
+  const bool ok = __all_sync(0xffffffffu, tc_wait_long(bar, parity, abort_flag)) != 0;
+  __syncwarp();
+  return ok;
 }
 
 // Holds the barrier's phase open until every cp.async this thread issued so far
