@@ -549,7 +549,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const int pw = warp - 9;
     const int rlo = lane / CH, ch = lane % CH;
     bool ok = true, bad = false;
-    uint32_t it = 0, nseg = 0;
+    uint32_t it = 0, nseg = 0, nq = 0;   // nq: segments whose Q this warp asked for
     auto wait = [&](uint32_t bar, uint32_t parity) {
       if (ok) ok = tc_wait(bar, parity, abort_flag);
       return ok;
@@ -572,6 +572,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int tiles = s.both() ? 2 : 1;
         if (lane == 0) mbar_arrive_expect_tx(qfull, tiles * C::TILE);
         __syncwarp();
+        ++nq;
         if (lane < tiles * 2 * (D / 64)) {
           const int h = lane % (2 * tiles), cb = lane / (2 * tiles);   // 64 rows, 64 columns
           tma_load_2d(sQ + (h >> 1) * C::TILE + cb * C::CB + (h & 1) * (64 * 128), &map_q, qfull, 64 * cb,
@@ -682,16 +683,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
       }
     }
-    // every copy of this thread has landed before the CTA can exit
+    if (!ok) *abort_flag = 1;
+    // Every copy of this warp has landed before the CTA can exit, whoever gave up and when:
+    // its own cp.async, the last items of the ring, the last Q.
     cp_async_commit();
     cp_async_wait<0>();
+    for (uint32_t i = it > C::NS ? it - C::NS : 0; i < it; ++i) mbar_wait(full(i), (i / C::NS) & 1, nullptr);
+    if (nq > 0) mbar_wait(qfull, (nq - 1) & 1, nullptr);
     if (__any_sync(0xffffffffu, bad) && lane == 0) record_error(DSA_DEV_ERR_BAD_PAGE);
-    if (!ok) {
-      *abort_flag = 1;
-      // nor may a TMA write land after that
-      for (uint32_t i = it > C::NS ? it - C::NS : 0; i < it; ++i) mbar_wait(full(i), (i / C::NS) & 1, nullptr);
-      if (nseg > 0 || it > 0) mbar_wait(qfull, nseg & 1, nullptr);
-    }
   } else if (warp == 8) {
     // ------------------------------------------------------------ MMA issuer
     // All lanes go through the loop together, so that what they hand to the MMAs

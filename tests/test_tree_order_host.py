@@ -29,3 +29,18 @@ def test_a_vote_over_barriers_is_followed_by_a_warp_barrier():
     for at in votes:
         rest = body[at:]
         assert rest.index("__syncwarp()") < rest.index("return")
+
+
+def test_fetching_warps_wait_for_what_they_asked_for():
+    """Each Q that a warp asks for is a phase of its barrier, so behind n of them the last phase has parity (n - 1) & 1; the last
+    items of the ring are waited for too.  Both whether this warp gave up or not: another may have, and a TMA copy must not
+    land behind the CTA's end."""
+    code = _code()
+    ask = _body(code, "if (pw == 0) {")
+    assert len(re.findall(r"mbar_arrive_expect_tx\(qfull", code)) == 1 and "mbar_arrive_expect_tx(qfull" in ask and "++nq;" in ask
+    assert code.count("++nq;") == 1 and "nq = 0;" in code
+    fetch = _body(code, "if (warp >= 9) {")
+    end = fetch[fetch.rindex("cp_async_wait<0>();"):]
+    assert "if (nq > 0) mbar_wait(qfull, (nq - 1) & 1, nullptr);" in end and end.count("qfull") == 1
+    assert "for (uint32_t i = it > C::NS ? it - C::NS : 0; i < it; ++i) mbar_wait(full(i), (i / C::NS) & 1, nullptr);" in end
+    assert "{" not in end   # on every way out
