@@ -29,9 +29,10 @@
  *   - Checked where they are used, and reported by dsa_check_device_error: a
  *     row whose offsets do not ascend or that has too many nodes is skipped,
  *     its outputs left as they were (DSA_ERR_BAD_PAGE; of nodes that two other
- *     rows then claim the outputs are undefined); a row of bad length is
- *     taken as empty (DSA_ERR_BAD_PAGE); a parent outside -1 .. i-1 is taken
- *     as -1 (DSA_ERR_BAD_INDEX).
+ *     rows then claim the outputs are undefined, and where offsets[0] or
+ *     offsets[batch] is bad, nodes of other rows that lie outside of it may be
+ *     left alone); a row of bad length is taken as empty (DSA_ERR_BAD_PAGE); a
+ *     parent outside -1 .. i-1 is taken as -1 (DSA_ERR_BAD_INDEX).
  */
 #ifndef DSA_GB300_TREE_H
 #define DSA_GB300_TREE_H

@@ -39,6 +39,7 @@ struct TreeScratch {
 
 // Node t's row, by all threads; -1 where it has none.
 __device__ __forceinline__ int find_row(const TreeView& tv, int64_t t, TreeScratch& ts) {
+  constexpr int kAstray = -2;
   if (threadIdx.x == 0) ts.row = -1;
   __syncthreads();
   auto holds = [&](int64_t b) {
@@ -46,22 +47,35 @@ __device__ __forceinline__ int find_row(const TreeView& tv, int64_t t, TreeScrat
     int n;
     return tree_row(tv, b, from, n) && from <= t && t < from + n;
   };
-  if (tv.batch <= 4 * kAttnThreads) {   // a few loads at once; the offsets of a good batch name one row only
-    for (int64_t b = threadIdx.x; b < tv.batch; b += kAttnThreads)
-      if (holds(b)) atomicMax(&ts.row, (int)b);
-  } else if (threadIdx.x == 0) {
-    int64_t lo = 0, hi = tv.batch;   // offsets[lo] <= t < offsets[hi], if they ascend
-    while (hi - lo > 1) {
-      const int64_t mid = (lo + hi) >> 1;
-      if ((int64_t)ld_live(tv.offsets + mid) <= t)
-        lo = mid;
-      else
-        hi = mid;
+  if (tv.batch > 4 * kAttnThreads) {
+    if (threadIdx.x == 0) {
+      const int64_t half = tv.batch >> 1;
+      const int first = ld_live(tv.offsets), end = ld_live(tv.offsets + tv.batch), middle = ld_live(tv.offsets + half);
+      if (first <= t && t < end) {
+        int64_t lo = middle <= t ? half : 0, hi = middle <= t ? tv.batch : half;   // offsets[lo] <= t < offsets[hi]
+        while (hi - lo > 1) {
+          const int64_t mid = (lo + hi) >> 1;
+          if ((int64_t)ld_live(tv.offsets + mid) <= t)
+            lo = mid;
+          else
+            hi = mid;
+        }
+        ts.row = holds(lo) ? (int)lo : kAstray;
+      }
     }
-    if (holds(lo)) ts.row = (int)lo;
+    __syncthreads();
+    const int row = ts.row;
+    if (row != kAstray) return row;
+    // A bad row's node, or one that bad offsets led astray from its row: those cost their own
+    // rows, and no other.  (All rows for every node that the search finds no row for: 65535
+    // rows and as many nodes behind them 7.9 ms instead of 1.0.)
+    __syncthreads();
   }
+#pragma unroll 4
+  for (int64_t b = threadIdx.x; b < tv.batch; b += kAttnThreads)
+    if (holds(b)) atomicMax(&ts.row, (int)b);   // one row, if they are good
   __syncthreads();
-  return ts.row;
+  return max(ts.row, -1);
 }
 
 template <typename T, int D, int MAXH, bool SEL>
