@@ -51,8 +51,9 @@ size_t dsa_page_workspace_bytes(const dsa_dims *dims, const dsa_paged_cache *cac
  *   block_table  [batch, ceil(L / page_size)], in and out
  *   missing      [1] int32, output: pages that were wanting; 0: all done
  *   cache        k, v, kpool and ktail as in dsa_cache_append
- * A row with a bad length, or with a bad page where its next token goes, asks
- * for nothing (DSA_ERR_BAD_PAGE). */
+ * A row with a bad length, or whose next token would go to a page that lies
+ * outside the cache or that refs counts for nobody, asks for nothing
+ * (DSA_ERR_BAD_PAGE). */
 dsa_status dsa_cache_reserve(const dsa_dims *dims, const dsa_paged_cache *cache, int32_t *refs, int64_t batch,
                              const int32_t *lens, const int32_t *new_lens, int32_t *block_table, int32_t *missing,
                              void *ws, size_t ws_bytes, dsa_stream_t stream);

@@ -239,10 +239,11 @@ __device__ __forceinline__ uint32_t row_wants(const PagesArgs& a, const int32_t*
     n = (uint32_t)(pages_of(to, a.page_size) - pages_of(len, a.page_size));
     if (len % a.page_size) {
       page = ld_live(a.pv.table + b * a.pv.cols + len / a.page_size);
-      if (!page_ok(a, page)) {
+      const int held = page_ok(a, page) ? page_count(a, page) : 0;
+      if (held < 1) {   // not there, or nobody's, which this call may give away
         off = true;
         n = 0;
-      } else if (page_count(a, page) > 1) {
+      } else if (held > 1) {
         n = (n + 1) | kCopyBit;
       }
     }
