@@ -5,12 +5,22 @@
  * refs [num_pages] int32 (device, owned by the caller, all 0 for an empty cache)
  * counts the block-table entries that name a page; a page with 0 is free.  A
  * row of n tokens holds the first ceil(n / page_size) entries of its
- * block-table row.  A decoder's life with it:
+ * block-table row, where n is its length or, while it has room that is not used
+ * yet, the length that the room was reserved for.  A decoder's life with it:
  *   dsa_cache_reserve   before tokens are appended: room for them
  *   dsa_cache_fork      branches of a sequence share all of its pages
  *   dsa_cache_release   a row's end, or its being cut back
  *   dsa_cache_compact   the used pages to the front, before the rest is given up
  *   dsa_cache_copy_pages  pages to another cache, a larger one, say
+ * Entries behind a row's pages are not looked at, so no call can tell unused room
+ * from what an entry happens to hold.  A row with more room than it came to use
+ * (reserved for the deepest drafts, and a shorter path was accepted) gives the rest
+ * back before its next reserve: dsa_cache_release with lens the length that was
+ * reserved and keep the row's own.  A reserve from the row's own length would give
+ * the same columns other pages, and the first ones would stay counted for ever.
+ * dsa_cache_compact in between takes the reserved length too: with the row's own,
+ * the room's entries would keep their old numbers.  A row is forked when its room
+ * has been given back, and reserves again before it grows: it shares its open page.
  * A page that several rows hold is read by all and written by none of them:
  * dsa_cache_reserve gives a row that is going to write to such a page a copy of
  * its own.  Appending past the room that was reserved is not prevented here.
@@ -36,7 +46,8 @@ extern "C" {
 size_t dsa_page_workspace_bytes(const dsa_dims *dims, const dsa_paged_cache *cache, int64_t batch);
 
 /* Room for rows to grow from lens[b] to new_lens[b] tokens (a row with
- * new_lens[b] <= lens[b] asks for nothing):
+ * new_lens[b] <= lens[b] asks for nothing).  Of a row that has room left, the
+ * rest is given back before (above):
  *   - the page that its next token goes to, where lens[b] is not a multiple of
  *     page_size and refs of the page is above 1 before the call, is replaced by
  *     a free one with a copy of the row's tokens in it: the first lens[b] %
@@ -79,15 +90,18 @@ dsa_status dsa_cache_fork(const dsa_dims *dims, const dsa_paged_cache *cache, in
  *         nothing back
  * A row with a bad length or a negative keep is left alone, an entry outside
  * the cache or with no count left is skipped (DSA_ERR_BAD_PAGE).
- * A row that is cut back and then grows again needs the keys of its open pool
- * (ktail), and the cache has those of the last one only: keep[b] has to be a
- * multiple of 4 or within the pool that lens[b] leaves open. */
+ * A row whose tokens are cut back and then grows again needs the keys of its open
+ * pool (ktail), and the cache has those of the last one only: keep[b] has to be a
+ * multiple of 4 or within the pool that the row's last token is in.  Room without
+ * tokens may be given back to any length. */
 dsa_status dsa_cache_release(const dsa_dims *dims, const dsa_paged_cache *cache, int32_t *refs, int64_t batch,
                              const int32_t *lens, const int32_t *keep, int32_t *block_table, dsa_stream_t stream);
 
 /* The used pages to the front: with U pages in use, those numbered U and
  * higher move, in ascending order, to the free pages below U, ascending, with
  * their counts; the rows' tables follow.
+ *   lens         where a row has room that is not used yet, the reserved length:
+ *                columns behind ceil(lens[b] / page_size) keep their old numbers
  *   refs         [num_pages], in and out: 0 from U on
  *   block_table  [batch, ..], in and out.  Rows outside the call that hold
  *                pages have to be mapped by the caller, with remap

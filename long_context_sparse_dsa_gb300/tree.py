@@ -142,7 +142,8 @@ def alloc_page_workspace(dims, cache, batch: int):
 def cache_reserve(dims, cache, refs, lens, new_lens, block_table, missing, ws, stream=None):
     """Pages for rows to grow from lens [batch] to new_lens [batch] int32: free ones, ascending, into block_table, and a
     page of its own, with a copy, for a row whose next token would go to a page that others hold too.  Nothing is changed
-    where missing [1] int32 comes back above 0: so many pages are wanting."""
+    where missing [1] int32 comes back above 0: so many pages are wanting.  Room that a row did not use is given back before
+    the next reserve: ``cache_release`` with lens = the reserved lengths, keep = the rows' own."""
     i32, dev, batch, cols = _dec.torch.int32, cache._device, lens.numel(), -(-dims.L // cache.page_size)
     if not (_dec._cache_ok(dims, cache, _dec._DTYPES[dims.dtype]) and
             refs.dtype is i32 and refs.shape == (cache.pages,) and refs.get_device() == dev and refs.is_contiguous() and
@@ -188,7 +189,8 @@ def cache_fork(dims, cache, refs, lens, block_table, parents, lens_out, table_ou
 
 
 def cache_release(dims, cache, refs, lens, block_table, keep=None, stream=None):
-    """Rows give back the pages behind their first keep [batch] int32 tokens (None: all of them)."""
+    """Rows give back the pages behind their first keep [batch] int32 tokens (None: all of them).  lens: the rows' lengths or,
+    of rows with room that is not used, the reserved ones."""
     i32, dev, batch, cols = _dec.torch.int32, cache._device, lens.numel(), -(-dims.L // cache.page_size)
     if not (_dec._cache_ok(dims, cache, _dec._DTYPES[dims.dtype]) and
             refs.dtype is i32 and refs.shape == (cache.pages,) and refs.get_device() == dev and refs.is_contiguous() and
@@ -207,8 +209,8 @@ def cache_release(dims, cache, refs, lens, block_table, keep=None, stream=None):
 
 
 def cache_compact(dims, cache, refs, lens, block_table, remap, used, ws, stream=None):
-    """The used pages to the front of the cache; the rows' tables follow.  remap [pages] int32: a page's new number, -1 for
-    free ones; used [1] int32: how many are in use."""
+    """The used pages to the front of the cache; the rows' tables follow, as far as lens (reserved lengths, where rows have room
+    that is not used).  remap [pages] int32: a page's new number, -1 for free ones; used [1] int32: how many are in use."""
     i32, batch = _dec.torch.int32, lens.numel()
     _check_all("cache_compact", dims, cache, (
         ("refs", refs, i32, (cache.pages,)), ("lens", lens, i32, (batch,)),
