@@ -382,7 +382,8 @@ __global__ void __launch_bounds__(kHeadThreads, 2)
   }
 }
 
-// s + c with x added: s the rounded sum, c what its roundings left out.
+// s + c with x added: s the rounded sum, c what its roundings left out, each found exactly by
+// Knuth's two-sum (The Art of Computer Programming, volume 2, 4.2.2).
 __device__ __forceinline__ void add_exact(float& s, float& c, float x) {
   const float t = __fadd_rn(s, x), z = __fsub_rn(t, s);
   c = __fadd_rn(c, __fadd_rn(__fsub_rn(s, __fsub_rn(t, z)), __fsub_rn(x, z)));

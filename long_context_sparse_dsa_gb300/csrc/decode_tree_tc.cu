@@ -39,12 +39,13 @@
 // from 0 times infinity.
 //
 // Bound: the MMAs and what lies between them.  2 rows of 128 nodes of 32 heads over
-// 32000 tokens take 143 us: 940 TFLOP/s, or 1410 with both terms of P counted, the
+// 32000 tokens take 144 us: 930 TFLOP/s, or 1400 with both terms of P counted, the
 // tensor pipe active on 59% of the cycles.  A tile of 128 keys and 256 query rows takes
 // 2.3 us, 2.16 with the softmax taken out, 1.5 with S and P V alone, one behind the
-// other.  (Two threads for each query row: 119 us against 110 for 64 rows of 8 nodes
-// over 16000 tokens, which ask for 78 us of HBM.)  Few nodes are bound by the two launches and the first and last
-// tiles, about 15 us, then by HBM at 5.5 TB/s.
+// other.  64 rows of 8 nodes over 16000 tokens take 112 us and ask for 78 of HBM.  (Two
+// threads for each query row: 119 us against 110, before the warp barriers behind the
+// waits.)  Few nodes are bound by the two launches and the first and last tiles, about 15
+// us, then by HBM at 5.5 TB/s.
 //
 // Every wait is bounded; on expiry the CTA records a timeout, waits for its own
 // copies and MMAs and ends (its results are then undefined).
