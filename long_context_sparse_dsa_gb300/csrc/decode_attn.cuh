@@ -911,13 +911,12 @@ __device__ __forceinline__ SlotRow slot_row(const AttnArgs<T>& a, int64_t b, boo
   return sr;
 }
 
-// Query b by one cluster of gridDim.x CTAs: n_steps steps of `sr`.
+// Query b by one cluster of `splits` CTAs, of which this is number `rank`: n_steps steps of `sr`.
 template <typename T, int D, int MAXH, bool SEL, typename ROW>
-__device__ __forceinline__ void attn_by_cluster(const AttnArgs<T>& a, const ROW& sr, int64_t b, int n_steps,
+__device__ __forceinline__ void attn_by_cluster(const AttnArgs<T>& a, const ROW& sr, int64_t b, int n_steps, int splits, int rank,
                                                 unsigned char* dec_smem, bool& bad_page, bool& bad_idx) {
   using P = Piece<T, D, MAXH, SEL>;
   AttnScratch& sc = *reinterpret_cast<AttnScratch*>(dec_smem + P::TILES);
-  const int splits = gridDim.x, rank = blockIdx.x;
   P::run(
       a, sr, b, rank * P::MIN_STEPS, n_steps, splits * P::MIN_STEPS, dec_smem, sc, splits > 1,
       [&](int i, int h, float4 x, float4* at) {

@@ -115,7 +115,8 @@ __global__ void __launch_bounds__(kAttnThreads, (Piece<T, D, MAXH, SEL>::CTAS))
   sr.list = ts.list;
   sr.k_rows = a.k + from * D;
   sr.v_rows = a.v + from * D;
-  attn_by_cluster<T, D, MAXH, SEL>(a.at, sr, t, sr.first + ((sr.count + 3) >> 2), dec_smem, bad_page, bad_idx);
+  attn_by_cluster<T, D, MAXH, SEL>(a.at, sr, t, sr.first + ((sr.count + 3) >> 2), gridDim.x, blockIdx.x,
+                                   dec_smem, bad_page, bad_idx);
   if (bad_idx) record_error(DSA_DEV_ERR_BAD_INDEX);
   if (bad_page) record_error(DSA_DEV_ERR_BAD_PAGE);
 }
