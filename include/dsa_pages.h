@@ -92,7 +92,7 @@ dsa_status dsa_cache_fork(const dsa_dims *dims, const dsa_paged_cache *cache, in
  * the cache or with no count left is skipped (DSA_ERR_BAD_PAGE).
  * A row whose tokens are cut back and then grows again needs the keys of its open
  * pool (ktail), and the cache has those of the last one only: keep[b] has to be a
- * multiple of 4 or within the pool that the row's last token is in.  Room without
+ * multiple of 4 or within the pool that the row's tokens leave open.  Room without
  * tokens may be given back to any length. */
 dsa_status dsa_cache_release(const dsa_dims *dims, const dsa_paged_cache *cache, int32_t *refs, int64_t batch,
                              const int32_t *lens, const int32_t *keep, int32_t *block_table, dsa_stream_t stream);
